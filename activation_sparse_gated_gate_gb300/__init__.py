@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -27,6 +28,9 @@ __all__ = [
     "library",
     "WS_HYBRID_FWD", "WS_HYBRID_BWD", "WS_HYBRID_FWD_TC", "WS_HYBRID_BWD_TC", "WS_FFN_FWD_TC",
     "WS_FFN_FWD_TC_SORTED",
+    "RmsNorm", "twell_rms_norm", "twell_rms_norm_bwd", "twell_rms_norm_bwd_workspace",
+    "QuantFp8", "twell_quant_fp8", "twell_gemm_fp8", "twell_gate_pack_fp8", "status_word",
+    "FP8_BLOCK",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,8 +42,10 @@ FLAG_DENSE_FULL = 2
 FLAG_TIMEOUT = 4
 FLAG_RANGE = 8
 FLAG_BOUNDS = 16
+FP8_BLOCK = 128
 
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_ptr = ctypes.c_void_p
 
 
@@ -99,6 +105,19 @@ _SIGNATURES = {
                                   c_ptr, c_ptr, ctypes.c_size_t, c_ptr, c_ptr]),
     "hybrid_ffn_fwd_noalloc": (c_i32, [c_ptr, ctypes.POINTER(HybridStruct), c_ptr, c_ptr, c_i32,
                                        c_ptr, c_ptr, c_ptr, c_ptr, c_ptr]),
+    "twell_rms_norm": (c_i32, [c_ptr, c_i32, c_i64, c_ptr, c_i32, c_i64, c_ptr, c_i32, c_i32,
+                               c_i32, ctypes.c_float, c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_i64,
+                               c_ptr, c_ptr, c_ptr]),
+    "twell_rms_norm_bwd": (c_i32, [c_ptr, c_i32, c_i64, c_ptr, c_i32, c_ptr, c_ptr, c_i32, c_i64,
+                                   c_ptr, c_i64, c_i32, c_i32, c_ptr, c_i64, c_ptr, c_ptr,
+                                   ctypes.c_size_t, c_ptr]),
+    "twell_rms_norm_bwd_workspace": (ctypes.c_size_t, [c_i32, c_i32]),
+    "twell_quant_fp8": (c_i32, [c_ptr, c_i32, c_i64, c_i32, c_i32, c_i32, c_ptr, c_i64, c_ptr,
+                                c_ptr, c_i64, c_ptr, c_ptr]),
+    "twell_gemm_fp8": (c_i32, [c_ptr, c_i64, c_ptr, c_ptr, c_i64, c_ptr, c_i32, c_i32, c_i32,
+                               c_i32, c_ptr, c_i32, c_i64, c_ptr, c_ptr]),
+    "twell_gate_pack_fp8": (c_i32, [c_ptr, c_i64, c_ptr, c_ptr, c_i64, c_ptr, c_i32, c_i32, c_i32,
+                                    ctypes.POINTER(TwellStruct), c_ptr, c_ptr, c_ptr]),
     "twell_status_string": (ctypes.c_char_p, [c_i32]),
     "twell_gate_pack_wait_limit": (ctypes.c_uint64, [ctypes.c_uint64]),
     "twell_probe_fma": (c_i32, [c_i32, c_i32, c_ptr, ctypes.c_size_t,
@@ -526,3 +545,294 @@ def twell_probe_fma(packed: bool, iters: int, out=None, stream=None, device=None
                                      ctypes.byref(threads), _stream(stream)),
                "twell_probe_fma")
     return out, 2.0 * 16 * iters * threads.value
+
+
+# ------------------------------------------- norm and 8-bit products
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_E4M3 = torch.float8_e4m3fn
+_FLOATS = (torch.bfloat16, torch.float32)
+_STATUS = {}
+
+
+def status_word(device=None):
+    """The device int32 that ``twell_gemm_fp8`` ORs its flags into when the
+    caller gives none (one per device, never cleared by the library)."""
+    device = torch.device(device if device is not None else "cuda")
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    if index not in _STATUS:
+        if torch.cuda.is_current_stream_capturing():
+            # it would live in the graph's own memory
+            raise RuntimeError("call status_word() before the capture begins")
+        _STATUS[index] = torch.zeros((1,), dtype=torch.int32, device=f"cuda:{index}")
+    return _STATUS[index]
+
+
+def _mat(t, dtypes, name, device, shape=None):
+    """Check a [rows][columns] operand whose rows may be apart; returns the
+    elements between rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        want = "a matrix" if shape is None else f"of shape {tuple(shape)}"
+        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s columns must be contiguous")
+    # (a single row has no pitch of its own; any valid one will do)
+    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _vec(t, dtypes, name, device, shape):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _on(stream):
+    """What is allocated for a call belongs to the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _run(name, device, stream, *args):
+    raw = (torch._C._cuda_getCurrentRawStream(device) if stream is None
+           else stream.cuda_stream)
+    fn = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == device:
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, raw)
+    if code != 0:
+        raise TwellError(code, name)
+
+
+def _empty_e4m3(rows, cols, device):
+    """[rows][cols] with its rows on 16-byte boundaries, as the 8-bit products
+    read them."""
+    pitch = (cols + 15) // 16 * 16
+    t = torch.empty((rows, pitch), dtype=_E4M3, device=device)
+    return t if pitch == cols else t[:, :cols]
+
+
+class RmsNorm(NamedTuple):
+    """What ``twell_rms_norm`` returns; None where not asked for."""
+    y: torch.Tensor | None
+    total: torch.Tensor | None
+    q: torch.Tensor | None
+    scale: torch.Tensor | None
+    rstd: torch.Tensor | None
+
+
+def twell_rms_norm(x, weight, residual=None, eps=1e-6, y=None, total=None, q=None, scale=None,
+                   rstd=None, bf16=True, fp8=False, stream=None) -> RmsNorm:
+    """Residual addition and root-mean-square norm of the rows of x [T][D]:
+    total = x + residual, y = total / sqrt(mean(total^2) + eps) * weight.
+
+    x, residual and weight are bf16 or fp32 each; total has residual's type
+    (and may be residual itself).  y is bf16; q and scale hold the same y in
+    e4m3 with a scale for each 128 columns.  Outputs may be given; otherwise
+    y is allocated when ``bf16``, q and scale when ``fp8``, total when there is
+    a residual, and rstd (fp32 [T], for the backward) when ``rstd`` is True."""
+    dev = _device_of(x, "x")
+    ldx = _mat(x, _FLOATS, "x", dev)
+    shape = x.shape
+    T, D = shape
+    _vec(weight, _FLOATS, "weight", dev, (D,))
+    with _on(stream):
+        ldr = ldt = ldy = ldq = r_type = 0
+        if residual is not None:
+            ldr = _mat(residual, _FLOATS, "residual", dev, shape)
+            r_type = _TYPES[residual.dtype]
+            if total is None:
+                total = torch.empty((T, D), dtype=residual.dtype, device=x.device)
+            ldt = _mat(total, (residual.dtype,), "total", dev, shape)
+        elif total is not None:
+            raise ValueError("total is an output of the residual's addition: none is given")
+        if y is None and bf16 and (q is None or fp8):
+            y = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
+        if y is not None:
+            ldy = _mat(y, (torch.bfloat16,), "y", dev, shape)
+        if fp8:
+            if q is None:
+                q = _empty_e4m3(T, D, x.device)
+            if scale is None:
+                scale = torch.empty((T, -(-D // FP8_BLOCK)), dtype=torch.float32,
+                                    device=x.device)
+        if (q is None) != (scale is None):
+            raise ValueError("q and scale are given together")
+        if q is not None:
+            ldq = _mat(q, (_E4M3,), "q", dev, shape)
+            _vec(scale, (torch.float32,), "scale", dev, (T, -(-D // FP8_BLOCK)))
+        if rstd is True:
+            rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
+        elif rstd is False:
+            rstd = None
+        if rstd is not None:
+            _vec(rstd, (torch.float32,), "rstd", dev, (T,))
+        _run("twell_rms_norm", dev, stream, x.data_ptr(), _TYPES[x.dtype], ldx, _addr(residual),
+             r_type, ldr, weight.data_ptr(), _TYPES[weight.dtype], T, D, float(eps), _addr(total),
+             ldt, _addr(y), ldy, _addr(q), ldq, _addr(scale), _addr(rstd))
+    return RmsNorm(y, total, q, scale, rstd)
+
+
+def twell_rms_norm_bwd_workspace(T: int, D: int) -> int:
+    return int(lib().twell_rms_norm_bwd_workspace(T, D))
+
+
+def twell_rms_norm_bwd(total, weight, rstd, dy, dtotal=None, dx=None, dw=None, ws=None,
+                       stream=None):
+    """Backward of ``twell_rms_norm``: (dx, dw), dx in total's type (the
+    gradient of x and of the residual alike) and dw fp32.  ``total`` is the
+    stream after the addition (x itself where there was none), ``dtotal`` its
+    own gradient from further on (may be dx)."""
+    dev = _device_of(total, "total")
+    ld = _mat(total, _FLOATS, "total", dev)
+    shape = total.shape
+    T, D = shape
+    _vec(weight, _FLOATS, "weight", dev, (D,))
+    _vec(rstd, (torch.float32,), "rstd", dev, (T,))
+    lddy = _mat(dy, _FLOATS, "dy", dev, shape)
+    lddt = 0 if dtotal is None else _mat(dtotal, (total.dtype,), "dtotal", dev, shape)
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty((T, D), dtype=total.dtype, device=total.device)
+        if dw is None:
+            dw = torch.empty((D,), dtype=torch.float32, device=total.device)
+        lddx = _mat(dx, (total.dtype,), "dx", dev, shape)
+        _vec(dw, (torch.float32,), "dw", dev, (D,))
+        if ws is None:
+            with torch.cuda.device(dev):
+                ws = _workspace(twell_rms_norm_bwd_workspace(T, D), total.device)
+        _run("twell_rms_norm_bwd", dev, stream, total.data_ptr(), _TYPES[total.dtype], ld,
+             weight.data_ptr(), _TYPES[weight.dtype], rstd.data_ptr(), dy.data_ptr(),
+             _TYPES[dy.dtype], lddy, _addr(dtotal), lddt, T, D, dx.data_ptr(), lddx,
+             dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return dx, dw
+
+
+class QuantFp8(NamedTuple):
+    """What ``twell_quant_fp8`` returns: x [R][C] as q * scale, and (where
+    asked for) its transpose [C][R] as qt * scale_t."""
+    q: torch.Tensor | None
+    scale: torch.Tensor | None
+    qt: torch.Tensor | None
+    scale_t: torch.Tensor | None
+
+
+def twell_quant_fp8(x, block_rows=1, rows=True, transposed=False, out=None,
+                    stream=None) -> QuantFp8:
+    """e4m3 values of x [R][C] (bf16 or fp32) with an fp32 scale for each block
+    of ``block_rows`` (1: activations and gradients, 128: weights) by 128
+    columns; with ``transposed`` also of x's transpose, by its own blocks.
+    ``rows=False`` leaves the untransposed pair out.  ``out``: a QuantFp8 of an
+    earlier call of the same kind to write into."""
+    dev = _device_of(x, "x")
+    ld = _mat(x, _FLOATS, "x", dev)
+    R, C = x.shape
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    if not rows and not transposed:
+        raise ValueError("neither rows nor transposed asked for")
+    sr, sc = -(-R // block_rows), -(-C // FP8_BLOCK)
+    tr, tc = -(-C // block_rows), -(-R // FP8_BLOCK)
+    with _on(stream):
+        f32 = torch.float32
+        q, scale, qt, scale_t = out if out is not None else (None,) * 4
+        if rows and q is None:
+            q = _empty_e4m3(R, C, x.device)
+            scale = torch.empty((sr, sc), dtype=f32, device=x.device)
+        if transposed and qt is None:
+            qt = _empty_e4m3(C, R, x.device)
+            scale_t = torch.empty((tr, tc), dtype=f32, device=x.device)
+        if not rows:
+            q = scale = None
+        if not transposed:
+            qt = scale_t = None
+        ldq = ldqt = 0
+        if rows:
+            ldq = _mat(q, (_E4M3,), "q", dev, (R, C))
+            _vec(scale, (f32,), "scale", dev, (sr, sc))
+        if transposed:
+            ldqt = _mat(qt, (_E4M3,), "qt", dev, (C, R))
+            _vec(scale_t, (f32,), "scale_t", dev, (tr, tc))
+        _run("twell_quant_fp8", dev, stream, x.data_ptr(), _TYPES[x.dtype], ld, R, C, block_rows,
+             _addr(q), ldq, _addr(scale), _addr(qt), ldqt, _addr(scale_t))
+    return QuantFp8(q, scale, qt, scale_t)
+
+
+def _operand(v, name, dev):
+    ld = _mat(v, (_E4M3,), name, dev)
+    if ld % 16 or v.data_ptr() % 16:
+        raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
+    return ld
+
+
+def twell_gemm_fp8(a, a_scale, b, b_scale, out=None, dtype=torch.bfloat16, status=None,
+                   stream=None):
+    """out [M][N] = (a a_scale) (b b_scale)^T on the tensor cores: a [M][K] e4m3
+    with a scale for each 128 of a row, b [N][K] e4m3 with a scale for each
+    128 of a row (b_scale [N][ceil(K/128)]) or each 128 x 128 block (b_scale
+    [ceil(N/128)][ceil(K/128)]); out bf16 or fp32 (``dtype`` where not given)."""
+    dev = _device_of(a, "a")
+    lda, ldb = _operand(a, "a", dev), _operand(b, "b", dev)
+    (M, K), (N, Kb) = a.shape, b.shape
+    if Kb != K:
+        raise ValueError(f"a and b differ in K: {K} and {Kb}")
+    nk = -(-K // FP8_BLOCK)
+    _vec(a_scale, (torch.float32,), "a_scale", dev, (M, nk))
+    block = 1 if isinstance(b_scale, torch.Tensor) and b_scale.shape[0] == N else FP8_BLOCK
+    _vec(b_scale, (torch.float32,), "b_scale", dev, (-(-N // block), nk))
+    with _on(stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype, device=a.device)
+        ldc = _mat(out, _FLOATS, "out", dev, (M, N))
+        if status is None:
+            status = _STATUS.get(dev)
+            if status is None:
+                status = status_word(a.device)
+        _run("twell_gemm_fp8", dev, stream, a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(),
+             ldb, b_scale.data_ptr(), block, M, N, K, out.data_ptr(), _TYPES[out.dtype], ldc,
+             status.data_ptr())
+    return out
+
+
+def twell_gate_pack_fp8(xq, x_scale, wq, w_scale, out: TwELL, z_debug=None, status=None,
+                        stream=None):
+    """``twell_gate_pack`` from 8-bit operands: xq [T][D] with a scale for each
+    128 of a row, wq [F][D] (= W_g^T) with one for each 128 x 128 block."""
+    dev = _device_of(xq, "xq")
+    ldx, ldw = _operand(xq, "xq", dev), _operand(wq, "wq", dev)
+    (T, D), (F, Dw) = xq.shape, wq.shape
+    if Dw != D or out.T != T or out.F != F:
+        raise ValueError("shape mismatch: xq [T][D], wq [F][D], out of T and F")
+    nk = -(-D // FP8_BLOCK)
+    _vec(x_scale, (torch.float32,), "x_scale", dev, (T, nk))
+    _vec(w_scale, (torch.float32,), "w_scale", dev, (-(-F // FP8_BLOCK), nk))
+    if z_debug is not None:
+        _vec(z_debug, (torch.float32,), "z_debug", dev, (T, F))
+    _run("twell_gate_pack_fp8", dev, stream, xq.data_ptr(), ldx, x_scale.data_ptr(),
+         wq.data_ptr(), ldw, w_scale.data_ptr(), T, D, F, ctypes.byref(out.struct),
+         _addr(z_debug), _addr(out.status if status is None else status))
+    return out

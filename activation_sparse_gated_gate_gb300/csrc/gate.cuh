@@ -6,6 +6,9 @@
 
 namespace twell {
 
+// Bound on each pipeline wait, in nanoseconds (twell_gate_pack_wait_limit).
+uint64_t gate_wait_ns();
+
 // True when the decode-size gate kernel handles T tokens of width D
 // (1 <= T <= 256 and at least two K blocks of 64 to split).
 bool gate_decode_supported(int32_t T, int32_t D);

@@ -35,6 +35,7 @@
 #include "common.cuh"
 #include "fused.cuh"
 #include "gate.cuh"
+#include "pack.cuh"
 #include "ptx.cuh"
 
 namespace twell {
@@ -52,21 +53,12 @@ constexpr int32_t kDecodeProjectMaxT = 8;
 constexpr int32_t kGateDecodeMaxT = 192;  // twell_gate_pack: the decode kernel up to here
 constexpr int32_t kFusedMaxD = 256 * 12;
 
-std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};
+std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};  // twell_gate_pack_wait_limit
 
 struct GatePackParams {
-  int32_t T, D, F, n_t, W;
+  int32_t T, D, F;
   int32_t num_m, num_n, num_kb, num_tiles;
-  float* val;
-  uint8_t* col;
-  uint8_t* cnt;
-  int32_t* spill_slot;
-  int32_t spill_cap;
-  int32_t* spill_n;
-  int32_t* spill_rt;
-  float* spill_val;
-  uint32_t* block_bits;  // optional [num_m][F / 32]
-  float* z_debug;
+  PackOut out;
   int32_t* status;
   uint64_t wait_ns;  // bound on each pipeline wait
 };
@@ -81,10 +73,6 @@ struct GateCfg {
   static constexpr int STAGING = 128 * 128;  // a 32-column chunk per epilogue thread
   static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + BAR_BYTES + 1024;
 };
-
-__device__ __forceinline__ void flag(int32_t* status, int32_t bit) {
-  if (status) atomicOr(status, bit);
-}
 
 // A pipeline wait under the call's bound (short bounds are checked on every
 // retry, the default one every 64).
@@ -213,7 +201,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;              // TMEM lane quarter this warp may read
     const int row = q * 32 + lane;       // row of the 128-row tile
-    const int W = p.W;
     int local = 0;
     for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++local) {
       const int m_blk = tile / p.num_n;
@@ -235,97 +222,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int sub = 0; sub < BN / TWELL_TILE; ++sub) {
         const int kt = n_blk * (BN / TWELL_TILE) + sub;
-        if (kt >= p.n_t) break;  // uniform over the CTA
+        if (kt >= p.out.n_t) break;  // uniform over the CTA
         const uint32_t taddr = tmem_base + static_cast<uint32_t>(acc * BN + sub * TWELL_TILE) +
                                (static_cast<uint32_t>(q * 32) << 16);
-        const size_t rt = static_cast<size_t>(valid ? t : 0) * p.n_t + kt;
-        float* vrow = p.val + rt * W;
-        uint8_t* crow = p.col + rt * W;
         uint32_t r[4][32];
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld_32x32b_x32(taddr + ch * 32, r[ch]);
         ptx::tmem_wait_ld();
-        // bitmask of the positive gates of each 32-column chunk of the row
-        uint32_t mk[4];
+        float z[4][32];
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t m = 0;
+        for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (__uint_as_float(r[ch][i]) > 0.0f) m |= 1u << i;
-          mk[ch] = valid ? m : 0u;
-        }
-        if (p.block_bits) {
-          // OR over the warp's 32 rows, one atomic per word and warp
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            const uint32_t any = __reduce_or_sync(0xffffffffu, mk[ch]);
-            if (lane == 0 && any)
-              atomicOr(p.block_bits + static_cast<size_t>(m_blk) * (p.F / 32) + kt * 4 + ch, any);
-          }
-        }
-        int c = 0;
-        if (valid) {
-          if (p.z_debug) {
-            float4* zd = reinterpret_cast<float4*>(p.z_debug + static_cast<size_t>(t) * p.F +
-                                                   kt * TWELL_TILE);
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                zd[ch * 8 + i] = make_float4(
-                    __uint_as_float(r[ch][4 * i]), __uint_as_float(r[ch][4 * i + 1]),
-                    __uint_as_float(r[ch][4 * i + 2]), __uint_as_float(r[ch][4 * i + 3]));
-          }
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            const uint32_t m = mk[ch];
-            if (m == 0u) continue;
-            const int n = __popc(m);
-            if (c < W) {
-              // stage the chunk, then store its actives in column order
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(my_stage + ((j ^ (row & 7)) << 4)) =
-                    make_uint4(r[ch][4 * j], r[ch][4 * j + 1], r[ch][4 * j + 2],
-                               r[ch][4 * j + 3]);
-              uint32_t mm = m;
-              for (int e = c; e < W && mm != 0u; ++e) {
-                const int i = __ffs(mm) - 1;
-                mm &= mm - 1u;
-                vrow[e] = *reinterpret_cast<const float*>(
-                    my_stage + ((((i >> 2) ^ (row & 7)) << 4) | ((i & 3) << 2)));
-                crow[e] = static_cast<uint8_t>(ch * 32 + i);
-              }
-            }
-            c += n;
-          }
-          p.cnt[rt] = static_cast<uint8_t>(c);
-        }
-        const bool spill = valid && c > W;
-        if (spill) {
-          const int slot = atomicAdd(p.spill_n, 1);
-          p.spill_slot[rt] = slot;
-          if (slot < p.spill_cap) {
-            p.spill_rt[slot] = static_cast<int32_t>(rt);
-            float4* dst = reinterpret_cast<float4*>(p.spill_val +
-                                                    static_cast<size_t>(slot) * TWELL_TILE);
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float e[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float v = __uint_as_float(r[ch][4 * i + k]);
-                  e[k] = v > 0.0f ? v : 0.0f;
-                }
-                dst[ch * 8 + i] = make_float4(e[0], e[1], e[2], e[3]);
-              }
-          } else {
-            flag(p.status, TWELL_FLAG_SPILL_FULL);
-          }
-        }
+          for (int i = 0; i < 32; ++i) z[ch][i] = __uint_as_float(r[ch][i]);
+        pack_row_slice(p.out, z, t, valid, m_blk, kt, lane, row, my_stage);
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(&tempty[acc]);
@@ -375,6 +284,9 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& mx, const CUtensor
 }
 
 }  // namespace
+
+uint64_t gate_wait_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+
 }  // namespace twell
 
 extern "C" twell_status twell_gate_pack(const uint16_t* x, const uint16_t* Wg_t, int32_t T,
@@ -395,22 +307,11 @@ extern "C" twell_status twell_gate_pack(const uint16_t* x, const uint16_t* Wg_t,
   p.T = T;
   p.D = D;
   p.F = F;
-  p.n_t = F / TWELL_TILE;
-  p.W = out->width;
   p.num_m = (T + BM - 1) / BM;
   p.num_kb = (D + BK - 1) / BK;
-  p.val = out->val;
-  p.col = out->col;
-  p.cnt = out->cnt;
-  p.spill_slot = out->spill_slot;
-  p.spill_cap = out->spill_cap;
-  p.spill_n = out->spill_n;
-  p.spill_rt = out->spill_rt;
-  p.spill_val = out->spill_val;
-  p.block_bits = out->block_bits;
-  p.z_debug = z_debug;
+  p.out = pack_out(*out, z_debug, status_dev);
   p.status = status_dev;
-  p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  p.wait_ns = gate_wait_ns();
 
   if (cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s) != cudaSuccess) return TWELL_ERR_CUDA;
 
@@ -462,7 +363,7 @@ extern "C" twell_status twell_ffn_decode(const uint16_t* x, const uint16_t* Wg_t
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s) != cudaSuccess) return TWELL_ERR_CUDA;
-  const uint64_t wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  const uint64_t wait_ns = gate_wait_ns();
   // A few tokens: the projection inside the gate kernel (each entry adds a
   // whole row of y with atomics, cheap while entries are few).  More: the
   // gate kernel prefetches the active rows into L2 and the CUDA-core fused

@@ -1,0 +1,128 @@
+// Eight-element pieces of a row: loads widened to fp32, stores rounded once,
+// and e4m3 with the scale of a block of 128.  With VEC the piece is whole and
+// 16-byte aligned; without, its first n elements are touched one by one.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace twell {
+
+constexpr int kFp8Block = 128;                // elements of a row that share a scale
+constexpr float kFp8Max = 448.0f;             // e4m3's largest value
+constexpr float kFp8AmaxMin = 5.42101086e-20f;  // 2^-64: 448 / amax stays finite
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) {
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+// bf16 of two values (round to nearest even), lo in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void narrow(float v, float& o) { o = v; }
+__device__ __forceinline__ void narrow(float v, uint16_t& o) {
+  o = static_cast<uint16_t>(bf16x2(v, 0.0f));
+}
+
+// e4m3 of four values (round to nearest even, saturating; NaN stays NaN), in
+// order from the low byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const float* p, int n, float (&f)[8]) {
+  if (VEC) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < n ? p[j] : 0.0f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&f)[8]) {
+  if (VEC) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(u[k] << 16);
+      f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < n ? widen(p[j]) : 0.0f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, int n, const float (&f)[8]) {
+  if (VEC) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = f[j];
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&f)[8]) {
+  if (VEC) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]),
+                                              bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) narrow(f[j], p[j]);
+  }
+}
+
+// e4m3 of f * inv.
+template <bool VEC>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, int n, const float (&f)[8], float inv) {
+  const uint32_t lo = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+  const uint32_t hi = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+  if (VEC) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = static_cast<uint8_t>((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)));
+  }
+}
+
+__device__ __forceinline__ float amax8(const float (&f)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+  return m;
+}
+
+// Maximum over the 16 lanes (a block of 128 elements) of each half-warp.
+__device__ __forceinline__ float half_warp_max(float m) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+}  // namespace twell

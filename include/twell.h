@@ -156,8 +156,8 @@ twell_status twell_ffn_decode(const uint16_t* x, const uint16_t* Wg_t, const uin
                               void* stream);
 
 /*
- * Bound, in nanoseconds, on each pipeline wait of the gate kernel launched
- * by later twell_gate_pack calls (process-wide; 0 restores the default of
+ * Bound, in nanoseconds, on each pipeline wait of the kernels launched by
+ * later twell_gate_pack, twell_gate_pack_fp8 and twell_gemm_fp8 calls (process-wide; 0 restores the default of
  * 1e9 ns); returns the previous bound.  A wait that runs out sets
  * TWELL_FLAG_TIMEOUT; the kernel then waits (up to 1 s each) for the TMA
  * loads and MMAs it already issued, frees its tensor memory and returns, so
@@ -423,6 +423,111 @@ twell_status hybrid_ffn_bwd_tc(const uint16_t* x, const hybrid_t* h, const float
 twell_status hybrid_ffn_fwd_noalloc(const uint16_t* x, const hybrid_t* h, const uint16_t* Wu_t,
                                     const uint16_t* Wd, int32_t D, float* y, float* u_ell,
                                     float* U_dense, int32_t* status_dev, void* stream);
+
+/* Element types of the operands below that may have either. */
+typedef enum {
+  TWELL_BF16 = 0,
+  TWELL_F32 = 1
+} twell_dtype;
+
+/*
+ * Residual addition and root-mean-square norm, the operator in front of a
+ * (sparse) FFN:  s = x + r,  rstd = 1 / sqrt(mean(s^2) + eps),
+ * y = s rstd w.  s and the statistics are fp32; y comes from the unrounded s.
+ * (The pages leave the block around the FFN open.)
+ *   x [T][D] of x_type, rows ldx elements apart (the other ld's likewise)
+ *   r, total  [T][D] of r_type: the residual stream before and after (total = s
+ *             rounded to r_type; may be r itself).  Both NULL: s = x
+ *   w [D] of w_type
+ *   y         [T][D] bf16, or NULL
+ *   q, scale  [T][D] e4m3 and [T][ceil(D/128)] fp32: y with a scale for each
+ *             128 columns as twell_quant_fp8 gives them, from the unrounded y; or
+ *             both NULL.  At least one of y and q is written
+ *   rstd      [T] fp32 for the backward, or NULL
+ * Any D up to 16384 (TWELL_ERR_UNSUPPORTED above) and any row pitch; pointers
+ * aligned to their elements.  Rows and pitches on 16-byte boundaries with
+ * D % 8 == 0 are read and written 16 bytes at a time, others element by
+ * element.  T may be 0.
+ */
+twell_status twell_rms_norm(const void* x, int32_t x_type, int64_t ldx, const void* r,
+                            int32_t r_type, int64_t ldr, const void* w, int32_t w_type, int32_t T,
+                            int32_t D, float eps, void* total, int64_t ldt, uint16_t* y,
+                            int64_t ldy, uint8_t* q, int64_t ldq, float* scale, float* rstd,
+                            void* stream);
+
+/*
+ * Its backward.  With n = total rstd and g = dy w:
+ *   dx = rstd (g - n mean(g n)) + dtotal      dw = sum over rows of dy n
+ * dx is the gradient of x and of r alike.
+ *   total [T][D] of `type` and rstd [T] as the forward left them (without a
+ *   residual, total is x);  dy [T][D] of dy_type;  dtotal, dx [T][D] of `type`
+ *   (dtotal NULL: the stream ends here; dtotal may be dx itself);
+ *   dw [D] fp32 (overwritten; zeros when T is 0)
+ *   ws: twell_rms_norm_bwd_workspace(T, D) bytes
+ * dw is summed in a fixed order: repeated calls agree bit for bit.
+ */
+twell_status twell_rms_norm_bwd(const void* total, int32_t type, int64_t ld, const void* w,
+                                int32_t w_type, const float* rstd, const void* dy,
+                                int32_t dy_type, int64_t lddy, const void* dtotal, int64_t lddt,
+                                int32_t T, int32_t D, void* dx, int64_t lddx, float* dw, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of twell_rms_norm_bwd on the current device (0 on bad
+ * arguments). */
+size_t twell_rms_norm_bwd_workspace(int32_t T, int32_t D);
+
+/*
+ * Quantisation to 8-bit floating point (e4m3: 4 exponent and 3 mantissa bits,
+ * largest value 448) with an fp32 scale for each block of block_rows x 128
+ * elements, block_rows 1 (activations, gradients) or 128 (weights):
+ *   amax = max(max |v| over the block, 2^-64),
+ *   q = e4m3(v (448 / amax)) (nearest, ties to even),  scale = amax / 448,
+ * so that v is about q scale.  A NaN becomes e4m3's NaN and does not enter
+ * the block's maximum; infinities give an infinite scale and NaN.
+ *   src       [R][C] of `type`, rows ld elements apart
+ *   q, scale  [R][C] (rows ldq bytes apart), [ceil(R/block_rows)][ceil(C/128)]
+ *   qt, scale_t  the transpose [C][R] (rows ldqt bytes apart),
+ *             [ceil(C/block_rows)][ceil(R/128)]; with block_rows 1 its blocks are
+ *             128 rows of one column of src, with 128 they are q's own
+ * Either pair may be NULL.  R or C may be 0 (nothing is written).
+ */
+twell_status twell_quant_fp8(const void* src, int32_t type, int64_t ld, int32_t R, int32_t C,
+                             int32_t block_rows, uint8_t* q, int64_t ldq, float* scale,
+                             uint8_t* qt, int64_t ldqt, float* scale_t, void* stream);
+
+/*
+ * Product of two e4m3 operands with block scales on the tensor cores:
+ *   c[m][n] = sum_k (a[m][k] a_scale[m][k/128]) (b[n][k] b_scale[n/b_block][k/128])
+ * Sums are fp32: in the tensor core within a block of 128, in registers
+ * across blocks, rounded once to c's type.
+ *   a [M][K], a_scale [M][ceil(K/128)]
+ *   b [N][K], b_scale [ceil(N/b_block)][ceil(K/128)], b_block 1 or 128
+ *   lda, ldb  bytes between rows, multiples of 16;  a and b 16-byte aligned
+ *   c [M][N] of c_type, rows ldc elements apart
+ * Any M, N and K >= 1 (M or N 0: nothing to do).  Bytes past K of a row are not
+ * used.  A wait that runs out (twell_gate_pack_wait_limit's bound) sets
+ * TWELL_FLAG_TIMEOUT in *status_dev (may be NULL), c then being undefined.
+ * Repeated calls agree bit for bit.
+ * A linear layer y = x W^T trains on the same product: dx takes (dy, W^T),
+ * dW takes (dy^T, x^T) with b_block 1.
+ */
+twell_status twell_gemm_fp8(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* b,
+                            int64_t ldb, const float* b_scale, int32_t b_block, int32_t M,
+                            int32_t N, int32_t K, void* c, int32_t c_type, int64_t ldc,
+                            int32_t* status_dev, void* stream);
+
+/*
+ * twell_gate_pack from 8-bit operands: z = x W_g as twell_gemm_fp8 computes
+ * it, packed into `out` in the same kernel.
+ *   xq [T][D], x_scale [T][ceil(D/128)]        rows ldx bytes apart
+ *   wq [F][D] (= W_g^T), w_scale [F/128][ceil(D/128)]   rows ldw bytes apart
+ * Any D >= 1; the operands' alignment as in twell_gemm_fp8, the rest as in
+ * twell_gate_pack.
+ */
+twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, const float* x_scale,
+                                 const uint8_t* wq, int64_t ldw, const float* w_scale, int32_t T,
+                                 int32_t D, int32_t F, const twell_t* out, float* z_debug,
+                                 int32_t* status_dev, void* stream);
 
 /*
  * FP32 FMA throughput probe (a measurement helper; the paper has no
