@@ -4,23 +4,42 @@
 // a, b e4m3, and the gate product that ends in the TwELL epilogue.
 //
 // The scales change every 128 of K and along M, so a tile's sum cannot stay
-// in the tensor core's accumulator: each K block is one set of four 128 x BN x 32
-// MMAs into a TMEM buffer of its own, and the epilogue warps add it, scaled,
-// to fp32 sums in registers while the next block's MMAs run into another
-// buffer.  e4m3 products are exact in fp32, so the rounding is that of the
-// fp32 sums alone.
+// in the tensor core's accumulator: each K block is one set of four MMAs (32
+// along K) into a TMEM buffer of its own, and the epilogue warps add it,
+// scaled, to fp32 sums in registers while the next block's MMAs run into
+// another buffer.  e4m3 products are exact in fp32, so the rounding is that of
+// the fp32 sums alone.
 //
-// Persistent kernel, one CTA per SM, 2 + BN / 32 warps:
-//   warp 0    TMA producer: tiles of 128 (K) bytes by 128 rows of a and BN rows
-//             of b, 128-byte swizzle, through a ring of stages
-//   warp 1    TMEM allocator and MMA issuer
-//   the rest  BN / 128 sets of four warps; a thread owns a row and 128 columns:
-//             128 fp32 sums in registers (packed fp32 pairs), read from TMEM in
-//             pieces of 16 columns, two in flight
+// Persistent kernel, one CTA per SM, warps:
+//   0         TMA producer: tiles of 128 bytes (K) by 128 rows, 128-byte
+//             swizzle, through a ring of stages
+//   1         TMEM allocator and MMA issuer
+//   2 ..      BN / 128 sets of four epilogue warps; a thread owns a row and 128
+//             columns: 128 fp32 sums in registers (packed fp32 pairs), read from
+//             TMEM in pieces of 16 columns, two in flight
+// With PAIR two CTAs of a cluster share a tile of 256 x 256 (cta_group::2): each
+// loads its 128 rows of a and half of b's 256 rows, the even CTA issues MMAs of
+// M = 256, and each CTA's TMEM and epilogue hold its own 128 rows by 256
+// columns.  A K block then costs a CTA 32 KB of loads for the MMA work that
+// takes 48 KB in a 128 x 256 tile of its own.  Without PAIR the tile is
+// 128 x 128.
+//
+// TMEM holds two K blocks of a tile, so in the steady state a block's sums have
+// to be in registers 512 cycles after the block before it: the epilogue's
+// chain (wait, read, multiply-add, hand the buffer back) is kept short.  A
+// block's barrier is tried before the block before is done, and its first
+// piece is on its way while the last multiply-adds run; the scales come through
+// shared memory, a round of K blocks at a time, loaded with the K blocks along
+// the lanes (a row's scales are neighbours) one round ahead.
+//
+// C leaves through shared memory: a warp stages 32 rows of 64 bytes (64-byte
+// swizzle) and stores them with TMA, two such pieces in flight, which also
+// clips the tile to M x N.
 //
 // Waits are bounded as in the bf16 gate kernel: a role whose wait runs out sets
-// TWELL_FLAG_TIMEOUT, and the CTA drains its TMA loads and MMAs before it frees
-// the TMEM.
+// TWELL_FLAG_TIMEOUT and waits no more (an epilogue warp still meets the others
+// at their barriers); the CTA drains its TMA loads and MMAs before it frees the
+// TMEM, and both CTAs of a pair meet once more before either leaves.
 #include "common.cuh"
 #include "gate.cuh"
 #include "pack.cuh"
@@ -32,6 +51,11 @@ namespace {
 
 constexpr int BM = 128;
 constexpr int BK = 128;             // e4m3 of a 128-byte row: one scale block
+#ifndef PIECE
+#define PIECE 16
+#endif
+constexpr int kPiece = PIECE;
+constexpr int kPieces = 128 / kPiece;
 constexpr int kTmemCols = 512;
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
 
@@ -48,18 +72,30 @@ struct GemmFp8Params {
   uint64_t wait_ns;
 };
 
-template <int BN>
+template <bool PAIR, bool BROWS>
 struct Fp8Cfg {
-  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int CTAS = PAIR ? 2 : 1;
+  static constexpr int BN = PAIR ? 256 : 128;   // columns of a tile
+  static constexpr int STAGES = 5;
   static constexpr int A_BYTES = BM * BK;
-  static constexpr int B_BYTES = BN * BK;
+  static constexpr int B_ROWS = BN / CTAS;      // rows of b a CTA loads
+  static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int SETS = BN / 128;
+  static constexpr int EPI = 128 * SETS;        // epilogue threads
   static constexpr int BUFS = kTmemCols / BN;
-  static constexpr int STAGING = SETS * 128 * 128;  // 128 bytes per epilogue thread
+  static constexpr int STAGING = EPI * 128;     // 128 bytes per epilogue thread
+  // scales of a round of K blocks, [K block][row], two rounds; rows padded so
+  // that the lanes, along K blocks first, hit different banks
+  static constexpr int ROUND = BROWS ? 4 : 8;
+  static constexpr int A_PITCH = 128 + 32 / ROUND;
+  static constexpr int B_PER = BROWS ? BN : BN / 128;
+  static constexpr int B_PITCH = B_PER + 32 / ROUND;
+  static constexpr int SCALES = 2 * ROUND * (A_PITCH + B_PITCH) * 4;
   static constexpr int BAR_BYTES = 256;
-  static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + BAR_BYTES + 1024;
-  static constexpr int THREADS = 64 + 128 * SETS;
+  static constexpr int SMEM =
+      STAGES * STAGE_BYTES + STAGING + SCALES + BAR_BYTES + 1024;
+  static constexpr int THREADS = 64 + EPI;
 };
 
 // A pipeline wait under the call's bound (short bounds are checked on every
@@ -67,6 +103,14 @@ struct Fp8Cfg {
 __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   return limit_ns >= kDefaultWaitNs ? ptx::mbar_wait(bar, parity, limit_ns)
                                     : ptx::mbar_wait_strict(bar, parity, limit_ns);
+}
+
+__device__ __forceinline__ void tmem_ld_piece(uint32_t taddr, uint32_t (&r)[kPiece]) {
+#if PIECE == 32
+  ptx::tmem_ld_32x32b_x32(taddr, r);
+#else
+  ptx::tmem_ld_32x32b_x16(taddr, r);
+#endif
 }
 
 typedef unsigned long long f32x2;
@@ -90,11 +134,13 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
 
 // BROWS: b has a scale per row (of 1 x 128 blocks), else per 128 x 128 block.
 // PACK: the sums are gate pre-activations and go to a TwELL.
-template <int BN, bool BROWS, bool PACK>
-__global__ void __launch_bounds__(Fp8Cfg<BN>::THREADS, 1)
+template <bool PAIR, bool BROWS, bool PACK>
+__global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                    const __grid_constant__ CUtensorMap tmap_b, const GemmFp8Params p) {
-  using Cfg = Fp8Cfg<BN>;
+                    const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_c, const GemmFp8Params p) {
+  using Cfg = Fp8Cfg<PAIR, BROWS>;
+  constexpr int BN = Cfg::BN;
   constexpr int STAGES = Cfg::STAGES;
   constexpr int BUFS = Cfg::BUFS;
   extern __shared__ uint8_t smem_raw[];
@@ -103,15 +149,18 @@ __global__ void __launch_bounds__(Fp8Cfg<BN>::THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * Cfg::A_BYTES;
   uint8_t* staging = smem + STAGES * Cfg::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING);
+  float* scales = reinterpret_cast<float*>(staging + Cfg::STAGING);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING + Cfg::SCALES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + BUFS;
   uint64_t* drain = tempty + BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* aborted = tmem_slot + 1;
-  uint32_t n_loads = 0;  // stage fills issued (producer thread)
 
+  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+  const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+  const int units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -124,18 +173,23 @@ __global__ void __launch_bounds__(Fp8Cfg<BN>::THREADS, 1)
     }
     for (int b = 0; b < BUFS; ++b) {
       ptx::mbar_init(&tfull[b], 1);
-      ptx::mbar_init(&tempty[b], 4 * Cfg::SETS);
+      ptx::mbar_init(&tempty[b], 4 * Cfg::SETS * Cfg::CTAS);
     }
     ptx::mbar_init(drain, 1);
     *aborted = 0u;
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, kTmemCols);
-    ptx::tmem_relinquish();
+    if (PAIR) {
+      ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
+    } else {
+      ptx::tmem_alloc(tmem_slot, kTmemCols);
+      ptx::tmem_relinquish();
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (PAIR) ptx::cluster_sync();  // both CTAs' barriers and TMEM are there
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -144,50 +198,92 @@ __global__ void __launch_bounds__(Fp8Cfg<BN>::THREADS, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x) {
-        const int m0 = tile / p.num_n * BM;
-        const int n0 = tile % p.num_n * BN;
+      for (int tile = unit; tile < p.num_tiles; tile += units) {
+        const int m0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM;
+        const int n0 = tile % p.num_n * BN + static_cast<int>(rank) * Cfg::B_ROWS;
         for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!pipe_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
             flag(p.status, TWELL_FLAG_TIMEOUT);
             *aborted = 1u;
             goto done;
           }
-          ptx::mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
-          ptx::tma_load_2d(sA + stage * Cfg::A_BYTES, &tmap_a, &full[stage], kb * BK, m0);
-          ptx::tma_load_2d(sB + stage * Cfg::B_BYTES, &tmap_b, &full[stage], kb * BK, n0);
-          ++n_loads;
+          uint8_t* a_dst = sA + stage * Cfg::A_BYTES;
+          uint8_t* b_dst = sB + stage * Cfg::B_BYTES;
+          if (PAIR) {
+            // the even CTA's barrier counts the bytes of both; the odd CTA's loads
+            // of the same phase may be counted before it expects them
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * Cfg::STAGE_BYTES);
+            const uint32_t bar = ptx::mapa(ptx::smem_u32(&full[stage]), 0);
+            ptx::tma_load_2d_pair(a_dst, &tmap_a, bar, kb * BK, m0);
+            ptx::tma_load_2d_pair(b_dst, &tmap_b, bar, kb * BK, n0);
+          } else {
+            ptx::mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
+            ptx::tma_load_2d(a_dst, &tmap_a, &full[stage], kb * BK, m0);
+            ptx::tma_load_2d(b_dst, &tmap_b, &full[stage], kb * BK, n0);
+          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
+      // every stage released: no commit of the even CTA is still on its way to
+      // this CTA's barriers when the two part
+      for (int i = 0; PAIR && i < STAGES; ++i) {
+        if (!pipe_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
+          flag(p.status, TWELL_FLAG_TIMEOUT);
+          *aborted = 1u;
+          goto done;
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(BM, BN);
+    // (the whole warp walks the loop, so that addresses and descriptors stay in
+    // uniform registers; one elected lane issues)
+    if (rank == 0) {
+      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(BM * Cfg::CTAS, BN);
+      const uint64_t desc_a = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sA));
+      const uint64_t desc_b = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sB));
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
-      for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x) {
+      for (int tile = unit; tile < p.num_tiles; tile += units) {
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!pipe_wait(&tempty[buf], bphase ^ 1u, p.wait_ns) ||
-              !pipe_wait(&full[stage], phase, p.wait_ns)) {
-            flag(p.status, TWELL_FLAG_TIMEOUT);
-            *aborted = 1u;
+          // (both barriers are asked before either answer is needed)
+          const bool loaded = ptx::mbar_test_wait(&full[stage], phase);
+          const bool room = ptx::mbar_test_wait(&tempty[buf], bphase ^ 1u);
+          const bool late = (!loaded && !pipe_wait(&full[stage], phase, p.wait_ns)) ||
+                            (!room && !pipe_wait(&tempty[buf], bphase ^ 1u, p.wait_ns));
+          if (__any_sync(0xffffffffu, late)) {
+            if (lane == 0) {
+              flag(p.status, TWELL_FLAG_TIMEOUT);
+              *aborted = 1u;
+            }
             goto done;
           }
           ptx::tc_fence_after();
-          const uint32_t a_addr = ptx::smem_u32(sA + stage * Cfg::A_BYTES);
-          const uint32_t b_addr = ptx::smem_u32(sB + stage * Cfg::B_BYTES);
+          const uint64_t da = desc_a + static_cast<uint32_t>(stage * (Cfg::A_BYTES / 16));
+          const uint64_t db = desc_b + static_cast<uint32_t>(stage * (Cfg::B_BYTES / 16));
+          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+          if (ptx::elect_one_sync()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            ptx::mma_f8(tmem_base + static_cast<uint32_t>(buf * BN),
-                        ptx::sdesc_kmajor_sw128(a_addr + kk * 32),
-                        ptx::sdesc_kmajor_sw128(b_addr + kk * 32), idesc, kk > 0 ? 1u : 0u);
-          ptx::mma_commit(&empty[stage]);
-          ptx::mma_commit(&tfull[buf]);
+            for (int kk = 0; kk < BK / 32; ++kk) {  // 32 bytes along the swizzled row
+              if (PAIR) ptx::mma_f8_pair(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              else ptx::mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            }
+            if (PAIR) {
+              ptx::mma_commit_pair(&tfull[buf]);
+              ptx::mma_commit_pair(&empty[stage]);
+            } else {
+              ptx::mma_commit(&tfull[buf]);
+              ptx::mma_commit(&empty[stage]);
+            }
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -204,75 +300,125 @@ __global__ void __launch_bounds__(Fp8Cfg<BN>::THREADS, 1)
     const int q = warp & 3;                // TMEM lane quarter this warp may read
     const int set = (warp - 2) >> 2;       // its 128 columns of the tile
     const int row = q * 32 + lane;         // its thread's row
-    const int tid = (threadIdx.x - 64) & 127;
-    uint8_t* my_stage = staging + set * 128 * 128 + row * 128;
-    // b's row scales of two K blocks (the staging area is the packing's)
-    float* sb = reinterpret_cast<float*>(staging + set * 128 * 128);
+    const int et = threadIdx.x - 64;       // epilogue thread
+    uint8_t* my_stage = staging + et * 128;
+    constexpr int kRound = Cfg::ROUND;
+    float* a_sc = scales;                                     // [2][kRound][A_PITCH]
+    float* b_sc = scales + 2 * kRound * Cfg::A_PITCH;         // [2][kRound][B_PITCH]
+    constexpr int A_LD = 128 * kRound / Cfg::EPI;
+    constexpr int B_LD = (Cfg::B_PER * kRound + Cfg::EPI - 1) / Cfg::EPI;
+    float a_nx[A_LD], b_nx[B_LD];
+    // this thread's share of the scales of K blocks kb0 .. kb0 + kRound of a tile
+    const auto load_round = [&](int tile, int kb0) {
+      const int r0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM;
+      const int c0 = tile % p.num_n * (BROWS ? BN : BN / 128);
+      const int nb = BROWS ? p.N : (p.N + 127) / 128;
+#pragma unroll
+      for (int j = 0; j < A_LD; ++j) {
+        const int i = et + j * Cfg::EPI, kb = kb0 + i % kRound, r = r0 + i / kRound;
+        a_nx[j] = r < p.M && kb < p.num_kb
+                      ? p.a_scale[static_cast<size_t>(r) * p.num_kb + kb] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < B_LD; ++j) {
+        const int i = et + j * Cfg::EPI, kb = kb0 + i % kRound, c = c0 + i / kRound;
+        b_nx[j] = i < Cfg::B_PER * kRound && c < nb && kb < p.num_kb
+                      ? p.b_scale[static_cast<size_t>(c) * p.num_kb + kb] : 0.0f;
+      }
+    };
     int buf = 0, par = 0;
     uint32_t bphase = 0;
-    for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x) {
-      const int m_blk = tile / p.num_n;
-      const int t = m_blk * BM + row;
-      const int col0 = tile % p.num_n * BN + set * 128;
-      const bool valid = t < p.M;
-      const float* as = p.a_scale + static_cast<size_t>(valid ? t : 0) * p.num_kb;
-      const int bcol = BROWS ? col0 + tid : col0;
-      const bool bvalid = bcol < p.N;
-      const float* bs =
-          p.b_scale + static_cast<size_t>(bvalid ? (BROWS ? bcol : bcol / 128) : 0) * p.num_kb;
-      float sa = valid ? as[0] : 0.0f;
-      float sbv = bvalid ? bs[0] : 0.0f;
+    bool dead = false;
+    const uint32_t tempty0 =
+        ptx::mapa(ptx::smem_u32(tempty), 0);
+    const uint32_t taddr0 =
+        tmem_base + static_cast<uint32_t>(set * 128) + (static_cast<uint32_t>(q * 32) << 16);
+    if (unit < p.num_tiles) load_round(unit, 0);
+    for (int tile = unit; tile < p.num_tiles; tile += units) {
       f32x2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        const float s = BROWS ? sa : sa * sbv;
-        // two buffers of b's scales in turn: whoever writes one again has
-        // passed the barrier that follows its last reads
-        if (BROWS) sb[par * 128 + tid] = sbv;
-        if (kb + 1 < p.num_kb) {
-          sa = valid ? as[kb + 1] : 0.0f;
-          sbv = bvalid ? bs[kb + 1] : 0.0f;
+      // the sums of piece ch of a K block, with its scales
+      uint32_t r[2][kPiece];
+      f32x2 s2 = 0ull;
+      const float* bs = b_sc;
+      const auto add_piece = [&](int ch) {
+#pragma unroll
+        for (int i = 0; i < kPiece / 4; ++i) {
+          f32x2 f0 = s2, f1 = s2;
+          if (BROWS) {
+            const float4 b4 = *reinterpret_cast<const float4*>(bs + ch * kPiece + 4 * i);
+            f0 = mul2(s2, pack2(__float_as_uint(b4.x), __float_as_uint(b4.y)));
+            f1 = mul2(s2, pack2(__float_as_uint(b4.z), __float_as_uint(b4.w)));
+          }
+          const uint32_t* rr = r[ch & 1] + 4 * i;
+          fma2(acc[ch * (kPiece / 2) + 2 * i], pack2(rr[0], rr[1]), f0);
+          fma2(acc[ch * (kPiece / 2) + 2 * i + 1], pack2(rr[2], rr[3]), f1);
         }
-        // the decision must be the same in the whole warp (tcgen05.ld below is
-        // warp-collective), and in the whole set where it meets at a barrier
-        const bool late = !pipe_wait(&tfull[buf], bphase, p.wait_ns);
-        if (BROWS ? ptx::bar_any(1 + set, 128, late) : __any_sync(0xffffffffu, late)) {
+      };
+      bool ready = false;  // this block's barrier has been seen complete
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        const int k8 = kb % kRound;
+        if (k8 == 0) {
+          // two rounds of scales in turn: whoever writes one again has passed
+          // the barrier that follows its last reads
+          par ^= 1;
+#pragma unroll
+          for (int j = 0; j < A_LD; ++j) {
+            const int i = et + j * Cfg::EPI;
+            a_sc[(par * kRound + i % kRound) * Cfg::A_PITCH + i / kRound] = a_nx[j];
+          }
+#pragma unroll
+          for (int j = 0; j < B_LD; ++j) {
+            const int i = et + j * Cfg::EPI;
+            if (i < Cfg::B_PER * kRound)
+              b_sc[(par * kRound + i % kRound) * Cfg::B_PITCH + i / kRound] = b_nx[j];
+          }
+          ptx::bar_sync(1, Cfg::EPI);
+          if (kb + kRound < p.num_kb) load_round(tile, kb + kRound);
+          else if (tile + units < p.num_tiles) load_round(tile + units, 0);
+        }
+        if (dead) continue;
+        // the decision must be warp-uniform: tcgen05.ld is warp-collective
+        if (!__all_sync(0xffffffffu, ready) &&
+            !__all_sync(0xffffffffu, pipe_wait(&tfull[buf], bphase, p.wait_ns))) {
           if (lane == 0) {
             flag(p.status, TWELL_FLAG_TIMEOUT);
             *aborted = 1u;
           }
-          goto done;
+          dead = true;
+          continue;
         }
         ptx::tc_fence_after();
-        const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf * BN + set * 128) +
-                               (static_cast<uint32_t>(q * 32) << 16);
-        const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
-        uint32_t r[2][16];
-        ptx::tmem_ld_32x32b_x16(taddr, r[0]);
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          ptx::tmem_wait_ld();
-          if (ch < 7) {
-            ptx::tmem_ld_32x32b_x16(taddr + (ch + 1) * 16, r[(ch + 1) & 1]);
-          } else {
-            ptx::tc_fence_before();
-            if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            f32x2 f = s2;
-            if (BROWS)
-              f = mul2(s2, *reinterpret_cast<const f32x2*>(sb + par * 128 + ch * 16 + 2 * i));
-            fma2(acc[ch * 8 + i], pack2(r[ch & 1][2 * i], r[ch & 1][2 * i + 1]), f);
-          }
-        }
-        par ^= 1;
+        const uint32_t taddr = taddr0 + static_cast<uint32_t>(buf * BN);
+        tmem_ld_piece(taddr, r[0]);
+        float s = a_sc[(par * kRound + k8) * Cfg::A_PITCH + row];
+        bs = b_sc + (par * kRound + k8) * Cfg::B_PITCH + (BROWS ? set * 128 : set);
+        if (!BROWS) s *= bs[0];
+        s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+        const uint32_t done_bar = tempty0 + buf * 8;
         if (++buf == BUFS) {
           buf = 0;
           bphase ^= 1u;
         }
+#pragma unroll
+        for (int ch = 0; ch < kPieces - 1; ++ch) {
+          ptx::tmem_wait_ld();
+          tmem_ld_piece(taddr + (ch + 1) * kPiece, r[(ch + 1) & 1]);
+          if (ch == kPieces - 2)
+            ready = kb + 1 < p.num_kb && ptx::mbar_test_wait(&tfull[buf], bphase);
+          add_piece(ch);
+        }
+        ptx::tmem_wait_ld();
+        ptx::tc_fence_before();
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar);
+        add_piece(kPieces - 1);
       }
+      if (dead) continue;
+      const int m_blk = tile / p.num_n * Cfg::CTAS + static_cast<int>(rank);
+      const int t = m_blk * BM + row;
+      const int col0 = tile % p.num_n * BN + set * 128;
+      const bool valid = t < p.M;
       float z[4][32];
 #pragma unroll
       for (int i = 0; i < 64; ++i)
@@ -280,27 +426,64 @@ __global__ void __launch_bounds__(Fp8Cfg<BN>::THREADS, 1)
       if (PACK) {
         if (col0 < p.N)
           pack_row_slice(p.out, z, t, valid, m_blk, col0 / TWELL_TILE, lane, row, my_stage);
-      } else if (valid) {
-        const size_t o = static_cast<size_t>(t) * p.ldc + col0;
+      } else {
+        // pieces of 32 rows by 64 bytes, two in flight
+        const int sw = (row >> 1) & 3;
+        uint8_t* mine = staging + (warp - 2) * 4096;
+        const int t0 = m_blk * BM + q * 32;
+        const int cols = p.c_bf16 ? 32 : 16;  // of a piece
+        const auto store_piece = [&](int i, const uint32_t (&v)[16]) {
+          uint8_t* piece = mine + (i & 1) * 2048;
+          const int col = col0 + i * cols;
+          if (lane == 0) ptx::bulk_wait_read<1>();  // the piece before last has left
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int left = p.N - (col0 + 8 * i);
-          if (left <= 0) break;
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = z[i / 4][(i % 4) * 8 + j];
-          if (p.c_bf16) {
-            uint16_t* c = static_cast<uint16_t*>(p.c) + o + 8 * i;
-            if (p.c_vec && left >= 8) store8<true>(c, 8, f);
-            else store8<false>(c, left, f);
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(piece + lane * 64 + ((j ^ sw) << 4)) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          if (p.c_vec) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (t0 < p.M && col < p.N) ptx::tma_store_2d(&tmap_c, piece, col, t0);
+              ptx::bulk_commit();
+            }
           } else {
-            float* c = static_cast<float*>(p.c) + o + 8 * i;
-            if (p.c_vec && left >= 8) store8<true>(c, 8, f);
-            else store8<false>(c, left, f);
+            // rows of C off 16-byte boundaries: element by element
+            __syncwarp();
+            for (int e = lane; e < 32 * cols; e += 32) {
+              const int rr = e / cols, cc = e % cols, b = cc * (64 / cols);
+              if (t0 + rr >= p.M || col + cc >= p.N) continue;
+              const uint8_t* at = piece + rr * 64 + (((b >> 4) ^ ((rr >> 1) & 3)) << 4) + (b & 15);
+              const size_t o = static_cast<size_t>(t0 + rr) * p.ldc + col + cc;
+              if (p.c_bf16)
+                static_cast<uint16_t*>(p.c)[o] = *reinterpret_cast<const uint16_t*>(at);
+              else
+                static_cast<float*>(p.c)[o] = *reinterpret_cast<const float*>(at);
+            }
+            __syncwarp();
+          }
+        };
+        if (p.c_bf16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = bf16x2(z[i][2 * j], z[i][2 * j + 1]);
+            store_piece(i, v);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(z[i / 2][i % 2 * 16 + j]);
+            store_piece(i, v);
           }
         }
       }
     }
+    if (!PACK && lane == 0) ptx::bulk_wait_all();
   }
 
 done:
@@ -308,40 +491,52 @@ done:
   ptx::tc_fence_before();
   __syncthreads();
   if (*aborted) {  // read after the barrier: the same value in every thread
-    if (warp == 0 && lane == 0) {
-      // the last fill of each stage: fills went round the ring in order
-      for (int s = 0; s < STAGES; ++s) {
-        const uint32_t n_s = (n_loads + STAGES - 1 - s) / STAGES;
-        if (n_s > 0 && !ptx::mbar_wait(&full[s], (n_s - 1) & 1u)) break;
-      }
-    }
-    if (warp == 1 && lane == 0) {
+    // the loads in flight may signal a barrier that can no longer complete
+    if (warp == 0 && lane == 0) ptx::spin_ns(1000000);
+    if (warp == 1 && lane == 0 && rank == 0) {
       ptx::tc_fence_after();
-      ptx::mma_commit(drain);  // arrives once every MMA this thread issued is done
+      // arrives once every MMA this thread issued is done
+      if (PAIR) ptx::mma_commit_pair(drain);
+      else ptx::mma_commit(drain);
       ptx::mbar_wait(drain, 0);
     }
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
   }
+  // neither CTA's barriers or TMEM are used by the other from here on
+  if (PAIR) ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, kTmemCols);
+    if (PAIR) ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+    else ptx::tmem_dealloc(tmem_base, kTmemCols);
   }
 }
 
-template <int BN, bool BROWS, bool PACK>
+template <bool PAIR, bool BROWS, bool PACK>
 twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensorMap& mb,
-                    const GemmFp8Params& p, cudaStream_t s) {
-  using Cfg = Fp8Cfg<BN>;
+                    const CUtensorMap& mc, const GemmFp8Params& p, cudaStream_t s) {
+  using Cfg = Fp8Cfg<PAIR, BROWS>;
   static_assert(Cfg::SMEM <= 232448, "shared memory budget");
-  auto kern = gemm_fp8_kernel<BN, BROWS, PACK>;
+  auto kern = gemm_fp8_kernel<PAIR, BROWS, PACK>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) !=
       cudaSuccess)
     return TWELL_ERR_CUDA;
-  const int grid = p.num_tiles < dev.sm_count ? p.num_tiles : dev.sm_count;
-  kern<<<grid, Cfg::THREADS, Cfg::SMEM, s>>>(ma, mb, p);
-  return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+  const int most = dev.sm_count / Cfg::CTAS;
+  const int units = p.num_tiles < most ? p.num_tiles : most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * Cfg::CTAS);
+  cfg.blockDim = dim3(Cfg::THREADS);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = Cfg::CTAS;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, p) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
 // Operand checks shared by the entry points: e4m3 rows on 16-byte boundaries.
@@ -353,24 +548,29 @@ bool operand_ok(const uint8_t* v, int64_t ld, int32_t K, const float* scale) {
 template <bool PACK>
 twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uint8_t* b,
                  int64_t ldb, int32_t b_block, int32_t K, GemmFp8Params p, cudaStream_t s) {
-  const int64_t num_m = (static_cast<int64_t>(p.M) + BM - 1) / BM;
   p.num_kb = (K + BK - 1) / BK;
-  // Wide tiles (N = 256) when they still give every SM work; N = 128 otherwise.
-  const bool wide = num_m * ((p.N + 255) / 256) >= dev.sm_count;
-  const int BN = wide ? 256 : 128;
-  p.num_n = (p.N + BN - 1) / BN;
+  // Pairs of CTAs on 256 x 256 tiles when they still give every SM work, tiles
+  // of 128 x 128 otherwise.
+  const int64_t wide_m = (static_cast<int64_t>(p.M) + 255) / 256;
+  const bool pair = 2 * wide_m * ((p.N + 255) / 256) >= dev.sm_count;
+  const int64_t num_m = pair ? wide_m : (static_cast<int64_t>(p.M) + 127) / 128;
+  p.num_n = pair ? (p.N + 255) / 256 : (p.N + 127) / 128;
   const int64_t tiles = num_m * p.num_n;
   if (tiles > 0x7fffffff - dev.sm_count) return TWELL_ERR_UNSUPPORTED;
   p.num_tiles = static_cast<int32_t>(tiles);
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mc = {};
   twell_status st;
   if ((st = make_tmap_2d(&ma, 1, a, K, p.M, BK, BM, lda, 128)) != TWELL_OK) return st;
-  if ((st = make_tmap_2d(&mb, 1, b, K, p.N, BK, BN, ldb, 128)) != TWELL_OK) return st;
+  if ((st = make_tmap_2d(&mb, 1, b, K, p.N, BK, 128, ldb, 128)) != TWELL_OK) return st;
+  const int ce = p.c_bf16 ? 2 : 4;
+  if (!PACK && p.c_vec &&
+      (st = make_tmap_2d(&mc, ce, p.c, p.N, p.M, 64 / ce, 32, p.ldc * ce, 64)) != TWELL_OK)
+    return st;
   if (PACK || b_block == 128)
-    return wide ? launch<256, false, PACK>(dev, ma, mb, p, s)
-                : launch<128, false, PACK>(dev, ma, mb, p, s);
-  return wide ? launch<256, true, false>(dev, ma, mb, p, s)
-              : launch<128, true, false>(dev, ma, mb, p, s);
+    return pair ? launch<true, false, PACK>(dev, ma, mb, mc, p, s)
+                : launch<false, false, PACK>(dev, ma, mb, mc, p, s);
+  return pair ? launch<true, true, false>(dev, ma, mb, mc, p, s)
+              : launch<false, true, false>(dev, ma, mb, mc, p, s);
 }
 
 }  // namespace
