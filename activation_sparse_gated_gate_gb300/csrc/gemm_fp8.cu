@@ -14,7 +14,9 @@
 //   0         TMA producer: tiles of 128 bytes (K) by 128 rows, 128-byte
 //             swizzle, through a ring of stages
 //   1         TMEM allocator and MMA issuer
-//   2 ..      BN / 128 sets of four epilogue warps; a thread owns a row and 128
+//   2, 3      copy the scales, a round of eight K blocks at a time, into shared
+//             memory (lanes along the K blocks: a row's scales are neighbours)
+//   4 ..      BN / 128 sets of four epilogue warps; a thread owns a row and 128
 //             columns: 128 fp32 sums in registers (packed fp32 pairs), read from
 //             TMEM in pieces of 16 columns, two in flight
 // With PAIR two CTAs of a cluster share a tile of 256 x 256 (cta_group::2): each
@@ -26,20 +28,22 @@
 //
 // TMEM holds two K blocks of a tile, so in the steady state a block's sums have
 // to be in registers 512 cycles after the block before it: the epilogue's
-// chain (wait, read, multiply-add, hand the buffer back) is kept short.  A
-// block's barrier is tried before the block before is done, and its first
-// piece is on its way while the last multiply-adds run; the scales come through
-// shared memory, a round of K blocks at a time, loaded with the K blocks along
-// the lanes (a row's scales are neighbours) one round ahead.
+// chain (wait, read, multiply-add, hand the buffer back) is kept short and
+// in registers: the scales are other warps' work, a block's barrier is tried
+// before the block before is done, and the pair kernel's epilogue warps take
+// registers from the others.  (The shared memory leaves so little L1 that a
+// spilled register comes back from L2: at 8192 x 6144 x 1536 the same loop took
+// 147 us with about 300 bytes of spills in 168 registers, 88 us with 30, and
+// takes 76 us with none in 224.)
 //
 // C leaves through shared memory: a warp stages 32 rows of 64 bytes (64-byte
 // swizzle) and stores them with TMA, two such pieces in flight, which also
 // clips the tile to M x N.
 //
 // Waits are bounded as in the bf16 gate kernel: a role whose wait runs out sets
-// TWELL_FLAG_TIMEOUT and waits no more (an epilogue warp still meets the others
-// at their barriers); the CTA drains its TMA loads and MMAs before it frees the
-// TMEM, and both CTAs of a pair meet once more before either leaves.
+// TWELL_FLAG_TIMEOUT and leaves its loop, the others' waits then run out too; the
+// CTA drains its TMA loads and MMAs before it frees the TMEM, and both CTAs of a
+// pair meet once more before either leaves.
 #include "common.cuh"
 #include "gate.cuh"
 #include "pack.cuh"
@@ -51,12 +55,12 @@ namespace {
 
 constexpr int BM = 128;
 constexpr int BK = 128;             // e4m3 of a 128-byte row: one scale block
-#ifndef PIECE
-#define PIECE 16
-#endif
-constexpr int kPiece = PIECE;
+constexpr int kPiece = 16;            // columns of a TMEM read
 constexpr int kPieces = 128 / kPiece;
 constexpr int kTmemCols = 512;
+// The pair kernel's 384 threads start with 168 registers each; its epilogue
+// threads take 224 and the others keep 56 (4 x 56 + 8 x 224 = 12 x 168).
+constexpr int kRegsStart = 168, kRegsEpi = 224, kRegsOther = 56;
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
 
 struct GemmFp8Params {
@@ -87,7 +91,7 @@ struct Fp8Cfg {
   static constexpr int STAGING = EPI * 128;     // 128 bytes per epilogue thread
   // scales of a round of K blocks, [K block][row], two rounds; rows padded so
   // that the lanes, along K blocks first, hit different banks
-  static constexpr int ROUND = BROWS ? 4 : 8;
+  static constexpr int ROUND = 8;
   static constexpr int A_PITCH = 128 + 32 / ROUND;
   static constexpr int B_PER = BROWS ? BN : BN / 128;
   static constexpr int B_PITCH = B_PER + 32 / ROUND;
@@ -95,7 +99,7 @@ struct Fp8Cfg {
   static constexpr int BAR_BYTES = 256;
   static constexpr int SMEM =
       STAGES * STAGE_BYTES + STAGING + SCALES + BAR_BYTES + 1024;
-  static constexpr int THREADS = 64 + EPI;
+  static constexpr int THREADS = 64 + EPI + 64;
 };
 
 // A pipeline wait under the call's bound (short bounds are checked on every
@@ -103,14 +107,6 @@ struct Fp8Cfg {
 __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   return limit_ns >= kDefaultWaitNs ? ptx::mbar_wait(bar, parity, limit_ns)
                                     : ptx::mbar_wait_strict(bar, parity, limit_ns);
-}
-
-__device__ __forceinline__ void tmem_ld_piece(uint32_t taddr, uint32_t (&r)[kPiece]) {
-#if PIECE == 32
-  ptx::tmem_ld_32x32b_x32(taddr, r);
-#else
-  ptx::tmem_ld_32x32b_x16(taddr, r);
-#endif
 }
 
 typedef unsigned long long f32x2;
@@ -149,12 +145,15 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * Cfg::A_BYTES;
   uint8_t* staging = smem + STAGES * Cfg::STAGE_BYTES;
-  float* scales = reinterpret_cast<float*>(staging + Cfg::STAGING);
+  float* a_sc = reinterpret_cast<float*>(staging + Cfg::STAGING);  // [2][ROUND][A_PITCH]
+  float* b_sc = a_sc + 2 * Cfg::ROUND * Cfg::A_PITCH;               // [2][ROUND][B_PITCH]
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING + Cfg::SCALES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + BUFS;
-  uint64_t* drain = tempty + BUFS;
+  uint64_t* sfull = tempty + BUFS;
+  uint64_t* sempty = sfull + 2;
+  uint64_t* drain = sempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* aborted = tmem_slot + 1;
 
@@ -175,6 +174,10 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
       ptx::mbar_init(&tfull[b], 1);
       ptx::mbar_init(&tempty[b], 4 * Cfg::SETS * Cfg::CTAS);
     }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sfull[i], 64);
+      ptx::mbar_init(&sempty[i], 4 * Cfg::SETS);
+    }
     ptx::mbar_init(drain, 1);
     *aborted = 0u;
     ptx::fence_mbar_init();
@@ -193,228 +196,226 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int tile = unit; tile < p.num_tiles; tile += units) {
-        const int m0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM;
-        const int n0 = tile % p.num_n * BN + static_cast<int>(rank) * Cfg::B_ROWS;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+  if (warp < 4) {
+    if (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int tile = unit; tile < p.num_tiles; tile += units) {
+          const int m0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM;
+          const int n0 = tile % p.num_n * BN + static_cast<int>(rank) * Cfg::B_ROWS;
+          for (int kb = 0; kb < p.num_kb; ++kb) {
+            if (!pipe_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
+              flag(p.status, TWELL_FLAG_TIMEOUT);
+              *aborted = 1u;
+              goto done;
+            }
+            uint8_t* a_dst = sA + stage * Cfg::A_BYTES;
+            uint8_t* b_dst = sB + stage * Cfg::B_BYTES;
+            if (PAIR) {
+              // the even CTA's barrier counts the bytes of both; the odd CTA's loads
+              // of the same phase may be counted before it expects them
+              if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * Cfg::STAGE_BYTES);
+              const uint32_t bar = ptx::mapa(ptx::smem_u32(&full[stage]), 0);
+              ptx::tma_load_2d_pair(a_dst, &tmap_a, bar, kb * BK, m0);
+              ptx::tma_load_2d_pair(b_dst, &tmap_b, bar, kb * BK, n0);
+            } else {
+              ptx::mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
+              ptx::tma_load_2d(a_dst, &tmap_a, &full[stage], kb * BK, m0);
+              ptx::tma_load_2d(b_dst, &tmap_b, &full[stage], kb * BK, n0);
+            }
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // every stage released: no commit of the even CTA is still on its way to
+        // this CTA's barriers when the two part
+        for (int i = 0; PAIR && i < STAGES; ++i) {
           if (!pipe_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
             flag(p.status, TWELL_FLAG_TIMEOUT);
             *aborted = 1u;
             goto done;
           }
-          uint8_t* a_dst = sA + stage * Cfg::A_BYTES;
-          uint8_t* b_dst = sB + stage * Cfg::B_BYTES;
-          if (PAIR) {
-            // the even CTA's barrier counts the bytes of both; the odd CTA's loads
-            // of the same phase may be counted before it expects them
-            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * Cfg::STAGE_BYTES);
-            const uint32_t bar = ptx::mapa(ptx::smem_u32(&full[stage]), 0);
-            ptx::tma_load_2d_pair(a_dst, &tmap_a, bar, kb * BK, m0);
-            ptx::tma_load_2d_pair(b_dst, &tmap_b, bar, kb * BK, n0);
-          } else {
-            ptx::mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
-            ptx::tma_load_2d(a_dst, &tmap_a, &full[stage], kb * BK, m0);
-            ptx::tma_load_2d(b_dst, &tmap_b, &full[stage], kb * BK, n0);
-          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // every stage released: no commit of the even CTA is still on its way to
-      // this CTA's barriers when the two part
-      for (int i = 0; PAIR && i < STAGES; ++i) {
-        if (!pipe_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
-          flag(p.status, TWELL_FLAG_TIMEOUT);
-          *aborted = 1u;
-          goto done;
-        }
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      // (the whole warp walks the loop, so that addresses and descriptors stay in
+      // uniform registers; one elected lane issues)
+      if (rank == 0) {
+        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(BM * Cfg::CTAS, BN);
+        const uint64_t desc_a = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sA));
+        const uint64_t desc_b = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sB));
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, bphase = 0;
+        for (int tile = unit; tile < p.num_tiles; tile += units) {
+          for (int kb = 0; kb < p.num_kb; ++kb) {
+            // (both barriers are asked before either answer is needed)
+            const bool loaded = ptx::mbar_test_wait(&full[stage], phase);
+            const bool room = ptx::mbar_test_wait(&tempty[buf], bphase ^ 1u);
+            const bool late = (!loaded && !pipe_wait(&full[stage], phase, p.wait_ns)) ||
+                              (!room && !pipe_wait(&tempty[buf], bphase ^ 1u, p.wait_ns));
+            if (__any_sync(0xffffffffu, late)) {
+              if (lane == 0) {
+                flag(p.status, TWELL_FLAG_TIMEOUT);
+                *aborted = 1u;
+              }
+              goto done;
+            }
+            ptx::tc_fence_after();
+            const uint64_t da = desc_a + static_cast<uint32_t>(stage * (Cfg::A_BYTES / 16));
+            const uint64_t db = desc_b + static_cast<uint32_t>(stage * (Cfg::B_BYTES / 16));
+            const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+            if (ptx::elect_one_sync()) {
+#pragma unroll
+              for (int kk = 0; kk < BK / 32; ++kk) {  // 32 bytes along the swizzled row
+                if (PAIR) ptx::mma_f8_pair(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                else ptx::mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              }
+              if (PAIR) {
+                ptx::mma_commit_pair(&tfull[buf]);
+                ptx::mma_commit_pair(&empty[stage]);
+              } else {
+                ptx::mma_commit(&tfull[buf]);
+                ptx::mma_commit(&empty[stage]);
+              }
+            }
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if (++buf == BUFS) {
+              buf = 0;
+              bphase ^= 1u;
+            }
+          }
         }
       }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
-    // (the whole warp walks the loop, so that addresses and descriptors stay in
-    // uniform registers; one elected lane issues)
-    if (rank == 0) {
-      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(BM * Cfg::CTAS, BN);
-      const uint64_t desc_a = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sA));
-      const uint64_t desc_b = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sB));
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
+    } else {
+      // -------------------------------------------------------------- scales
+      // thread (r, k) of 8 x 8 copies every eighth row's scale of K block k of a
+      // round (zeros past M, N and the last block); a round has the time of the
+      // eight K blocks before it to arrive
+      constexpr int R = Cfg::ROUND, STEP = 64 / R;
+      const int lt = threadIdx.x - 64, k = lt % R, r = lt / R;
+      const int nb = BROWS ? p.N : (p.N + 127) / 128;
+      int par = 0;
+      uint32_t phase = 0;
       for (int tile = unit; tile < p.num_tiles; tile += units) {
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          // (both barriers are asked before either answer is needed)
-          const bool loaded = ptx::mbar_test_wait(&full[stage], phase);
-          const bool room = ptx::mbar_test_wait(&tempty[buf], bphase ^ 1u);
-          const bool late = (!loaded && !pipe_wait(&full[stage], phase, p.wait_ns)) ||
-                            (!room && !pipe_wait(&tempty[buf], bphase ^ 1u, p.wait_ns));
-          if (__any_sync(0xffffffffu, late)) {
-            if (lane == 0) {
-              flag(p.status, TWELL_FLAG_TIMEOUT);
-              *aborted = 1u;
-            }
+        const int a0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM + r;
+        const int b0 = tile % p.num_n * Cfg::B_PER + r;
+        for (int kb = k; kb < p.num_kb + k; kb += R) {
+          if (!pipe_wait(&sempty[par], phase ^ 1u, p.wait_ns)) {
+            flag(p.status, TWELL_FLAG_TIMEOUT);
+            *aborted = 1u;
             goto done;
           }
-          ptx::tc_fence_after();
-          const uint64_t da = desc_a + static_cast<uint32_t>(stage * (Cfg::A_BYTES / 16));
-          const uint64_t db = desc_b + static_cast<uint32_t>(stage * (Cfg::B_BYTES / 16));
-          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-          if (ptx::elect_one_sync()) {
-#pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk) {  // 32 bytes along the swizzled row
-              if (PAIR) ptx::mma_f8_pair(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-              else ptx::mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-            }
-            if (PAIR) {
-              ptx::mma_commit_pair(&tfull[buf]);
-              ptx::mma_commit_pair(&empty[stage]);
-            } else {
-              ptx::mma_commit(&tfull[buf]);
-              ptx::mma_commit(&empty[stage]);
-            }
+          const uint32_t a_to = ptx::smem_u32(a_sc + (par * R + k) * Cfg::A_PITCH + r);
+          const uint32_t b_to = ptx::smem_u32(b_sc + (par * R + k) * Cfg::B_PITCH + r);
+          for (int j = 0; j < 128; j += STEP) {
+            const bool in = a0 + j < p.M && kb < p.num_kb;
+            ptx::cp_async4(a_to + j * 4,
+                           p.a_scale + (in ? static_cast<size_t>(a0 + j) * p.num_kb + kb : 0),
+                           in ? 4u : 0u);
           }
-          __syncwarp();
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          for (int j = 0; r + j < Cfg::B_PER; j += STEP) {
+            const bool in = b0 + j < nb && kb < p.num_kb;
+            ptx::cp_async4(b_to + j * 4,
+                           p.b_scale + (in ? static_cast<size_t>(b0 + j) * p.num_kb + kb : 0),
+                           in ? 4u : 0u);
           }
-          if (++buf == BUFS) {
-            buf = 0;
-            bphase ^= 1u;
-          }
+          ptx::cp_async_commit();
+          ptx::cp_async_wait<0>();
+          ptx::mbar_arrive(&sfull[par]);
+          par ^= 1;
+          if (par == 0) phase ^= 1u;
         }
       }
     }
   } else {
+    if (PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                // TMEM lane quarter this warp may read
-    const int set = (warp - 2) >> 2;       // its 128 columns of the tile
+    const int set = (warp - 4) >> 2;       // its 128 columns of the tile
     const int row = q * 32 + lane;         // its thread's row
-    const int et = threadIdx.x - 64;       // epilogue thread
-    uint8_t* my_stage = staging + et * 128;
+    uint8_t* my_stage = staging + (threadIdx.x - 128) * 128;
     constexpr int kRound = Cfg::ROUND;
-    float* a_sc = scales;                                     // [2][kRound][A_PITCH]
-    float* b_sc = scales + 2 * kRound * Cfg::A_PITCH;         // [2][kRound][B_PITCH]
-    constexpr int A_LD = 128 * kRound / Cfg::EPI;
-    constexpr int B_LD = (Cfg::B_PER * kRound + Cfg::EPI - 1) / Cfg::EPI;
-    float a_nx[A_LD], b_nx[B_LD];
-    // this thread's share of the scales of K blocks kb0 .. kb0 + kRound of a tile
-    const auto load_round = [&](int tile, int kb0) {
-      const int r0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM;
-      const int c0 = tile % p.num_n * (BROWS ? BN : BN / 128);
-      const int nb = BROWS ? p.N : (p.N + 127) / 128;
-#pragma unroll
-      for (int j = 0; j < A_LD; ++j) {
-        const int i = et + j * Cfg::EPI, kb = kb0 + i % kRound, r = r0 + i / kRound;
-        a_nx[j] = r < p.M && kb < p.num_kb
-                      ? p.a_scale[static_cast<size_t>(r) * p.num_kb + kb] : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < B_LD; ++j) {
-        const int i = et + j * Cfg::EPI, kb = kb0 + i % kRound, c = c0 + i / kRound;
-        b_nx[j] = i < Cfg::B_PER * kRound && c < nb && kb < p.num_kb
-                      ? p.b_scale[static_cast<size_t>(c) * p.num_kb + kb] : 0.0f;
-      }
-    };
     int buf = 0, par = 0;
-    uint32_t bphase = 0;
-    bool dead = false;
-    const uint32_t tempty0 =
-        ptx::mapa(ptx::smem_u32(tempty), 0);
+    uint32_t bphase = 0, sphase = 0;
+    const uint32_t tempty0 = ptx::mapa(ptx::smem_u32(tempty), 0);
     const uint32_t taddr0 =
         tmem_base + static_cast<uint32_t>(set * 128) + (static_cast<uint32_t>(q * 32) << 16);
-    if (unit < p.num_tiles) load_round(unit, 0);
     for (int tile = unit; tile < p.num_tiles; tile += units) {
       f32x2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      // the sums of piece ch of a K block, with its scales
-      uint32_t r[2][kPiece];
-      f32x2 s2 = 0ull;
-      const float* bs = b_sc;
-      const auto add_piece = [&](int ch) {
-#pragma unroll
-        for (int i = 0; i < kPiece / 4; ++i) {
-          f32x2 f0 = s2, f1 = s2;
-          if (BROWS) {
-            const float4 b4 = *reinterpret_cast<const float4*>(bs + ch * kPiece + 4 * i);
-            f0 = mul2(s2, pack2(__float_as_uint(b4.x), __float_as_uint(b4.y)));
-            f1 = mul2(s2, pack2(__float_as_uint(b4.z), __float_as_uint(b4.w)));
-          }
-          const uint32_t* rr = r[ch & 1] + 4 * i;
-          fma2(acc[ch * (kPiece / 2) + 2 * i], pack2(rr[0], rr[1]), f0);
-          fma2(acc[ch * (kPiece / 2) + 2 * i + 1], pack2(rr[2], rr[3]), f1);
-        }
-      };
       bool ready = false;  // this block's barrier has been seen complete
       for (int kb = 0; kb < p.num_kb; ++kb) {
         const int k8 = kb % kRound;
-        if (k8 == 0) {
-          // two rounds of scales in turn: whoever writes one again has passed
-          // the barrier that follows its last reads
-          par ^= 1;
-#pragma unroll
-          for (int j = 0; j < A_LD; ++j) {
-            const int i = et + j * Cfg::EPI;
-            a_sc[(par * kRound + i % kRound) * Cfg::A_PITCH + i / kRound] = a_nx[j];
-          }
-#pragma unroll
-          for (int j = 0; j < B_LD; ++j) {
-            const int i = et + j * Cfg::EPI;
-            if (i < Cfg::B_PER * kRound)
-              b_sc[(par * kRound + i % kRound) * Cfg::B_PITCH + i / kRound] = b_nx[j];
-          }
-          ptx::bar_sync(1, Cfg::EPI);
-          if (kb + kRound < p.num_kb) load_round(tile, kb + kRound);
-          else if (tile + units < p.num_tiles) load_round(tile + units, 0);
-        }
-        if (dead) continue;
-        // the decision must be warp-uniform: tcgen05.ld is warp-collective
-        if (!__all_sync(0xffffffffu, ready) &&
-            !__all_sync(0xffffffffu, pipe_wait(&tfull[buf], bphase, p.wait_ns))) {
+        // the decisions must be warp-uniform: tcgen05.ld is warp-collective
+        bool late = k8 == 0 && !pipe_wait(&sfull[par], sphase, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ready) && !late)
+          late = !pipe_wait(&tfull[buf], bphase, p.wait_ns);
+        if (__any_sync(0xffffffffu, late)) {
           if (lane == 0) {
             flag(p.status, TWELL_FLAG_TIMEOUT);
             *aborted = 1u;
           }
-          dead = true;
-          continue;
+          goto done;
         }
         ptx::tc_fence_after();
         const uint32_t taddr = taddr0 + static_cast<uint32_t>(buf * BN);
-        tmem_ld_piece(taddr, r[0]);
+        uint32_t r[2][kPiece];
+        ptx::tmem_ld_32x32b_x16(taddr, r[0]);
         float s = a_sc[(par * kRound + k8) * Cfg::A_PITCH + row];
-        bs = b_sc + (par * kRound + k8) * Cfg::B_PITCH + (BROWS ? set * 128 : set);
+        const float* bs = b_sc + (par * kRound + k8) * Cfg::B_PITCH + (BROWS ? set * 128 : set);
         if (!BROWS) s *= bs[0];
-        s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+        const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
         const uint32_t done_bar = tempty0 + buf * 8;
         if (++buf == BUFS) {
           buf = 0;
           bphase ^= 1u;
         }
 #pragma unroll
-        for (int ch = 0; ch < kPieces - 1; ++ch) {
+        for (int ch = 0; ch < kPieces; ++ch) {
           ptx::tmem_wait_ld();
-          tmem_ld_piece(taddr + (ch + 1) * kPiece, r[(ch + 1) & 1]);
-          if (ch == kPieces - 2)
-            ready = kb + 1 < p.num_kb && ptx::mbar_test_wait(&tfull[buf], bphase);
-          add_piece(ch);
+          if (ch < kPieces - 1) {
+            ptx::tmem_ld_32x32b_x16(taddr + (ch + 1) * kPiece, r[(ch + 1) & 1]);
+            if (ch == kPieces - 2)
+              ready = kb + 1 < p.num_kb && ptx::mbar_test_wait(&tfull[buf], bphase);
+          } else {
+            ptx::tc_fence_before();
+            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar);
+          }
+#pragma unroll
+          for (int i = 0; i < kPiece / 4; ++i) {
+            f32x2 f0 = s2, f1 = s2;
+            if (BROWS) {
+              const float4 b4 = *reinterpret_cast<const float4*>(bs + ch * kPiece + 4 * i);
+              f0 = mul2(s2, pack2(__float_as_uint(b4.x), __float_as_uint(b4.y)));
+              f1 = mul2(s2, pack2(__float_as_uint(b4.z), __float_as_uint(b4.w)));
+            }
+            const uint32_t* rr = r[ch & 1] + 4 * i;
+            fma2(acc[ch * (kPiece / 2) + 2 * i], pack2(rr[0], rr[1]), f0);
+            fma2(acc[ch * (kPiece / 2) + 2 * i + 1], pack2(rr[2], rr[3]), f1);
+          }
         }
-        ptx::tmem_wait_ld();
-        ptx::tc_fence_before();
-        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar);
-        add_piece(kPieces - 1);
+        if (k8 == kRound - 1 || kb + 1 == p.num_kb) {  // this round's scales are read
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sempty[par]);
+          par ^= 1;
+          if (par == 0) sphase ^= 1u;
+        }
       }
-      if (dead) continue;
       const int m_blk = tile / p.num_n * Cfg::CTAS + static_cast<int>(rank);
       const int t = m_blk * BM + row;
       const int col0 = tile % p.num_n * BN + set * 128;
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
       } else {
         // pieces of 32 rows by 64 bytes, two in flight
         const int sw = (row >> 1) & 3;
-        uint8_t* mine = staging + (warp - 2) * 4096;
+        uint8_t* mine = staging + (warp - 4) * 4096;
         const int t0 = m_blk * BM + q * 32;
         const int cols = p.c_bf16 ? 32 : 16;  // of a piece
         const auto store_piece = [&](int i, const uint32_t (&v)[16]) {
@@ -522,6 +523,14 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) !=
       cudaSuccess)
     return TWELL_ERR_CUDA;
+  if (PAIR) {
+    // the register split draws on what the block starts with: never launched with less
+    static const int regs = [&] {
+      cudaFuncAttributes at;
+      return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != kRegsStart) return TWELL_ERR_UNSUPPORTED;
+  }
   const int most = dev.sm_count / Cfg::CTAS;
   const int units = p.num_tiles < most ? p.num_tiles : most;
   cudaLaunchConfig_t cfg = {};

@@ -421,6 +421,14 @@ __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* gsrc,
                : "memory");
 }
 
+// The same for 4 bytes (src_bytes 4, or 0 for zeros).
+__device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* gsrc,
+                                          uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst),
+               "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(src_bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
