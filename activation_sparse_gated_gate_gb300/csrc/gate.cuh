@@ -36,4 +36,22 @@ twell_status launch_gate_decode(const DeviceInfo& dev, const uint16_t* x, const 
                                 float* z_debug, int32_t* status_dev, uint64_t wait_ns,
                                 const DecodeFfn* ffn, cudaStream_t s);
 
+// The same kernel on e4m3 operands with scales for each 128 of K (x per row, W
+// per 128 x 128 block): true when it handles T tokens and K = D (all of a CTA's K
+// blocks have their own TMEM columns).
+bool decode_fp8_supported(int32_t T, int32_t K);
+
+twell_status launch_gate_decode_fp8(const DeviceInfo& dev, const uint8_t* xq, int64_t ldx,
+                                    const float* x_scale, const uint8_t* wq, int64_t ldw,
+                                    const float* w_scale, int32_t T, int32_t D, int32_t F,
+                                    const twell_t* out, float* z_debug, int32_t* status_dev,
+                                    uint64_t wait_ns, cudaStream_t s);
+
+// c [M][N] = a b^T of such operands (twell_gemm_fp8 with b_block 128).
+twell_status launch_gemm_decode_fp8(const DeviceInfo& dev, const uint8_t* a, int64_t lda,
+                                    const float* a_scale, const uint8_t* b, int64_t ldb,
+                                    const float* b_scale, int32_t M, int32_t N, int32_t K,
+                                    void* c, bool c_bf16, int64_t ldc, int32_t* status_dev,
+                                    uint64_t wait_ns, cudaStream_t s);
+
 }  // namespace twell

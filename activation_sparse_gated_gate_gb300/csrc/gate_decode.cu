@@ -35,6 +35,11 @@
 //     OR of the ballots of that quarter's warps (a shared-memory word each
 //     CTA clears in its prologue): rank 1 hands its part of block 0 to rank 0
 //     with a remote store, and each word is stored once (no zeroing).
+// With e4m3 operands and block scales (FP8) a K block is 128 wide, the same
+// 128-byte rows, and its MMAs go to N TMEM columns of their own (all of a CTA's
+// K blocks fit: that bounds the tokens this form takes); whoever reads a chunk's
+// sums adds the blocks' columns, scaled, in fp32.  Without PACK the sums are the
+// result, stored as a row of C per token.
 // Roles per CTA: warp 0 TMA producer, warp 1 TMEM allocation and MMA issue,
 // warps 2-9 epilogue (warp w reads TMEM lanes 32 (w mod 4) .. + 31).
 //
@@ -50,14 +55,15 @@
 #include "common.cuh"
 #include "gate.cuh"
 #include "ptx.cuh"
+#include "vec.cuh"
 
 namespace twell {
 namespace {
 
 constexpr int DM = 128;              // neurons per CTA tile = one TwELL tile
-constexpr int DK = 64;               // K block: 128-byte rows, 128B swizzle
+constexpr int kTmemCols = 512;
 constexpr int kThreads = 320;        // producer, MMA issuer, two sets of four epilogue warps
-constexpr int kA = DM * DK * 2;      // W_g tile of a stage (16 KB)
+constexpr int kA = DM * 128;         // W_g tile of a stage (16 KB)
 constexpr int kMaxStages = 8;
 constexpr int kRowBytes = DM * 4;    // one token's 128 fp32 values
 // barrier area, byte offsets: full[8] 0, empty[8] 64, tfull 128, drain 136,
@@ -66,6 +72,8 @@ constexpr int kRowBytes = DM * 4;    // one token's 128 fp32 values
 // entry count 224, ballots [2 sets][2][16 tokens][4 quarters] 256, spill
 // slots [2 sets][2][16] 1280
 constexpr int kBarBytes = 2048;
+// FP8: x's scales [K block][token column] and W_g's [K block] of this CTA
+constexpr int kScaleBytes = (kTmemCols + kTmemCols / 16) * 4;
 constexpr int kEntryBytes = 8;       // (token * 128 + neuron, gate value) of an active entry
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
 
@@ -96,6 +104,13 @@ struct DecParams {
   const uint16_t* Wd;
   float* y;
   float* y_zero;      // prefetch mode: y of the forward that follows, zeroed here
+  // FP8: [T][nkb] and [n_t][nkb] fp32
+  const float* x_scale;
+  const float* w_scale;
+  // without PACK: [T][F] of fp32 or bf16, rows ldc elements apart
+  void* c;
+  int64_t ldc;
+  int32_t c_bf16;
 };
 
 __device__ __forceinline__ void flag(int32_t* status, int32_t bit) {
@@ -129,9 +144,11 @@ __device__ __forceinline__ float dot8_bf16(const uint4 a, const uint4 b) {
   return s;
 }
 
+template <bool FP8, bool PACK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gate_decode_kernel(const __grid_constant__ CUtensorMap tmap_x,
                        const __grid_constant__ CUtensorMap tmap_w, const DecParams p) {
+  constexpr int DK = FP8 ? 128 : 64;  // K block: 128-byte rows, 128B swizzle
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_u32(smem_raw);
   uint8_t* region = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -152,6 +169,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint2* ent = reinterpret_cast<uint2*>(region);
   uint32_t* masks = reinterpret_cast<uint32_t*>(bars + 256);
   int32_t* sslot = reinterpret_cast<int32_t*>(bars + 1280);
+  float* xs = reinterpret_cast<float*>(bars + kBarBytes);   // FP8: [nloc][N]
+  float* ws = xs + kTmemCols;                               // FP8: [nloc]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -165,8 +184,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int stage = 0;
   uint32_t phase = 0;
 
+  // K block of this CTA's i-th step
+  const auto block_of = [&](int i) { return kb0 + (i + rot < nloc ? i + rot : i + rot - nloc); };
   auto fill = [&](int i) {
-    const int kb = kb0 + (i + rot < nloc ? i + rot : i + rot - nloc);
+    const int kb = block_of(i);
     uint8_t* st = region + static_cast<size_t>(stage) * p.stage_bytes;
     ptx::mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(p.stage_bytes));
     ptx::tma_load_2d(st, &tmap_w, &full[stage], kb * DK, tile * DM);
@@ -222,7 +243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      const uint32_t idesc = ptx::idesc_bf16_f32(DM, p.N);
+      const uint32_t idesc =
+          FP8 ? ptx::idesc_e4m3_f32(DM, p.N) : ptx::idesc_bf16_f32(DM, p.N);
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -237,10 +259,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t a_addr = ptx::smem_u32(region + static_cast<size_t>(st) * p.stage_bytes);
         const uint32_t b_addr = a_addr + kA;
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk)
-          ptx::mma_bf16(tmem_base, ptx::sdesc_kmajor_sw128(a_addr + kk * 32),
-                        ptx::sdesc_kmajor_sw128(b_addr + kk * 32), idesc,
-                        (i > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {  // 32 bytes along K each
+          const uint64_t da = ptx::sdesc_kmajor_sw128(a_addr + kk * 32);
+          const uint64_t db = ptx::sdesc_kmajor_sw128(b_addr + kk * 32);
+          if (FP8)
+            ptx::mma_f8(tmem_base + static_cast<uint32_t>(i * p.N), da, db, idesc,
+                        kk > 0 ? 1u : 0u);
+          else
+            ptx::mma_bf16(tmem_base, da, db, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        }
         ptx::mma_commit(&empty[st]);
         if (++st == S) {
           st = 0;
@@ -261,6 +288,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (size_t i = static_cast<size_t>(blockIdx.x) * (kThreads - 64) + (threadIdx.x - 64);
            i < n4; i += nthr)
         y4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (FP8) {
+      // the scales, by step (the block barrier below publishes them)
+      const int e = threadIdx.x - 64;
+      for (int j = e; j < nloc * p.N; j += kThreads - 64) {
+        const int t = j % p.N;
+        xs[j] = t < p.T ? p.x_scale[static_cast<size_t>(t) * p.nkb + block_of(j / p.N)] : 0.0f;
+      }
+      for (int j = e; j < nloc; j += kThreads - 64)
+        ws[j] = p.w_scale[static_cast<size_t>(tile) * p.nkb + block_of(j)];
     }
     if (!__all_sync(0xffffffffu, pipe_wait(tfull, 0, p.wait_ns)) && lane == 0) {
       flag(p.status, TWELL_FLAG_TIMEOUT);
@@ -301,6 +338,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int oth1 = rank == 0 ? p.N : p.half;
   const uint32_t peer = rank ^ 1u;
 
+  // This CTA's partial sums of tokens c .. c + 15 at this thread's neuron (whole
+  // warps; every chunk is read once).
+  const auto partial_sums = [&](int c, float (&v)[16]) {
+    uint32_t r[2][16];
+    const uint32_t taddr = tmem_base + lane_base + static_cast<uint32_t>(c);
+    ptx::tmem_ld_32x32b_x16(taddr, r[0]);
+    if (!FP8) {
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[0][j]);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+    const auto add = [&](int i, const uint32_t (&b)[16]) {
+      const float w = ws[i];
+      const float4* s4 = reinterpret_cast<const float4*>(xs + i * p.N + c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 s = s4[j];
+        v[4 * j] = fmaf(__uint_as_float(b[4 * j]), w * s.x, v[4 * j]);
+        v[4 * j + 1] = fmaf(__uint_as_float(b[4 * j + 1]), w * s.y, v[4 * j + 1]);
+        v[4 * j + 2] = fmaf(__uint_as_float(b[4 * j + 2]), w * s.z, v[4 * j + 2]);
+        v[4 * j + 3] = fmaf(__uint_as_float(b[4 * j + 3]), w * s.w, v[4 * j + 3]);
+      }
+    };
+    for (int i = 0; i < nloc; i += 2) {  // the next block's columns on their way
+      ptx::tmem_wait_ld();
+      if (i + 1 < nloc)
+        ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>((i + 1) * p.N), r[1]);
+      add(i, r[0]);
+      if (i + 1 < nloc) {
+        ptx::tmem_wait_ld();
+        if (i + 2 < nloc)
+          ptx::tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>((i + 2) * p.N), r[0]);
+        add(i + 1, r[1]);
+      }
+    }
+  };
+
   ptx::cluster_wait();  // the partner has started: its shared memory may be written
   if (epi) {
     if (!aborted_here) {
@@ -308,12 +385,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::tc_fence_after();
       const uint32_t rx = ptx::mapa(ptx::smem_u32(xch), peer) + static_cast<uint32_t>(n * 4);
       for (int c = oth0 + 16 * set; c < oth1; c += 32) {
-        uint32_t r[16];
-        ptx::tmem_ld_32x32b_x16(tmem_base + lane_base + static_cast<uint32_t>(c), r);
-        ptx::tmem_wait_ld();
+        float r[16];
+        partial_sums(c, r);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          ptx::st_cluster_u32(rx + static_cast<uint32_t>((c - oth0 + j) * kRowBytes), r[j]);
+          ptx::st_cluster_u32(rx + static_cast<uint32_t>((c - oth0 + j) * kRowBytes),
+                              __float_as_uint(r[j]));
       }
     }
     if (warp == 2 && lane == 0)
@@ -325,33 +402,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_wait();  // the partner's partial sums and abort flag are here
 
   const bool go = !aborted_here && *peer_aborted == 0u;  // the same value in every thread
-  if (epi && !go) {
+  if (PACK && epi && !go) {
     // nothing is packed: the tile's counts of this CTA's tokens say so, so
     // a consumer of the TwELL (the CUDA-core kernel that twell_ffn_decode
     // runs next, for one) finds it empty rather than undefined
     const int t = own0 + (warp - 2) * 32 + lane;
     if (t < own1 && t < p.T) p.cnt[static_cast<size_t>(t) * p.n_t + tile] = 0;
   }
-  if (epi && go) {
+  if (!PACK && epi && go) {
+    ptx::tc_fence_after();
+    const int col = tile * DM + n;
+    for (int c = own0 + 16 * set; c < own1; c += 32) {
+      float r[16];
+      partial_sums(c, r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float v =
+            r[j] + *reinterpret_cast<const float*>(xch + (c - own0 + j) * kRowBytes + n * 4);
+        if (c + j < p.T && col < p.F) {
+          const size_t o = static_cast<size_t>(c + j) * p.ldc + col;
+          if (p.c_bf16) narrow(v, static_cast<uint16_t*>(p.c)[o]);
+          else static_cast<float*>(p.c)[o] = v;
+        }
+      }
+    }
+  }
+  if (PACK && epi && go) {
     ptx::tc_fence_after();
     const uint32_t lt = (1u << lane) - 1u;
     const uint32_t bar_id = 1u + static_cast<uint32_t>(set);
     uint32_t bw0 = 0u, bw1 = 0u;  // this warp's block-bitmap words (blocks 0 and 1)
     int par = 0;
     for (int c = own0 + 16 * set; c < own1; c += 32, par ^= 1) {
-      uint32_t r[16];
-      ptx::tmem_ld_32x32b_x16(tmem_base + lane_base + static_cast<uint32_t>(c), r);
-      float v[16];
+      float r[16], v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         v[j] = *reinterpret_cast<const float*>(xch + (c - own0 + j) * kRowBytes + n * 4);
-      ptx::tmem_wait_ld();
+      partial_sums(c, r);
       uint32_t* mk = masks + (set * 2 + par) * 64;  // [token j][warp quarter]
       int32_t* ss = sslot + (set * 2 + par) * 16;
       uint32_t m[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        v[j] += __uint_as_float(r[j]);
+        v[j] += r[j];
         m[j] = __ballot_sync(0xffffffffu, c + j < p.T && v[j] > 0.0f);
         if (lane == j) mk[j * 4 + q] = m[j];
         if (c + j < 128) bw0 |= m[j];
@@ -396,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           p.col[o] = static_cast<uint8_t>(n);
         }
       }
-      if (p.Wu_t) {
+      if (!FP8 && p.Wu_t) {
         // the chunk's active neurons: their W_u and W_d rows on their way to
         // L2, read next by the projection (in this kernel, or the CUDA-core
         // forward right after it); with the projection here, every active
@@ -449,8 +542,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (bw1 != 0u) atomicOr(&bacc[4 + q], bw1);
     }
   }
-  if (epi) ptx::bar_sync(3, 256);  // both sets' block words and entries are in
-  if (epi && go && p.y) {
+  if (PACK && epi) ptx::bar_sync(3, 256);  // both sets' block words and entries are in
+  if (PACK && !FP8 && epi && go && p.y) {
     // fused projection: each epilogue warp takes whole entries in turn;
     // u = x_t . W_u[:, j] over 16-byte chunks of the rows (lane-strided),
     // reduced across the warp, then y_t += (h u) W_d[j, :] with float4
@@ -509,11 +602,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // block words: rank 0's tokens all lie in block 0, rank 1's in block 0
   // and / or block 1; rank 1's part of block 0 goes to rank 0
-  if (epi && rank == 1 && set == 0 && lane == 0)
+  if (PACK && epi && rank == 1 && set == 0 && lane == 0)
     ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(bx + q), 0), bacc[q]);
   ptx::cluster_arrive();
   ptx::cluster_wait();  // rank 1's words are here; neither CTA's memory is read afterwards
-  if (epi && set == 0 && go && lane == 0 && p.block_bits) {
+  if (PACK && epi && set == 0 && go && lane == 0 && p.block_bits) {
     if (rank == 0) p.block_bits[tile * 4 + q] = bacc[q] | bx[q];
     else if (p.N > DM) p.block_bits[static_cast<size_t>(p.F / 32) + tile * 4 + q] = bacc[4 + q];
   }
@@ -523,31 +616,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-}  // namespace
-
-bool gate_decode_supported(int32_t T, int32_t D) {
-  return T >= 1 && T <= 256 && (D + DK - 1) / DK >= 2;
-}
-
-twell_status launch_gate_decode(const DeviceInfo& dev, const uint16_t* x, const uint16_t* Wg_t,
-                                int32_t T, int32_t D, int32_t F, const twell_t* out,
-                                float* z_debug, int32_t* status_dev, uint64_t wait_ns,
-                                const DecodeFfn* ffn, cudaStream_t s) {
-  if (!gate_decode_supported(T, D)) return TWELL_ERR_UNSUPPORTED;
-  DecParams p;
-  p.T = T;
-  p.D = D;
-  p.F = F;
-  p.n_t = F / TWELL_TILE;
-  p.W = out->width;
-  p.N = (T + 15) / 16 * 16;
-  p.nkb = (D + DK - 1) / DK;
+// What the forms share: shapes, shared memory, tensor maps and the launch.  p
+// holds T, D, F, n_t and the form's own fields.
+template <bool FP8, bool PACK>
+twell_status launch(const DeviceInfo& dev, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                    DecParams p, cudaStream_t s) {
+  constexpr int DK = FP8 ? 128 : 64;
+  p.N = (p.T + 15) / 16 * 16;
+  p.nkb = (p.D + DK - 1) / DK;
   p.kb_split = (p.nkb + 1) / 2;
-  p.stage_bytes = kA + p.N * DK * 2;
+  p.stage_bytes = kA + p.N * 128;
   p.half = (p.N / 16 + 1) / 2 * 16;
   p.xch_bytes = p.half * kRowBytes;
+  const int scales = FP8 ? kScaleBytes : 0;
   const int budget = (dev.max_smem_optin < 232448 ? dev.max_smem_optin : 232448) - 1024 -
-                     kBarBytes - p.xch_bytes;
+                     kBarBytes - scales - p.xch_bytes;
   int stages = budget / p.stage_bytes;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) return TWELL_ERR_UNSUPPORTED;
@@ -555,9 +638,36 @@ twell_status launch_gate_decode(const DeviceInfo& dev, const uint16_t* x, const 
   p.region = stages * p.stage_bytes;
   // the entry list of the fused projection: at most every neuron of every
   // token of rank 0 (the larger half)
-  if (ffn && ffn->y && p.region < p.half * DM * kEntryBytes) return TWELL_ERR_UNSUPPORTED;
+  if (p.y && p.region < p.half * DM * kEntryBytes) return TWELL_ERR_UNSUPPORTED;
+  const uint32_t cols = static_cast<uint32_t>(p.N * (FP8 ? p.kb_split : 1));
+  if (cols > kTmemCols) return TWELL_ERR_UNSUPPORTED;
   p.tmem_cols = 32;
-  while (p.tmem_cols < static_cast<uint32_t>(p.N)) p.tmem_cols <<= 1;
+  while (p.tmem_cols < cols) p.tmem_cols <<= 1;
+  constexpr int E = FP8 ? 1 : 2;
+  CUtensorMap mx, mw;
+  twell_status st;
+  if ((st = make_tmap_2d(&mw, E, w, p.D, p.F, DK, DM, ldw, 128)) != TWELL_OK) return st;
+  if ((st = make_tmap_2d(&mx, E, x, p.D, p.T, DK, static_cast<uint32_t>(p.N), ldx, 128)) !=
+      TWELL_OK)
+    return st;
+  const int smem = p.region + p.xch_bytes + kBarBytes + scales + 1024;
+  auto kern = gate_decode_kernel<FP8, PACK>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return TWELL_ERR_CUDA;
+  kern<<<2 * p.n_t, kThreads, smem, s>>>(mx, mw, p);
+  return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+// The fields of a call that packs into `out`.
+DecParams pack_params(int32_t T, int32_t D, int32_t F, const twell_t* out, float* z_debug,
+                      int32_t* status_dev, uint64_t wait_ns) {
+  DecParams p{};
+  p.T = T;
+  p.D = D;
+  p.F = F;
+  p.n_t = F / TWELL_TILE;
+  p.W = out->width;
   p.val = out->val;
   p.col = out->col;
   p.cnt = out->cnt;
@@ -570,23 +680,66 @@ twell_status launch_gate_decode(const DeviceInfo& dev, const uint16_t* x, const 
   p.z_debug = z_debug;
   p.status = status_dev;
   p.wait_ns = wait_ns;
+  return p;
+}
+
+}  // namespace
+
+bool gate_decode_supported(int32_t T, int32_t D) {
+  return T >= 1 && T <= 256 && (D + 63) / 64 >= 2;
+}
+
+bool decode_fp8_supported(int32_t T, int32_t K) {
+  const int64_t nkb = (static_cast<int64_t>(K) + 127) / 128;
+  return T >= 1 && T <= 256 && nkb >= 2 && (nkb + 1) / 2 * ((T + 15) / 16 * 16) <= kTmemCols;
+}
+
+twell_status launch_gate_decode(const DeviceInfo& dev, const uint16_t* x, const uint16_t* Wg_t,
+                                int32_t T, int32_t D, int32_t F, const twell_t* out,
+                                float* z_debug, int32_t* status_dev, uint64_t wait_ns,
+                                const DecodeFfn* ffn, cudaStream_t s) {
+  if (!gate_decode_supported(T, D)) return TWELL_ERR_UNSUPPORTED;
+  DecParams p = pack_params(T, D, F, out, z_debug, status_dev, wait_ns);
   p.x = x;
   p.Wu_t = ffn ? ffn->Wu_t : nullptr;
   p.Wd = ffn ? ffn->Wd : nullptr;
   p.y = ffn ? ffn->y : nullptr;
   p.y_zero = ffn && !ffn->y ? ffn->y_zero : nullptr;
+  return launch<false, true>(dev, x, 2 * static_cast<int64_t>(D), Wg_t,
+                             2 * static_cast<int64_t>(D), p, s);
+}
 
-  CUtensorMap mx, mw;
-  twell_status st;
-  if ((st = make_tmap_bf16_2d(&mw, Wg_t, D, F, DK, DM)) != TWELL_OK) return st;
-  if ((st = make_tmap_bf16_2d(&mx, x, D, T, DK, static_cast<uint32_t>(p.N))) != TWELL_OK)
-    return st;
-  const int smem = p.region + p.xch_bytes + kBarBytes + 1024;
-  if (cudaFuncSetAttribute(gate_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem) != cudaSuccess)
-    return TWELL_ERR_CUDA;
-  gate_decode_kernel<<<2 * p.n_t, kThreads, smem, s>>>(mx, mw, p);
-  return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+twell_status launch_gate_decode_fp8(const DeviceInfo& dev, const uint8_t* xq, int64_t ldx,
+                                    const float* x_scale, const uint8_t* wq, int64_t ldw,
+                                    const float* w_scale, int32_t T, int32_t D, int32_t F,
+                                    const twell_t* out, float* z_debug, int32_t* status_dev,
+                                    uint64_t wait_ns, cudaStream_t s) {
+  if (!decode_fp8_supported(T, D)) return TWELL_ERR_UNSUPPORTED;
+  DecParams p = pack_params(T, D, F, out, z_debug, status_dev, wait_ns);
+  p.x_scale = x_scale;
+  p.w_scale = w_scale;
+  return launch<true, true>(dev, xq, ldx, wq, ldw, p, s);
+}
+
+twell_status launch_gemm_decode_fp8(const DeviceInfo& dev, const uint8_t* a, int64_t lda,
+                                    const float* a_scale, const uint8_t* b, int64_t ldb,
+                                    const float* b_scale, int32_t M, int32_t N, int32_t K,
+                                    void* c, bool c_bf16, int64_t ldc, int32_t* status_dev,
+                                    uint64_t wait_ns, cudaStream_t s) {
+  if (!decode_fp8_supported(M, K)) return TWELL_ERR_UNSUPPORTED;
+  DecParams p{};
+  p.T = M;
+  p.D = K;
+  p.F = N;
+  p.n_t = (N + DM - 1) / DM;
+  p.status = status_dev;
+  p.wait_ns = wait_ns;
+  p.x_scale = a_scale;
+  p.w_scale = b_scale;
+  p.c = c;
+  p.ldc = ldc;
+  p.c_bf16 = c_bf16;
+  return launch<true, false>(dev, a, lda, b, ldb, p, s);
 }
 
 }  // namespace twell

@@ -601,6 +601,11 @@ extern "C" twell_status twell_gemm_fp8(const uint8_t* a, int64_t lda, const floa
   DeviceInfo dev;
   twell_status st;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
+  // few rows: the tokens as the MMA's N and K split over two CTAs
+  if (b_block == 128 && decode_fp8_supported(M, K))
+    return launch_gemm_decode_fp8(dev, a, lda, a_scale, b, ldb, b_scale, M, N, K, c,
+                                  c_type == TWELL_BF16, ldc, status_dev, gate_wait_ns(),
+                                  static_cast<cudaStream_t>(stream));
   GemmFp8Params p{};
   p.M = M;
   p.N = N;
@@ -631,6 +636,9 @@ extern "C" twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, cons
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s) != cudaSuccess) return TWELL_ERR_CUDA;
+  if (decode_fp8_supported(T, D))  // (it stores every word of the block bitmap itself)
+    return launch_gate_decode_fp8(dev, xq, ldx, x_scale, wq, ldw, w_scale, T, D, F, out, z_debug,
+                                  status_dev, gate_wait_ns(), s);
   const size_t words = (static_cast<size_t>(T) + BM - 1) / BM * (F / 32);
   if (out->block_bits &&
       cudaMemsetAsync(out->block_bits, 0, words * sizeof(uint32_t), s) != cudaSuccess)
