@@ -242,40 +242,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc =
-          FP8 ? ptx::idesc_e4m3_f32(DM, p.N) : ptx::idesc_bf16_f32(DM, p.N);
-      int st = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int i = 0; i < nloc; ++i) {
-        if (!pipe_wait(&full[st], ph, p.wait_ns)) {
+    // (the whole warp walks the loop, so that addresses and descriptors stay in
+    // uniform registers; one elected lane issues)
+    const uint32_t idesc = FP8 ? ptx::idesc_e4m3_f32(DM, p.N) : ptx::idesc_bf16_f32(DM, p.N);
+    const uint64_t desc0 = ptx::sdesc_kmajor_sw128(ptx::smem_u32(region));
+    int st = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; i < nloc; ++i) {
+      if (!__all_sync(0xffffffffu, pipe_wait(&full[st], ph, p.wait_ns))) {
+        if (lane == 0) {
           flag(p.status, TWELL_FLAG_TIMEOUT);
           *aborted = 1u;
-          ok = false;
-          break;
         }
-        ptx::tc_fence_after();
-        const uint32_t a_addr = ptx::smem_u32(region + static_cast<size_t>(st) * p.stage_bytes);
-        const uint32_t b_addr = a_addr + kA;
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint64_t da = desc0 + static_cast<uint32_t>(st * (p.stage_bytes / 16));
+      const uint64_t db = da + kA / 16;
+      if (ptx::elect_one_sync()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {  // 32 bytes along K each
-          const uint64_t da = ptx::sdesc_kmajor_sw128(a_addr + kk * 32);
-          const uint64_t db = ptx::sdesc_kmajor_sw128(b_addr + kk * 32);
           if (FP8)
-            ptx::mma_f8(tmem_base + static_cast<uint32_t>(i * p.N), da, db, idesc,
-                        kk > 0 ? 1u : 0u);
+            ptx::mma_f8(tmem_base + static_cast<uint32_t>(i * p.N), da + 2 * kk, db + 2 * kk,
+                        idesc, kk > 0 ? 1u : 0u);
           else
-            ptx::mma_bf16(tmem_base, da, db, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_bf16(tmem_base, da + 2 * kk, db + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
         }
         ptx::mma_commit(&empty[st]);
-        if (++st == S) {
-          st = 0;
-          ph ^= 1u;
-        }
+        if (i + 1 == nloc) ptx::mma_commit(tfull);
       }
-      if (ok) ptx::mma_commit(tfull);
+      __syncwarp();
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
+    // (rank 1 of a K of one block: nothing to wait for)
+    if (ok && nloc == 0 && lane == 0) ptx::mma_commit(tfull);
   } else {
     // epilogue warps: first, in prefetch mode, zero this CTA's share of the
     // forward's y while W_g streams (the forward adds into y); then wait
@@ -317,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (n_s > 0 && !ptx::mbar_wait(&full[s], (n_s - 1) & 1u)) break;
       }
     }
-    if (warp == 1 && lane == 0) {
+    if (warp == 1 && ptx::elect_one_sync()) {
       ptx::tc_fence_after();
       ptx::mma_commit(drain);  // arrives once every MMA this thread issued is done
       ptx::mbar_wait(drain, 0);

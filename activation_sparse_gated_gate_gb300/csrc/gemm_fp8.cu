@@ -494,7 +494,7 @@ done:
   if (*aborted) {  // read after the barrier: the same value in every thread
     // the loads in flight may signal a barrier that can no longer complete
     if (warp == 0 && lane == 0) ptx::spin_ns(1000000);
-    if (warp == 1 && lane == 0 && rank == 0) {
+    if (warp == 1 && rank == 0 && ptx::elect_one_sync()) {
       ptx::tc_fence_after();
       // arrives once every MMA this thread issued is done
       if (PAIR) ptx::mma_commit_pair(drain);
