@@ -550,8 +550,9 @@ def twell_probe_fma(packed: bool, iters: int, out=None, stream=None, device=None
 # ------------------------------------------- norm and 8-bit products
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
-_E4M3 = torch.float8_e4m3fn
-_FLOATS = (torch.bfloat16, torch.float32)
+_BF16 = {torch.bfloat16: 0}
+_F32 = {torch.float32: 1}
+_E4M3 = {torch.float8_e4m3fn: 0}
 _STATUS = {}
 
 
@@ -568,57 +569,64 @@ def status_word(device=None):
     return _STATUS[index]
 
 
-def _mat(t, dtypes, name, device, shape=None):
-    """Check a [rows][columns] operand whose rows may be apart; returns the
-    elements between rows."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        want = "a matrix" if shape is None else f"of shape {tuple(shape)}"
-        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on another device")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}'s columns must be contiguous")
-    # (a single row has no pitch of its own; any valid one will do)
-    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+# The checks below run on every call of a decode step, where the host's time is the
+# call's: each looks at the few attributes that decide, and only a tensor that
+# fails is looked at again for what to say.
 
 
-def _vec(t, dtypes, name, device, shape):
+def _mat(t, types, name, device, shape):
+    """Check a [rows][columns] operand whose rows may be apart; returns its
+    element type's code and the elements between its rows."""
+    try:
+        code = types[t.dtype]
+        if t.get_device() == device and t.shape == shape:
+            if t.is_contiguous():
+                return code, shape[1]
+            rows, columns = t.stride()
+            if columns == 1 or shape[1] == 1:
+                # (a single row has no pitch of its own; any valid one will do)
+                return code, rows if shape[0] > 1 else (shape[1] + 15) // 16 * 16
+    except (AttributeError, KeyError, TypeError):
+        pass
+    _refuse(t, types, name, device, shape, "columns")
+
+
+def _vec(t, types, name, device, shape):
+    """Check a contiguous operand; returns its element type's code."""
+    try:
+        code = types[t.dtype]
+        if t.get_device() == device and t.shape == shape and t.is_contiguous():
+            return code
+    except (AttributeError, KeyError, TypeError):
+        pass
+    _refuse(t, types, name, device, shape, "elements")
+
+
+def _refuse(t, types, name, device, shape, what):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be {' or '.join(map(str, types))}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on another device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name}'s {what} must be contiguous")
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _device_of(t, name):
+def _first(t, name):
+    """Device and shape of the operand that the others are held against."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(shape)}")
+    return t.get_device(), shape
 
 
-def _on(stream):
-    """What is allocated for a call belongs to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _run(name, device, stream, *args):
-    raw = (torch._C._cuda_getCurrentRawStream(device) if stream is None
-           else stream.cuda_stream)
-    fn = getattr(lib(), name)
+def _run(name, device, *args):
+    fn = getattr(_LIB if _LIB is not None else lib(), name)
+    raw = torch._C._cuda_getCurrentRawStream(device)
     if torch._C._cuda_getDevice() == device:
         code = fn(*args, raw)
     else:
@@ -632,7 +640,7 @@ def _empty_e4m3(rows, cols, device):
     """[rows][cols] with its rows on 16-byte boundaries, as the 8-bit products
     read them."""
     pitch = (cols + 15) // 16 * 16
-    t = torch.empty((rows, pitch), dtype=_E4M3, device=device)
+    t = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
     return t if pitch == cols else t[:, :cols]
 
 
@@ -655,45 +663,53 @@ def twell_rms_norm(x, weight, residual=None, eps=1e-6, y=None, total=None, q=Non
     e4m3 with a scale for each 128 columns.  Outputs may be given; otherwise
     y is allocated when ``bf16``, q and scale when ``fp8``, total when there is
     a residual, and rstd (fp32 [T], for the backward) when ``rstd`` is True."""
-    dev = _device_of(x, "x")
-    ldx = _mat(x, _FLOATS, "x", dev)
-    shape = x.shape
+    if stream is not None:  # what is allocated belongs to the stream it is used on
+        with torch.cuda.stream(stream):
+            return twell_rms_norm(x, weight, residual, eps, y, total, q, scale, rstd, bf16, fp8)
+    dev, shape = _first(x, "x")
     T, D = shape
-    _vec(weight, _FLOATS, "weight", dev, (D,))
-    with _on(stream):
-        ldr = ldt = ldy = ldq = r_type = 0
-        if residual is not None:
-            ldr = _mat(residual, _FLOATS, "residual", dev, shape)
-            r_type = _TYPES[residual.dtype]
-            if total is None:
-                total = torch.empty((T, D), dtype=residual.dtype, device=x.device)
-            ldt = _mat(total, (residual.dtype,), "total", dev, shape)
-        elif total is not None:
-            raise ValueError("total is an output of the residual's addition: none is given")
-        if y is None and bf16 and (q is None or fp8):
-            y = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
-        if y is not None:
-            ldy = _mat(y, (torch.bfloat16,), "y", dev, shape)
-        if fp8:
-            if q is None:
-                q = _empty_e4m3(T, D, x.device)
-            if scale is None:
-                scale = torch.empty((T, -(-D // FP8_BLOCK)), dtype=torch.float32,
-                                    device=x.device)
-        if (q is None) != (scale is None):
+    x_type, ldx = _mat(x, _TYPES, "x", dev, shape)
+    w_type = _vec(weight, _TYPES, "weight", dev, (D,))
+    ldr = ldt = ldy = ldq = r_type = 0
+    p_res = p_total = p_y = p_q = p_scale = p_rstd = None
+    if residual is not None:
+        r_type, ldr = _mat(residual, _TYPES, "residual", dev, shape)
+        if total is None:
+            total = torch.empty((T, D), dtype=residual.dtype, device=x.device)
+        t_type, ldt = _mat(total, _TYPES, "total", dev, shape)
+        if t_type != r_type:
+            raise TypeError(f"total must be {residual.dtype}, got {total.dtype}")
+        p_res, p_total = residual.data_ptr(), total.data_ptr()
+    elif total is not None:
+        raise ValueError("total is an output of the residual's addition: none is given")
+    if y is None and bf16 and (q is None or fp8):
+        y = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
+    if y is not None:
+        ldy = _mat(y, _BF16, "y", dev, shape)[1]
+        p_y = y.data_ptr()
+    nb = (D + 127) // 128
+    if fp8:
+        if q is None:
+            q = _empty_e4m3(T, D, x.device)
+        if scale is None:
+            scale = torch.empty((T, nb), dtype=torch.float32, device=x.device)
+    if q is not None:
+        ldq = _mat(q, _E4M3, "q", dev, shape)[1]
+        if scale is None:
             raise ValueError("q and scale are given together")
-        if q is not None:
-            ldq = _mat(q, (_E4M3,), "q", dev, shape)
-            _vec(scale, (torch.float32,), "scale", dev, (T, -(-D // FP8_BLOCK)))
-        if rstd is True:
-            rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
-        elif rstd is False:
-            rstd = None
-        if rstd is not None:
-            _vec(rstd, (torch.float32,), "rstd", dev, (T,))
-        _run("twell_rms_norm", dev, stream, x.data_ptr(), _TYPES[x.dtype], ldx, _addr(residual),
-             r_type, ldr, weight.data_ptr(), _TYPES[weight.dtype], T, D, float(eps), _addr(total),
-             ldt, _addr(y), ldy, _addr(q), ldq, _addr(scale), _addr(rstd))
+        _vec(scale, _F32, "scale", dev, (T, nb))
+        p_q, p_scale = q.data_ptr(), scale.data_ptr()
+    elif scale is not None:
+        raise ValueError("q and scale are given together")
+    if rstd is True:
+        rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
+    elif rstd is False:
+        rstd = None
+    if rstd is not None:
+        _vec(rstd, _F32, "rstd", dev, (T,))
+        p_rstd = rstd.data_ptr()
+    _run("twell_rms_norm", dev, x.data_ptr(), x_type, ldx, p_res, r_type, ldr, weight.data_ptr(),
+         w_type, T, D, eps, p_total, ldt, p_y, ldy, p_q, ldq, p_scale, p_rstd)
     return RmsNorm(y, total, q, scale, rstd)
 
 
@@ -707,28 +723,36 @@ def twell_rms_norm_bwd(total, weight, rstd, dy, dtotal=None, dx=None, dw=None, w
     gradient of x and of the residual alike) and dw fp32.  ``total`` is the
     stream after the addition (x itself where there was none), ``dtotal`` its
     own gradient from further on (may be dx)."""
-    dev = _device_of(total, "total")
-    ld = _mat(total, _FLOATS, "total", dev)
-    shape = total.shape
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_rms_norm_bwd(total, weight, rstd, dy, dtotal, dx, dw, ws)
+    dev, shape = _first(total, "total")
     T, D = shape
-    _vec(weight, _FLOATS, "weight", dev, (D,))
-    _vec(rstd, (torch.float32,), "rstd", dev, (T,))
-    lddy = _mat(dy, _FLOATS, "dy", dev, shape)
-    lddt = 0 if dtotal is None else _mat(dtotal, (total.dtype,), "dtotal", dev, shape)
-    with _on(stream):
-        if dx is None:
-            dx = torch.empty((T, D), dtype=total.dtype, device=total.device)
-        if dw is None:
-            dw = torch.empty((D,), dtype=torch.float32, device=total.device)
-        lddx = _mat(dx, (total.dtype,), "dx", dev, shape)
-        _vec(dw, (torch.float32,), "dw", dev, (D,))
-        if ws is None:
+    code, ld = _mat(total, _TYPES, "total", dev, shape)
+    same = {total.dtype: code}
+    w_type = _vec(weight, _TYPES, "weight", dev, (D,))
+    _vec(rstd, _F32, "rstd", dev, (T,))
+    dy_type, lddy = _mat(dy, _TYPES, "dy", dev, shape)
+    lddt, p_dt = 0, None
+    if dtotal is not None:
+        lddt = _mat(dtotal, same, "dtotal", dev, shape)[1]
+        p_dt = dtotal.data_ptr()
+    if dx is None:
+        dx = torch.empty((T, D), dtype=total.dtype, device=total.device)
+    if dw is None:
+        dw = torch.empty((D,), dtype=torch.float32, device=total.device)
+    lddx = _mat(dx, same, "dx", dev, shape)[1]
+    _vec(dw, _F32, "dw", dev, (D,))
+    if ws is None:
+        if torch._C._cuda_getDevice() == dev:
+            need = twell_rms_norm_bwd_workspace(T, D)
+        else:
             with torch.cuda.device(dev):
-                ws = _workspace(twell_rms_norm_bwd_workspace(T, D), total.device)
-        _run("twell_rms_norm_bwd", dev, stream, total.data_ptr(), _TYPES[total.dtype], ld,
-             weight.data_ptr(), _TYPES[weight.dtype], rstd.data_ptr(), dy.data_ptr(),
-             _TYPES[dy.dtype], lddy, _addr(dtotal), lddt, T, D, dx.data_ptr(), lddx,
-             dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+                need = twell_rms_norm_bwd_workspace(T, D)
+        ws = _workspace(need, total.device)
+    _run("twell_rms_norm_bwd", dev, total.data_ptr(), code, ld, weight.data_ptr(), w_type,
+         rstd.data_ptr(), dy.data_ptr(), dy_type, lddy, p_dt, lddt, T, D, dx.data_ptr(), lddx,
+         dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dx, dw
 
 
@@ -748,45 +772,53 @@ def twell_quant_fp8(x, block_rows=1, rows=True, transposed=False, out=None,
     columns; with ``transposed`` also of x's transpose, by its own blocks.
     ``rows=False`` leaves the untransposed pair out.  ``out``: a QuantFp8 of an
     earlier call of the same kind to write into."""
-    dev = _device_of(x, "x")
-    ld = _mat(x, _FLOATS, "x", dev)
-    R, C = x.shape
-    if block_rows not in (1, FP8_BLOCK):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_quant_fp8(x, block_rows, rows, transposed, out)
+    dev, shape = _first(x, "x")
+    R, C = shape
+    x_type, ld = _mat(x, _TYPES, "x", dev, shape)
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     if not rows and not transposed:
         raise ValueError("neither rows nor transposed asked for")
-    sr, sc = -(-R // block_rows), -(-C // FP8_BLOCK)
-    tr, tc = -(-C // block_rows), -(-R // FP8_BLOCK)
-    with _on(stream):
-        f32 = torch.float32
-        q, scale, qt, scale_t = out if out is not None else (None,) * 4
-        if rows and q is None:
+    q, scale, qt, scale_t = out if out is not None else (None, None, None, None)
+    f32 = torch.float32
+    ldq = ldqt = 0
+    p_q = p_scale = p_qt = p_scale_t = None
+    if rows:
+        at = (-(-R // block_rows), (C + 127) // 128)
+        if q is None:
             q = _empty_e4m3(R, C, x.device)
-            scale = torch.empty((sr, sc), dtype=f32, device=x.device)
-        if transposed and qt is None:
+            scale = torch.empty(at, dtype=f32, device=x.device)
+        ldq = _mat(q, _E4M3, "q", dev, shape)[1]
+        _vec(scale, _F32, "scale", dev, at)
+        p_q, p_scale = q.data_ptr(), scale.data_ptr()
+    else:
+        q = scale = None
+    if transposed:
+        at = (-(-C // block_rows), (R + 127) // 128)
+        if qt is None:
             qt = _empty_e4m3(C, R, x.device)
-            scale_t = torch.empty((tr, tc), dtype=f32, device=x.device)
-        if not rows:
-            q = scale = None
-        if not transposed:
-            qt = scale_t = None
-        ldq = ldqt = 0
-        if rows:
-            ldq = _mat(q, (_E4M3,), "q", dev, (R, C))
-            _vec(scale, (f32,), "scale", dev, (sr, sc))
-        if transposed:
-            ldqt = _mat(qt, (_E4M3,), "qt", dev, (C, R))
-            _vec(scale_t, (f32,), "scale_t", dev, (tr, tc))
-        _run("twell_quant_fp8", dev, stream, x.data_ptr(), _TYPES[x.dtype], ld, R, C, block_rows,
-             _addr(q), ldq, _addr(scale), _addr(qt), ldqt, _addr(scale_t))
+            scale_t = torch.empty(at, dtype=f32, device=x.device)
+        ldqt = _mat(qt, _E4M3, "qt", dev, (C, R))[1]
+        _vec(scale_t, _F32, "scale_t", dev, at)
+        p_qt, p_scale_t = qt.data_ptr(), scale_t.data_ptr()
+    else:
+        qt = scale_t = None
+    _run("twell_quant_fp8", dev, x.data_ptr(), x_type, ld, R, C, block_rows, p_q, ldq, p_scale,
+         p_qt, ldqt, p_scale_t)
     return QuantFp8(q, scale, qt, scale_t)
 
 
-def _operand(v, name, dev):
-    ld = _mat(v, (_E4M3,), name, dev)
-    if ld % 16 or v.data_ptr() % 16:
-        raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
-    return ld
+def _operand(t, name, dev, shape):
+    ld = _mat(t, _E4M3, name, dev, shape)[1]
+    at = t.data_ptr()
+    if ld % 16 or at % 16:
+        if shape[0] != 1 or at % 16:
+            raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
+        ld = (shape[1] + 15) // 16 * 16  # of a single row
+    return at, ld
 
 
 def twell_gemm_fp8(a, a_scale, b, b_scale, out=None, dtype=torch.bfloat16, status=None,
@@ -795,26 +827,30 @@ def twell_gemm_fp8(a, a_scale, b, b_scale, out=None, dtype=torch.bfloat16, statu
     with a scale for each 128 of a row, b [N][K] e4m3 with a scale for each
     128 of a row (b_scale [N][ceil(K/128)]) or each 128 x 128 block (b_scale
     [ceil(N/128)][ceil(K/128)]); out bf16 or fp32 (``dtype`` where not given)."""
-    dev = _device_of(a, "a")
-    lda, ldb = _operand(a, "a", dev), _operand(b, "b", dev)
-    (M, K), (N, Kb) = a.shape, b.shape
-    if Kb != K:
-        raise ValueError(f"a and b differ in K: {K} and {Kb}")
-    nk = -(-K // FP8_BLOCK)
-    _vec(a_scale, (torch.float32,), "a_scale", dev, (M, nk))
-    block = 1 if isinstance(b_scale, torch.Tensor) and b_scale.shape[0] == N else FP8_BLOCK
-    _vec(b_scale, (torch.float32,), "b_scale", dev, (-(-N // block), nk))
-    with _on(stream):
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=a.device)
-        ldc = _mat(out, _FLOATS, "out", dev, (M, N))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_gemm_fp8(a, a_scale, b, b_scale, out, dtype, status)
+    dev, a_shape = _first(a, "a")
+    b_shape = _first(b, "b")[1]
+    M, K = a_shape
+    N = b_shape[0]
+    if b_shape[1] != K:
+        raise ValueError(f"a and b differ in K: {K} and {b_shape[1]}")
+    p_a, lda = _operand(a, "a", dev, a_shape)
+    p_b, ldb = _operand(b, "b", dev, b_shape)
+    nk = (K + 127) // 128
+    _vec(a_scale, _F32, "a_scale", dev, (M, nk))
+    block = 1 if isinstance(b_scale, torch.Tensor) and b_scale.shape == (N, nk) else 128
+    _vec(b_scale, _F32, "b_scale", dev, (-(-N // block), nk))
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    c_type, ldc = _mat(out, _TYPES, "out", dev, (M, N))
+    if status is None:
+        status = _STATUS.get(dev)
         if status is None:
-            status = _STATUS.get(dev)
-            if status is None:
-                status = status_word(a.device)
-        _run("twell_gemm_fp8", dev, stream, a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(),
-             ldb, b_scale.data_ptr(), block, M, N, K, out.data_ptr(), _TYPES[out.dtype], ldc,
-             status.data_ptr())
+            status = status_word(a.device)
+    _run("twell_gemm_fp8", dev, p_a, lda, a_scale.data_ptr(), p_b, ldb, b_scale.data_ptr(), block,
+         M, N, K, out.data_ptr(), c_type, ldc, status.data_ptr())
     return out
 
 
@@ -822,17 +858,25 @@ def twell_gate_pack_fp8(xq, x_scale, wq, w_scale, out: TwELL, z_debug=None, stat
                         stream=None):
     """``twell_gate_pack`` from 8-bit operands: xq [T][D] with a scale for each
     128 of a row, wq [F][D] (= W_g^T) with one for each 128 x 128 block."""
-    dev = _device_of(xq, "xq")
-    ldx, ldw = _operand(xq, "xq", dev), _operand(wq, "wq", dev)
-    (T, D), (F, Dw) = xq.shape, wq.shape
-    if Dw != D or out.T != T or out.F != F:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_gate_pack_fp8(xq, x_scale, wq, w_scale, out, z_debug, status)
+    dev, x_shape = _first(xq, "xq")
+    w_shape = _first(wq, "wq")[1]
+    T, D = x_shape
+    F = w_shape[0]
+    if w_shape[1] != D or out.T != T or out.F != F:
         raise ValueError("shape mismatch: xq [T][D], wq [F][D], out of T and F")
-    nk = -(-D // FP8_BLOCK)
-    _vec(x_scale, (torch.float32,), "x_scale", dev, (T, nk))
-    _vec(w_scale, (torch.float32,), "w_scale", dev, (-(-F // FP8_BLOCK), nk))
+    p_x, ldx = _operand(xq, "xq", dev, x_shape)
+    p_w, ldw = _operand(wq, "wq", dev, w_shape)
+    nk = (D + 127) // 128
+    _vec(x_scale, _F32, "x_scale", dev, (T, nk))
+    _vec(w_scale, _F32, "w_scale", dev, (-(-F // 128), nk))
+    p_z = None
     if z_debug is not None:
-        _vec(z_debug, (torch.float32,), "z_debug", dev, (T, F))
-    _run("twell_gate_pack_fp8", dev, stream, xq.data_ptr(), ldx, x_scale.data_ptr(),
-         wq.data_ptr(), ldw, w_scale.data_ptr(), T, D, F, ctypes.byref(out.struct),
-         _addr(z_debug), _addr(out.status if status is None else status))
+        _vec(z_debug, _F32, "z_debug", dev, (T, F))
+        p_z = z_debug.data_ptr()
+    _run("twell_gate_pack_fp8", dev, p_x, ldx, x_scale.data_ptr(), p_w, ldw, w_scale.data_ptr(),
+         T, D, F, ctypes.byref(out.struct), p_z,
+         (out.status if status is None else status).data_ptr())
     return out

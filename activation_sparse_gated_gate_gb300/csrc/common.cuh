@@ -2,6 +2,7 @@
 // properties, argument checks and tensor-map encoding.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -25,6 +26,28 @@ bool current_device(DeviceInfo* out);
 // TWELL_OK if the current device is an sm_103 part, else
 // TWELL_ERR_UNSUPPORTED (or TWELL_ERR_CUDA if it cannot be queried).
 twell_status require_sm103(DeviceInfo* info);
+
+// The dynamic shared memory limit of a kernel, raised to `bytes` by the first
+// launch on each device (`set`: one bit per device, a static of the launching
+// code).  A launch that fails clears its device's bit (smem_launched), so a
+// context created again after a reset is set up again by the next call.
+template <typename K>
+bool smem_limit(K kern, int bytes, const DeviceInfo& dev, std::atomic<uint64_t>& set) {
+  const uint64_t bit = 1ull << dev.ordinal;
+  if (set.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  set.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+inline twell_status smem_launched(cudaError_t e, const DeviceInfo& dev,
+                                  std::atomic<uint64_t>& set) {
+  if (e == cudaSuccess) return TWELL_OK;
+  set.fetch_and(~(1ull << dev.ordinal), std::memory_order_relaxed);
+  return TWELL_ERR_CUDA;
+}
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -657,11 +657,10 @@ twell_status launch(const DeviceInfo& dev, const void* x, int64_t ldx, const voi
     return st;
   const int smem = p.region + p.xch_bytes + kBarBytes + scales + 1024;
   auto kern = gate_decode_kernel<FP8, PACK>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return TWELL_ERR_CUDA;
+  static std::atomic<uint64_t> set{0};
+  if (!smem_limit(kern, dev.max_smem_optin, dev, set)) return TWELL_ERR_CUDA;
   kern<<<2 * p.n_t, kThreads, smem, s>>>(mx, mw, p);
-  return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+  return smem_launched(cudaGetLastError(), dev, set);
 }
 
 // The fields of a call that packs into `out`.

@@ -520,9 +520,8 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
   using Cfg = Fp8Cfg<PAIR, BROWS>;
   static_assert(Cfg::SMEM <= 232448, "shared memory budget");
   auto kern = gemm_fp8_kernel<PAIR, BROWS, PACK>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) !=
-      cudaSuccess)
-    return TWELL_ERR_CUDA;
+  static std::atomic<uint64_t> set{0};
+  if (!smem_limit(kern, Cfg::SMEM, dev, set)) return TWELL_ERR_CUDA;
   if (PAIR) {
     // the register split draws on what the block starts with: never launched with less
     static const int regs = [&] {
@@ -545,7 +544,7 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, p) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+  return smem_launched(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, p), dev, set);
 }
 
 // Operand checks shared by the entry points: e4m3 rows on 16-byte boundaries.
