@@ -737,19 +737,22 @@ def twell_rms_norm_bwd(total, weight, rstd, dy, dtotal=None, dx=None, dw=None, w
     if dtotal is not None:
         lddt = _mat(dtotal, same, "dtotal", dev, shape)[1]
         p_dt = dtotal.data_ptr()
+    device, lddx = total.device, D
     if dx is None:
-        dx = torch.empty((T, D), dtype=total.dtype, device=total.device)
+        dx = torch.empty((T, D), dtype=total.dtype, device=device)
+    else:
+        lddx = _mat(dx, same, "dx", dev, shape)[1]
     if dw is None:
-        dw = torch.empty((D,), dtype=torch.float32, device=total.device)
-    lddx = _mat(dx, same, "dx", dev, shape)[1]
-    _vec(dw, _F32, "dw", dev, (D,))
+        dw = torch.empty((D,), dtype=torch.float32, device=device)
+    else:
+        _vec(dw, _F32, "dw", dev, (D,))
     if ws is None:
         if torch._C._cuda_getDevice() == dev:
             need = twell_rms_norm_bwd_workspace(T, D)
         else:
             with torch.cuda.device(dev):
                 need = twell_rms_norm_bwd_workspace(T, D)
-        ws = _workspace(need, total.device)
+        ws = _workspace(need, device)
     _run("twell_rms_norm_bwd", dev, total.data_ptr(), code, ld, weight.data_ptr(), w_type,
          rstd.data_ptr(), dy.data_ptr(), dy_type, lddy, p_dt, lddt, T, D, dx.data_ptr(), lddx,
          dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
@@ -791,8 +794,10 @@ def twell_quant_fp8(x, block_rows=1, rows=True, transposed=False, out=None,
         if q is None:
             q = _empty_e4m3(R, C, x.device)
             scale = torch.empty(at, dtype=f32, device=x.device)
-        ldq = _mat(q, _E4M3, "q", dev, shape)[1]
-        _vec(scale, _F32, "scale", dev, at)
+            ldq = (C + 15) // 16 * 16
+        else:
+            ldq = _mat(q, _E4M3, "q", dev, shape)[1]
+            _vec(scale, _F32, "scale", dev, at)
         p_q, p_scale = q.data_ptr(), scale.data_ptr()
     else:
         q = scale = None
@@ -801,8 +806,10 @@ def twell_quant_fp8(x, block_rows=1, rows=True, transposed=False, out=None,
         if qt is None:
             qt = _empty_e4m3(C, R, x.device)
             scale_t = torch.empty(at, dtype=f32, device=x.device)
-        ldqt = _mat(qt, _E4M3, "qt", dev, (C, R))[1]
-        _vec(scale_t, _F32, "scale_t", dev, at)
+            ldqt = (R + 15) // 16 * 16
+        else:
+            ldqt = _mat(qt, _E4M3, "qt", dev, (C, R))[1]
+            _vec(scale_t, _F32, "scale_t", dev, at)
         p_qt, p_scale_t = qt.data_ptr(), scale_t.data_ptr()
     else:
         qt = scale_t = None
@@ -830,21 +837,42 @@ def twell_gemm_fp8(a, a_scale, b, b_scale, out=None, dtype=torch.bfloat16, statu
     if stream is not None:
         with torch.cuda.stream(stream):
             return twell_gemm_fp8(a, a_scale, b, b_scale, out, dtype, status)
-    dev, a_shape = _first(a, "a")
-    b_shape = _first(b, "b")[1]
-    M, K = a_shape
-    N = b_shape[0]
-    if b_shape[1] != K:
-        raise ValueError(f"a and b differ in K: {K} and {b_shape[1]}")
-    p_a, lda = _operand(a, "a", dev, a_shape)
-    p_b, ldb = _operand(b, "b", dev, b_shape)
-    nk = (K + 127) // 128
-    _vec(a_scale, _F32, "a_scale", dev, (M, nk))
-    block = 1 if isinstance(b_scale, torch.Tensor) and b_scale.shape == (N, nk) else 128
-    _vec(b_scale, _F32, "b_scale", dev, (-(-N // block), nk))
+    f32, e4m3 = torch.float32, torch.float8_e4m3fn
+    try:
+        (M, K), (N, Kb), nk = a.shape, b.shape, a_scale.shape[1]
+        dev = a.get_device()
+        block = 1 if b_scale.shape[0] == N else 128
+        plain = (a.dtype is e4m3 and b.dtype is e4m3 and a_scale.dtype is f32
+                 and b_scale.dtype is f32 and Kb == K and nk == (K + 127) // 128
+                 and a_scale.shape == (M, nk) and b_scale.shape == (-(-N // block), nk)
+                 and 0 <= dev == b.get_device() == a_scale.get_device() == b_scale.get_device()
+                 and K % 16 == 0 and a.is_contiguous() and b.is_contiguous()
+                 and a_scale.is_contiguous() and b_scale.is_contiguous())
+    except (AttributeError, IndexError, TypeError, ValueError):
+        plain = False
+    lda = ldb = 0
+    if plain:
+        p_a, p_b = a.data_ptr(), b.data_ptr()
+        if p_a % 16 or p_b % 16:
+            plain = False
+        lda = ldb = K
+    if not plain:  # rows apart, or something to refuse
+        dev, a_shape = _first(a, "a")
+        b_shape = _first(b, "b")[1]
+        (M, K), N = a_shape, b_shape[0]
+        if b_shape[1] != K:
+            raise ValueError(f"a and b differ in K: {K} and {b_shape[1]}")
+        p_a, lda = _operand(a, "a", dev, a_shape)
+        p_b, ldb = _operand(b, "b", dev, b_shape)
+        nk = (K + 127) // 128
+        _vec(a_scale, _F32, "a_scale", dev, (M, nk))
+        block = 1 if isinstance(b_scale, torch.Tensor) and b_scale.shape == (N, nk) else 128
+        _vec(b_scale, _F32, "b_scale", dev, (-(-N // block), nk))
     if out is None:
         out = torch.empty((M, N), dtype=dtype, device=a.device)
-    c_type, ldc = _mat(out, _TYPES, "out", dev, (M, N))
+        c_type, ldc = _TYPES.get(dtype, -1), N
+    else:
+        c_type, ldc = _mat(out, _TYPES, "out", dev, (M, N))
     if status is None:
         status = _STATUS.get(dev)
         if status is None:
