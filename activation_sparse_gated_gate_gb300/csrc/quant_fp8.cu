@@ -6,12 +6,15 @@
 // the source for 1 x 128 blocks (the operand of a product that sums over the
 // source's rows), the same 128 x 128 blocks otherwise.
 //
-// Bound by memory.  One CTA takes a tile of 128 x 128: thread (g, c) of
-// 16 x 16 holds rows 8 g .. 8 g + 7 of columns 8 c .. 8 c + 7 in registers, so
-// the source is read once for both outputs; a row's maximum is taken over the
-// 16 lanes of a half-warp, a column's over the thread's rows and then the 16
-// row groups through shared memory, and a thread already holds eight rows of
-// a column, the eight bytes it puts into the transposed tile.
+// Bound by memory.  One CTA takes a tile of 128 columns by 128 rows (16 x 16
+// threads, thread (g, c) holding rows 8 g .. 8 g + 7 of columns 8 c .. 8 c + 7) so
+// that the source is read once for both outputs; a row's maximum is taken over
+// the 16 lanes of a half-warp, a column's over the thread's rows and then the 16
+// row groups through shared memory, and a thread already holds eight rows of a
+// column, the eight bytes it puts into the transposed tile.  bf16 stays packed
+// in registers until it is scaled (64 values in 32 registers: 4 CTAs per SM).
+// Without the transpose there is no shared memory and a thread holds two rows,
+// so that more of them are in flight.
 #include "common.cuh"
 #include "vec.cuh"
 
@@ -28,120 +31,223 @@ struct QuantParams {
   float* scale_t;
 };
 
-constexpr int kPitch = 144;   // bytes of a row of the transposed tile in shared memory
+// Eight neighbouring values of a row as they were loaded.
+template <typename T>
+struct Piece;
+
+template <>
+struct Piece<float> {
+  float v[8];
+  typedef float Max;  // largest |v| so far of one column
+  static constexpr int MAXES = 8;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const float* p, int n) {
+    load8<VEC>(p, n, v);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  }
+  __device__ __forceinline__ float get(int j) const { return v[j]; }
+  __device__ __forceinline__ float amax() const { return amax8(v); }
+  __device__ __forceinline__ void fold(Max (&m)[MAXES]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], fabsf(v[j]));
+  }
+  static __device__ __forceinline__ float max_of(const Max (&m)[MAXES], int j) { return m[j]; }
+};
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));  // of a number and a NaN: the number
+  return r;
+}
+
+template <>
+struct Piece<uint16_t> {
+  uint32_t v[4];
+  typedef uint32_t Max;  // of two columns
+  static constexpr int MAXES = 4;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (VEC) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = (2 * k < n ? p[2 * k] : 0u) |
+               (2 * k + 1 < n ? static_cast<uint32_t>(p[2 * k + 1]) << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = 0u;
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return __uint_as_float(j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16);
+  }
+  __device__ __forceinline__ float amax() const {
+    Max m = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = max_bf16x2(m, v[k] & 0x7fff7fffu);
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  __device__ __forceinline__ void fold(Max (&m)[MAXES]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = max_bf16x2(m[k], v[k] & 0x7fff7fffu);
+  }
+  static __device__ __forceinline__ float max_of(const Max (&m)[MAXES], int j) {
+    return __uint_as_float(j & 1 ? m[j / 2] & 0xffff0000u : m[j / 2] << 16);
+  }
+};
+
+// e4m3 of four values times their scales.
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float inv) {
+  return e4m3x4(a * inv, b * inv, c * inv, d * inv);
+}
 
 // VEC: 16-byte aligned source rows, C % 8 == 0 and 8-byte aligned rows of q.
-// WIDE_T: rows of qt on 16-byte boundaries.
-template <typename T, bool VEC, bool SQUARE>
+// SQUARE: blocks of 128 x 128 (else 1 x 128).  TRANS: qt is written; with
+// neither a thread holds two rows of a tile of 32.  wide_t: rows of qt on
+// 16-byte boundaries.
+template <typename T, bool VEC, bool SQUARE, bool TRANS>
 __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, const bool wide_t) {
-  __shared__ float colmax[16][128 + 4];
-  __shared__ __align__(16) uint8_t tile[128 * kPitch];
+  constexpr int ROWS = SQUARE || TRANS ? 8 : 2;
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 128 + 8 * g;
-  const int c0 = blockIdx.x * 128 + 8 * c;
-  const int nc = p.C - c0;
-  float v[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    if (r0 + i < p.R && nc > 0)
-      load8<VEC>(static_cast<const T*>(p.src) + (r0 + i) * p.ld + c0, nc, v[i]);
-  }
   const int64_t nbc = (p.C + 127) / 128, nbr = (p.R + 127) / 128;
+  const int bx = blockIdx.x % static_cast<unsigned>(nbc);  // the tile's columns and rows
+  const int64_t by = blockIdx.x / static_cast<unsigned>(nbc);
+  const int64_t r0 = (by * 16 + g) * ROWS;
+  const int c0 = bx * 128 + 8 * c;
+  const int nc = p.C - c0;
+  Piece<T> v[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (r0 + i < p.R && nc > 0)
+      v[i].template load<VEC>(static_cast<const T*>(p.src) + (r0 + i) * p.ld + c0, nc);
+    else v[i].clear();
+  }
   float inv_all = 0.0f;
-  if (SQUARE) {
+  if constexpr (SQUARE) {
+    __shared__ float wmax[8];
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, amax8(v[i]));
+    for (int i = 0; i < ROWS; ++i) m = fmaxf(m, v[i].amax());
     m = half_warp_max(m);
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-    if ((threadIdx.x & 31) == 0) colmax[0][threadIdx.x >> 5] = m;
+    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, colmax[0][i]);
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, wmax[i]);
     m = fmaxf(m, kFp8AmaxMin);
     inv_all = kFp8Max / m;
     if (threadIdx.x == 0) {
-      if (p.scale) p.scale[blockIdx.y * nbc + blockIdx.x] = m / kFp8Max;
-      if (p.scale_t) p.scale_t[blockIdx.x * nbr + blockIdx.y] = m / kFp8Max;
+      if (p.scale) p.scale[by * nbc + bx] = m / kFp8Max;
+      if (p.scale_t) p.scale_t[bx * nbr + by] = m / kFp8Max;
     }
   }
   if (p.q) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       float inv = inv_all;
       if (!SQUARE) {
-        const float m = fmaxf(half_warp_max(amax8(v[i])), kFp8AmaxMin);
+        const float m = fmaxf(half_warp_max(v[i].amax()), kFp8AmaxMin);
         inv = kFp8Max / m;
-        if (c == 0 && r0 + i < p.R) p.scale[(r0 + i) * nbc + blockIdx.x] = m / kFp8Max;
+        if (c == 0 && r0 + i < p.R) p.scale[(r0 + i) * nbc + bx] = m / kFp8Max;
       }
-      if (r0 + i < p.R && nc > 0) store8_e4m3<VEC>(p.q + (r0 + i) * p.ldq + c0, nc, v[i], inv);
+      if (r0 + i < p.R && nc > 0) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[i].get(j);
+        store8_e4m3<VEC>(p.q + (r0 + i) * p.ldq + c0, nc, f, inv);
+      }
     }
   }
-  if (!p.qt) return;
-  float inv[8];
-  if (SQUARE) {
+  if constexpr (TRANS) {
+    // the transposed tile: row = column of the source, 16 units of 8 bytes (one
+    // per row group), unit u of row r at u ^ (r / 8): the 16 lanes of a half-warp
+    // write one unit of 16 rows without bank conflicts
+    __shared__ __align__(16) uint2 tile[128][16];
+    float inv[8];
+    if constexpr (SQUARE) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) inv[j] = inv_all;
-  } else {
-    float m[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[j] = fmaxf(m[j], fabsf(v[i][j]));
-    }
-    *reinterpret_cast<float4*>(&colmax[g][8 * c]) = make_float4(m[0], m[1], m[2], m[3]);
-    *reinterpret_cast<float4*>(&colmax[g][8 * c + 4]) = make_float4(m[4], m[5], m[6], m[7]);
-    __syncthreads();
-    if (threadIdx.x < 128) {
-      float a = kFp8AmaxMin;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) a = fmaxf(a, colmax[i][threadIdx.x]);
-      const int64_t col = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-      if (col < p.C) p.scale_t[col * nbr + blockIdx.y] = a / kFp8Max;
-      colmax[0][threadIdx.x] = kFp8Max / a;   // this thread's own column
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) inv[j] = colmax[0][8 * c + j];
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint2*>(tile + (8 * c + j) * kPitch + 8 * g) =
-        make_uint2(e4m3x4(v[0][j] * inv[j], v[1][j] * inv[j], v[2][j] * inv[j], v[3][j] * inv[j]),
-                   e4m3x4(v[4][j] * inv[j], v[5][j] * inv[j], v[6][j] * inv[j], v[7][j] * inv[j]));
-  __syncthreads();
-  // rows of the transposed tile: 8 threads of 16 bytes each
-  const int64_t rt = static_cast<int64_t>(blockIdx.y) * 128;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int col = (threadIdx.x >> 3) + 32 * i, b = (threadIdx.x & 7) * 16;
-    const int64_t gc = static_cast<int64_t>(blockIdx.x) * 128 + col;
-    if (gc >= p.C) continue;
-    const uint8_t* s = tile + col * kPitch + b;
-    uint8_t* d = p.qt + gc * p.ldqt + rt + b;
-    const int64_t left = p.R - (rt + b);
-    if (wide_t && left >= 16) {
-      *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
+      for (int j = 0; j < 8; ++j) inv[j] = inv_all;
     } else {
-      for (int k = 0; k < 16 && k < left; ++k) d[k] = s[k];
+      typedef typename Piece<T>::Max Max;
+      constexpr int MAXES = Piece<T>::MAXES;
+      __shared__ __align__(16) Max colmax[16][16 * MAXES];
+      __shared__ float colinv[128];
+      Max m[MAXES];
+#pragma unroll
+      for (int k = 0; k < MAXES; ++k) m[k] = 0;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) v[i].fold(m);
+#pragma unroll
+      for (int k = 0; k < MAXES; k += 4)
+        *reinterpret_cast<uint4*>(&colmax[g][MAXES * c + k]) =
+            *reinterpret_cast<const uint4*>(&m[k]);
+      __syncthreads();
+      if (threadIdx.x < 128) {
+        constexpr int PER = 8 / MAXES;  // columns of a Max
+        float a = kFp8AmaxMin;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const Max one[1] = {colmax[i][threadIdx.x / PER]};
+          Max mm[MAXES];
+          mm[0] = one[0];
+          a = fmaxf(a, Piece<T>::max_of(mm, threadIdx.x % PER));
+        }
+        const int64_t col = static_cast<int64_t>(bx) * 128 + threadIdx.x;
+        if (col < p.C) p.scale_t[col * nbr + by] = a / kFp8Max;
+        colinv[threadIdx.x] = kFp8Max / a;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) inv[j] = colinv[8 * c + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      tile[8 * c + j][g ^ c] =
+          make_uint2(quant4(v[0].get(j), v[1].get(j), v[2].get(j), v[3].get(j), inv[j]),
+                     quant4(v[4].get(j), v[5].get(j), v[6].get(j), v[7].get(j), inv[j]));
+    __syncthreads();
+    // rows of the transposed tile: 8 threads of 16 bytes (two units) each
+    const int64_t rt = by * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (threadIdx.x >> 3) + 32 * i, b = threadIdx.x & 7;
+      const int64_t gc = static_cast<int64_t>(bx) * 128 + row;
+      if (gc >= p.C) continue;
+      const int x = row >> 3, odd = row & 1;  // (odd rows take their units in the other order)
+      const uint2 u0 = tile[row][(2 * b + odd) ^ x], u1 = tile[row][(2 * b + 1 - odd) ^ x];
+      const uint4 w = odd ? make_uint4(u1.x, u1.y, u0.x, u0.y) : make_uint4(u0.x, u0.y, u1.x, u1.y);
+      uint8_t* d = p.qt + gc * p.ldqt + rt + 16 * b;
+      const int64_t left = p.R - (rt + 16 * b);
+      if (wide_t && left >= 16) {
+        *reinterpret_cast<uint4*>(d) = w;
+      } else {
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (k < left) d[k] = static_cast<uint8_t>(ww[k / 4] >> (8 * (k % 4)));
+      }
     }
   }
 }
 
-template <typename T>
-twell_status launch(const QuantParams& p, int32_t block_rows, bool vec, bool wide_t,
-                    cudaStream_t s) {
-  const dim3 grid((p.C + 127) / 128, (p.R + 127) / 128);
-  if (block_rows == 1) {
-    if (vec) quant_fp8_kernel<T, true, false><<<grid, 256, 0, s>>>(p, wide_t);
-    else quant_fp8_kernel<T, false, false><<<grid, 256, 0, s>>>(p, wide_t);
-  } else {
-    if (vec) quant_fp8_kernel<T, true, true><<<grid, 256, 0, s>>>(p, wide_t);
-    else quant_fp8_kernel<T, false, true><<<grid, 256, 0, s>>>(p, wide_t);
-  }
+template <typename T, bool VEC>
+twell_status launch(const QuantParams& p, int32_t block_rows, bool wide_t, cudaStream_t s) {
+  const bool square = block_rows != 1, trans = p.qt != nullptr;
+  const int rows = square || trans ? 128 : 32;
+  const int64_t tiles =
+      (static_cast<int64_t>(p.C) + 127) / 128 * ((static_cast<int64_t>(p.R) + rows - 1) / rows);
+  if (tiles > 0x7fffffff) return TWELL_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(tiles);
+  if (square && trans) quant_fp8_kernel<T, VEC, true, true><<<grid, 256, 0, s>>>(p, wide_t);
+  else if (square) quant_fp8_kernel<T, VEC, true, false><<<grid, 256, 0, s>>>(p, wide_t);
+  else if (trans) quant_fp8_kernel<T, VEC, false, true><<<grid, 256, 0, s>>>(p, wide_t);
+  else quant_fp8_kernel<T, VEC, false, false><<<grid, 256, 0, s>>>(p, wide_t);
   return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
@@ -166,7 +272,6 @@ extern "C" twell_status twell_quant_fp8(const void* src, int32_t type, int64_t l
   if (a % elem != 0 || reinterpret_cast<uintptr_t>(scale) % 4 != 0 ||
       reinterpret_cast<uintptr_t>(scale_t) % 4 != 0)
     return TWELL_ERR_INVALID;
-  if ((static_cast<int64_t>(R) + 127) / 128 > 65535) return TWELL_ERR_UNSUPPORTED;  // grid rows
   DeviceInfo dev;
   twell_status st;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
@@ -175,6 +280,9 @@ extern "C" twell_status twell_quant_fp8(const void* src, int32_t type, int64_t l
                    (!q || (reinterpret_cast<uintptr_t>(q) % 8 == 0 && ldq % 8 == 0));
   const bool wide_t = qt && aligned16(qt) && ldqt % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return type == TWELL_BF16 ? launch<uint16_t>(p, block_rows, vec, wide_t, s)
-                            : launch<float>(p, block_rows, vec, wide_t, s);
+  if (type == TWELL_BF16)
+    return vec ? launch<uint16_t, true>(p, block_rows, wide_t, s)
+               : launch<uint16_t, false>(p, block_rows, wide_t, s);
+  return vec ? launch<float, true>(p, block_rows, wide_t, s)
+             : launch<float, false>(p, block_rows, wide_t, s);
 }
