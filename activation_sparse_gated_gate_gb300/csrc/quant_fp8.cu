@@ -102,6 +102,27 @@ struct Piece<uint16_t> {
   }
 };
 
+// The maxima of ROWS rows over the 16 lanes of a half-warp: the lanes halve the
+// rows between them as long as there are several (ROWS - 1 shuffles, then one
+// for each step left, where a butterfly for each row would take four).  Lane c
+// ends with the maximum of row c / (16 / ROWS).
+template <int ROWS>
+__device__ __forceinline__ float rows_max(float (&m)[ROWS], int c) {
+  int o = 8;
+#pragma unroll
+  for (int n = ROWS / 2; n > 0; n /= 2, o /= 2) {
+    const bool upper = (c & o) != 0;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float away = upper ? m[k] : m[k + n];
+      const float mine = upper ? m[k + n] : m[k];
+      m[k] = fmaxf(mine, __shfl_xor_sync(0xffffffffu, away, o));
+    }
+  }
+  for (; o > 0; o /= 2) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+  return m[0];
+}
+
 // e4m3 of four values times their scales.
 __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float inv) {
   return e4m3x4(a * inv, b * inv, c * inv, d * inv);
@@ -148,14 +169,21 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, con
     }
   }
   if (p.q) {
+    constexpr int SHARE = 16 / ROWS;  // lanes that end with the same row's maximum
+    float inv_row = 0.0f;             // of row c / SHARE
+    if (!SQUARE) {
+      float m[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) m[i] = v[i].amax();
+      const float a = fmaxf(rows_max(m, c), kFp8AmaxMin);
+      inv_row = kFp8Max / a;
+      const int64_t r = r0 + c / SHARE;
+      if (c % SHARE == 0 && r < p.R) p.scale[r * nbc + bx] = a / kFp8Max;
+    }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      float inv = inv_all;
-      if (!SQUARE) {
-        const float m = fmaxf(half_warp_max(v[i].amax()), kFp8AmaxMin);
-        inv = kFp8Max / m;
-        if (c == 0 && r0 + i < p.R) p.scale[(r0 + i) * nbc + bx] = m / kFp8Max;
-      }
+      const float inv =
+          SQUARE ? inv_all : __shfl_sync(0xffffffffu, inv_row, i * SHARE, 16);
       if (r0 + i < p.R && nc > 0) {
         float f[8];
 #pragma unroll
