@@ -421,6 +421,20 @@ __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* gsrc,
                : "memory");
 }
 
+// Asynchronous copy of 8 or 16 aligned bytes.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t smem_dst, const void* gsrc) {
+  static_assert(BYTES == 8 || BYTES == 16, "copy size");
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst),
+                 "l"(reinterpret_cast<uint64_t>(gsrc))
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_dst),
+                 "l"(reinterpret_cast<uint64_t>(gsrc))
+                 : "memory");
+}
+
 // The same for 4 bytes (src_bytes 4, or 0 for zeros).
 __device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* gsrc,
                                           uint32_t src_bytes) {

@@ -21,6 +21,7 @@
 namespace twell {
 namespace {
 
+constexpr int kPipeThreads = 640; // of the pipelined backward (96 registers each: no spills)
 constexpr int kMaxD = 16384;   // 1024 threads of two pieces
 
 struct NormParams {
@@ -123,6 +124,41 @@ struct NormBwdParams {
   float* part;        // [gridDim.x][D]
 };
 
+// The groups' shares of dw, added in order in shared memory (`join` [D], used
+// when there are several groups), into this block's row of the partial sums.
+template <int MAXC>
+__device__ __forceinline__ void join_dw(const NormBwdParams& p, float (&acc)[MAXC][8],
+                                        float* join) {
+  const int L = blockDim.x, G = blockDim.y, grp = threadIdx.y;
+  if (G > 1) {
+    for (int k = 0; k < G; ++k) {
+      if (grp == k) {
+#pragma unroll
+        for (int i = 0; i < MAXC; ++i) {
+          const int e = (threadIdx.x + i * L) * 8;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (e + j < p.D) {
+              if (k > 0) acc[i][j] += join[e + j];
+              join[e + j] = acc[i][j];
+            }
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (grp == G - 1) {
+    float* o = p.part + static_cast<size_t>(blockIdx.x) * p.D;
+#pragma unroll
+    for (int i = 0; i < MAXC; ++i) {
+      const int e = (threadIdx.x + i * L) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e + j < p.D) o[e + j] = acc[i][j];
+    }
+  }
+}
+
 // blockDim = (L, G): G groups of L threads, a row each at a time, each group
 // with named barrier 1 + group.  A thread's columns are the same in every
 // row, so its share of dw stays in registers until the block's last row; the
@@ -200,31 +236,123 @@ __global__ void __launch_bounds__(1024) rms_norm_bwd_kernel(const NormBwdParams 
       }
     }
   }
-  if (G > 1) {
-    for (int k = 0; k < G; ++k) {
-      if (grp == k) {
+  join_dw<MAXC>(p, acc, join);
+}
+
+// The same for rows on 16-byte boundaries of at most eight elements a thread:
+// each thread copies its own elements of the next P rows into shared memory
+// (cp.async), so several rows of every group are on their way while one is
+// worked on and nobody waits for another thread's copies.  A thread has two
+// quads, L quads apart, so that a warp's copy or store of one is a contiguous
+// run (with eight neighbours per thread, copies that bypass L1 fetch every
+// 32-byte sector of an fp32 row twice).
+template <typename ST, typename GT, int P>
+__global__ void __launch_bounds__(kPipeThreads) rms_norm_bwd_pipe_kernel(const NormBwdParams p) {
+  constexpr int SB = 4 * sizeof(ST), GB = 4 * sizeof(GT);  // bytes of a quad
+  extern __shared__ __align__(16) uint8_t ring[];  // [P][2 of s, 2 of dtotal, 2 of dy][threads]
+  __shared__ float red[2][32];
+  const int L = blockDim.x, G = blockDim.y, grp = threadIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = L >> 5;
+  const int nt = L * G, tid = grp * L + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  const int slot_bytes = nt * (4 * SB + 2 * GB);
+  const int e[2] = {4 * static_cast<int>(threadIdx.x), 4 * (L + static_cast<int>(threadIdx.x))};
+  float w[8], acc[8];
 #pragma unroll
-        for (int i = 0; i < MAXC; ++i) {
-          const int e = (threadIdx.x + i * L) * 8;
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (e + j < p.D) {
-              if (k > 0) acc[i][j] += join[e + j];
-              join[e + j] = acc[i][j];
-            }
+    for (int j = 0; j < 4; ++j) {
+      acc[4 * k + j] = 0.0f;
+      w[4 * k + j] = e[k] >= p.D ? 0.0f
+                     : p.w_bf16 ? widen(static_cast<const uint16_t*>(p.w)[e[k] + j])
+                                : static_cast<const float*>(p.w)[e[k] + j];
+    }
+  const uint32_t ring0 = ptx::smem_u32(ring);
+  const auto fetch = [&](int64_t t, int slot) {
+    if (t < p.T) {
+      const uint32_t to = ring0 + slot * slot_bytes + tid * SB;
+      const uint32_t tg = ring0 + slot * slot_bytes + 4 * nt * SB + tid * GB;
+      const ST* s = static_cast<const ST*>(p.s) + t * p.lds;
+      const GT* g = static_cast<const GT*>(p.dy) + t * p.lddy;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (e[k] < p.D) {
+          ptx::cp_async<SB>(to + k * nt * SB, s + e[k]);
+          if (p.dt)
+            ptx::cp_async<SB>(to + (2 + k) * nt * SB,
+                              static_cast<const ST*>(p.dt) + t * p.lddt + e[k]);
+          ptx::cp_async<GB>(tg + k * nt * GB, g + e[k]);
         }
-      }
-      __syncthreads();
+    }
+    ptx::cp_async_commit();  // (a group for every row, empty ones past T)
+  };
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * G + grp;
+#pragma unroll
+  for (int k = 0; k < P; ++k) fetch(t0 + k * step, k);
+  int par = 0, slot = 0;
+  const auto rstd_of = [&](int64_t t) { return t < p.T ? p.rstd[t] : 0.0f; };
+  float rstd1 = rstd_of(t0), rstd2 = rstd_of(t0 + step);  // this row's and the next's
+  for (int64_t t = t0; t < p.T; t += step, par ^= 1) {
+    const float rstd = rstd1;
+    rstd1 = rstd2;
+    rstd2 = rstd_of(t + 2 * step);
+    ptx::cp_async_wait<P - 1>();
+    const uint8_t* at = ring + slot * slot_bytes + tid * SB;
+    const uint8_t* ag = ring + slot * slot_bytes + 4 * nt * SB + tid * GB;
+    float n[8], g[8], d[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool have = e[k] < p.D;
+      quad<ST>(at + k * nt * SB, have, n + 4 * k);
+      quad<GT>(ag + k * nt * GB, have, g + 4 * k);
+      quad<ST>(at + (2 + k) * nt * SB, have && p.dt, d + 4 * k);
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      n[j] *= rstd;
+      acc[j] = fmaf(g[j], n[j], acc[j]);
+      g[j] *= w[j];
+      dot = fmaf(g[j], n[j], dot);
+    }
+    dot = warp_sum(dot);
+    fetch(t + P * step, slot);  // (this thread's values of the slot are in registers)
+    if (++slot == P) slot = 0;
+    if (nw > 1) {
+      // two buffers in turn, as above
+      if (lane == 0) red[par][grp * nw + warp] = dot;
+      ptx::bar_sync(1 + grp, L);
+      dot = warp_sum(lane < nw ? red[par][grp * nw + lane] : 0.0f);
+    }
+    dot *= inv_d;
+    ST* dxr = static_cast<ST*>(p.dx) + t * p.lddx;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int j = 4 * k; j < 4 * k + 4; ++j) n[j] = fmaf(rstd, g[j] - n[j] * dot, d[j]);
+      if (e[k] < p.D) store4(dxr + e[k], n + 4 * k);
     }
   }
-  if (grp == G - 1) {
-    float* o = p.part + static_cast<size_t>(blockIdx.x) * p.D;
+  ptx::cp_async_wait<0>();
+  // the groups' shares of dw, added in order in the ring
+  float* join = reinterpret_cast<float*>(ring);
+  for (int i = 0; i < G; ++i) {
+    __syncthreads();
+    if (grp == i) {
 #pragma unroll
-    for (int i = 0; i < MAXC; ++i) {
-      const int e = (threadIdx.x + i * L) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e + j < p.D) o[e + j] = acc[i][j];
+      for (int k = 0; k < 2; ++k)
+        if (e[k] < p.D) {
+          float4* o = reinterpret_cast<float4*>(join + e[k]);
+          float4 v = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+          if (i > 0) {
+            const float4 u = *o;
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+          }
+          if (i + 1 == G)
+            o = reinterpret_cast<float4*>(p.part + static_cast<size_t>(blockIdx.x) * p.D + e[k]);
+          *o = v;
+        }
     }
   }
 }
@@ -274,14 +402,17 @@ twell_status launch_fwd(const NormParams& p, cudaStream_t s) {
 
 struct BwdShape {
   int per, L, G, grid;
+  bool pipe;
 };
 
-BwdShape bwd_shape(int32_t T, int32_t D, int sms) {
+// `vec`: every row on 16-byte boundaries.
+BwdShape bwd_shape(int32_t T, int32_t D, bool vec, int sms) {
   BwdShape b;
   const int pieces = (D + 7) / 8;
   b.per = pieces <= 1024 ? 1 : 2;
   b.L = threads_for(D, b.per);
-  b.G = 1024 / b.L;
+  b.pipe = vec && b.per == 1 && b.L <= kPipeThreads;
+  b.G = (b.pipe ? kPipeThreads : 1024) / b.L;
   if (b.G > 15) b.G = 15;                 // named barriers
   if (b.G < 1) b.G = 1;
   const int64_t want = (static_cast<int64_t>(T) + b.G - 1) / b.G;
@@ -289,9 +420,29 @@ BwdShape bwd_shape(int32_t T, int32_t D, int sms) {
   return b;
 }
 
+template <typename ST, typename GT, int P>
+twell_status launch_pipe(const NormBwdParams& p, const BwdShape& b, int smem,
+                         const DeviceInfo& dev, cudaStream_t s) {
+  static std::atomic<uint64_t> set{0};
+  auto kern = rms_norm_bwd_pipe_kernel<ST, GT, P>;
+  if (!smem_limit(kern, dev.max_smem_optin - 1024, dev, set)) return TWELL_ERR_CUDA;
+  kern<<<b.grid, dim3(b.L, b.G), smem, s>>>(p);
+  return smem_launched(cudaGetLastError(), dev, set);
+}
+
 template <typename ST, typename GT, bool VEC>
-twell_status launch_bwd(const NormBwdParams& p, const BwdShape& b, cudaStream_t s) {
+twell_status launch_bwd(const NormBwdParams& p, const BwdShape& b, const DeviceInfo& dev,
+                        cudaStream_t s) {
   const dim3 block(b.L, b.G);
+  if (VEC && b.pipe) {
+    // rows in flight per group: what fits beside the static shared memory (one
+    // row's pieces and the join's D floats always do)
+    const int row = b.L * b.G * 8 * (2 * static_cast<int>(sizeof(ST)) + static_cast<int>(sizeof(GT)));
+    const int budget = dev.max_smem_optin - 2048;
+    if (4 * row <= budget) return launch_pipe<ST, GT, 4>(p, b, 4 * row, dev, s);
+    if (3 * row <= budget) return launch_pipe<ST, GT, 3>(p, b, 3 * row, dev, s);
+    return launch_pipe<ST, GT, 2>(p, b, 2 * row, dev, s);
+  }
   const size_t smem = b.G > 1 ? static_cast<size_t>(p.D) * sizeof(float) : 0;
   if (b.per == 1) rms_norm_bwd_kernel<ST, GT, VEC, 1><<<b.grid, block, smem, s>>>(p);
   else rms_norm_bwd_kernel<ST, GT, VEC, 2><<<b.grid, block, smem, s>>>(p);
@@ -350,7 +501,8 @@ extern "C" size_t twell_rms_norm_bwd_workspace(int32_t T, int32_t D) {
   DeviceInfo dev;
   // (without a device: the most blocks a call would use on the part this is for)
   const int sms = current_device(&dev) ? dev.sm_count : 152;
-  const BwdShape b = bwd_shape(T > 0 ? T : 1, D, sms);
+  // (the element-by-element form has as many blocks or fewer)
+  const BwdShape b = bwd_shape(T > 0 ? T : 1, D, true, sms);
   return static_cast<size_t>(b.grid) * D * sizeof(float);
 }
 
@@ -382,25 +534,25 @@ extern "C" twell_status twell_rms_norm_bwd(const void* total, int32_t type, int6
       (dtotal && !elem_aligned(dtotal, se)))
     return TWELL_ERR_INVALID;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
-  const BwdShape b = bwd_shape(T, D, dev.sm_count);
-  if (ws_bytes < static_cast<size_t>(b.grid) * D * sizeof(float)) return TWELL_ERR_INVALID;
   NormBwdParams p{total, w, rstd, dy, dtotal, ld, lddy, lddt, lddx, T, D, w_type == TWELL_BF16,
                   dx, static_cast<float*>(ws)};
   const bool vec = D % 8 == 0 && rows_aligned(total, ld, se) && rows_aligned(w, 0, we) &&
                    rows_aligned(dy, lddy, ge) && rows_aligned(dx, lddx, se) &&
                    (!dtotal || rows_aligned(dtotal, lddt, se));
+  const BwdShape b = bwd_shape(T, D, vec, dev.sm_count);
+  if (ws_bytes < static_cast<size_t>(b.grid) * D * sizeof(float)) return TWELL_ERR_INVALID;
   const bool sb = type == TWELL_BF16, gb = dy_type == TWELL_BF16;
   if (sb && gb)
-    st = vec ? launch_bwd<uint16_t, uint16_t, true>(p, b, s)
-             : launch_bwd<uint16_t, uint16_t, false>(p, b, s);
+    st = vec ? launch_bwd<uint16_t, uint16_t, true>(p, b, dev, s)
+             : launch_bwd<uint16_t, uint16_t, false>(p, b, dev, s);
   else if (sb)
-    st = vec ? launch_bwd<uint16_t, float, true>(p, b, s)
-             : launch_bwd<uint16_t, float, false>(p, b, s);
+    st = vec ? launch_bwd<uint16_t, float, true>(p, b, dev, s)
+             : launch_bwd<uint16_t, float, false>(p, b, dev, s);
   else if (gb)
-    st = vec ? launch_bwd<float, uint16_t, true>(p, b, s)
-             : launch_bwd<float, uint16_t, false>(p, b, s);
+    st = vec ? launch_bwd<float, uint16_t, true>(p, b, dev, s)
+             : launch_bwd<float, uint16_t, false>(p, b, dev, s);
   else
-    st = vec ? launch_bwd<float, float, true>(p, b, s) : launch_bwd<float, float, false>(p, b, s);
+    st = vec ? launch_bwd<float, float, true>(p, b, dev, s) : launch_bwd<float, float, false>(p, b, dev, s);
   if (st != TWELL_OK) return st;
   norm_dw_kernel<<<(D + 31) / 32, dim3(32, 32), 0, s>>>(p.part, b.grid, D, dw);
   return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;

@@ -67,6 +67,27 @@ __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&f)[8]) {
   }
 }
 
+// Four values from an aligned place in shared memory (zeros without `have`), and
+// to an aligned place in a row.
+template <typename T>
+__device__ __forceinline__ void quad(const uint8_t* at, bool have, float* f) {
+  if (sizeof(T) == 4) {
+    const float4 a = have ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+  } else {
+    const uint2 a = have ? *reinterpret_cast<const uint2*>(at) : make_uint2(0u, 0u);
+    f[0] = __uint_as_float(a.x << 16), f[1] = __uint_as_float(a.x & 0xffff0000u);
+    f[2] = __uint_as_float(a.y << 16), f[3] = __uint_as_float(a.y & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void store4(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float* f) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]));
+}
+
 template <bool VEC>
 __device__ __forceinline__ void store8(float* p, int n, const float (&f)[8]) {
   if (VEC) {
