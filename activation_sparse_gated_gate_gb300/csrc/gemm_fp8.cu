@@ -400,9 +400,10 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
           for (int i = 0; i < kPiece / 4; ++i) {
             f32x2 f0 = s2, f1 = s2;
             if (BROWS) {
-              const float4 b4 = *reinterpret_cast<const float4*>(bs + ch * kPiece + 4 * i);
-              f0 = mul2(s2, pack2(__float_as_uint(b4.x), __float_as_uint(b4.y)));
-              f1 = mul2(s2, pack2(__float_as_uint(b4.z), __float_as_uint(b4.w)));
+              const ulonglong2 b4 =
+                  *reinterpret_cast<const ulonglong2*>(bs + ch * kPiece + 4 * i);
+              f0 = mul2(s2, b4.x);
+              f1 = mul2(s2, b4.y);
             }
             const uint32_t* rr = r[ch & 1] + 4 * i;
             fma2(acc[ch * (kPiece / 2) + 2 * i], pack2(rr[0], rr[1]), f0);
