@@ -14,13 +14,93 @@ Weights may be bf16 or fp32 master copies (cast to bf16 for the kernels on
 every call); their gradients come back from the library in fp32 and are
 returned in the weights' own dtype, as autograd requires, so fp32 masters keep
 fp32 gradients.  The activation stream x is bf16 (its gradient too).
+
+``AddRMSNormFunction`` is the residual addition and norm in front of an FFN
+(fused forward and backward), and ``Fp8LinearFunction`` a linear layer whose
+three products (y, dx, dW) run on e4m3 operands with block scales.
 """
 from __future__ import annotations
 
 import torch
 
 from . import (Hybrid, TwELL, hybrid_ffn_bwd, hybrid_ffn_bwd_tc, hybrid_ffn_fwd,
-               hybrid_ffn_fwd_tc, twell_gate_pack, twell_to_hybrid)
+               hybrid_ffn_fwd_tc, twell_gate_pack, twell_gemm_fp8, twell_quant_fp8,
+               twell_rms_norm, twell_rms_norm_bwd, twell_to_hybrid)
+
+
+def _rows(g):
+    """A gradient as the kernels read it: autograd may hand over an expanded or
+    a transposed one."""
+    return g if g.stride(-1) == 1 and (g.shape[0] < 2 or g.stride(0) >= g.shape[1]) \
+        else g.contiguous()
+
+
+class AddRMSNormFunction(torch.autograd.Function):
+    """(y, total): total = x + residual, y = bf16 of the norm of total times
+    weight.  x and residual [T][D] and weight [D] are bf16 or fp32 each, total has
+    residual's type.  Without a residual total is x and only y is returned."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        o = twell_rms_norm(x, weight, residual=residual, eps=eps, rstd=True)
+        total = x if residual is None else o.total
+        ctx.save_for_backward(total, weight, o.rstd)
+        ctx.types = (x.dtype, weight.dtype)
+        ctx.added = residual is not None
+        return (o.y, total) if ctx.added else o.y
+
+    @staticmethod
+    def backward(ctx, dy, dtotal=None):
+        total, weight, rstd = ctx.saved_tensors
+        if dtotal is not None:
+            dtotal = _rows(dtotal)
+        dx, dw = twell_rms_norm_bwd(total, weight, rstd, _rows(dy), dtotal=dtotal)
+        return (dx.to(ctx.types[0]), dw.to(ctx.types[1]), dx if ctx.added else None, None)
+
+
+class Fp8LinearFunction(torch.autograd.Function):
+    """y [T][N] = x W^T on e4m3 operands: x [T][K] and the gradient dy in blocks of
+    1 x 128 along the dimension each product sums over (so both are also quantised
+    transposed, for dW), W [N][K] in blocks of 128 x 128.  x and W are bf16 or
+    fp32; y has x's type, dx too, and dW is computed in fp32."""
+
+    @staticmethod
+    def forward(ctx, x, weight):
+        need_x, need_w = ctx.needs_input_grad
+        qx = twell_quant_fp8(x, transposed=need_w)
+        qw = twell_quant_fp8(weight, block_rows=128, transposed=need_x)
+        ctx.save_for_backward(qx.qt, qx.scale_t, qw.qt, qw.scale_t)
+        ctx.sizes = (x.shape, weight.shape)
+        ctx.types = (x.dtype, weight.dtype)
+        return twell_gemm_fp8(qx.q, qx.scale, qw.q, qw.scale, dtype=x.dtype)
+
+    @staticmethod
+    def backward(ctx, dy):
+        xt, xt_scale, wt, wt_scale = ctx.saved_tensors
+        need_x, need_w = ctx.needs_input_grad
+        (T, K), (N, _) = ctx.sizes
+        dx = dw = None
+        q = twell_quant_fp8(_rows(dy), rows=need_x, transposed=need_w)
+        if need_x:
+            dx = twell_gemm_fp8(q.q, q.scale, wt, wt_scale, dtype=ctx.types[0])
+        if need_w:
+            # (a sum over no rows is not a product the kernel takes)
+            dw = (twell_gemm_fp8(q.qt, q.scale_t, xt, xt_scale, dtype=torch.float32) if T
+                  else torch.zeros((N, K), dtype=torch.float32, device=dy.device))
+            dw = dw.to(ctx.types[1])
+        return dx, dw
+
+
+class Fp8Linear(torch.nn.Module):
+    """Linear layer without a bias whose products run on e4m3 operands
+    (``Fp8LinearFunction``); the parameter is an fp32 master copy."""
+
+    def __init__(self, weight):
+        super().__init__()
+        self.weight = torch.nn.Parameter(weight.detach().float())
+
+    def forward(self, x):
+        return Fp8LinearFunction.apply(x, self.weight)
 
 
 class SparseGatedFFNFunction(torch.autograd.Function):
@@ -78,11 +158,20 @@ class SparseFFNStack(torch.nn.Module):
     ``bias_feature``: when set, feature D - 1 of x is a constant bias input
     (the gate's threshold feature, as in the synthetic workloads) and the
     residual update leaves it unchanged, so every layer sees the same
-    activation-density control."""
+    activation-density control.
+
+    ``norms``: norm weights [D], one per layer, make the blocks pre-norm: each
+    layer's input is the bf16 RMS norm of the stream, computed together with
+    the addition of the layer before it (``AddRMSNormFunction``)."""
 
     def __init__(self, weights, l1_coeff=2e-5, cap=32, max_dense=1024, tensor_cores=True,
-                 bias_feature=True):
+                 bias_feature=True, norms=None, eps=1e-6):
         super().__init__()
+        if norms is not None and len(norms) != len(weights):
+            raise ValueError("one norm weight per layer")
+        self.norms = None if norms is None else torch.nn.ParameterList(
+            torch.nn.Parameter(n.detach().float()) for n in norms)
+        self.eps = eps
         self.Wg = torch.nn.ParameterList(torch.nn.Parameter(w[0].float()) for w in weights)
         self.Wu = torch.nn.ParameterList(torch.nn.Parameter(w[1].float()) for w in weights)
         self.Wd = torch.nn.ParameterList(torch.nn.Parameter(w[2].float()) for w in weights)
@@ -97,13 +186,21 @@ class SparseFFNStack(torch.nn.Module):
         """x [T][D] (any float dtype) -> the fp32 stream after the last layer."""
         self.last_status = []
         s = x.float()
-        for Wg, Wu, Wd in zip(self.Wg, self.Wu, self.Wd):
-            y = SparseGatedFFNFunction.apply(s.to(torch.bfloat16), Wg, Wu, Wd, self.l1, self.cap,
-                                             self.max_dense, self.tc, self.last_status)
+        y = None  # the last layer's output, not yet added where the next norm adds it
+        for i, (Wg, Wu, Wd) in enumerate(zip(self.Wg, self.Wu, self.Wd)):
+            if self.norms is None:
+                a = s.to(torch.bfloat16)
+            elif y is None:
+                a = AddRMSNormFunction.apply(s, self.norms[i], None, self.eps)
+            else:
+                a, s = AddRMSNormFunction.apply(y, self.norms[i], s, self.eps)
+            y = SparseGatedFFNFunction.apply(a, Wg, Wu, Wd, self.l1, self.cap, self.max_dense,
+                                             self.tc, self.last_status)
             if self.bias_feature:
                 y = torch.cat([y[:, :-1], torch.zeros_like(y[:, -1:])], dim=1)
-            s = s + y
-        return s
+            if self.norms is None:
+                s, y = s + y, None
+        return s if y is None else s + y
 
     def status_flags(self) -> int:
         """OR of the device status words of the last forward (synchronises)."""
