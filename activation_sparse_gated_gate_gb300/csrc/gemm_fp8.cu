@@ -105,7 +105,7 @@ struct Fp8Cfg {
 // A pipeline wait under the call's bound (short bounds are checked on every
 // retry, the default one every 64).
 __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  return limit_ns >= kDefaultWaitNs ? ptx::mbar_wait(bar, parity, limit_ns)
+  return limit_ns >= kDefaultWaitNs ? ptx::mbar_wait_short(bar, parity, limit_ns)
                                     : ptx::mbar_wait_strict(bar, parity, limit_ns);
 }
 

@@ -70,20 +70,27 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Wait for the phase with the given parity to complete.  Gives up after
-// about `limit_ns` nanoseconds and returns false.  The clock is read only once
-// the wait has already been long (a read of the global timer costs about as
-// much as a short wait).
+// about `limit_ns` nanoseconds and returns false.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
                                           uint64_t limit_ns = 1000000000ull) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   uint32_t spins = 0;
   while (!mbar_try_wait(bar, parity)) {
     if ((++spins & 63u) == 0 && globaltimer_ns() - t0 > limit_ns) return false;
   }
   return true;
+}
+
+// The same for waits that are mostly short: the clock is read only once the
+// wait has already been long (a read of the global timer costs about as much as
+// such a wait).
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity,
+                                                uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, limit_ns);
 }
 
 // Whether the phase is complete, without suspending.
