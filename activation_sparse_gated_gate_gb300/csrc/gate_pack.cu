@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
           for (int i = 0; i < 32; ++i) z[ch][i] = __uint_as_float(r[ch][i]);
-        pack_row_slice(p.out, z, t, valid, m_blk, kt, lane, row, my_stage);
+        pack_row_slice<false>(p.out, z, t, valid, m_blk, kt, lane, row, my_stage);
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(&tempty[acc]);

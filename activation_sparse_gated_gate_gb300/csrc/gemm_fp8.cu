@@ -105,7 +105,7 @@ struct Fp8Cfg {
 // A pipeline wait under the call's bound (short bounds are checked on every
 // retry, the default one every 64).
 __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  return limit_ns >= kDefaultWaitNs ? ptx::mbar_wait_short(bar, parity, limit_ns)
+  return limit_ns >= kDefaultWaitNs ? ptx::mbar_wait(bar, parity, limit_ns)
                                     : ptx::mbar_wait_strict(bar, parity, limit_ns);
 }
 
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
         unpack2(acc[i], z[i / 16][2 * (i % 16)], z[i / 16][2 * (i % 16) + 1]);
       if (PACK) {
         if (col0 < p.N)
-          pack_row_slice(p.out, z, t, valid, m_blk, col0 / TWELL_TILE, lane, row, my_stage);
+          pack_row_slice<true>(p.out, z, t, valid, m_blk, col0 / TWELL_TILE, lane, row, my_stage);
       } else {
         // pieces of 32 rows by 64 bytes, two in flight
         const int sw = (row >> 1) & 3;

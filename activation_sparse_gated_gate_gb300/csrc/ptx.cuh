@@ -82,17 +82,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   return true;
 }
 
-// The same for waits that are mostly short: the clock is read only once the
-// wait has already been long (a read of the global timer costs about as much as
-// such a wait).
-__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity,
-                                                uint64_t limit_ns) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, limit_ns);
-}
-
 // Whether the phase is complete, without suspending.
 __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
