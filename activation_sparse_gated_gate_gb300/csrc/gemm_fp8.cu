@@ -16,9 +16,10 @@
 //   1         TMEM allocator and MMA issuer
 //   2, 3      copy the scales, a round of eight K blocks at a time, into shared
 //             memory (lanes along the K blocks: a row's scales are neighbours)
-//   4 ..      BN / 128 sets of four epilogue warps; a thread owns a row and 128
-//             columns: 128 fp32 sums in registers (packed fp32 pairs), read from
-//             TMEM in pieces of 16 columns, two in flight
+//   4 ..      sets of four epilogue warps; a thread owns a row and 128 columns (64
+//             without PAIR, where two sets share the 128 and halve the time a K
+//             block's sums take): fp32 sums in registers (packed pairs), read
+//             from TMEM in pieces of 16 columns, two in flight
 // With PAIR two CTAs of a cluster share a tile of 256 x 256 (cta_group::2): each
 // loads its 128 rows of a and half of b's 256 rows, the even CTA issues MMAs of
 // M = 256, and each CTA's TMEM and epilogue hold its own 128 rows by 256
@@ -56,8 +57,8 @@ namespace {
 constexpr int BM = 128;
 constexpr int BK = 128;             // e4m3 of a 128-byte row: one scale block
 constexpr int kPiece = 16;            // columns of a TMEM read
-constexpr int kPieces = 128 / kPiece;
 constexpr int kTmemCols = 512;
+constexpr int kSplitBlocks = 32;      // K blocks from which a ragged last round is split
 // The pair kernel's 384 threads start with 168 registers each; its epilogue
 // threads take 224 and the others keep 56 (4 x 56 + 8 x 224 = 12 x 168).
 constexpr int kRegsStart = 168, kRegsEpi = 224, kRegsOther = 56;
@@ -65,7 +66,9 @@ constexpr uint64_t kDefaultWaitNs = 1000000000ull;
 
 struct GemmFp8Params {
   int32_t M, N;
-  int32_t num_n, num_kb, num_tiles;
+  int32_t num_n, num_kb;
+  int32_t first_tile, num_tiles;   // this launch's tiles, of num_n to a row of them
+  int32_t quarters;  // without PAIR: the tiles are quarters of 256 x 256 tiles
   const float* a_scale;   // [M][num_kb]
   const float* b_scale;   // [N or ceil(N / 128)][num_kb]
   void* c;
@@ -76,7 +79,7 @@ struct GemmFp8Params {
   uint64_t wait_ns;
 };
 
-template <bool PAIR, bool BROWS>
+template <bool PAIR, bool BROWS, bool PACK>
 struct Fp8Cfg {
   static constexpr int CTAS = PAIR ? 2 : 1;
   static constexpr int BN = PAIR ? 256 : 128;   // columns of a tile
@@ -85,7 +88,9 @@ struct Fp8Cfg {
   static constexpr int B_ROWS = BN / CTAS;      // rows of b a CTA loads
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int SETS = BN / 128;
+  // columns of an epilogue thread (packing wants a row's 128)
+  static constexpr int COLS = PAIR || PACK ? 128 : 64;
+  static constexpr int SETS = BN / COLS;
   static constexpr int EPI = 128 * SETS;        // epilogue threads
   static constexpr int BUFS = kTmemCols / BN;
   static constexpr int STAGING = EPI * 128;     // 128 bytes per epilogue thread
@@ -128,14 +133,29 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   return d;
 }
 
+// Where a launch's tile starts, in units of 128 rows and of 128 columns.
+struct TileAt {
+  int m, n;
+};
+
+template <bool PAIR>
+__device__ __forceinline__ TileAt tile_at(const GemmFp8Params& p, int tile) {
+  if (!PAIR && p.quarters) {
+    const int big = p.first_tile + (tile >> 2);
+    return {big / p.num_n * 2 + ((tile >> 1) & 1), big % p.num_n * 2 + (tile & 1)};
+  }
+  constexpr int S = PAIR ? 2 : 1;
+  return {tile / p.num_n * S, tile % p.num_n * S};
+}
+
 // BROWS: b has a scale per row (of 1 x 128 blocks), else per 128 x 128 block.
 // PACK: the sums are gate pre-activations and go to a TwELL.
 template <bool PAIR, bool BROWS, bool PACK>
-__global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
+__global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_c, const GemmFp8Params p) {
-  using Cfg = Fp8Cfg<PAIR, BROWS>;
+  using Cfg = Fp8Cfg<PAIR, BROWS, PACK>;
   constexpr int BN = Cfg::BN;
   constexpr int STAGES = Cfg::STAGES;
   constexpr int BUFS = Cfg::BUFS;
@@ -204,8 +224,9 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
         int stage = 0;
         uint32_t phase = 0;
         for (int tile = unit; tile < p.num_tiles; tile += units) {
-          const int m0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM;
-          const int n0 = tile % p.num_n * BN + static_cast<int>(rank) * Cfg::B_ROWS;
+          const TileAt at = tile_at<PAIR>(p, tile);
+          const int m0 = (at.m + static_cast<int>(rank)) * BM;
+          const int n0 = at.n * 128 + static_cast<int>(rank) * Cfg::B_ROWS;
           for (int kb = 0; kb < p.num_kb; ++kb) {
             if (!pipe_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
               flag(p.status, TWELL_FLAG_TIMEOUT);
@@ -311,8 +332,9 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
       int par = 0;
       uint32_t phase = 0;
       for (int tile = unit; tile < p.num_tiles; tile += units) {
-        const int a0 = (tile / p.num_n * Cfg::CTAS + static_cast<int>(rank)) * BM + r;
-        const int b0 = tile % p.num_n * Cfg::B_PER + r;
+        const TileAt at = tile_at<PAIR>(p, tile);
+        const int a0 = (at.m + static_cast<int>(rank)) * BM + r;
+        const int b0 = at.n * (BROWS ? 128 : 1) + r;
         for (int kb = k; kb < p.num_kb + k; kb += R) {
           if (!pipe_wait(&sempty[par], phase ^ 1u, p.wait_ns)) {
             flag(p.status, TWELL_FLAG_TIMEOUT);
@@ -345,7 +367,8 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
     if (PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                // TMEM lane quarter this warp may read
-    const int set = (warp - 4) >> 2;       // its 128 columns of the tile
+    constexpr int COLS = Cfg::COLS, kPieces = COLS / kPiece;
+    const int set = (warp - 4) >> 2;       // its COLS columns of the tile
     const int row = q * 32 + lane;         // its thread's row
     uint8_t* my_stage = staging + (threadIdx.x - 128) * 128;
     constexpr int kRound = Cfg::ROUND;
@@ -353,11 +376,11 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
     uint32_t bphase = 0, sphase = 0;
     const uint32_t tempty0 = ptx::mapa(ptx::smem_u32(tempty), 0);
     const uint32_t taddr0 =
-        tmem_base + static_cast<uint32_t>(set * 128) + (static_cast<uint32_t>(q * 32) << 16);
+        tmem_base + static_cast<uint32_t>(set * COLS) + (static_cast<uint32_t>(q * 32) << 16);
     for (int tile = unit; tile < p.num_tiles; tile += units) {
-      f32x2 acc[64];
+      f32x2 acc[COLS / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
       bool ready = false;  // this block's barrier has been seen complete
       for (int kb = 0; kb < p.num_kb; ++kb) {
         const int k8 = kb % kRound;
@@ -377,7 +400,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
         uint32_t r[2][kPiece];
         ptx::tmem_ld_32x32b_x16(taddr, r[0]);
         float s = a_sc[(par * kRound + k8) * Cfg::A_PITCH + row];
-        const float* bs = b_sc + (par * kRound + k8) * Cfg::B_PITCH + (BROWS ? set * 128 : set);
+        const float* bs = b_sc + (par * kRound + k8) * Cfg::B_PITCH + (BROWS ? set * COLS : set * COLS / 128);
         if (!BROWS) s *= bs[0];
         const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
         const uint32_t done_bar = tempty0 + buf * 8;
@@ -417,15 +440,16 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
           if (par == 0) sphase ^= 1u;
         }
       }
-      const int m_blk = tile / p.num_n * Cfg::CTAS + static_cast<int>(rank);
+      const TileAt at = tile_at<PAIR>(p, tile);
+      const int m_blk = at.m + static_cast<int>(rank);
       const int t = m_blk * BM + row;
-      const int col0 = tile % p.num_n * BN + set * 128;
+      const int col0 = at.n * 128 + set * COLS;
       const bool valid = t < p.M;
-      float z[4][32];
+      float z[COLS / 32][32];
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
+      for (int i = 0; i < COLS / 2; ++i)
         unpack2(acc[i], z[i / 16][2 * (i % 16)], z[i / 16][2 * (i % 16) + 1]);
-      if (PACK) {
+      if constexpr (PACK) {
         if (col0 < p.N)
           pack_row_slice<true>(p.out, z, t, valid, m_blk, col0 / TWELL_TILE, lane, row, my_stage);
       } else {
@@ -468,7 +492,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
         };
         if (p.c_bf16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < COLS / 32; ++i) {
             uint32_t v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = bf16x2(z[i][2 * j], z[i][2 * j + 1]);
@@ -476,7 +500,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS>::THREADS, 1)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < COLS / 16; ++i) {
             uint32_t v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(z[i / 2][i % 2 * 16 + j]);
@@ -518,7 +542,7 @@ done:
 template <bool PAIR, bool BROWS, bool PACK>
 twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensorMap& mb,
                     const CUtensorMap& mc, const GemmFp8Params& p, cudaStream_t s) {
-  using Cfg = Fp8Cfg<PAIR, BROWS>;
+  using Cfg = Fp8Cfg<PAIR, BROWS, PACK>;
   static_assert(Cfg::SMEM <= 232448, "shared memory budget");
   auto kern = gemm_fp8_kernel<PAIR, BROWS, PACK>;
   static std::atomic<uint64_t> set{0};
@@ -565,7 +589,7 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
   const int64_t num_m = pair ? wide_m : (static_cast<int64_t>(p.M) + 127) / 128;
   p.num_n = pair ? (p.N + 255) / 256 : (p.N + 127) / 128;
   const int64_t tiles = num_m * p.num_n;
-  if (tiles > 0x7fffffff - dev.sm_count) return TWELL_ERR_UNSUPPORTED;
+  if (tiles > 0x7fffffff / 4 - dev.sm_count) return TWELL_ERR_UNSUPPORTED;
   p.num_tiles = static_cast<int32_t>(tiles);
   CUtensorMap ma, mb, mc = {};
   twell_status st;
@@ -575,11 +599,25 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
   if (!PACK && p.c_vec &&
       (st = make_tmap_2d(&mc, ce, p.c, p.N, p.M, 64 / ce, 32, p.ldc * ce, 64)) != TWELL_OK)
     return st;
-  if (PACK || b_block == 128)
-    return pair ? launch<true, false, PACK>(dev, ma, mb, mc, p, s)
-                : launch<false, false, PACK>(dev, ma, mb, mc, p, s);
-  return pair ? launch<true, true, false>(dev, ma, mb, mc, p, s)
-              : launch<false, true, false>(dev, ma, mb, mc, p, s);
+  const bool brows = !PACK && b_block == 1;
+  if (pair) {
+    // A last round of tiles that leaves most pairs idle runs as quarters, one per
+    // CTA, in a launch of its own, where K is long enough to pay for it.
+    const int32_t pairs = dev.sm_count / 2;
+    const int32_t rest = p.num_tiles % pairs;
+    const bool split = p.num_kb >= kSplitBlocks && p.num_tiles > pairs && rest > 0 &&
+                       4 * rest <= dev.sm_count;
+    GemmFp8Params q = p;
+    q.num_tiles = split ? p.num_tiles - rest : p.num_tiles;
+    st = brows ? launch<true, true, false>(dev, ma, mb, mc, q, s)
+               : launch<true, false, PACK>(dev, ma, mb, mc, q, s);
+    if (st != TWELL_OK || !split) return st;
+    p.first_tile = p.num_tiles - rest;
+    p.num_tiles = 4 * rest;
+    p.quarters = 1;
+  }
+  return brows ? launch<false, true, false>(dev, ma, mb, mc, p, s)
+               : launch<false, false, PACK>(dev, ma, mb, mc, p, s);
 }
 
 }  // namespace
