@@ -377,68 +377,75 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     const uint32_t tempty0 = ptx::mapa(ptx::smem_u32(tempty), 0);
     const uint32_t taddr0 =
         tmem_base + static_cast<uint32_t>(set * COLS) + (static_cast<uint32_t>(q * 32) << 16);
+    bool ready = false;  // the next block's barrier has been seen complete
     for (int tile = unit; tile < p.num_tiles; tile += units) {
       f32x2 acc[COLS / 2];
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
-      bool ready = false;  // this block's barrier has been seen complete
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        const int k8 = kb % kRound;
-        // the decisions must be warp-uniform: tcgen05.ld is warp-collective
-        bool late = k8 == 0 && !pipe_wait(&sfull[par], sphase, p.wait_ns);
-        if (!__all_sync(0xffffffffu, ready) && !late)
-          late = !pipe_wait(&tfull[buf], bphase, p.wait_ns);
-        if (__any_sync(0xffffffffu, late)) {
+      for (int kb0 = 0; kb0 < p.num_kb; kb0 += kRound) {
+        // the decisions to leave must be warp-uniform: tcgen05.ld is warp-collective
+        if (__any_sync(0xffffffffu, !pipe_wait(&sfull[par], sphase, p.wait_ns))) {
           if (lane == 0) {
             flag(p.status, TWELL_FLAG_TIMEOUT);
             *aborted = 1u;
           }
           goto done;
         }
-        ptx::tc_fence_after();
-        const uint32_t taddr = taddr0 + static_cast<uint32_t>(buf * BN);
-        uint32_t r[2][kPiece];
-        ptx::tmem_ld_32x32b_x16(taddr, r[0]);
-        float s = a_sc[(par * kRound + k8) * Cfg::A_PITCH + row];
-        const float* bs = b_sc + (par * kRound + k8) * Cfg::B_PITCH + (BROWS ? set * COLS : set * COLS / 128);
-        if (!BROWS) s *= bs[0];
-        const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
-        const uint32_t done_bar = tempty0 + buf * 8;
-        if (++buf == BUFS) {
-          buf = 0;
-          bphase ^= 1u;
-        }
-#pragma unroll
-        for (int ch = 0; ch < kPieces; ++ch) {
-          ptx::tmem_wait_ld();
-          if (ch < kPieces - 1) {
-            ptx::tmem_ld_32x32b_x16(taddr + (ch + 1) * kPiece, r[(ch + 1) & 1]);
-            if (ch == kPieces - 2)
-              ready = kb + 1 < p.num_kb && ptx::mbar_test_wait(&tfull[buf], bphase);
-          } else {
-            ptx::tc_fence_before();
-            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar);
-          }
-#pragma unroll
-          for (int i = 0; i < kPiece / 4; ++i) {
-            f32x2 f0 = s2, f1 = s2;
-            if (BROWS) {
-              const ulonglong2 b4 =
-                  *reinterpret_cast<const ulonglong2*>(bs + ch * kPiece + 4 * i);
-              f0 = mul2(s2, b4.x);
-              f1 = mul2(s2, b4.y);
+        const float* as = a_sc + par * kRound * Cfg::A_PITCH + row;
+        const float* bs =
+            b_sc + par * kRound * Cfg::B_PITCH + (BROWS ? set * COLS : set * COLS / 128);
+        const int left = p.num_kb - kb0;
+        const float* as_end = as + (left < kRound ? left : kRound) * Cfg::A_PITCH;
+        for (; as != as_end; as += Cfg::A_PITCH, bs += Cfg::B_PITCH) {
+          if (!__all_sync(0xffffffffu, ready) &&
+              __any_sync(0xffffffffu, !pipe_wait(&tfull[buf], bphase, p.wait_ns))) {
+            if (lane == 0) {
+              flag(p.status, TWELL_FLAG_TIMEOUT);
+              *aborted = 1u;
             }
-            const uint32_t* rr = r[ch & 1] + 4 * i;
-            fma2(acc[ch * (kPiece / 2) + 2 * i], pack2(rr[0], rr[1]), f0);
-            fma2(acc[ch * (kPiece / 2) + 2 * i + 1], pack2(rr[2], rr[3]), f1);
+            goto done;
+          }
+          ptx::tc_fence_after();
+          const uint32_t taddr = taddr0 + static_cast<uint32_t>(buf * BN);
+          uint32_t r[2][kPiece];
+          ptx::tmem_ld_32x32b_x16(taddr, r[0]);
+          const float s = BROWS ? as[0] : as[0] * bs[0];
+          const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+          const uint32_t done_bar = tempty0 + buf * 8;
+          if (++buf == BUFS) {
+            buf = 0;
+            bphase ^= 1u;
+          }
+#pragma unroll
+          for (int ch = 0; ch < kPieces; ++ch) {
+            ptx::tmem_wait_ld();
+            if (ch < kPieces - 1) {
+              ptx::tmem_ld_32x32b_x16(taddr + (ch + 1) * kPiece, r[(ch + 1) & 1]);
+              if (ch == kPieces - 2) ready = ptx::mbar_test_wait(&tfull[buf], bphase);
+            } else {
+              ptx::tc_fence_before();
+              if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar);
+            }
+#pragma unroll
+            for (int i = 0; i < kPiece / 4; ++i) {
+              f32x2 f0 = s2, f1 = s2;
+              if (BROWS) {
+                const ulonglong2 b4 =
+                    *reinterpret_cast<const ulonglong2*>(bs + ch * kPiece + 4 * i);
+                f0 = mul2(s2, b4.x);
+                f1 = mul2(s2, b4.y);
+              }
+              const uint32_t* rr = r[ch & 1] + 4 * i;
+              fma2(acc[ch * (kPiece / 2) + 2 * i], pack2(rr[0], rr[1]), f0);
+              fma2(acc[ch * (kPiece / 2) + 2 * i + 1], pack2(rr[2], rr[3]), f1);
+            }
           }
         }
-        if (k8 == kRound - 1 || kb + 1 == p.num_kb) {  // this round's scales are read
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sempty[par]);
-          par ^= 1;
-          if (par == 0) sphase ^= 1u;
-        }
+        // this round's scales are read
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sempty[par]);
+        par ^= 1;
+        if (par == 0) sphase ^= 1u;
       }
       const TileAt at = tile_at<PAIR>(p, tile);
       const int m_blk = at.m + static_cast<int>(rank);
