@@ -60,7 +60,9 @@ constexpr int kPiece = 16;            // columns of a TMEM read
 constexpr int kTmemCols = 512;
 constexpr int kSplitBlocks = 32;      // K blocks from which a ragged last round is split
 // The pair kernel's 384 threads start with 168 registers each; its epilogue
-// threads take 224 and the others keep 56 (4 x 56 + 8 x 224 = 12 x 168).
+// threads take 224 and the others keep 56 (4 x 56 + 8 x 224 = 12 x 168).  (With
+// 208 and 88 nothing spills either, but the loop is scheduled less well: 403
+// against 385 us at 8192^3.)
 constexpr int kRegsStart = 168, kRegsEpi = 224, kRegsOther = 56;
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
 
@@ -104,7 +106,7 @@ struct Fp8Cfg {
   static constexpr int BAR_BYTES = 256;
   static constexpr int SMEM =
       STAGES * STAGE_BYTES + STAGING + SCALES + BAR_BYTES + 1024;
-  static constexpr int THREADS = 64 + EPI + 64;
+  static constexpr int THREADS = 128 + EPI;
 };
 
 // A pipeline wait under the call's bound (short bounds are checked on every
@@ -424,7 +426,10 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
               if (ch == kPieces - 2) ready = ptx::mbar_test_wait(&tfull[buf], bphase);
             } else {
               ptx::tc_fence_before();
-              if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar);
+              // (predicated; with b's row scales the predicate costs the loop spills,
+              // and a branch is the faster: 377 against 430 us at dW's 9216 x 2304 x 16384)
+              if (!BROWS) ptx::mbar_arrive_cluster_relaxed(done_bar, lane == 0);
+              else if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar, true);
             }
 #pragma unroll
             for (int i = 0; i < kPiece / 4; ++i) {

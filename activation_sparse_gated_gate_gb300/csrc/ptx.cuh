@@ -502,12 +502,19 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
-// Arrive on a barrier of the cluster (a mapa address) without ordering this
-// thread's other memory accesses (a release would wait for them): for barriers
-// that hand over TMEM, whose loads tcgen05.wait::ld has already completed.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+// Arrive, where `pred` holds, on a barrier of the cluster (a mapa address) without
+// ordering this thread's other memory accesses (a release would wait for them):
+// for barriers that hand over TMEM, whose loads tcgen05.wait::ld has already
+// completed.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr, bool pred) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %1, 0;\n"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n"
+      "}\n" ::"r"(cluster_addr),
+      "r"(static_cast<uint32_t>(pred))
+      : "memory");
 }
 
 // Address of the same shared-memory variable in CTA `rank` of the cluster.
