@@ -31,7 +31,7 @@ struct QuantParams {
   float* scale_t;
 };
 
-// Eight neighbouring values of a row as they were loaded.
+// Eight values of a row as they were loaded: neighbours, or every 16th (vec.cuh).
 template <typename T>
 struct Piece;
 
@@ -42,7 +42,7 @@ struct Piece<float> {
   static constexpr int MAXES = 8;
   template <bool VEC>
   __device__ __forceinline__ void load(const float* p, int n) {
-    load8<VEC>(p, n, v);
+    load8<VEC, 16>(p, n, v);
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -76,8 +76,8 @@ struct Piece<uint16_t> {
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        v[k] = (2 * k < n ? p[2 * k] : 0u) |
-               (2 * k + 1 < n ? static_cast<uint32_t>(p[2 * k + 1]) << 16 : 0u);
+        v[k] = (32 * k < n ? p[32 * k] : 0u) |
+               (32 * k + 16 < n ? static_cast<uint32_t>(p[32 * k + 16]) << 16 : 0u);
     }
   }
   __device__ __forceinline__ void clear() {
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, con
   const int bx = blockIdx.x % static_cast<unsigned>(nbc);  // the tile's columns and rows
   const int64_t by = blockIdx.x / static_cast<unsigned>(nbc);
   const int64_t r0 = (by * 16 + g) * ROWS;
-  const int c0 = bx * 128 + 8 * c;
+  const int c0 = bx * 128 + (VEC ? 8 * c : c);
   const int nc = p.C - c0;
   Piece<T> v[ROWS];
 #pragma unroll
@@ -188,14 +188,15 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, con
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = v[i].get(j);
-        store8_e4m3<VEC>(p.q + (r0 + i) * p.ldq + c0, nc, f, inv);
+        store8_e4m3<VEC, 16>(p.q + (r0 + i) * p.ldq + c0, nc, f, inv, inv);
       }
     }
   }
   if constexpr (TRANS) {
     // the transposed tile: row = column of the source, 16 units of 8 bytes (one
-    // per row group), unit u of row r at u ^ (r / 8): the 16 lanes of a half-warp
-    // write one unit of 16 rows without bank conflicts
+    // per row group), unit u of row r at u ^ (r / 8): with VEC the 16 lanes of a
+    // half-warp write one unit of 16 rows without bank conflicts
+    const auto column = [&](int j) { return VEC ? 8 * c + j : 16 * j + c; };  // of value j
     __shared__ __align__(16) uint2 tile[128][16];
     float inv[8];
     if constexpr (SQUARE) {
@@ -218,13 +219,15 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, con
       __syncthreads();
       if (threadIdx.x < 128) {
         constexpr int PER = 8 / MAXES;  // columns of a Max
+        // the lane and the value that hold this thread's column
+        const int cc = VEC ? threadIdx.x / 8 : threadIdx.x % 16;
+        const int jj = VEC ? threadIdx.x % 8 : threadIdx.x / 16;
         float a = kFp8AmaxMin;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const Max one[1] = {colmax[i][threadIdx.x / PER]};
-          Max mm[MAXES];
-          mm[0] = one[0];
-          a = fmaxf(a, Piece<T>::max_of(mm, threadIdx.x % PER));
+          Max m1[MAXES];
+          m1[0] = colmax[i][MAXES * cc + jj / PER];
+          a = fmaxf(a, Piece<T>::max_of(m1, jj % PER));
         }
         const int64_t col = static_cast<int64_t>(bx) * 128 + threadIdx.x;
         if (col < p.C) p.scale_t[col * nbr + by] = a / kFp8Max;
@@ -232,11 +235,11 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, con
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) inv[j] = colinv[8 * c + j];
+      for (int j = 0; j < 8; ++j) inv[j] = colinv[column(j)];
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      tile[8 * c + j][g ^ c] =
+      tile[column(j)][g ^ (column(j) >> 3)] =
           make_uint2(quant4(v[0].get(j), v[1].get(j), v[2].get(j), v[3].get(j), inv[j]),
                      quant4(v[4].get(j), v[5].get(j), v[6].get(j), v[7].get(j), inv[j]));
     __syncthreads();

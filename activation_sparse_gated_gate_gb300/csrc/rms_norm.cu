@@ -13,7 +13,10 @@
 // written once, a row held in registers between its two uses.  A row belongs
 // to L threads (a multiple of 32) in pieces of eight elements, piece i of
 // thread l being piece l + i L of the row, so the 16 pieces of a scale's block
-// lie in 16 neighbouring lanes and its maximum takes four shuffles.
+// lie in 16 neighbouring lanes and its maximum takes four shuffles.  Rows off
+// 16-byte boundaries are read and written element by element, a warp's 256
+// elements 32 side by side at a time (two scale blocks, four elements of each in
+// a lane).
 #include "common.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -45,6 +48,13 @@ __device__ __forceinline__ void load_w(const void* w, int32_t w_bf16, int e, int
   else load8<VEC>(static_cast<const float*>(w) + e, n, f);
 }
 
+// First element of piece i of a thread (the others: vec.cuh).
+template <bool VEC>
+__device__ __forceinline__ int piece_at(int i) {
+  const int l = threadIdx.x + i * blockDim.x;
+  return VEC ? l * 8 : (l & ~31) * 8 + (l & 31);
+}
+
 // blockDim = (L, rows); rows > 1 only where L is one warp.
 template <typename XT, typename RT, bool VEC, int MAXC>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
@@ -58,7 +68,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < MAXC; ++i) {
-    const int e = (threadIdx.x + i * L) * 8;
+    const int e = piece_at<VEC>(i);
     const int n = p.D - e;
     if (n > 0) {
       load8<VEC>(xr + e, n, v[i]);
@@ -77,7 +87,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
   for (int i = 0; i < MAXC; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-    const int e = (threadIdx.x + i * L) * 8;
+    const int e = piece_at<VEC>(i);
     if (rr && e < p.D)
       store8<VEC>(static_cast<RT*>(p.total) + t * p.ldt + e, p.D - e, v[i]);
   }
@@ -93,7 +103,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
   const int nb = (p.D + kFp8Block - 1) / kFp8Block;
 #pragma unroll
   for (int i = 0; i < MAXC; ++i) {
-    const int e = (threadIdx.x + i * L) * 8;
+    const int e = piece_at<VEC>(i);
     const int n = p.D - e;
     if (n > 0) {
       float w[8];
@@ -102,12 +112,26 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
       for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
       if (p.y) store8<VEC>(p.y + t * p.ldy + e, n, v[i]);
     }
-    if (p.q) {
+    if (p.q && VEC) {
       const float amax = fmaxf(half_warp_max(amax8(v[i])), kFp8AmaxMin);
       if (n > 0) {
-        store8_e4m3<VEC>(p.q + t * p.ldq + e, n, v[i], kFp8Max / amax);
+        const float inv = kFp8Max / amax;
+        store8_e4m3<VEC>(p.q + t * p.ldq + e, n, v[i], inv, inv);
         if ((threadIdx.x & 15) == 0) p.scale[t * nb + e / kFp8Block] = amax / kFp8Max;
       }
+    }
+    if (p.q && !VEC) {
+      float a[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        a[k] = kFp8AmaxMin;
+#pragma unroll
+        for (int j = 4 * k; j < 4 * k + 4; ++j) a[k] = fmaxf(a[k], fabsf(v[i][j]));
+        a[k] = warp_max(a[k]);
+      }
+      store8_e4m3<VEC>(p.q + t * p.ldq + e, n, v[i], kFp8Max / a[0], kFp8Max / a[1]);
+      const int lane = threadIdx.x & 31, b = e / kFp8Block + lane;  // (lanes 0 and 1)
+      if (lane < 2 && b < nb) p.scale[t * nb + b] = (lane ? a[1] : a[0]) / kFp8Max;
     }
   }
 }
@@ -126,21 +150,22 @@ struct NormBwdParams {
 
 // The groups' shares of dw, added in order in shared memory (`join` [D], used
 // when there are several groups), into this block's row of the partial sums.
-template <int MAXC>
+template <bool VEC, int MAXC>
 __device__ __forceinline__ void join_dw(const NormBwdParams& p, float (&acc)[MAXC][8],
                                         float* join) {
-  const int L = blockDim.x, G = blockDim.y, grp = threadIdx.y;
+  constexpr int step = VEC ? 1 : 32;
+  const int G = blockDim.y, grp = threadIdx.y;
   if (G > 1) {
     for (int k = 0; k < G; ++k) {
       if (grp == k) {
 #pragma unroll
         for (int i = 0; i < MAXC; ++i) {
-          const int e = (threadIdx.x + i * L) * 8;
+          const int e = piece_at<VEC>(i);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (e + j < p.D) {
-              if (k > 0) acc[i][j] += join[e + j];
-              join[e + j] = acc[i][j];
+            if (e + j * step < p.D) {
+              if (k > 0) acc[i][j] += join[e + j * step];
+              join[e + j * step] = acc[i][j];
             }
         }
       }
@@ -151,10 +176,10 @@ __device__ __forceinline__ void join_dw(const NormBwdParams& p, float (&acc)[MAX
     float* o = p.part + static_cast<size_t>(blockIdx.x) * p.D;
 #pragma unroll
     for (int i = 0; i < MAXC; ++i) {
-      const int e = (threadIdx.x + i * L) * 8;
+      const int e = piece_at<VEC>(i);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (e + j < p.D) o[e + j] = acc[i][j];
+        if (e + j * step < p.D) o[e + j * step] = acc[i][j];
     }
   }
 }
@@ -177,8 +202,8 @@ __global__ void __launch_bounds__(1024) rms_norm_bwd_kernel(const NormBwdParams 
   for (int i = 0; i < MAXC; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  if (kHold && static_cast<int>(threadIdx.x) * 8 < p.D)
-    load_w<VEC>(p.w, p.w_bf16, threadIdx.x * 8, p.D - threadIdx.x * 8, w);
+  if (kHold && piece_at<VEC>(0) < p.D)
+    load_w<VEC>(p.w, p.w_bf16, piece_at<VEC>(0), p.D - piece_at<VEC>(0), w);
   const float inv_d = 1.0f / static_cast<float>(p.D);
   int par = 0;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * G + grp; t < p.T;
@@ -190,7 +215,7 @@ __global__ void __launch_bounds__(1024) rms_norm_bwd_kernel(const NormBwdParams 
     float n[MAXC][8], g[MAXC][8], d[8];
 #pragma unroll
     for (int i = 0; i < MAXC; ++i) {
-      const int e = (threadIdx.x + i * L) * 8;
+      const int e = piece_at<VEC>(i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) n[i][j] = g[i][j] = 0.0f;
       if (e < p.D) {
@@ -202,7 +227,7 @@ __global__ void __launch_bounds__(1024) rms_norm_bwd_kernel(const NormBwdParams 
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < MAXC; ++i) {
-      const int e = (threadIdx.x + i * L) * 8;
+      const int e = piece_at<VEC>(i);
       if (e < p.D) {
         if (!kHold) load_w<VEC>(p.w, p.w_bf16, e, p.D - e, w);
 #pragma unroll
@@ -226,7 +251,7 @@ __global__ void __launch_bounds__(1024) rms_norm_bwd_kernel(const NormBwdParams 
     ST* dxr = static_cast<ST*>(p.dx) + t * p.lddx;
 #pragma unroll
     for (int i = 0; i < MAXC; ++i) {
-      const int e = (threadIdx.x + i * L) * 8;
+      const int e = piece_at<VEC>(i);
       if (e < p.D) {
         if (!kHold && tr) load8<VEC>(tr + e, p.D - e, d);
 #pragma unroll
@@ -236,7 +261,7 @@ __global__ void __launch_bounds__(1024) rms_norm_bwd_kernel(const NormBwdParams 
       }
     }
   }
-  join_dw<MAXC>(p, acc, join);
+  join_dw<VEC, MAXC>(p, acc, join);
 }
 
 // The same for rows on 16-byte boundaries of at most eight elements a thread:

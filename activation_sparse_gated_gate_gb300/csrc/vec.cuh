@@ -1,6 +1,8 @@
 // Eight-element pieces of a row: loads widened to fp32, stores rounded once,
-// and e4m3 with the scale of a block of 128.  With VEC the piece is whole and
-// 16-byte aligned; without, its first n elements are touched one by one.
+// and e4m3 with the scale of a block of 128.  With VEC a thread's piece is eight
+// neighbours, whole and 16-byte aligned.  Without, rows may start anywhere: the
+// piece is every STEP-th element (STEP lanes side by side cover a run of 8 STEP),
+// so that each access of theirs is one run too, and those below n are touched.
 #pragma once
 
 #include <cstdint>
@@ -38,7 +40,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-template <bool VEC>
+template <bool VEC, int STEP = 32>
 __device__ __forceinline__ void load8(const float* p, int n, float (&f)[8]) {
   if (VEC) {
     const float4 a = *reinterpret_cast<const float4*>(p);
@@ -47,11 +49,11 @@ __device__ __forceinline__ void load8(const float* p, int n, float (&f)[8]) {
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = j < n ? p[j] : 0.0f;
+    for (int j = 0; j < 8; ++j) f[j] = j * STEP < n ? p[j * STEP] : 0.0f;
   }
 }
 
-template <bool VEC>
+template <bool VEC, int STEP = 32>
 __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&f)[8]) {
   if (VEC) {
     const uint4 a = *reinterpret_cast<const uint4*>(p);
@@ -63,7 +65,7 @@ __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&f)[8]) {
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = j < n ? widen(p[j]) : 0.0f;
+    for (int j = 0; j < 8; ++j) f[j] = j * STEP < n ? widen(p[j * STEP]) : 0.0f;
   }
 }
 
@@ -88,7 +90,7 @@ __device__ __forceinline__ void store4(uint16_t* p, const float* f) {
   *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]));
 }
 
-template <bool VEC>
+template <bool VEC, int STEP = 32>
 __device__ __forceinline__ void store8(float* p, int n, const float (&f)[8]) {
   if (VEC) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
@@ -96,11 +98,11 @@ __device__ __forceinline__ void store8(float* p, int n, const float (&f)[8]) {
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = f[j];
+      if (j * STEP < n) p[j * STEP] = f[j];
   }
 }
 
-template <bool VEC>
+template <bool VEC, int STEP = 32>
 __device__ __forceinline__ void store8(uint16_t* p, int n, const float (&f)[8]) {
   if (VEC) {
     *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]),
@@ -108,21 +110,23 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, const float (&f)[8]) 
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) narrow(f[j], p[j]);
+      if (j * STEP < n) narrow(f[j], p[j * STEP]);
   }
 }
 
-// e4m3 of f * inv.
-template <bool VEC>
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, int n, const float (&f)[8], float inv) {
+// e4m3 of f * inv (of its last four elements: f * inv2).
+template <bool VEC, int STEP = 32>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, int n, const float (&f)[8], float inv,
+                                            float inv2) {
   const uint32_t lo = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-  const uint32_t hi = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+  const uint32_t hi = e4m3x4(f[4] * inv2, f[5] * inv2, f[6] * inv2, f[7] * inv2);
   if (VEC) {
     *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = static_cast<uint8_t>((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)));
+      if (j * STEP < n)
+        p[j * STEP] = static_cast<uint8_t>((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)));
   }
 }
 
@@ -137,6 +141,12 @@ __device__ __forceinline__ float amax8(const float (&f)[8]) {
 __device__ __forceinline__ float half_warp_max(float m) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
