@@ -41,6 +41,10 @@
 // swizzle) and stores them with TMA, two such pieces in flight, which also
 // clips the tile to M x N.
 //
+// With SPLIT (few tiles: few rows of a) the K blocks of a 128 x 128 tile are
+// shared by the CTAs of a cluster; each leaves its sums in its stages' shared
+// memory, and each then adds its share of the rows over all of them, in order.
+//
 // Waits are bounded as in the bf16 gate kernel: a role whose wait runs out sets
 // TWELL_FLAG_TIMEOUT and leaves its loop, the others' waits then run out too; the
 // CTA drains its TMA loads and MMAs before it frees the TMEM, and both CTAs of a
@@ -71,6 +75,7 @@ struct GemmFp8Params {
   int32_t num_n, num_kb;
   int32_t first_tile, num_tiles;   // this launch's tiles, of num_n to a row of them
   int32_t quarters;  // without PAIR: the tiles are quarters of 256 x 256 tiles
+  int32_t split;     // SPLIT: CTAs of a cluster
   const float* a_scale;   // [M][num_kb]
   const float* b_scale;   // [N or ceil(N / 128)][num_kb]
   void* c;
@@ -152,7 +157,8 @@ __device__ __forceinline__ TileAt tile_at(const GemmFp8Params& p, int tile) {
 
 // BROWS: b has a scale per row (of 1 x 128 blocks), else per 128 x 128 block.
 // PACK: the sums are gate pre-activations and go to a TwELL.
-template <bool PAIR, bool BROWS, bool PACK>
+// SPLIT: a cluster per tile.
+template <bool PAIR, bool BROWS, bool PACK, bool SPLIT>
 __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
@@ -179,9 +185,14 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* aborted = tmem_slot + 1;
 
-  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
-  const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+  const uint32_t crank = PAIR || SPLIT ? ptx::cluster_ctarank() : 0u;
+  const uint32_t rank = PAIR ? crank : 0u;                    // this CTA's half of the tile
+  const int ctas = PAIR ? 2 : SPLIT ? p.split : 1;
+  const int unit = static_cast<int>(blockIdx.x) / ctas;
+  const int units = static_cast<int>(gridDim.x) / ctas;
+  // SPLIT: this CTA's K blocks
+  const int kb_lo = SPLIT ? p.num_kb * static_cast<int>(crank) / ctas : 0;
+  const int kb_hi = SPLIT ? p.num_kb * (static_cast<int>(crank) + 1) / ctas : p.num_kb;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -229,7 +240,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
           const TileAt at = tile_at<PAIR>(p, tile);
           const int m0 = (at.m + static_cast<int>(rank)) * BM;
           const int n0 = at.n * 128 + static_cast<int>(rank) * Cfg::B_ROWS;
-          for (int kb = 0; kb < p.num_kb; ++kb) {
+          for (int kb = kb_lo; kb < kb_hi; ++kb) {
             if (!pipe_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
               flag(p.status, TWELL_FLAG_TIMEOUT);
               *aborted = 1u;
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
         int stage = 0, buf = 0;
         uint32_t phase = 0, bphase = 0;
         for (int tile = unit; tile < p.num_tiles; tile += units) {
-          for (int kb = 0; kb < p.num_kb; ++kb) {
+          for (int kb = kb_lo; kb < kb_hi; ++kb) {
             // (both barriers are asked before either answer is needed)
             const bool loaded = ptx::mbar_test_wait(&full[stage], phase);
             const bool room = ptx::mbar_test_wait(&tempty[buf], bphase ^ 1u);
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
         const TileAt at = tile_at<PAIR>(p, tile);
         const int a0 = (at.m + static_cast<int>(rank)) * BM + r;
         const int b0 = at.n * (BROWS ? 128 : 1) + r;
-        for (int kb = k; kb < p.num_kb + k; kb += R) {
+        for (int kb = kb_lo + k; kb < kb_hi + k; kb += R) {
           if (!pipe_wait(&sempty[par], phase ^ 1u, p.wait_ns)) {
             flag(p.status, TWELL_FLAG_TIMEOUT);
             *aborted = 1u;
@@ -376,7 +387,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     constexpr int kRound = Cfg::ROUND;
     int buf = 0, par = 0;
     uint32_t bphase = 0, sphase = 0;
-    const uint32_t tempty0 = ptx::mapa(ptx::smem_u32(tempty), 0);
+    const uint32_t tempty0 = ptx::mapa(ptx::smem_u32(tempty), PAIR ? 0 : crank);
     const uint32_t taddr0 =
         tmem_base + static_cast<uint32_t>(set * COLS) + (static_cast<uint32_t>(q * 32) << 16);
     bool ready = false;  // the next block's barrier has been seen complete
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
       f32x2 acc[COLS / 2];
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
-      for (int kb0 = 0; kb0 < p.num_kb; kb0 += kRound) {
+      for (int kb0 = kb_lo; kb0 < kb_hi; kb0 += kRound) {
         // the decisions to leave must be warp-uniform: tcgen05.ld is warp-collective
         if (__any_sync(0xffffffffu, !pipe_wait(&sfull[par], sphase, p.wait_ns))) {
           if (lane == 0) {
@@ -396,7 +407,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
         const float* as = a_sc + par * kRound * Cfg::A_PITCH + row;
         const float* bs =
             b_sc + par * kRound * Cfg::B_PITCH + (BROWS ? set * COLS : set * COLS / 128);
-        const int left = p.num_kb - kb0;
+        const int left = kb_hi - kb0;
         const float* as_end = as + (left < kRound ? left : kRound) * Cfg::A_PITCH;
         for (; as != as_end; as += Cfg::A_PITCH, bs += Cfg::B_PITCH) {
           if (!__all_sync(0xffffffffu, ready) &&
@@ -464,6 +475,17 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
       if constexpr (PACK) {
         if (col0 < p.N)
           pack_row_slice<true>(p.out, z, t, valid, m_blk, col0 / TWELL_TILE, lane, row, my_stage);
+      } else if constexpr (SPLIT) {
+        // (every stage has been read: the last block's barrier has been seen)
+        if (valid) {
+#pragma unroll
+          for (int j = 0; j < COLS / 4; ++j) {
+            const int c = set * (COLS / 4) + j;
+            *reinterpret_cast<float4*>(smem + row * 512 + ((c ^ (row & 31)) << 4)) =
+                make_float4(z[j / 8][j % 8 * 4], z[j / 8][j % 8 * 4 + 1], z[j / 8][j % 8 * 4 + 2],
+                            z[j / 8][j % 8 * 4 + 3]);
+          }
+        }
       } else {
         // pieces of 32 rows by 64 bytes, two in flight
         const int sw = (row >> 1) & 3;
@@ -521,7 +543,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
         }
       }
     }
-    if (!PACK && lane == 0) ptx::bulk_wait_all();
+    if (!PACK && !SPLIT && lane == 0) ptx::bulk_wait_all();
   }
 
 done:
@@ -542,8 +564,41 @@ done:
     ptx::tc_fence_before();
     __syncthreads();
   }
-  // neither CTA's barriers or TMEM are used by the other from here on
-  if (PAIR) ptx::cluster_sync();
+  // PAIR: neither CTA's barriers or TMEM are used by the other from here on.
+  // SPLIT: every CTA's sums of the tile are in its shared memory.
+  if (PAIR || SPLIT) ptx::cluster_sync();
+  if (SPLIT) {
+    const TileAt at = tile_at<PAIR>(p, unit);
+    const int left = p.M - at.m * BM, rows = left < BM ? left : BM;
+    const uint32_t part = ptx::smem_u32(smem);
+    // this CTA's rows: every ctas-th
+    for (int i = threadIdx.x;; i += Cfg::THREADS) {
+      const int row = (i >> 5) * ctas + static_cast<int>(crank), c = i & 31;
+      if (row >= rows) break;
+      const uint32_t off = static_cast<uint32_t>(row * 512 + ((c ^ (row & 31)) << 4));
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < ctas; ++k) {
+        const float4 u = ptx::ld_cluster_f32x4(ptx::mapa(part, k) + off);
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
+      const int col = at.n * 128 + 4 * c, n = p.N - col;
+      if (n <= 0) continue;
+      const size_t o = static_cast<size_t>(at.m * BM + row) * p.ldc + col;
+      const float f[4] = {v.x, v.y, v.z, v.w};
+      uint16_t* c16 = static_cast<uint16_t*>(p.c) + o;
+      float* c32 = static_cast<float*>(p.c) + o;
+      if (p.c_vec && n >= 4) {
+        if (p.c_bf16) store4(c16, f);
+        else store4(c32, f);
+      } else {
+        for (int j = 0; j < 4 && j < n; ++j) {
+          if (p.c_bf16) narrow(f[j], c16[j]);
+          else c32[j] = f[j];
+        }
+      }
+    }
+    ptx::cluster_sync();  // nobody leaves while its sums are read
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     if (PAIR) ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
@@ -551,12 +606,12 @@ done:
   }
 }
 
-template <bool PAIR, bool BROWS, bool PACK>
+template <bool PAIR, bool BROWS, bool PACK, bool SPLIT>
 twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensorMap& mb,
                     const CUtensorMap& mc, const GemmFp8Params& p, cudaStream_t s) {
   using Cfg = Fp8Cfg<PAIR, BROWS, PACK>;
   static_assert(Cfg::SMEM <= 232448, "shared memory budget");
-  auto kern = gemm_fp8_kernel<PAIR, BROWS, PACK>;
+  auto kern = gemm_fp8_kernel<PAIR, BROWS, PACK, SPLIT>;
   static std::atomic<uint64_t> set{0};
   if (!smem_limit(kern, Cfg::SMEM, dev, set)) return TWELL_ERR_CUDA;
   if (PAIR) {
@@ -567,21 +622,58 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
     }();
     if (regs != kRegsStart) return TWELL_ERR_UNSUPPORTED;
   }
-  const int most = dev.sm_count / Cfg::CTAS;
-  const int units = p.num_tiles < most ? p.num_tiles : most;
+  const int ctas = SPLIT ? p.split : Cfg::CTAS;
+  const int most = dev.sm_count / ctas;
+  const int units = SPLIT || p.num_tiles < most ? p.num_tiles : most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units * Cfg::CTAS);
+  cfg.gridDim = dim3(units * ctas);
   cfg.blockDim = dim3(Cfg::THREADS);
   cfg.dynamicSmemBytes = Cfg::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = Cfg::CTAS;
+  attr.val.clusterDim.x = ctas;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return smem_launched(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, p), dev, set);
+}
+
+// CTAs of a cluster that share a tile's K blocks: as many as let every cluster run
+// at once (the part holds 76 clusters of two of these CTAs, 36 of four and 15 of
+// eight: they have to lie within a GPC) and leave each CTA four K blocks or more.
+template <bool BROWS>
+int split_for(int64_t tiles, int32_t num_kb) {
+  static std::atomic<int> fit[3] = {{-1}, {-1}, {-1}};
+  int split = 1;
+  for (int i = 0; i < 3; ++i) {
+    const int n = 2 << i;
+    if (num_kb < 4 * n) break;
+    int have = fit[i].load(std::memory_order_relaxed);
+    if (have < 0) {
+      using Cfg = Fp8Cfg<false, BROWS, false>;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(n);
+      cfg.blockDim = dim3(Cfg::THREADS);
+      cfg.dynamicSmemBytes = Cfg::SMEM;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = n;
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      auto kern = gemm_fp8_kernel<false, BROWS, false, true>;
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) !=
+              cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&have, kern, &cfg) != cudaSuccess)
+        have = 0;
+      fit[i].store(have, std::memory_order_relaxed);
+    }
+    if (tiles <= have) split = n;
+  }
+  return split;
 }
 
 // Operand checks shared by the entry points: e4m3 rows on 16-byte boundaries.
@@ -593,7 +685,7 @@ bool operand_ok(const uint8_t* v, int64_t ld, int32_t K, const float* scale) {
 template <bool PACK>
 twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uint8_t* b,
                  int64_t ldb, int32_t b_block, int32_t K, GemmFp8Params p, cudaStream_t s) {
-  p.num_kb = (K + BK - 1) / BK;
+  p.num_kb = static_cast<int32_t>((static_cast<int64_t>(K) + BK - 1) / BK);
   // Pairs of CTAs on 256 x 256 tiles when they still give every SM work, tiles
   // of 128 x 128 otherwise.
   const int64_t wide_m = (static_cast<int64_t>(p.M) + 255) / 256;
@@ -621,15 +713,23 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
                        4 * rest <= dev.sm_count;
     GemmFp8Params q = p;
     q.num_tiles = split ? p.num_tiles - rest : p.num_tiles;
-    st = brows ? launch<true, true, false>(dev, ma, mb, mc, q, s)
-               : launch<true, false, PACK>(dev, ma, mb, mc, q, s);
+    st = brows ? launch<true, true, false, false>(dev, ma, mb, mc, q, s)
+               : launch<true, false, PACK, false>(dev, ma, mb, mc, q, s);
     if (st != TWELL_OK || !split) return st;
     p.first_tile = p.num_tiles - rest;
     p.num_tiles = 4 * rest;
     p.quarters = 1;
   }
-  return brows ? launch<false, true, false>(dev, ma, mb, mc, p, s)
-               : launch<false, false, PACK>(dev, ma, mb, mc, p, s);
+  if constexpr (!PACK) {
+    p.split = p.quarters ? 1
+              : brows    ? split_for<true>(p.num_tiles, p.num_kb)
+                         : split_for<false>(p.num_tiles, p.num_kb);
+    if (p.split > 1)
+      return brows ? launch<false, true, false, true>(dev, ma, mb, mc, p, s)
+                   : launch<false, false, false, true>(dev, ma, mb, mc, p, s);
+  }
+  return brows ? launch<false, true, false, false>(dev, ma, mb, mc, p, s)
+               : launch<false, false, PACK, false>(dev, ma, mb, mc, p, s);
 }
 
 }  // namespace
@@ -651,8 +751,12 @@ extern "C" twell_status twell_gemm_fp8(const uint8_t* a, int64_t lda, const floa
   DeviceInfo dev;
   twell_status st;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
-  // few rows: the tokens as the MMA's N and K split over two CTAs
-  if (b_block == 128 && decode_fp8_supported(M, K))
+  // Few rows: the tokens as the MMA's N and K split over two CTAs, unless the tiles
+  // are so few that larger clusters share K (at 16 rows: 7.5 against 8.9 us for
+  // N 8192, K 2048 with 64 tiles, but 15.9 against 9.1 for N 2048, K 8192 with 16).
+  if (b_block == 128 && decode_fp8_supported(M, K) &&
+      split_for<false>((static_cast<int64_t>(M) + 127) / 128 * ((static_cast<int64_t>(N) + 127) / 128),
+                       static_cast<int32_t>((static_cast<int64_t>(K) + 127) / 128)) < 4)
     return launch_gemm_decode_fp8(dev, a, lda, a_scale, b, ldb, b_scale, M, N, K, c,
                                   c_type == TWELL_BF16, ldc, status_dev, gate_wait_ns(),
                                   static_cast<cudaStream_t>(stream));
