@@ -382,6 +382,132 @@ __global__ void __launch_bounds__(kPipeThreads) rms_norm_bwd_pipe_kernel(const N
   }
 }
 
+// The same for wider rows, one row at a time per block.  Nothing would run
+// while a row's sum is joined: so a row is read from the ring twice, for its sum
+// while the row before it is finished and once more for dx, with one barrier a
+// row between.  The ring holds s and dy only (dtotal is needed once, and is
+// loaded where it has the next row's sum to arrive): P rows of it, one in use, one
+// summed, with P > 2 others on their way.  A warp has Q x 128 elements of the row
+// side by side, quad k of lane l at 128 k + 4 l, so that a thread's places are
+// constants from its first.  What is left is bound by issue slots where all is
+// bf16 (5000 x 8192, against the kernel above with two pieces a thread: fp32
+// stream and bf16 dy 119 -> 87 us, 0.98 of the HBM rate; all bf16 80 -> 74;
+// 3000 x 12288: 123 -> 88).
+template <typename ST, typename GT, int P, int Q>
+__global__ void __launch_bounds__(1024) rms_norm_bwd_wide_kernel(const NormBwdParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];  // [P][s of the row, dy of the row]
+  __shared__ float red[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int e0 = warp * 128 * Q + lane * 4;
+  const uint32_t s_bytes = blockDim.x * 4 * Q * sizeof(ST);
+  const uint32_t slot_bytes = s_bytes + blockDim.x * 4 * Q * sizeof(GT);
+  const uint32_t last = (P - 1) * slot_bytes;
+  bool have[Q];
+  float w[4 * Q], acc[4 * Q];
+#pragma unroll
+  for (int k = 0; k < Q; ++k) {
+    have[k] = e0 + 128 * k < p.D;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + 128 * k + j;
+      acc[4 * k + j] = 0.0f;
+      w[4 * k + j] = !have[k]   ? 0.0f
+                     : p.w_bf16 ? widen(static_cast<const uint16_t*>(p.w)[e])
+                                : static_cast<const float*>(p.w)[e];
+    }
+  }
+  // This thread's place in the rows, advanced a row of this block at a time.
+  const uint32_t T = p.T, step = gridDim.x;  // (t + P step stays below 2^32)
+  const ST* s_at = static_cast<const ST*>(p.s) + blockIdx.x * p.lds + e0;
+  const GT* g_at = static_cast<const GT*>(p.dy) + blockIdx.x * p.lddy + e0;
+  const ST* d_at = static_cast<const ST*>(p.dt) + (p.dt ? blockIdx.x * p.lddt + e0 : 0);
+  ST* dx_at = static_cast<ST*>(p.dx) + blockIdx.x * p.lddx + e0;
+  const int64_t s_step = step * p.lds, g_step = step * p.lddy, d_step = step * p.lddt,
+                dx_step = step * p.lddx;
+  const uint8_t* const own = ring + e0 * sizeof(ST);
+  const uint8_t* const own_g = ring + s_bytes + e0 * sizeof(GT);
+  const uint32_t to = ptx::smem_u32(own), to_g = ptx::smem_u32(own_g);
+  const auto fetch = [&](uint32_t t, uint32_t slot) {
+    if (t < T) {
+#pragma unroll
+      for (int k = 0; k < Q; ++k)
+        if (have[k]) {
+          ptx::cp_async<4 * sizeof(ST)>(to + slot + 128 * k * sizeof(ST), s_at + 128 * k);
+          ptx::cp_async<4 * sizeof(GT)>(to_g + slot + 128 * k * sizeof(GT), g_at + 128 * k);
+        }
+    }
+    ptx::cp_async_commit();  // (a group for every row, empty ones past T)
+    s_at += s_step;
+    g_at += g_step;
+  };
+  // n = s rstd and dy of quad k of the row in a slot
+  const auto read = [&](uint32_t slot, int k, float rstd, float (&n)[4], float (&g)[4]) {
+    quad<ST>(own + slot + 128 * k * sizeof(ST), have[k], n);
+    quad<GT>(own_g + slot + 128 * k * sizeof(GT), have[k], g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) n[j] *= rstd;
+  };
+  // a row's share of dw and this warp's of its sum
+  const auto sum = [&](uint32_t slot, float rstd, int par) {
+    float dot = 0.0f;
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      float n[4], g[4];
+      read(slot, k, rstd, n, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[4 * k + j] = fmaf(g[j], n[j], acc[4 * k + j]);
+        dot = fmaf(g[j] * w[4 * k + j], n[j], dot);
+      }
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) red[par][warp] = dot;
+  };
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+  uint32_t t = blockIdx.x;
+  float rstd = p.rstd[t], rstd1 = t + step < T ? p.rstd[t + step] : 0.0f;  // this row's, the next's
+#pragma unroll
+  for (int k = 0; k < P; ++k) fetch(t + k * step, k * slot_bytes);
+  ptx::cp_async_wait<P - 1>();
+  sum(0, rstd, 0);
+  __syncthreads();
+  uint32_t slot = 0;
+  int par = 0;
+  for (; t < T; t += step, par ^= 1) {
+    float d[4 * Q];
+#pragma unroll
+    for (int k = 0; k < Q; ++k)
+      quad<ST>(reinterpret_cast<const uint8_t*>(d_at + 128 * k), p.dt && have[k], d + 4 * k);
+    d_at += d_step;
+    const float rstd2 = t + 2 * step < T ? p.rstd[t + 2 * step] : 0.0f;
+    const uint32_t ahead = slot == last ? 0 : slot + slot_bytes;
+    ptx::cp_async_wait<P - 2>();
+    if (t + step < T) sum(ahead, rstd1, par ^ 1);
+    // (the row's sum was published by the barrier of the row before)
+    const float dot = warp_sum(lane < nw ? red[par][lane] : 0.0f) * inv_d;
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      float n[4], g[4];
+      read(slot, k, rstd, n, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        n[j] = fmaf(rstd, g[j] * w[4 * k + j] - n[j] * dot, d[4 * k + j]);
+      if (have[k]) store4(dx_at + 128 * k, n);
+    }
+    dx_at += dx_step;
+    fetch(t + P * step, slot);  // (this thread is done with the slot)
+    slot = ahead;
+    rstd = rstd1;
+    rstd1 = rstd2;
+    __syncthreads();
+  }
+  ptx::cp_async_wait<0>();
+#pragma unroll
+  for (int k = 0; k < Q; ++k)
+    if (have[k])
+      store4(p.part + static_cast<size_t>(blockIdx.x) * p.D + e0 + 128 * k, acc + 4 * k);
+}
+
 // dw[c] = sum over the P blocks' shares, in a fixed order.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int32_t P, int32_t D,
                                                        float* dw) {
@@ -425,33 +551,58 @@ twell_status launch_fwd(const NormParams& p, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
+enum class BwdForm { kPlain, kPipe, kWide };
 struct BwdShape {
-  int per, L, G, grid;
-  bool pipe;
+  BwdForm form;
+  int per;   // pieces (plain), quads (wide) of a thread
+  int L, G, grid;
+  int rows;  // in flight per group
 };
 
-// `vec`: every row on 16-byte boundaries.
-BwdShape bwd_shape(int32_t T, int32_t D, bool vec, int sms) {
+// `vec`: every row on 16-byte boundaries; se, ge: bytes of an element of s and dy.
+// The wide form's limit is 1024 threads of three quads (64 registers each).
+BwdShape bwd_shape(int32_t T, int32_t D, bool vec, int se, int ge, const DeviceInfo& dev) {
   BwdShape b;
   const int pieces = (D + 7) / 8;
-  b.per = pieces <= 1024 ? 1 : 2;
-  b.L = threads_for(D, b.per);
-  b.pipe = vec && b.per == 1 && b.L <= kPipeThreads;
-  b.G = (b.pipe ? kPipeThreads : 1024) / b.L;
-  if (b.G > 15) b.G = 15;                 // named barriers
-  if (b.G < 1) b.G = 1;
+  // rows in flight are what fits beside the static shared memory
+  const int budget = dev.max_smem_optin - 2048;
+  if (vec && pieces <= kPipeThreads) {
+    b.form = BwdForm::kPipe;
+    b.per = 1;
+    b.L = threads_for(D, 1);
+    b.G = kPipeThreads / b.L < 15 ? kPipeThreads / b.L : 15;  // named barriers
+    const int fit = budget / (b.L * b.G * 8 * (2 * se + ge));
+    b.rows = fit < 4 ? fit : 4;
+  } else if (vec && D <= 3 * 4096) {
+    b.form = BwdForm::kWide;
+    b.per = D <= 2 * 4096 ? 2 : 3;
+    b.L = (D / 4 + 32 * b.per - 1) / (32 * b.per) * 32;
+    b.G = 1;
+    const int fit = budget / (b.L * b.per * 4 * (se + ge));
+    b.rows = fit < 4 ? fit : 4;
+  } else {
+    b.form = BwdForm::kPlain;
+    b.per = pieces <= 1024 ? 1 : 2;
+    b.L = threads_for(D, b.per);
+    b.G = 1024 / b.L < 15 ? 1024 / b.L : 15;
+    b.rows = 1;
+  }
   const int64_t want = (static_cast<int64_t>(T) + b.G - 1) / b.G;
-  b.grid = static_cast<int>(want < sms ? want : sms);
+  b.grid = static_cast<int>(want < dev.sm_count ? want : dev.sm_count);
   return b;
 }
 
-template <typename ST, typename GT, int P>
-twell_status launch_pipe(const NormBwdParams& p, const BwdShape& b, int smem,
-                         const DeviceInfo& dev, cudaStream_t s) {
+// Q: quads of a thread in the wide form, 0 for the other.
+template <typename ST, typename GT, int P, int Q>
+twell_status launch_pipe(const NormBwdParams& p, const BwdShape& b, const DeviceInfo& dev,
+                         cudaStream_t s) {
   static std::atomic<uint64_t> set{0};
-  auto kern = rms_norm_bwd_pipe_kernel<ST, GT, P>;
+  void (*kern)(NormBwdParams);
+  if constexpr (Q > 0) kern = rms_norm_bwd_wide_kernel<ST, GT, P, Q>;
+  else kern = rms_norm_bwd_pipe_kernel<ST, GT, P>;
   if (!smem_limit(kern, dev.max_smem_optin - 1024, dev, set)) return TWELL_ERR_CUDA;
-  kern<<<b.grid, dim3(b.L, b.G), smem, s>>>(p);
+  const int per = Q > 0 ? 4 * Q * (sizeof(ST) + sizeof(GT)) : 8 * (2 * sizeof(ST) + sizeof(GT));
+  kern<<<b.grid, dim3(b.L, b.G), P * b.L * b.G * per, s>>>(p);
   return smem_launched(cudaGetLastError(), dev, set);
 }
 
@@ -459,15 +610,19 @@ template <typename ST, typename GT, bool VEC>
 twell_status launch_bwd(const NormBwdParams& p, const BwdShape& b, const DeviceInfo& dev,
                         cudaStream_t s) {
   const dim3 block(b.L, b.G);
-  if (VEC && b.pipe) {
-    // rows in flight per group: what fits beside the static shared memory (one
-    // row's pieces and the join's D floats always do)
-    const int row = b.L * b.G * 8 * (2 * static_cast<int>(sizeof(ST)) + static_cast<int>(sizeof(GT)));
-    const int budget = dev.max_smem_optin - 2048;
-    if (4 * row <= budget) return launch_pipe<ST, GT, 4>(p, b, 4 * row, dev, s);
-    if (3 * row <= budget) return launch_pipe<ST, GT, 3>(p, b, 3 * row, dev, s);
-    return launch_pipe<ST, GT, 2>(p, b, 2 * row, dev, s);
+  // (two rows always fit, three of a wide form's narrower rows)
+  if (VEC && b.form == BwdForm::kWide) {
+    if (b.per == 2)
+      return b.rows == 4 ? launch_pipe<ST, GT, 4, 2>(p, b, dev, s)
+                         : launch_pipe<ST, GT, 3, 2>(p, b, dev, s);
+    return b.rows == 4   ? launch_pipe<ST, GT, 4, 3>(p, b, dev, s)
+           : b.rows == 3 ? launch_pipe<ST, GT, 3, 3>(p, b, dev, s)
+                         : launch_pipe<ST, GT, 2, 3>(p, b, dev, s);
   }
+  if (VEC && b.form == BwdForm::kPipe)
+    return b.rows == 4   ? launch_pipe<ST, GT, 4, 0>(p, b, dev, s)
+           : b.rows == 3 ? launch_pipe<ST, GT, 3, 0>(p, b, dev, s)
+                         : launch_pipe<ST, GT, 2, 0>(p, b, dev, s);
   const size_t smem = b.G > 1 ? static_cast<size_t>(p.D) * sizeof(float) : 0;
   if (b.per == 1) rms_norm_bwd_kernel<ST, GT, VEC, 1><<<b.grid, block, smem, s>>>(p);
   else rms_norm_bwd_kernel<ST, GT, VEC, 2><<<b.grid, block, smem, s>>>(p);
@@ -525,9 +680,12 @@ extern "C" size_t twell_rms_norm_bwd_workspace(int32_t T, int32_t D) {
   if (T < 0 || D <= 0 || D > kMaxD) return 0;
   DeviceInfo dev;
   // (without a device: the most blocks a call would use on the part this is for)
-  const int sms = current_device(&dev) ? dev.sm_count : 152;
-  // (the element-by-element form has as many blocks or fewer)
-  const BwdShape b = bwd_shape(T > 0 ? T : 1, D, true, sms);
+  if (!current_device(&dev)) {
+    dev.sm_count = 152;
+    dev.max_smem_optin = 232448;
+  }
+  // (other types and the element-by-element form have as many blocks or fewer)
+  const BwdShape b = bwd_shape(T > 0 ? T : 1, D, true, 2, 2, dev);
   return static_cast<size_t>(b.grid) * D * sizeof(float);
 }
 
@@ -564,7 +722,7 @@ extern "C" twell_status twell_rms_norm_bwd(const void* total, int32_t type, int6
   const bool vec = D % 8 == 0 && rows_aligned(total, ld, se) && rows_aligned(w, 0, we) &&
                    rows_aligned(dy, lddy, ge) && rows_aligned(dx, lddx, se) &&
                    (!dtotal || rows_aligned(dtotal, lddt, se));
-  const BwdShape b = bwd_shape(T, D, vec, dev.sm_count);
+  const BwdShape b = bwd_shape(T, D, vec, se, ge, dev);
   if (ws_bytes < static_cast<size_t>(b.grid) * D * sizeof(float)) return TWELL_ERR_INVALID;
   const bool sb = type == TWELL_BF16, gb = dy_type == TWELL_BF16;
   if (sb && gb)

@@ -183,6 +183,17 @@ def test_backward(T, D, st, gt, wt, stream):
     assert (dx2 == dx).all() and (dw2 == dw).all()
 
 
+# rows of many threads: either side of where a thread's share of a row and the
+# rows in flight change, more rows than blocks and fewer
+@pytest.mark.parametrize("T,D", [(1, 5120), (311, 5128), (460, 8192), (2, 8200), (333, 9216),
+                                 (170, 10240), (170, 10248), (1001, 5632), (950, 8192),
+                                 (800, 12288), (3, 12296)])
+@pytest.mark.parametrize("st,gt,wt,stream", [(BF16, BF16, BF16, True), (F32, BF16, F32, True),
+                                             (F32, F32, BF16, True), (BF16, F32, BF16, False)])
+def test_backward_wide(T, D, st, gt, wt, stream):
+    test_backward(T, D, st, gt, wt, stream)
+
+
 def test_backward_against_differences():
     # central differences of L = sum(c y) + sum(d total) in 64 bits, through the
     # forward's definition; a step of 1e-5 leaves about 1e-9 relative
