@@ -177,8 +177,14 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
   float* b_sc = a_sc + 2 * Cfg::ROUND * Cfg::A_PITCH;               // [2][ROUND][B_PITCH]
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING + Cfg::SCALES);
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + BUFS;
+  // Without PAIR a stage's barrier also says that its block's sums are there: one
+  // commit a block, not two, for MMAs of N = 128, which a second one holds up (66 of
+  // 570 cycles a block; of a pair's N = 256 none, and there the shared barrier's
+  // second counter costs the epilogue 3 %).  A stage comes round no sooner than its
+  // sums' TMEM buffer.
+  static_assert(PAIR || STAGES >= BUFS, "a barrier that producer and epilogue wait for");
+  uint64_t* tfull = PAIR ? empty + STAGES : empty;
+  uint64_t* tempty = empty + STAGES + (PAIR ? BUFS : 0);
   uint64_t* sfull = tempty + BUFS;
   uint64_t* sempty = sfull + 2;
   uint64_t* drain = sempty + 2;
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
       ptx::mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < BUFS; ++b) {
-      ptx::mbar_init(&tfull[b], 1);
+      if (PAIR) ptx::mbar_init(&tfull[b], 1);
       ptx::mbar_init(&tempty[b], 4 * Cfg::SETS * Cfg::CTAS);
     }
     for (int i = 0; i < 2; ++i) {
@@ -318,7 +324,6 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
                 ptx::mma_commit_pair(&tfull[buf]);
                 ptx::mma_commit_pair(&empty[stage]);
               } else {
-                ptx::mma_commit(&tfull[buf]);
                 ptx::mma_commit(&empty[stage]);
               }
             }
@@ -385,8 +390,9 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     const int row = q * 32 + lane;         // its thread's row
     uint8_t* my_stage = staging + (threadIdx.x - 128) * 128;
     constexpr int kRound = Cfg::ROUND;
-    int buf = 0, par = 0;
-    uint32_t bphase = 0, sphase = 0;
+    int buf = 0, par = 0, stage = 0;
+    const int& sums = PAIR ? buf : stage;  // of tfull
+    uint32_t phase = 0, sphase = 0;
     const uint32_t tempty0 = ptx::mapa(ptx::smem_u32(tempty), PAIR ? 0 : crank);
     const uint32_t taddr0 =
         tmem_base + static_cast<uint32_t>(set * COLS) + (static_cast<uint32_t>(q * 32) << 16);
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
         const float* as_end = as + (left < kRound ? left : kRound) * Cfg::A_PITCH;
         for (; as != as_end; as += Cfg::A_PITCH, bs += Cfg::B_PITCH) {
           if (!__all_sync(0xffffffffu, ready) &&
-              __any_sync(0xffffffffu, !pipe_wait(&tfull[buf], bphase, p.wait_ns))) {
+              __any_sync(0xffffffffu, !pipe_wait(&tfull[sums], phase, p.wait_ns))) {
             if (lane == 0) {
               flag(p.status, TWELL_FLAG_TIMEOUT);
               *aborted = 1u;
@@ -427,14 +433,18 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
           const uint32_t done_bar = tempty0 + buf * 8;
           if (++buf == BUFS) {
             buf = 0;
-            bphase ^= 1u;
+            if (PAIR) phase ^= 1u;
+          }
+          if (!PAIR && ++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
           }
 #pragma unroll
           for (int ch = 0; ch < kPieces; ++ch) {
             ptx::tmem_wait_ld();
             if (ch < kPieces - 1) {
               ptx::tmem_ld_32x32b_x16(taddr + (ch + 1) * kPiece, r[(ch + 1) & 1]);
-              if (ch == kPieces - 2) ready = ptx::mbar_test_wait(&tfull[buf], bphase);
+              if (ch == kPieces - 2) ready = ptx::mbar_test_wait(&tfull[sums], phase);
             } else {
               ptx::tc_fence_before();
               // (predicated; with b's row scales the predicate costs the loop spills,
