@@ -387,11 +387,18 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     const int q = warp & 3;                // TMEM lane quarter this warp may read
     constexpr int COLS = Cfg::COLS, kPieces = COLS / kPiece;
     const int set = (warp - 4) >> 2;       // its COLS columns of the tile
-    const int row = q * 32 + lane;         // its thread's row
+    // A thread's sums: of row 32 q + lane, all COLS columns; or with FRAG, of rows
+    // 32 q + 8 i + lane / 4, i = 0..3, columns 8 j + 2 (lane mod 4) and the next: it
+    // needs the scales of a quarter of the columns only.  Reading those of all of
+    // them from shared memory costs a pair more than the slower TMEM reads of 16
+    // lanes (345 against 368 us at dW's 9216 x 2304 x 16384), a single CTA less
+    // (47.9 against 44.8 us at 283 x 3424 x 15616).
+    constexpr bool FRAG = PAIR && BROWS;
+    const int row = FRAG ? q * 32 + (lane >> 2) : q * 32 + lane;
     uint8_t* my_stage = staging + (threadIdx.x - 128) * 128;
     constexpr int kRound = Cfg::ROUND;
     int buf = 0, par = 0, stage = 0;
-    const int& sums = PAIR ? buf : stage;  // of tfull
+    const int& next = PAIR ? buf : stage;  // of tfull
     uint32_t phase = 0, sphase = 0;
     const uint32_t tempty0 = ptx::mapa(ptx::smem_u32(tempty), PAIR ? 0 : crank);
     const uint32_t taddr0 =
@@ -412,12 +419,13 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
         }
         const float* as = a_sc + par * kRound * Cfg::A_PITCH + row;
         const float* bs =
-            b_sc + par * kRound * Cfg::B_PITCH + (BROWS ? set * COLS : set * COLS / 128);
+            b_sc + par * kRound * Cfg::B_PITCH +
+            (BROWS ? set * COLS + (FRAG ? 2 * (lane & 3) : 0) : set * COLS / 128);
         const int left = kb_hi - kb0;
         const float* as_end = as + (left < kRound ? left : kRound) * Cfg::A_PITCH;
         for (; as != as_end; as += Cfg::A_PITCH, bs += Cfg::B_PITCH) {
           if (!__all_sync(0xffffffffu, ready) &&
-              __any_sync(0xffffffffu, !pipe_wait(&tfull[sums], phase, p.wait_ns))) {
+              __any_sync(0xffffffffu, !pipe_wait(&tfull[next], phase, p.wait_ns))) {
             if (lane == 0) {
               flag(p.status, TWELL_FLAG_TIMEOUT);
               *aborted = 1u;
@@ -427,9 +435,35 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
           ptx::tc_fence_after();
           const uint32_t taddr = taddr0 + static_cast<uint32_t>(buf * BN);
           uint32_t r[2][kPiece];
-          ptx::tmem_ld_32x32b_x16(taddr, r[0]);
-          const float s = BROWS ? as[0] : as[0] * bs[0];
-          const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+          // piece ch's sums and b's scales, the latter in pairs of columns
+          f32x2 b2[2][BROWS ? (FRAG ? 2 : kPiece / 2) : 1];
+          const auto read = [&](int ch) {
+            const uint32_t at = taddr + static_cast<uint32_t>(ch * kPiece);
+            if (FRAG) {
+              ptx::tmem_ld_16x256b_x2(at, r[ch & 1]);
+              ptx::tmem_ld_16x256b_x2(at + (16u << 16), r[ch & 1] + 8);
+            } else {
+              ptx::tmem_ld_32x32b_x16(at, r[ch & 1]);
+            }
+            const float* b = bs + ch * kPiece;
+#pragma unroll
+            for (int j = 0; BROWS && j < (FRAG ? 2 : kPiece / 4); ++j) {
+              if (FRAG) {
+                b2[ch & 1][j] = *reinterpret_cast<const f32x2*>(b + 8 * j);
+              } else {
+                const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(b + 4 * j);
+                b2[ch & 1][2 * j] = b4.x;
+                b2[ch & 1][2 * j + 1] = b4.y;
+              }
+            }
+          };
+          read(0);
+          f32x2 s2[FRAG ? 4 : 1];
+#pragma unroll
+          for (int i = 0; i < (FRAG ? 4 : 1); ++i) {
+            const float s = BROWS ? as[8 * i] : as[0] * bs[0];
+            s2[i] = pack2(__float_as_uint(s), __float_as_uint(s));
+          }
           const uint32_t done_bar = tempty0 + buf * 8;
           if (++buf == BUFS) {
             buf = 0;
@@ -443,27 +477,24 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
           for (int ch = 0; ch < kPieces; ++ch) {
             ptx::tmem_wait_ld();
             if (ch < kPieces - 1) {
-              ptx::tmem_ld_32x32b_x16(taddr + (ch + 1) * kPiece, r[(ch + 1) & 1]);
-              if (ch == kPieces - 2) ready = ptx::mbar_test_wait(&tfull[sums], phase);
+              read(ch + 1);
+              if (ch == kPieces - 2) ready = ptx::mbar_test_wait(&tfull[next], phase);
             } else {
               ptx::tc_fence_before();
-              // (predicated; with b's row scales the predicate costs the loop spills,
-              // and a branch is the faster: 377 against 430 us at dW's 9216 x 2304 x 16384)
+              // (predicated; with b's row scales a branch is the faster: 45.0 against
+              // 47.3 us at 283 x 3424 x 15616)
               if (!BROWS) ptx::mbar_arrive_cluster_relaxed(done_bar, lane == 0);
               else if (lane == 0) ptx::mbar_arrive_cluster_relaxed(done_bar, true);
             }
+            const uint32_t* rr = r[ch & 1];
 #pragma unroll
-            for (int i = 0; i < kPiece / 4; ++i) {
-              f32x2 f0 = s2, f1 = s2;
-              if (BROWS) {
-                const ulonglong2 b4 =
-                    *reinterpret_cast<const ulonglong2*>(bs + ch * kPiece + 4 * i);
-                f0 = mul2(s2, b4.x);
-                f1 = mul2(s2, b4.y);
-              }
-              const uint32_t* rr = r[ch & 1] + 4 * i;
-              fma2(acc[ch * (kPiece / 2) + 2 * i], pack2(rr[0], rr[1]), f0);
-              fma2(acc[ch * (kPiece / 2) + 2 * i + 1], pack2(rr[2], rr[3]), f1);
+            for (int i = 0; i < kPiece / 2; ++i) {
+              // FRAG: row i mod 4, columns 8 (i / 4)
+              const uint32_t* v = FRAG ? rr + (i & 2) * 4 + (i >> 2) * 4 + (i & 1) * 2 : rr + 2 * i;
+              fma2(acc[ch * (kPiece / 2) + i], pack2(v[0], v[1]),
+                   FRAG    ? mul2(s2[i & 3], b2[ch & 1][i >> 2])
+                   : BROWS ? mul2(s2[0], b2[ch & 1][i])
+                           : s2[0]);
             }
           }
         }
@@ -475,42 +506,50 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
       }
       const TileAt at = tile_at<PAIR>(p, tile);
       const int m_blk = at.m + static_cast<int>(rank);
-      const int t = m_blk * BM + row;
       const int col0 = at.n * 128 + set * COLS;
-      const bool valid = t < p.M;
-      float z[COLS / 32][32];
+      // FRAG: f(row, column, its sum, the next column's) of the thread's sums in piece ch
+      const auto each_pair = [&](int ch, auto&& f) {
 #pragma unroll
-      for (int i = 0; i < COLS / 2; ++i)
-        unpack2(acc[i], z[i / 16][2 * (i % 16)], z[i / 16][2 * (i % 16) + 1]);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            unpack2(acc[ch * (kPiece / 2) + 4 * j + i], lo, hi);
+            f(8 * i + (lane >> 2), 8 * j + 2 * (lane & 3), lo, hi);
+          }
+      };
+      float z[COLS / 32][32];
+      if (!FRAG) {
+#pragma unroll
+        for (int i = 0; i < COLS / 2; ++i)
+          unpack2(acc[i], z[i / 16][2 * (i % 16)], z[i / 16][2 * (i % 16) + 1]);
+      }
       if constexpr (PACK) {
+        const int t = m_blk * BM + row;
         if (col0 < p.N)
-          pack_row_slice<true>(p.out, z, t, valid, m_blk, col0 / TWELL_TILE, lane, row, my_stage);
+          pack_row_slice<true>(p.out, z, t, t < p.M, m_blk, col0 / TWELL_TILE, lane, row,
+                               my_stage);
       } else if constexpr (SPLIT) {
         // (every stage has been read: the last block's barrier has been seen)
-        if (valid) {
 #pragma unroll
-          for (int j = 0; j < COLS / 4; ++j) {
-            const int c = set * (COLS / 4) + j;
-            *reinterpret_cast<float4*>(smem + row * 512 + ((c ^ (row & 31)) << 4)) =
-                make_float4(z[j / 8][j % 8 * 4], z[j / 8][j % 8 * 4 + 1], z[j / 8][j % 8 * 4 + 2],
-                            z[j / 8][j % 8 * 4 + 3]);
-          }
+        for (int j = 0; j < COLS / 4; ++j) {
+          const int c = set * (COLS / 4) + j;
+          *reinterpret_cast<float4*>(smem + row * 512 + ((c ^ (row & 31)) << 4)) =
+              make_float4(z[j / 8][j % 8 * 4], z[j / 8][j % 8 * 4 + 1], z[j / 8][j % 8 * 4 + 2],
+                          z[j / 8][j % 8 * 4 + 3]);
         }
       } else {
         // pieces of 32 rows by 64 bytes, two in flight
-        const int sw = (row >> 1) & 3;
+        const int sw = (lane >> 1) & 3;
         uint8_t* mine = staging + (warp - 4) * 4096;
         const int t0 = m_blk * BM + q * 32;
         const int cols = p.c_bf16 ? 32 : 16;  // of a piece
-        const auto store_piece = [&](int i, const uint32_t (&v)[16]) {
+        const auto store_piece = [&](int i, auto&& fill) {
           uint8_t* piece = mine + (i & 1) * 2048;
           const int col = col0 + i * cols;
           if (lane == 0) ptx::bulk_wait_read<1>();  // the piece before last has left
           __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(piece + lane * 64 + ((j ^ sw) << 4)) =
-                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          fill(piece);
           if (p.c_vec) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -534,21 +573,51 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
             __syncwarp();
           }
         };
+        // byte b of row r of a piece
+        const auto place = [&](uint8_t* piece, int r, int b) {
+          return piece + r * 64 + (((b >> 4) ^ ((r >> 1) & 3)) << 4) + (b & 15);
+        };
+        const auto row_of = [&](int i, const uint32_t (&v)[16]) {
+          store_piece(i, [&](uint8_t* piece) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(piece + lane * 64 + ((j ^ sw) << 4)) =
+                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          });
+        };
         if (p.c_bf16) {
 #pragma unroll
           for (int i = 0; i < COLS / 32; ++i) {
-            uint32_t v[16];
+            if constexpr (FRAG) {
+              store_piece(i, [&](uint8_t* piece) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = bf16x2(z[i][2 * j], z[i][2 * j + 1]);
-            store_piece(i, v);
+                for (int h = 0; h < 2; ++h)
+                  each_pair(2 * i + h, [&](int r, int c, float lo, float hi) {
+                    *reinterpret_cast<uint32_t*>(place(piece, r, 32 * h + 2 * c)) = bf16x2(lo, hi);
+                  });
+              });
+            } else {
+              uint32_t v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = bf16x2(z[i][2 * j], z[i][2 * j + 1]);
+              row_of(i, v);
+            }
           }
         } else {
 #pragma unroll
           for (int i = 0; i < COLS / 16; ++i) {
-            uint32_t v[16];
+            if constexpr (FRAG) {
+              store_piece(i, [&](uint8_t* piece) {
+                each_pair(i, [&](int r, int c, float lo, float hi) {
+                  *reinterpret_cast<float2*>(place(piece, r, 4 * c)) = make_float2(lo, hi);
+                });
+              });
+            } else {
+              uint32_t v[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(z[i / 2][i % 2 * 16 + j]);
-            store_piece(i, v);
+              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(z[i / 2][i % 2 * 16 + j]);
+              row_of(i, v);
+            }
           }
         }
       }
