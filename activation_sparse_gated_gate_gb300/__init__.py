@@ -636,10 +636,16 @@ def _run(name, device, *args):
         raise TwellError(code, name)
 
 
+def _pitch_e4m3(cols):
+    """Bytes between the rows of a new e4m3 matrix: the 8-bit products read rows
+    on 16-byte boundaries, and faster where a block of 128 is one memory line
+    (593 x 5560 x 4452: 32.6 us with rows 4464 apart, 23.0 with 4480)."""
+    return (cols + 127) // 128 * 128 if cols > 128 else (cols + 15) // 16 * 16
+
+
 def _empty_e4m3(rows, cols, device):
-    """[rows][cols] with its rows on 16-byte boundaries, as the 8-bit products
-    read them."""
-    pitch = (cols + 15) // 16 * 16
+    """[rows][cols] for the 8-bit products to read."""
+    pitch = _pitch_e4m3(cols)
     t = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
     return t if pitch == cols else t[:, :cols]
 
@@ -794,7 +800,7 @@ def twell_quant_fp8(x, block_rows=1, rows=True, transposed=False, out=None,
         if q is None:
             q = _empty_e4m3(R, C, x.device)
             scale = torch.empty(at, dtype=f32, device=x.device)
-            ldq = (C + 15) // 16 * 16
+            ldq = _pitch_e4m3(C)
         else:
             ldq = _mat(q, _E4M3, "q", dev, shape)[1]
             _vec(scale, _F32, "scale", dev, at)
@@ -806,7 +812,7 @@ def twell_quant_fp8(x, block_rows=1, rows=True, transposed=False, out=None,
         if qt is None:
             qt = _empty_e4m3(C, R, x.device)
             scale_t = torch.empty(at, dtype=f32, device=x.device)
-            ldqt = (R + 15) // 16 * 16
+            ldqt = _pitch_e4m3(R)
         else:
             ldqt = _mat(qt, _E4M3, "qt", dev, (C, R))[1]
             _vec(scale_t, _F32, "scale_t", dev, at)
