@@ -184,11 +184,14 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, con
     for (int i = 0; i < ROWS; ++i) {
       const float inv =
           SQUARE ? inv_all : __shfl_sync(0xffffffffu, inv_row, i * SHARE, 16);
-      if (r0 + i < p.R && nc > 0) {
-        float f[8];
+      float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = v[i].get(j);
-        store8_e4m3<VEC, 16>(p.q + (r0 + i) * p.ldq + c0, nc, f, inv, inv);
+      for (int j = 0; j < 8; ++j) f[j] = v[i].get(j);
+      uint8_t* to = p.q + (r0 + i) * p.ldq + c0;
+      if constexpr (VEC) {
+        if (r0 + i < p.R && nc > 0) store8_e4m3(to, f, inv);
+      } else {
+        store8_e4m3_lanes<16>(to, nc, r0 + i < p.R, f, inv, inv);
       }
     }
   }

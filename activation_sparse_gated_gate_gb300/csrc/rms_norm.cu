@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
       const float amax = fmaxf(half_warp_max(amax8(v[i])), kFp8AmaxMin);
       if (n > 0) {
         const float inv = kFp8Max / amax;
-        store8_e4m3<VEC>(p.q + t * p.ldq + e, n, v[i], inv, inv);
+        store8_e4m3(p.q + t * p.ldq + e, v[i], inv);
         if ((threadIdx.x & 15) == 0) p.scale[t * nb + e / kFp8Block] = amax / kFp8Max;
       }
     }
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         for (int j = 4 * k; j < 4 * k + 4; ++j) a[k] = fmaxf(a[k], fabsf(v[i][j]));
         a[k] = warp_max(a[k]);
       }
-      store8_e4m3<VEC>(p.q + t * p.ldq + e, n, v[i], kFp8Max / a[0], kFp8Max / a[1]);
+      store8_e4m3_lanes<32>(p.q + t * p.ldq + e, n, true, v[i], kFp8Max / a[0], kFp8Max / a[1]);
       const int lane = threadIdx.x & 31, b = e / kFp8Block + lane;  // (lanes 0 and 1)
       if (lane < 2 && b < nb) p.scale[t * nb + b] = (lane ? a[1] : a[0]) / kFp8Max;
     }
