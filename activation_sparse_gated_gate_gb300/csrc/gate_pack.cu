@@ -319,8 +319,8 @@ extern "C" twell_status twell_gate_pack(const uint16_t* x, const uint16_t* Wg_t,
   // (every TwELL tile on a 2-CTA cluster, W_g streamed once; it stores every
   // block-bitmap word itself).  Above 192 tokens its packing epilogue (16
   // tokens per step and set) outweighs the stream, and the batch kernel is
-  // the faster (d_model 2048, d_ff 8192, graph replay: 23.7 against 25.7 us
-  // at T = 224 and 256, equal at 128-192, 19.6 against 21.6 us at T = 96).
+  // the faster (d_model 2048, d_ff 8192, 0.5 %, graph replay: 20.2 against 21.0
+  // and 22.2 us at T = 224 and 256, 19.7 against 18.9 at 192, 18.7 against 16.5 at 96).
   if (gate_decode_supported(T, D) && T <= kGateDecodeMaxT)
     return launch_gate_decode(dev, x, Wg_t, T, D, F, out, z_debug, status_dev, p.wait_ns,
                               nullptr, s);
