@@ -35,7 +35,12 @@
 // registers from the others.  (The shared memory leaves so little L1 that a
 // spilled register comes back from L2: at 8192 x 6144 x 1536 the same loop took
 // 147 us with about 300 bytes of spills in 168 registers, 88 us with 30, and
-// takes 76 us with none in 224.)
+// takes 73 us with none in 224: 2.1 PFLOP/s.)  At 8192 x 8192 x 8192 it takes 390-430 us
+// (up to 2.8 PFLOP/s) as the power limit allows.
+//
+// Without PAIR TMEM holds four blocks and the MMAs themselves are the bound: 250
+// cycles a block alone, 134 more while the copies fill the stages' shared memory,
+// 570 with the epilogue's reads (512 x 4096 x 4096: 12.7 us).
 //
 // C leaves through shared memory: a warp stages 32 rows of 64 bytes (64-byte
 // swizzle) and stores them with TMA, two such pieces in flight, which also
