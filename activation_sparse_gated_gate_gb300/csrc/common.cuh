@@ -74,4 +74,23 @@ twell_status make_tmap_2d(CUtensorMap* map, int elem_bytes, const void* base, ui
                           uint64_t outer, uint32_t box_inner, uint32_t box_outer,
                           uint64_t pitch_bytes, int swizzle);
 
+// Launches a kernel that may start before the stream's last kernel is done and
+// waits for it by itself (ptx::grid_wait before the first use of what it wrote).
+// Everything before that kernel is done when this one starts.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 }  // namespace twell

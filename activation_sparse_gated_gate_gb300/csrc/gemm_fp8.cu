@@ -873,10 +873,10 @@ extern "C" twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, cons
   DeviceInfo dev;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s) != cudaSuccess) return TWELL_ERR_CUDA;
-  if (decode_fp8_supported(T, D))  // (it stores every word of the block bitmap itself)
+  if (decode_fp8_supported(T, D))  // (it zeroes and stores all its counters and words itself)
     return launch_gate_decode_fp8(dev, xq, ldx, x_scale, wq, ldw, w_scale, T, D, F, out, z_debug,
                                   status_dev, gate_wait_ns(), s);
+  if (cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s) != cudaSuccess) return TWELL_ERR_CUDA;
   const size_t words = (static_cast<size_t>(T) + BM - 1) / BM * (F / 32);
   if (out->block_bits &&
       cudaMemsetAsync(out->block_bits, 0, words * sizeof(uint32_t), s) != cudaSuccess)
