@@ -67,7 +67,8 @@ constexpr int BM = 128;
 constexpr int BK = 128;             // e4m3 of a 128-byte row: one scale block
 constexpr int kPiece = 16;            // columns of a TMEM read
 constexpr int kTmemCols = 512;
-constexpr int kSplitBlocks = 32;      // K blocks from which a ragged last round is split
+// K blocks from which a ragged last round is split; with packing
+constexpr int kSplitBlocks = 8, kSplitBlocksPack = 32;
 // The pair kernel's 384 threads start with 168 registers each; its epilogue
 // threads take 224 and the others keep 56 (4 x 56 + 8 x 224 = 12 x 168).  (With
 // 208 and 88 nothing spills either, but the loop is scheduled less well: 403
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* aborted = tmem_slot + 1;
 
+  if (PAIR) ptx::grid_launch_next();  // (of a last round's quarters)
   const uint32_t crank = PAIR || SPLIT ? ptx::cluster_ctarank() : 0u;
   const uint32_t rank = PAIR ? crank : 0u;                    // this CTA's half of the tile
   const int ctas = PAIR ? 2 : SPLIT ? p.split : 1;
@@ -688,6 +690,7 @@ done:
     if (PAIR) ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
     else ptx::tmem_dealloc(tmem_base, kTmemCols);
   }
+  if (!PAIR && !SPLIT && p.quarters) ptx::grid_wait();  // the call ends with both launches
 }
 
 template <bool PAIR, bool BROWS, bool PACK, bool SPLIT>
@@ -714,13 +717,16 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
   cfg.blockDim = dim3(Cfg::THREADS);
   cfg.dynamicSmemBytes = Cfg::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // quarters start as the full rounds' CTAs leave
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.quarters ? 2 : 1;
   return smem_launched(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, p), dev, set);
 }
 
@@ -790,10 +796,13 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
   const bool brows = !PACK && b_block == 1;
   if (pair) {
     // A last round of tiles that leaves most pairs idle runs as quarters, one per
-    // CTA, in a launch of its own, where K is long enough to pay for it.
+    // CTA, in a launch of its own that starts as the full rounds' CTAs leave, where K
+    // is long enough to pay for it (8192 x 6144 x 1536 with 12 blocks 72.9 -> 72.3 us,
+    // 8192 x 2560 x 4096 73.5 -> 71.2; with 8 blocks there is no difference.  Packing
+    // quarters takes longer: gate 8192 x 1536 x 6144 with 12 blocks 88 -> 95).
     const int32_t pairs = dev.sm_count / 2;
     const int32_t rest = p.num_tiles % pairs;
-    const bool split = p.num_kb >= kSplitBlocks && p.num_tiles > pairs && rest > 0 &&
+    const bool split = p.num_kb >= (PACK ? kSplitBlocksPack : kSplitBlocks) && p.num_tiles > pairs && rest > 0 &&
                        4 * rest <= dev.sm_count;
     GemmFp8Params q = p;
     q.num_tiles = split ? p.num_tiles - rest : p.num_tiles;

@@ -150,6 +150,44 @@ def test_product(M, N, K, block, dt):
     assert int(tw.status_word().item()) == 0
 
 
+# 80 and 81 tiles of 256 x 256: the last round's few run as quarters, in a second launch
+@pytest.mark.parametrize("M,N,K", [(2500, 2000, 1100), (2049, 2304, 1024)])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_product_with_a_ragged_last_round(M, N, K, block, dt):
+    test_product(M, N, K, block, dt)
+
+
+def test_second_launches_in_order():
+    # what follows a call on its stream sees both of its launches, what precedes it
+    # is done before either: outputs overwritten just before and read just after
+    qa, qb = operands(_gen(23), 2500, 2000, 1100, 128)
+    want = tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale)
+    gates = [gate_inputs(24 + i, 16, 512, 1024, 0.03 * (i + 1)) for i in range(2)]
+    h = tw.TwELL(16, 1024, 8)
+    wants = []
+    for x, w in gates:
+        tw.twell_gate_pack_fp8(x.q, x.scale, w.q, w.scale, h)
+        wants.append((h.cnt.clone(), int(h.spill_n.item())))
+    assert wants[0][1] != wants[1][1] > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c, seen, counts = torch.empty_like(want), [], []
+        for i in range(40):
+            c.zero_()
+            tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale, out=c)
+            seen.append((c != want).sum())
+            x, w = gates[i % 2]
+            h.spill_n.fill_(7)
+            tw.twell_gate_pack_fp8(x.q, x.scale, w.q, w.scale, h)
+            counts.append((h.cnt.clone(), h.spill_n.clone()))
+    side.synchronize()
+    assert sum(int(n) for n in seen) == 0
+    for i, (cnt, n) in enumerate(counts):
+        assert (cnt == wants[i % 2][0]).all() and int(n) == wants[i % 2][1]
+
+
 def test_product_into_wider_rows():
     qa, qb = operands(_gen(5), 70, 200, 256, 128)
     want = tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale)
@@ -213,7 +251,8 @@ def test_product_on_another_stream_and_in_a_graph():
     (512, 1024, 2048, 1), (4, 1024, 2048, 128),   # a cluster per tile
     (4, 8192, 512, 128),                          # the decode kernel
     (300, 8192, 512, 128), (1000, 3200, 384, 1),  # a CTA per tile
-    (4096, 4096, 512, 128), (4096, 4096, 512, 1)])  # pairs of CTAs
+    (4096, 4096, 512, 128), (4096, 4096, 512, 1),   # pairs of CTAs
+    (2500, 2000, 1100, 128)])                       # and a last round of quarters
 def test_a_wait_that_runs_out(M, N, K, block):
     # a bound of a few nanoseconds on every pipeline wait: the call returns, sets
     # the flag, and the next one is right again
@@ -267,6 +306,10 @@ def test_gate(T, D, F, p, W, cap):
         any_ = act[b * 128:(b + 1) * 128].any(0).reshape(-1, 32)
         want = (any_.astype(np.uint64) << np.arange(32, dtype=np.uint64)).sum(1)
         np.testing.assert_array_equal(bits[b].astype(np.uint64), want)
+
+
+def test_gate_with_a_ragged_last_round():
+    test_gate(2500, 4100, 2048, 0.02, 8, None)
 
 
 def test_gate_feeds_the_ffn():
