@@ -294,6 +294,10 @@ def twell_ffn_fwd(x, h: TwELL, Wu_t, Wd, y=None, status=None, stream=None):
     if Wu_t.shape != (h.F, D) or Wd.shape != (h.F, D) or T != h.T:
         raise ValueError("shape mismatch: x [T][D], Wu_t and Wd [F][D]")
     status = h.status if status is None else status
+    if stream is None:
+        _run("twell_ffn_fwd", x.get_device(), x.data_ptr(), ctypes.byref(h.struct),
+             Wu_t.data_ptr(), Wd.data_ptr(), D, y.data_ptr(), status.data_ptr())
+        return y
     with torch.cuda.device(x.device):
         _check(lib().twell_ffn_fwd(_ptr(x), ctypes.byref(h.struct), _ptr(Wu_t), _ptr(Wd), D,
                                    _ptr(y), _ptr(status), _stream(stream)),
