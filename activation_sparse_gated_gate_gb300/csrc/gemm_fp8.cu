@@ -798,12 +798,13 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
     // A last round of tiles that leaves most pairs idle runs as quarters, one per
     // CTA, in a launch of its own that starts as the full rounds' CTAs leave, where K
     // is long enough to pay for it (8192 x 6144 x 1536 with 12 blocks 72.9 -> 72.3 us,
-    // 8192 x 2560 x 4096 73.5 -> 71.2; with 8 blocks there is no difference.  Packing
-    // quarters takes longer: gate 8192 x 1536 x 6144 with 12 blocks 88 -> 95).
+    // with 8 blocks there is no difference; started early, 8192 x 2560 x 4096 takes 71.4,
+    // else 73.5).  Packing quarters takes longer: gate 8192 x 1536 x 6144 with 12 blocks
+    // 95 us, whole 88.
     const int32_t pairs = dev.sm_count / 2;
     const int32_t rest = p.num_tiles % pairs;
-    const bool split = p.num_kb >= (PACK ? kSplitBlocksPack : kSplitBlocks) && p.num_tiles > pairs && rest > 0 &&
-                       4 * rest <= dev.sm_count;
+    const bool split = p.num_kb >= (PACK ? kSplitBlocksPack : kSplitBlocks) &&
+                       p.num_tiles > pairs && rest > 0 && 4 * rest <= dev.sm_count;
     GemmFp8Params q = p;
     q.num_tiles = split ? p.num_tiles - rest : p.num_tiles;
     st = brows ? launch<true, true, false, false>(dev, ma, mb, mc, q, s)
