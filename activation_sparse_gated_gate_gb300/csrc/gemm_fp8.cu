@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
             }
           }
         }
-        // this round's scales are read
+        // the round's scales are read
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sempty[par]);
         par ^= 1;
