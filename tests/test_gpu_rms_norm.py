@@ -194,6 +194,18 @@ def test_backward_wide(T, D, st, gt, wt, stream):
     test_backward(T, D, st, gt, wt, stream)
 
 
+@pytest.mark.parametrize("D", [2048, 6144, 9216, 12296])
+def test_backward_over_dtotal(D):
+    # dx may be dtotal's own memory: the same values as into another
+    g = _gen(D)
+    s, dy = 2 * _randn(g, 700, D), _randn(g, 700, D).to(BF16)
+    w, dt = 1 + 0.1 * _randn(g, D), _randn(g, 700, D)
+    rstd = (s.square().mean(1) + 1e-6).rsqrt()
+    dx, dw = tw.twell_rms_norm_bwd(s, w, rstd, dy, dtotal=dt)
+    again, dw2 = tw.twell_rms_norm_bwd(s, w, rstd, dy, dtotal=dt, dx=dt)
+    assert again is dt and (dt == dx).all() and (dw == dw2).all()
+
+
 def test_backward_against_differences():
     # central differences of L = sum(c y) + sum(d total) in 64 bits, through the
     # forward's definition; a step of 1e-5 leaves about 1e-9 relative
