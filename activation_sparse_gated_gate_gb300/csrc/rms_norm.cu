@@ -715,7 +715,7 @@ extern "C" twell_status twell_rms_norm_bwd(const void* total, int32_t type, int6
   if (ld < D || lddy < D || lddx < D || (dtotal && lddt < D)) return TWELL_ERR_INVALID;
   const int se = elem_bytes(type), ge = elem_bytes(dy_type), we = elem_bytes(w_type);
   if (!elem_aligned(total, se) || !elem_aligned(dx, se) || !elem_aligned(dy, ge) ||
-      !elem_aligned(w, we) || !elem_aligned(rstd, 4) || !elem_aligned(ws, 4) ||
+      !elem_aligned(w, we) || !elem_aligned(rstd, 4) || !aligned16(ws) ||
       (dtotal && !elem_aligned(dtotal, se)))
     return TWELL_ERR_INVALID;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;

@@ -463,7 +463,7 @@ twell_status twell_rms_norm(const void* x, int32_t x_type, int64_t ldx, const vo
  *   residual, total is x);  dy [T][D] of dy_type;  dtotal, dx [T][D] of `type`
  *   (dtotal NULL: the stream ends here; dtotal may be dx itself);
  *   dw [D] fp32 (overwritten; zeros when T is 0)
- *   ws: twell_rms_norm_bwd_workspace(T, D) bytes
+ *   ws: twell_rms_norm_bwd_workspace(T, D) bytes, 16-byte aligned
  * dw is summed in a fixed order: repeated calls agree bit for bit.
  */
 twell_status twell_rms_norm_bwd(const void* total, int32_t type, int64_t ld, const void* w,

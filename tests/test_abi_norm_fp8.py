@@ -57,6 +57,12 @@ def test_norm_bwd_rejects(lib, bad):
     assert lib.twell_rms_norm_bwd(*{**BWD, **bad}.values()) == INVALID
 
 
+@pytest.mark.parametrize("off", [4, 8, 12])
+def test_norm_bwd_rejects_a_workspace_off_16_bytes(lib, off):
+    # its partial sums are stored 16 bytes at a time
+    assert lib.twell_rms_norm_bwd(*{**BWD, "ws": P + off}.values()) == INVALID
+
+
 def test_norm_bwd_workspace(lib):
     assert tw.twell_rms_norm_bwd_workspace(-1, 64) == 0
     assert tw.twell_rms_norm_bwd_workspace(4, 0) == 0
