@@ -606,6 +606,22 @@ def _vec(t, types, name, device, shape):
     _refuse(t, types, name, device, shape, "elements")
 
 
+def _word(status, device):
+    """Check a status word; returns its address."""
+    try:
+        if status.dtype is torch.int32 and status.get_device() == device and status.numel() > 0:
+            return status.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(status, torch.Tensor) or not status.is_cuda:
+        raise TypeError("status must be a CUDA tensor")
+    if status.dtype is not torch.int32:
+        raise TypeError(f"status must be torch.int32, got {status.dtype}")
+    if status.get_device() != device:
+        raise ValueError("status is on another device")
+    raise ValueError("status must have an element")
+
+
 def _refuse(t, types, name, device, shape, what):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -763,6 +779,12 @@ def twell_rms_norm_bwd(total, weight, rstd, dy, dtotal=None, dx=None, dw=None, w
             with torch.cuda.device(dev):
                 need = twell_rms_norm_bwd_workspace(T, D)
         ws = _workspace(need, device)
+    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda:
+        raise TypeError("ws must be a CUDA tensor")
+    elif ws.get_device() != dev:
+        raise ValueError("ws is on another device")
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     _run("twell_rms_norm_bwd", dev, total.data_ptr(), code, ld, weight.data_ptr(), w_type,
          rstd.data_ptr(), dy.data_ptr(), dy_type, lddy, p_dt, lddt, T, D, dx.data_ptr(), lddx,
          dw.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
@@ -887,8 +909,11 @@ def twell_gemm_fp8(a, a_scale, b, b_scale, out=None, dtype=torch.bfloat16, statu
         status = _STATUS.get(dev)
         if status is None:
             status = status_word(a.device)
+        p_status = status.data_ptr()
+    else:
+        p_status = _word(status, dev)
     _run("twell_gemm_fp8", dev, p_a, lda, a_scale.data_ptr(), p_b, ldb, b_scale.data_ptr(), block,
-         M, N, K, out.data_ptr(), c_type, ldc, status.data_ptr())
+         M, N, K, out.data_ptr(), c_type, ldc, p_status)
     return out
 
 
@@ -905,6 +930,8 @@ def twell_gate_pack_fp8(xq, x_scale, wq, w_scale, out: TwELL, z_debug=None, stat
     F = w_shape[0]
     if w_shape[1] != D or out.T != T or out.F != F:
         raise ValueError("shape mismatch: xq [T][D], wq [F][D], out of T and F")
+    if out.val.get_device() != dev:
+        raise ValueError("out is on another device")
     p_x, ldx = _operand(xq, "xq", dev, x_shape)
     p_w, ldw = _operand(wq, "wq", dev, w_shape)
     nk = (D + 127) // 128
@@ -916,5 +943,5 @@ def twell_gate_pack_fp8(xq, x_scale, wq, w_scale, out: TwELL, z_debug=None, stat
         p_z = z_debug.data_ptr()
     _run("twell_gate_pack_fp8", dev, p_x, ldx, x_scale.data_ptr(), p_w, ldw, w_scale.data_ptr(),
          T, D, F, ctypes.byref(out.struct), p_z,
-         (out.status if status is None else status).data_ptr())
+         _word(out.status if status is None else status, dev))
     return out

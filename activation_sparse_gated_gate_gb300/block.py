@@ -28,6 +28,8 @@ class Fp8GateFFN:
     def __init__(self, norm, Wg_t, Wu_t, Wd, width=8, eps=1e-6):
         if Wu_t.shape != Wg_t.shape or Wd.shape != Wg_t.shape or norm.shape != Wg_t.shape[1:]:
             raise ValueError("shape mismatch: norm [D], Wg_t, Wu_t and Wd [F][D]")
+        if any(w.device != Wg_t.device for w in (norm, Wu_t, Wd)):
+            raise ValueError("the weights are on different devices")
         self.norm, self.Wu_t, self.Wd = norm, Wu_t, Wd
         self.width, self.eps = width, eps
         gate = twell_quant_fp8(Wg_t, block_rows=128)

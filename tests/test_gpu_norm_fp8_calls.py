@@ -1,0 +1,83 @@
+"""What the norm and 8-bit calls do around their kernels: which tensors they refuse,
+whose status word they use, and the outputs that a caller hands in."""
+import pytest
+import torch
+
+import activation_sparse_gated_gate_gb300 as tw
+from _gpu import ensure_built
+from activation_sparse_gated_gate_gb300.block import Fp8GateFFN
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def _operands(g, M, N, K):
+    return tw.twell_quant_fp8(_randn(g, M, K)), tw.twell_quant_fp8(_randn(g, N, K), block_rows=128)
+
+
+# ---------------------------------------- refusals of tensors a kernel would write to
+
+
+BAD_STATUS = [
+    (lambda: torch.zeros(1, dtype=torch.int32), TypeError),                    # on the host
+    (lambda: torch.zeros(1, dtype=torch.int64, device="cuda"), TypeError),
+    (lambda: torch.zeros(1, device="cuda"), TypeError),
+    (lambda: torch.zeros(0, dtype=torch.int32, device="cuda"), ValueError),
+    (lambda: 7, TypeError)]
+
+
+@pytest.mark.parametrize("make,error", BAD_STATUS)
+def test_refuses_a_status_that_is_no_int32_word_of_the_device(make, error):
+    qa, qb = _operands(_gen(1), 16, 256, 256)
+    h = tw.TwELL(16, 256, 8)
+    with pytest.raises(error):
+        tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale, status=make())
+    with pytest.raises(error):
+        tw.twell_gate_pack_fp8(qa.q, qa.scale, qb.q, qb.scale, h, status=make())
+
+
+def test_refuses_a_twell_of_another_device():
+    qa, qb = _operands(_gen(2), 16, 256, 256)
+    with pytest.raises(ValueError):
+        tw.twell_gate_pack_fp8(qa.q, qa.scale, qb.q, qb.scale, tw.TwELL(16, 256, 8, device="cpu"))
+
+
+def test_refuses_a_workspace_it_cannot_write():
+    x, w, rstd = torch.ones((4, 64), device="cuda"), torch.ones(64, device="cuda"), \
+        torch.ones(4, device="cuda")
+    n = tw.twell_rms_norm_bwd_workspace(4, 64)
+    with pytest.raises(TypeError):
+        tw.twell_rms_norm_bwd(x, w, rstd, x, ws=torch.empty(n, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        tw.twell_rms_norm_bwd(x, w, rstd, x,
+                              ws=torch.empty((n, 2), dtype=torch.uint8, device="cuda")[:, 0])
+    wide = torch.empty(n + 16, dtype=torch.uint8, device="cuda")
+    for off in (4, 8):
+        with pytest.raises(tw.TwellError):
+            tw.twell_rms_norm_bwd(x, w, rstd, x, ws=wide[off:off + n])
+    a = tw.twell_rms_norm_bwd(x, w, rstd, x, ws=wide[16:])
+    b = tw.twell_rms_norm_bwd(x, w, rstd, x)
+    assert all((s == t).all() for s, t in zip(a, b))
+
+
+def test_block_refuses_weights_of_several_devices():
+    w, n = torch.zeros((128, 64), dtype=BF16, device="cuda"), torch.ones(64, device="cuda")
+    for bad in ((n.cpu(), w, w, w), (n, w, w.cpu(), w), (n, w, w, w.cpu())):
+        with pytest.raises(ValueError):
+            Fp8GateFFN(*bad)
