@@ -34,6 +34,8 @@ class Fp8GateFFN:
         self.width, self.eps = width, eps
         gate = twell_quant_fp8(Wg_t, block_rows=128)
         self.Wg_q, self.Wg_scale = gate.q, gate.scale
+        # of the calls that bring no TwELL of their own
+        self.status = torch.zeros((1,), dtype=torch.int32, device=Wg_t.device)
 
     def buffers(self, T):
         """The TwELL of a call of T rows; a decode loop keeps one per batch size."""
@@ -42,9 +44,17 @@ class Fp8GateFFN:
     def __call__(self, x, residual=None, h=None):
         """x [T][D] bf16 or fp32 (and the residual stream, added to it); returns
         (y [T][D] fp32, total).  ``h``: the TwELL to use (``buffers``); its status
-        word holds the call's flags."""
-        h = self.buffers(x.shape[0]) if h is None else h
+        word holds the call's flags.  Without one the call allocates its own, and
+        its flags go to the block's word (``status_flags``)."""
+        own = h is None
+        h = self.buffers(x.shape[0]) if own else h
+        status = self.status if own else h.status
         a = twell_rms_norm(x, self.norm, residual=residual, eps=self.eps, fp8=True)
-        twell_gate_pack_fp8(a.q, a.scale, self.Wg_q, self.Wg_scale, h)
-        y = twell_ffn_fwd(a.y, h, self.Wu_t, self.Wd)
+        twell_gate_pack_fp8(a.q, a.scale, self.Wg_q, self.Wg_scale, h, status=status)
+        y = twell_ffn_fwd(a.y, h, self.Wu_t, self.Wd, status=status)
         return y, (x if residual is None else a.total)
+
+    def status_flags(self) -> int:
+        """OR of the flags of every call without an ``h`` since ``status`` was last
+        zeroed (synchronises).  Zero: every y returned so far is complete."""
+        return int(self.status.item())

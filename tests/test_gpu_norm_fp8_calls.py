@@ -81,3 +81,40 @@ def test_block_refuses_weights_of_several_devices():
     for bad in ((n.cpu(), w, w, w), (n, w, w.cpu(), w), (n, w, w, w.cpu())):
         with pytest.raises(ValueError):
             Fp8GateFFN(*bad)
+
+
+# --------------------------------------------------------------- status of a call
+
+
+def _block(g, D=256, F=1024, p=0.02):
+    norm, wg = torch.ones(D, device="cuda"), _randn(g, F, D) / D ** 0.5
+    wu, wd = (_randn(g, F, D) / 16).to(BF16), (_randn(g, F, D) / 32).to(BF16)
+    return Fp8GateFFN(norm, wg - 1.0 / D ** 0.5, wu, wd)
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_block_without_buffers_keeps_the_flags(T):
+    g = _gen(T)
+    block, x = _block(g), _randn(g, T, 256)
+    y, _ = block(x)
+    assert block.status_flags() == 0
+    prev = tw.twell_gate_pack_wait_limit(5)
+    try:
+        block(x)
+        torch.cuda.synchronize()
+    finally:
+        tw.twell_gate_pack_wait_limit(prev)
+    assert block.status_flags() & tw.FLAG_TIMEOUT
+    block.status.zero_()
+    again, _ = block(x)
+    assert block.status_flags() == 0
+    assert float((again - y).abs().max()) <= 1e-5 * float(y.abs().max())
+    # with buffers of the caller's, in their own word
+    h = block.buffers(T)
+    prev = tw.twell_gate_pack_wait_limit(5)
+    try:
+        block(x, h=h)
+        torch.cuda.synchronize()
+    finally:
+        tw.twell_gate_pack_wait_limit(prev)
+    assert int(h.status.item()) & tw.FLAG_TIMEOUT and block.status_flags() == 0
