@@ -62,33 +62,38 @@ class Fp8LinearFunction(torch.autograd.Function):
     """y [T][N] = x W^T on e4m3 operands: x [T][K] and the gradient dy in blocks of
     1 x 128 along the dimension each product sums over (so both are also quantised
     transposed, for dW), W [N][K] in blocks of 128 x 128.  x and W are bf16 or
-    fp32; y has x's type, dx too, and dW is computed in fp32."""
+    fp32; y has x's type, dx too, and dW is computed in fp32.  ``status``: the
+    device int32 that the products OR their flags into (default:
+    ``status_word()``)."""
 
     @staticmethod
-    def forward(ctx, x, weight):
-        need_x, need_w = ctx.needs_input_grad
+    def forward(ctx, x, weight, status=None):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        ctx.status = status
         qx = twell_quant_fp8(x, transposed=need_w)
         qw = twell_quant_fp8(weight, block_rows=128, transposed=need_x)
         ctx.save_for_backward(qx.qt, qx.scale_t, qw.qt, qw.scale_t)
         ctx.sizes = (x.shape, weight.shape)
         ctx.types = (x.dtype, weight.dtype)
-        return twell_gemm_fp8(qx.q, qx.scale, qw.q, qw.scale, dtype=x.dtype)
+        return twell_gemm_fp8(qx.q, qx.scale, qw.q, qw.scale, dtype=x.dtype, status=status)
 
     @staticmethod
     def backward(ctx, dy):
         xt, xt_scale, wt, wt_scale = ctx.saved_tensors
-        need_x, need_w = ctx.needs_input_grad
+        need_x, need_w = ctx.needs_input_grad[:2]
         (T, K), (N, _) = ctx.sizes
         dx = dw = None
         q = twell_quant_fp8(_rows(dy), rows=need_x, transposed=need_w)
         if need_x:
-            dx = twell_gemm_fp8(q.q, q.scale, wt, wt_scale, dtype=ctx.types[0])
+            dx = twell_gemm_fp8(q.q, q.scale, wt, wt_scale, dtype=ctx.types[0],
+                                status=ctx.status)
         if need_w:
             # (a sum over no rows is not a product the kernel takes)
-            dw = (twell_gemm_fp8(q.qt, q.scale_t, xt, xt_scale, dtype=torch.float32) if T
+            dw = (twell_gemm_fp8(q.qt, q.scale_t, xt, xt_scale, dtype=torch.float32,
+                                 status=ctx.status) if T
                   else torch.zeros((N, K), dtype=torch.float32, device=dy.device))
             dw = dw.to(ctx.types[1])
-        return dx, dw
+        return dx, dw, None
 
 
 class Fp8Linear(torch.nn.Module):
@@ -98,9 +103,16 @@ class Fp8Linear(torch.nn.Module):
     def __init__(self, weight):
         super().__init__()
         self.weight = torch.nn.Parameter(weight.detach().float())
+        self.register_buffer("status", torch.zeros((1,), dtype=torch.int32, device=weight.device),
+                             persistent=False)
 
     def forward(self, x):
-        return Fp8LinearFunction.apply(x, self.weight)
+        return Fp8LinearFunction.apply(x, self.weight, self.status)
+
+    def status_flags(self) -> int:
+        """OR of the flags of the layer's products, forward and backward, since
+        ``status`` was last zeroed (synchronises)."""
+        return int(self.status.item())
 
 
 class SparseGatedFFNFunction(torch.autograd.Function):

@@ -5,6 +5,7 @@ import torch
 
 import activation_sparse_gated_gate_gb300 as tw
 from _gpu import ensure_built
+from activation_sparse_gated_gate_gb300.autograd import Fp8Linear, Fp8LinearFunction
 from activation_sparse_gated_gate_gb300.block import Fp8GateFFN
 
 pytestmark = pytest.mark.gpu
@@ -118,3 +119,25 @@ def test_block_without_buffers_keeps_the_flags(T):
     finally:
         tw.twell_gate_pack_wait_limit(prev)
     assert int(h.status.item()) & tw.FLAG_TIMEOUT and block.status_flags() == 0
+
+
+def test_linear_keeps_the_flags_of_its_products():
+    g = _gen(31)
+    lin = Fp8Linear(_randn(g, 384, 256))
+    x = _randn(g, 40, 256).requires_grad_(True)
+    shared = int(tw.status_word().item())
+    lin(x).sum().backward()
+    assert lin.status_flags() == 0 and "status" not in lin.state_dict()
+    for backward in (False, True):
+        y = lin(x)
+        prev = tw.twell_gate_pack_wait_limit(5)
+        try:
+            y.sum().backward() if backward else lin(x)
+            torch.cuda.synchronize()
+        finally:
+            tw.twell_gate_pack_wait_limit(prev)
+        assert lin.status_flags() & tw.FLAG_TIMEOUT
+        lin.status.zero_()
+    # none of it in the word that calls without a status share
+    assert int(tw.status_word().item()) == shared
+    assert Fp8LinearFunction.apply(x, lin.weight).shape == (40, 384)
