@@ -562,14 +562,18 @@ _STATUS = {}
 
 def status_word(device=None):
     """The device int32 that ``twell_gemm_fp8`` ORs its flags into when the
-    caller gives none (one per device, never cleared by the library)."""
+    caller gives none (one per device, never cleared by the library).  The first
+    call on a device makes it and synchronises the current stream."""
     device = torch.device(device if device is not None else "cuda")
     index = device.index if device.index is not None else torch.cuda.current_device()
     if index not in _STATUS:
         if torch.cuda.is_current_stream_capturing():
             # it would live in the graph's own memory
             raise RuntimeError("call status_word() before the capture begins")
-        _STATUS[index] = torch.zeros((1,), dtype=torch.int32, device=f"cuda:{index}")
+        word = torch.zeros((1,), dtype=torch.int32, device=f"cuda:{index}")
+        # zero for every stream that uses it from here on, not for this one alone
+        torch.cuda.current_stream(index).synchronize()
+        _STATUS[index] = word
     return _STATUS[index]
 
 

@@ -141,3 +141,21 @@ def test_linear_keeps_the_flags_of_its_products():
     # none of it in the word that calls without a status share
     assert int(tw.status_word().item()) == shared
     assert Fp8LinearFunction.apply(x, lin.weight).shape == (40, 384)
+
+
+def test_the_shared_status_word_is_zero_before_it_is_used(monkeypatch):
+    # first asked for on a stream with work in front of it, then written from another:
+    # the zeroing must not come after the flag
+    monkeypatch.setattr(tw, "_STATUS", {})
+    side = torch.cuda.Stream()
+    torch.zeros(1, dtype=torch.int32, device="cuda").bitwise_or_(1)  # (its kernels are loaded)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        word = tw.status_word()
+    word.bitwise_or_(tw.FLAG_TIMEOUT)
+    torch.cuda.synchronize()
+    assert int(word.item()) == tw.FLAG_TIMEOUT
+    assert tw.status_word() is word
