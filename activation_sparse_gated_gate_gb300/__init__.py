@@ -858,9 +858,10 @@ def _operand(t, name, dev, shape):
     ld = _mat(t, _E4M3, name, dev, shape)[1]
     at = t.data_ptr()
     if ld % 16 or at % 16:
-        if shape[0] != 1 or at % 16:
+        # (a slice without rows counts as contiguous, whatever it is a slice of)
+        if shape[0] > 1 or (shape[0] and at % 16):
             raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
-        ld = (shape[1] + 15) // 16 * 16  # of a single row
+        ld = (shape[1] + 15) // 16 * 16  # of a single row, or none
     return at, ld
 
 

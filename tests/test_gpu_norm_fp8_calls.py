@@ -159,3 +159,28 @@ def test_the_shared_status_word_is_zero_before_it_is_used(monkeypatch):
     torch.cuda.synchronize()
     assert int(word.item()) == tw.FLAG_TIMEOUT
     assert tw.status_word() is word
+
+
+# ------------------------------------------------------------------ empty batches
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_linear_of_an_empty_batch_with_odd_widths(dt):
+    # K = 130 and N = 300: neither a multiple of 16
+    g = _gen(41)
+    lin = Fp8Linear(_randn(g, 300, 130))
+    x = torch.empty((0, 130), dtype=dt, device="cuda", requires_grad=True)
+    y = lin(x)
+    assert y.shape == (0, 300) and y.dtype == dt
+    y.sum().backward()
+    assert x.grad.shape == (0, 130) and (lin.weight.grad == 0).all()
+
+
+def test_products_without_rows_or_columns():
+    qa, qb = _operands(_gen(42), 24, 200, 130)
+    for rows, cols in ((0, 200), (24, 0), (0, 0)):
+        c = tw.twell_gemm_fp8(qa.q[:rows], qa.scale[:rows], qb.q[:cols], qb.scale[:-(-cols // 128)])
+        assert c.shape == (rows, cols)
+    h = tw.TwELL(0, 256, 8)
+    wide = tw.twell_quant_fp8(torch.ones((256, 130), device="cuda"), block_rows=128)
+    assert tw.twell_gate_pack_fp8(qa.q[:0], qa.scale[:0], wide.q, wide.scale, h) is h
