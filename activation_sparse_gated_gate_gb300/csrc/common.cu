@@ -7,7 +7,6 @@
 namespace twell {
 
 namespace {
-constexpr int kMaxDevices = 64;
 DeviceInfo g_info[kMaxDevices];
 std::mutex g_info_mu;
 

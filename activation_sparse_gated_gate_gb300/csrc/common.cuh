@@ -11,6 +11,8 @@
 
 namespace twell {
 
+constexpr int kMaxDevices = 64;  // ordinals below it
+
 // Properties of the current device, cached per device ordinal.
 struct DeviceInfo {
   int ordinal = -1;
@@ -27,6 +29,33 @@ bool current_device(DeviceInfo* out);
 // TWELL_ERR_UNSUPPORTED (or TWELL_ERR_CUDA if it cannot be queried).
 twell_status require_sm103(DeviceInfo* info);
 
+// Whether a call succeeded.  The error of one that did not is consumed, so that a
+// later launch that asks for the last error does not take it for its own.
+inline bool cuda_ok(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
+// A number that the runtime is asked for once on each device (a static of the code
+// that needs it).  `ask` returns it, or a negative value where the question failed:
+// that is returned but not kept, and the next call asks again.
+class DeviceValue {
+ public:
+  template <typename Ask>
+  int get(const DeviceInfo& dev, Ask ask) {
+    int v = known_[dev.ordinal].load(std::memory_order_relaxed) - 1;
+    if (v < 0) {
+      v = ask();
+      if (v >= 0) known_[dev.ordinal].store(v + 1, std::memory_order_relaxed);
+    }
+    return v;
+  }
+
+ private:
+  std::atomic<int> known_[kMaxDevices] = {};  // the value + 1, 0 unknown
+};
+
 // The dynamic shared memory limit of a kernel, raised to `bytes` by the first
 // launch on each device (`set`: one bit per device, a static of the launching
 // code).  A launch that fails clears its device's bit (smem_launched), so a
@@ -35,8 +64,8 @@ template <typename K>
 bool smem_limit(K kern, int bytes, const DeviceInfo& dev, std::atomic<uint64_t>& set) {
   const uint64_t bit = 1ull << dev.ordinal;
   if (set.load(std::memory_order_relaxed) & bit) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess)
+  if (!cuda_ok(cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
     return false;
   set.fetch_or(bit, std::memory_order_relaxed);
   return true;
@@ -44,7 +73,7 @@ bool smem_limit(K kern, int bytes, const DeviceInfo& dev, std::atomic<uint64_t>&
 
 inline twell_status smem_launched(cudaError_t e, const DeviceInfo& dev,
                                   std::atomic<uint64_t>& set) {
-  if (e == cudaSuccess) return TWELL_OK;
+  if (cuda_ok(e)) return TWELL_OK;
   set.fetch_and(~(1ull << dev.ordinal), std::memory_order_relaxed);
   return TWELL_ERR_CUDA;
 }

@@ -701,14 +701,6 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
   auto kern = gemm_fp8_kernel<PAIR, BROWS, PACK, SPLIT>;
   static std::atomic<uint64_t> set{0};
   if (!smem_limit(kern, Cfg::SMEM, dev, set)) return TWELL_ERR_CUDA;
-  if (PAIR) {
-    // the register split draws on what the block starts with: never launched with less
-    static const int regs = [&] {
-      cudaFuncAttributes at;
-      return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs != kRegsStart) return TWELL_ERR_UNSUPPORTED;
-  }
   const int ctas = SPLIT ? p.split : Cfg::CTAS;
   const int most = dev.sm_count / ctas;
   const int units = SPLIT || p.num_tiles < most ? p.num_tiles : most;
@@ -730,18 +722,31 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
   return smem_launched(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, p), dev, set);
 }
 
+// Whether a pair's kernel may be launched: its register split draws on what the
+// block starts with, which must not be less.
+template <bool BROWS, bool PACK>
+bool pair_ok(const DeviceInfo& dev) {
+  static DeviceValue regs;
+  return regs.get(dev, [] {
+           cudaFuncAttributes at;
+           return cuda_ok(cudaFuncGetAttributes(
+                      &at, reinterpret_cast<const void*>(gemm_fp8_kernel<true, BROWS, PACK, false>)))
+                      ? at.numRegs
+                      : -1;
+         }) == kRegsStart;
+}
+
 // CTAs of a cluster that share a tile's K blocks: as many as let every cluster run
 // at once (the part holds 76 clusters of two of these CTAs, 36 of four and 15 of
 // eight: they have to lie within a GPC) and leave each CTA four K blocks or more.
 template <bool BROWS>
-int split_for(int64_t tiles, int32_t num_kb) {
-  static std::atomic<int> fit[3] = {{-1}, {-1}, {-1}};
+int split_for(const DeviceInfo& dev, int64_t tiles, int32_t num_kb) {
+  static DeviceValue fit[3];
   int split = 1;
   for (int i = 0; i < 3; ++i) {
     const int n = 2 << i;
     if (num_kb < 4 * n) break;
-    int have = fit[i].load(std::memory_order_relaxed);
-    if (have < 0) {
+    const int have = fit[i].get(dev, [n] {
       using Cfg = Fp8Cfg<false, BROWS, false>;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(n);
@@ -754,13 +759,15 @@ int split_for(int64_t tiles, int32_t num_kb) {
       attr.val.clusterDim.z = 1;
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
-      auto kern = gemm_fp8_kernel<false, BROWS, false, true>;
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) !=
-              cudaSuccess ||
-          cudaOccupancyMaxActiveClusters(&have, kern, &cfg) != cudaSuccess)
-        have = 0;
-      fit[i].store(have, std::memory_order_relaxed);
-    }
+      const void* kern =
+          reinterpret_cast<const void*>(gemm_fp8_kernel<false, BROWS, false, true>);
+      int clusters;
+      return cuda_ok(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          Cfg::SMEM)) &&
+                     cuda_ok(cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg))
+                 ? clusters
+                 : -1;
+    });
     if (tiles <= have) split = n;
   }
   return split;
@@ -776,10 +783,12 @@ template <bool PACK>
 twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uint8_t* b,
                  int64_t ldb, int32_t b_block, int32_t K, GemmFp8Params p, cudaStream_t s) {
   p.num_kb = static_cast<int32_t>((static_cast<int64_t>(K) + BK - 1) / BK);
+  const bool brows = !PACK && b_block == 1;
   // Pairs of CTAs on 256 x 256 tiles when they still give every SM work, tiles
   // of 128 x 128 otherwise.
   const int64_t wide_m = (static_cast<int64_t>(p.M) + 255) / 256;
-  const bool pair = 2 * wide_m * ((p.N + 255) / 256) >= dev.sm_count;
+  const bool pair = 2 * wide_m * ((p.N + 255) / 256) >= dev.sm_count &&
+                    (brows ? pair_ok<true, false>(dev) : pair_ok<false, PACK>(dev));
   const int64_t num_m = pair ? wide_m : (static_cast<int64_t>(p.M) + 127) / 128;
   p.num_n = pair ? (p.N + 255) / 256 : (p.N + 127) / 128;
   const int64_t tiles = num_m * p.num_n;
@@ -793,7 +802,6 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
   if (!PACK && p.c_vec &&
       (st = make_tmap_2d(&mc, ce, p.c, p.N, p.M, 64 / ce, 32, p.ldc * ce, 64)) != TWELL_OK)
     return st;
-  const bool brows = !PACK && b_block == 1;
   if (pair) {
     // A last round of tiles that leaves most pairs idle runs as quarters, one per
     // CTA, in a launch of its own that starts as the full rounds' CTAs leave, where K
@@ -816,8 +824,8 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
   }
   if constexpr (!PACK) {
     p.split = p.quarters ? 1
-              : brows    ? split_for<true>(p.num_tiles, p.num_kb)
-                         : split_for<false>(p.num_tiles, p.num_kb);
+              : brows    ? split_for<true>(dev, p.num_tiles, p.num_kb)
+                         : split_for<false>(dev, p.num_tiles, p.num_kb);
     if (p.split > 1)
       return brows ? launch<false, true, false, true>(dev, ma, mb, mc, p, s)
                    : launch<false, false, false, true>(dev, ma, mb, mc, p, s);
@@ -849,7 +857,8 @@ extern "C" twell_status twell_gemm_fp8(const uint8_t* a, int64_t lda, const floa
   // are so few that larger clusters share K (at 16 rows: 7.5 against 8.9 us for
   // N 8192, K 2048 with 64 tiles, but 15.9 against 9.1 for N 2048, K 8192 with 16).
   if (b_block == 128 && decode_fp8_supported(M, K) &&
-      split_for<false>((static_cast<int64_t>(M) + 127) / 128 * ((static_cast<int64_t>(N) + 127) / 128),
+      split_for<false>(dev,
+                       (static_cast<int64_t>(M) + 127) / 128 * ((static_cast<int64_t>(N) + 127) / 128),
                        static_cast<int32_t>((static_cast<int64_t>(K) + 127) / 128)) < 4)
     return launch_gemm_decode_fp8(dev, a, lda, a_scale, b, ldb, b_scale, M, N, K, c,
                                   c_type == TWELL_BF16, ldc, status_dev, gate_wait_ns(),
@@ -886,10 +895,10 @@ extern "C" twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, cons
   if (decode_fp8_supported(T, D))  // (it zeroes and stores all its counters and words itself)
     return launch_gate_decode_fp8(dev, xq, ldx, x_scale, wq, ldw, w_scale, T, D, F, out, z_debug,
                                   status_dev, gate_wait_ns(), s);
-  if (cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s) != cudaSuccess) return TWELL_ERR_CUDA;
+  if (!cuda_ok(cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s))) return TWELL_ERR_CUDA;
   const size_t words = (static_cast<size_t>(T) + BM - 1) / BM * (F / 32);
   if (out->block_bits &&
-      cudaMemsetAsync(out->block_bits, 0, words * sizeof(uint32_t), s) != cudaSuccess)
+      !cuda_ok(cudaMemsetAsync(out->block_bits, 0, words * sizeof(uint32_t), s)))
     return TWELL_ERR_CUDA;
   GemmFp8Params p{};
   p.M = T;

@@ -28,7 +28,6 @@ namespace twell {
 namespace {
 
 constexpr size_t kScratchBytes = size_t{64} << 20;  // 64 MiB
-constexpr int kMaxDevices = 64;
 
 __device__ __align__(256) uint8_t g_noalloc_scratch[kScratchBytes];
 

@@ -707,7 +707,7 @@ extern "C" twell_status twell_rms_norm_bwd(const void* total, int32_t type, int6
   twell_status st;
   if (T == 0) {  // no rows: the weight's gradient is an empty sum
     if ((st = require_sm103(&dev)) != TWELL_OK) return st;
-    return cudaMemsetAsync(dw, 0, static_cast<size_t>(D) * sizeof(float), s) == cudaSuccess
+    return cuda_ok(cudaMemsetAsync(dw, 0, static_cast<size_t>(D) * sizeof(float), s))
                ? TWELL_OK
                : TWELL_ERR_CUDA;
   }
