@@ -56,26 +56,53 @@ class DeviceValue {
   std::atomic<int> known_[kMaxDevices] = {};  // the value + 1, 0 unknown
 };
 
-// The dynamic shared memory limit of a kernel, raised to `bytes` by the first
-// launch on each device (`set`: one bit per device, a static of the launching
-// code).  A launch that fails clears its device's bit (smem_launched), so a
-// context created again after a reset is set up again by the next call.
-template <typename K>
-bool smem_limit(K kern, int bytes, const DeviceInfo& dev, std::atomic<uint64_t>& set) {
-  const uint64_t bit = 1ull << dev.ordinal;
-  if (set.load(std::memory_order_relaxed) & bit) return true;
-  if (!cuda_ok(cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
-    return false;
-  set.fetch_or(bit, std::memory_order_relaxed);
-  return true;
+inline cudaLaunchConfig_t launch_config(dim3 grid, dim3 block, size_t smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  return cfg;
 }
 
-inline twell_status smem_launched(cudaError_t e, const DeviceInfo& dev,
-                                  std::atomic<uint64_t>& set) {
-  if (cuda_ok(e)) return TWELL_OK;
-  set.fetch_and(~(1ull << dev.ordinal), std::memory_order_relaxed);
-  return TWELL_ERR_CUDA;
+// For a kernel that may start before the stream's last kernel is done and waits for
+// it by itself (ptx::grid_wait before the first use of what it wrote).  Everything
+// before that kernel is done when this one starts.
+inline cudaLaunchAttribute overlapped() {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
+// Launches a kernel that uses more dynamic shared memory than kernels may by
+// themselves: its limit is raised to `limit` before the first launch on each device
+// (`set`: one bit per device, a static of the launching code).  A context created
+// again after a reset has forgotten that, and a launch in it fails without enqueuing
+// anything: the limit is then raised again and the launch repeated.
+template <typename T>
+struct Same {
+  typedef T type;
+};
+
+template <typename... P>
+twell_status launch_large(void (*kern)(P...), int limit, const cudaLaunchConfig_t& cfg,
+                          const DeviceInfo& dev, std::atomic<uint64_t>& set,
+                          const typename Same<P>::type&... args) {
+  const uint64_t bit = 1ull << dev.ordinal;
+  const void* k = reinterpret_cast<const void*>(kern);
+  for (;;) {
+    const bool known = (set.load(std::memory_order_relaxed) & bit) != 0;
+    if (!known) {
+      if (!cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, limit)))
+        return TWELL_ERR_CUDA;
+      set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    void* at[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    if (cuda_ok(cudaLaunchKernelExC(&cfg, k, at))) return TWELL_OK;
+    set.fetch_and(~bit, std::memory_order_relaxed);
+    if (!known) return TWELL_ERR_CUDA;
+  }
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -102,24 +129,5 @@ twell_status make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inne
 twell_status make_tmap_2d(CUtensorMap* map, int elem_bytes, const void* base, uint64_t inner,
                           uint64_t outer, uint32_t box_inner, uint32_t box_outer,
                           uint64_t pitch_bytes, int swizzle);
-
-// Launches a kernel that may start before the stream's last kernel is done and
-// waits for it by itself (ptx::grid_wait before the first use of what it wrote).
-// Everything before that kernel is done when this one starts.
-template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t s, A&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
-}
 
 }  // namespace twell

@@ -665,17 +665,17 @@ twell_status launch(const DeviceInfo& dev, const void* x, int64_t ldx, const voi
   const int smem = p.region + p.xch_bytes + kBarBytes + scales + 1024;
   auto kern = gate_decode_kernel<FP8, PACK>;
   static std::atomic<uint64_t> set{0};
-  if (!smem_limit(kern, dev.max_smem_optin, dev, set)) return TWELL_ERR_CUDA;
+  cudaLaunchConfig_t cfg = launch_config(dim3(2 * p.n_t), dim3(kThreads), smem, s);
+  cudaLaunchAttribute attr = overlapped();
   if (FP8 && PACK) {
     // the spill counter is zeroed while this kernel streams W_g (16 x 2048 x 8192: 8.7 us,
     // 11.8 with a memset in front)
     zero_kernel<<<1, 32, 0, s>>>(p.spill_n);
     if (cudaGetLastError() != cudaSuccess) return TWELL_ERR_CUDA;
-    return smem_launched(launch_overlapped(kern, dim3(2 * p.n_t), dim3(kThreads), smem, s, mx, mw, p),
-                         dev, set);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
   }
-  kern<<<2 * p.n_t, kThreads, smem, s>>>(mx, mw, p);
-  return smem_launched(cudaGetLastError(), dev, set);
+  return launch_large(kern, dev.max_smem_optin, cfg, dev, set, mx, mw, p);
 }
 
 // The fields of a call that packs into `out`.

@@ -700,26 +700,20 @@ twell_status launch(const DeviceInfo& dev, const CUtensorMap& ma, const CUtensor
   static_assert(Cfg::SMEM <= 232448, "shared memory budget");
   auto kern = gemm_fp8_kernel<PAIR, BROWS, PACK, SPLIT>;
   static std::atomic<uint64_t> set{0};
-  if (!smem_limit(kern, Cfg::SMEM, dev, set)) return TWELL_ERR_CUDA;
   const int ctas = SPLIT ? p.split : Cfg::CTAS;
   const int most = dev.sm_count / ctas;
   const int units = SPLIT || p.num_tiles < most ? p.num_tiles : most;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units * ctas);
-  cfg.blockDim = dim3(Cfg::THREADS);
-  cfg.dynamicSmemBytes = Cfg::SMEM;
-  cfg.stream = s;
+  cudaLaunchConfig_t cfg = launch_config(dim3(units * ctas), dim3(Cfg::THREADS), Cfg::SMEM, s);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   // quarters start as the full rounds' CTAs leave
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1] = overlapped();
   cfg.attrs = attr;
   cfg.numAttrs = p.quarters ? 2 : 1;
-  return smem_launched(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, p), dev, set);
+  return launch_large(kern, Cfg::SMEM, cfg, dev, set, ma, mb, mc, p);
 }
 
 // Whether a pair's kernel may be launched: its register split draws on what the
@@ -748,10 +742,7 @@ int split_for(const DeviceInfo& dev, int64_t tiles, int32_t num_kb) {
     if (num_kb < 4 * n) break;
     const int have = fit[i].get(dev, [n] {
       using Cfg = Fp8Cfg<false, BROWS, false>;
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(n);
-      cfg.blockDim = dim3(Cfg::THREADS);
-      cfg.dynamicSmemBytes = Cfg::SMEM;
+      cudaLaunchConfig_t cfg = launch_config(dim3(n), dim3(Cfg::THREADS), Cfg::SMEM, nullptr);
       cudaLaunchAttribute attr;
       attr.id = cudaLaunchAttributeClusterDimension;
       attr.val.clusterDim.x = n;

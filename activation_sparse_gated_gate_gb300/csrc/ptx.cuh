@@ -559,7 +559,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
 
 // ------------------------------------------- launches that overlap the one before
 
-// The grid launched after this one with launch_overlapped may start where there
+// The grid launched after this one as overlapped() may start where there
 // is room; it waits for all of this one, and its memory, at grid_wait.
 __device__ __forceinline__ void grid_launch_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

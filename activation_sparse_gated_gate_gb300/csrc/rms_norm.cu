@@ -602,10 +602,10 @@ twell_status launch_pipe(const NormBwdParams& p, const BwdShape& b, const Device
   void (*kern)(NormBwdParams);
   if constexpr (Q > 0) kern = rms_norm_bwd_wide_kernel<ST, GT, P, Q>;
   else kern = rms_norm_bwd_pipe_kernel<ST, GT, P>;
-  if (!smem_limit(kern, dev.max_smem_optin - 1024, dev, set)) return TWELL_ERR_CUDA;
   const int per = Q > 0 ? 4 * Q * (sizeof(ST) + sizeof(GT)) : 8 * (2 * sizeof(ST) + sizeof(GT));
-  kern<<<b.grid, dim3(b.L, b.G), P * b.L * b.G * per, s>>>(p);
-  return smem_launched(cudaGetLastError(), dev, set);
+  return launch_large(kern, dev.max_smem_optin - 1024,
+                      launch_config(dim3(b.grid), dim3(b.L, b.G), P * b.L * b.G * per, s), dev,
+                      set, p);
 }
 
 template <typename ST, typename GT, bool VEC>

@@ -8,11 +8,13 @@
 namespace {
 int g_fail = 0;                      // the next calls that fail
 cudaError_t g_last = cudaSuccess;    // what cudaGetLastError would return
-int g_set = 0;                       // cudaFuncSetAttribute calls
+int g_limit = 0;                     // the kernel's shared memory limit, 0 in a new context
+int g_set = 0, g_launched = 0;       // limits set, kernels launched
+int g_args[2];                       // the arguments of the last of them
 
-cudaError_t result() {
-  if (g_fail == 0) return cudaSuccess;
-  --g_fail;
+cudaError_t result(bool ok) {
+  if (ok && g_fail == 0) return cudaSuccess;
+  if (g_fail > 0) --g_fail;
   g_last = cudaErrorInvalidValue;
   return g_last;
 }
@@ -23,9 +25,20 @@ extern "C" cudaError_t cudaGetLastError() {
   g_last = cudaSuccess;
   return e;
 }
-extern "C" cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) {
+extern "C" cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int bytes) {
   ++g_set;
-  return result();
+  const cudaError_t e = result(true);
+  if (e == cudaSuccess) g_limit = bytes;
+  return e;
+}
+extern "C" cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* cfg, const void*, void** at) {
+  const cudaError_t e = result(static_cast<int>(cfg->dynamicSmemBytes) <= g_limit);
+  if (e == cudaSuccess) {
+    ++g_launched;
+    g_args[0] = *static_cast<int*>(at[0]);
+    g_args[1] = *static_cast<char*>(at[1]);
+  }
+  return e;
 }
 
 #define CHECK(x)                                              \
@@ -36,7 +49,7 @@ extern "C" cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int)
     }                                                         \
   } while (0)
 
-void kernel() {}
+void kernel(int, char) {}
 
 void device_value() {
   using namespace twell;
@@ -60,24 +73,37 @@ void device_value() {
   CHECK(asked == 3);
 }
 
-void errors_are_consumed() {
+void launches() {
   using namespace twell;
   DeviceInfo dev;
   dev.ordinal = 3;
   std::atomic<uint64_t> set{0};
-  g_fail = 1;
-  CHECK(!smem_limit(kernel, 100000, dev, set));
-  CHECK(cudaGetLastError() == cudaSuccess && set.load() == 0);
-  CHECK(smem_limit(kernel, 100000, dev, set) && g_set == 2);
-  CHECK(smem_limit(kernel, 100000, dev, set) && g_set == 2);
+  const cudaLaunchConfig_t cfg = launch_config(dim3(1), dim3(32), 90000, nullptr);
+  const auto launch = [&] { return launch_large(kernel, 100000, cfg, dev, set, 5, 'c'); };
+  g_fail = 1;  // the limit cannot be raised
+  CHECK(launch() == TWELL_ERR_CUDA && g_launched == 0);
+  CHECK(cudaGetLastError() == cudaSuccess);  // (the error is consumed)
+  CHECK(launch() == TWELL_OK && g_launched == 1 && g_set == 2);
+  CHECK(g_args[0] == 5 && g_args[1] == 'c');
+  CHECK(launch() == TWELL_OK && g_launched == 2 && g_set == 2);  // raised once
+  g_limit = 0;                                                   // a new context
+  CHECK(launch() == TWELL_OK && g_launched == 3 && g_set == 3);
+  CHECK(cudaGetLastError() == cudaSuccess);
+  g_fail = 2;  // a launch that fails however the limit stands is not repeated for ever
+  CHECK(launch() == TWELL_ERR_CUDA && g_launched == 3);
+  CHECK(cudaGetLastError() == cudaSuccess);
+  g_fail = 3;
+  CHECK(launch() == TWELL_ERR_CUDA && g_fail == 2);  // (at the limit, not known any more)
+  g_fail = 0;
+  CHECK(launch() == TWELL_OK && g_launched == 4);
+  // an error that somebody else left behind is not this launch's
   g_last = cudaErrorInvalidValue;
-  CHECK(smem_launched(cudaErrorInvalidValue, dev, set) == TWELL_ERR_CUDA);
-  CHECK(cudaGetLastError() == cudaSuccess && set.load() == 0);
+  CHECK(launch() == TWELL_OK && g_launched == 5);
 }
 
 int main() {
   device_value();
-  errors_are_consumed();
+  launches();
   std::puts("ok");
   return 0;
 }
