@@ -75,6 +75,8 @@ constexpr int kSplitBlocks = 8, kSplitBlocksPack = 32;
 // against 385 us at 8192^3.)
 constexpr int kRegsStart = 168, kRegsEpi = 224, kRegsOther = 56;
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
+// rows of c and b: what a tile of 256 rounds up to stays in 32 bits
+constexpr int32_t kMaxRows = 0x7fffffff - 255;
 
 struct GemmFp8Params {
   int32_t M, N;
@@ -841,6 +843,7 @@ extern "C" twell_status twell_gemm_fp8(const uint8_t* a, int64_t lda, const floa
   if (!operand_ok(a, lda, K, a_scale) || !operand_ok(b, ldb, K, b_scale)) return TWELL_ERR_INVALID;
   const int ce = c_type == TWELL_BF16 ? 2 : 4;
   if (!c || ldc < N || reinterpret_cast<uintptr_t>(c) % ce != 0) return TWELL_ERR_INVALID;
+  if (M > kMaxRows || N > kMaxRows) return TWELL_ERR_UNSUPPORTED;
   DeviceInfo dev;
   twell_status st;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
@@ -880,6 +883,9 @@ extern "C" twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, cons
   if (!operand_ok(xq, ldx, D, x_scale) || !operand_ok(wq, ldw, D, w_scale))
     return TWELL_ERR_INVALID;
   if (z_debug && !aligned16(z_debug)) return TWELL_ERR_INVALID;
+  // (a spilled slice is noted by its row and tile in 32 bits)
+  if (T > kMaxRows || F > kMaxRows || static_cast<int64_t>(T) * (F / TWELL_TILE) > 0x7fffffff)
+    return TWELL_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

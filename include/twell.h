@@ -504,7 +504,8 @@ twell_status twell_quant_fp8(const void* src, int32_t type, int64_t ld, int32_t 
  *   b [N][K], b_scale [ceil(N/b_block)][ceil(K/128)], b_block 1 or 128
  *   lda, ldb  bytes between rows, multiples of 16;  a and b 16-byte aligned
  *   c [M][N] of c_type, rows ldc elements apart
- * Any M, N and K >= 1 (M or N 0: nothing to do).  Bytes past K of a row are not
+ * Any K >= 1, M and N up to 2^31 - 256 (TWELL_ERR_UNSUPPORTED above; M or N 0:
+ * nothing to do).  Bytes past K of a row are not
  * used.  A wait that runs out (twell_gate_pack_wait_limit's bound) sets
  * TWELL_FLAG_TIMEOUT in *status_dev (may be NULL), c then being undefined.
  * Repeated calls agree bit for bit.
@@ -521,8 +522,8 @@ twell_status twell_gemm_fp8(const uint8_t* a, int64_t lda, const float* a_scale,
  * it, packed into `out` in the same kernel.
  *   xq [T][D], x_scale [T][ceil(D/128)]        rows ldx bytes apart
  *   wq [F][D] (= W_g^T), w_scale [F/128][ceil(D/128)]   rows ldw bytes apart
- * Any D >= 1; the operands' alignment as in twell_gemm_fp8, the rest as in
- * twell_gate_pack.
+ * Any D >= 1; T and F as M and N of twell_gemm_fp8 and T F / 128 below 2^31; the
+ * operands' alignment as in twell_gemm_fp8, the rest as in twell_gate_pack.
  */
 twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, const float* x_scale,
                                  const uint8_t* wq, int64_t ldw, const float* w_scale, int32_t T,

@@ -105,6 +105,19 @@ def test_gemm_empty(lib):
     assert lib.twell_gemm_fp8(*{**GEMM, "N": 0, "c": None}.values()) == OK
 
 
+@pytest.mark.parametrize("big", [dict(M=2**31 - 1), dict(N=2**31 - 1, ldc=2**31),
+                                 dict(M=2**31 - 255), dict(N=2**31 - 255, ldc=2**31)])
+def test_gemm_limits(lib, big):
+    # tiles past them would not be numbered in 32 bits
+    assert lib.twell_gemm_fp8(*{**GEMM, **big}.values()) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("T,F", [(2**31 - 1, 128), (1, 2**31 - 128), (2**24, 2**14)])
+def test_gate_limits(lib, T, F):
+    s = tw.TwellStruct(T, F, 128, 8, P, P, P, P, 16, P, P, P, None)
+    assert gate(lib, s, T=T, F=F) == UNSUPPORTED
+
+
 def gate(lib, s=None, **kw):
     s = tw.TwellStruct(4, 256, 128, 8, P, P, P, P, 16, P, P, P, None) if s is None else s
     args = dict(xq=P, ldx=64, sx=P, wq=P, ldw=64, sw=P, T=4, D=64, F=256, out=ctypes.byref(s),

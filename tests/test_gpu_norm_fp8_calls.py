@@ -184,3 +184,30 @@ def test_products_without_rows_or_columns():
     h = tw.TwELL(0, 256, 8)
     wide = tw.twell_quant_fp8(torch.ones((256, 130), device="cuda"), block_rows=128)
     assert tw.twell_gate_pack_fp8(qa.q[:0], qa.scale[:0], wide.q, wide.scale, h) is h
+
+
+# --------------------------------------------------------- sizes near 32 bits' end
+
+
+@pytest.mark.parametrize("axis", [0, 1])
+def test_quant_of_2_31_rows_or_columns(axis):
+    # 2^31 - 8 of them: rounded up to whole blocks they pass 31 bits.  Every stretch as by
+    # itself
+    n, step = 2**31 - 8, 2**28
+    v = torch.empty(n, dtype=BF16, device="cuda")
+    for a in range(0, n, step):
+        v[a:a + step] = _randn(_gen(a // step), min(step, n - a)).to(BF16)
+    if axis == 0:
+        o = tw.twell_quant_fp8(v.view(n, 1), rows=False, transposed=True)
+        q, scale = o.qt, o.scale_t
+    else:
+        o = tw.twell_quant_fp8(v.view(1, n))
+        q, scale = o.q, o.scale
+    assert q.shape == (1, n) and scale.shape == (1, 2**24)
+    for a in range(0, n, step):
+        b = min(a + step, n)
+        part = tw.twell_quant_fp8(v[a:b].view(1, b - a))
+        assert (part.q.view(torch.uint8) == q[:, a:b].view(torch.uint8)).all()
+        assert (part.scale == scale[:, a // 128:-(-b // 128)]).all()
+    del v, o, q, scale
+    torch.cuda.empty_cache()
