@@ -52,8 +52,8 @@
 //
 // Waits are bounded as in the bf16 gate kernel: a role whose wait runs out sets
 // TWELL_FLAG_TIMEOUT and leaves its loop, the others' waits then run out too; the
-// CTA drains its TMA loads and MMAs before it frees the TMEM, and both CTAs of a
-// pair meet once more before either leaves.
+// CTA drains its TMA loads and stores and its MMAs before it frees the TMEM, and both
+// CTAs of a pair meet once more before either leaves.
 #include "common.cuh"
 #include "gate.cuh"
 #include "pack.cuh"
@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
   uint64_t* drain = sempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* aborted = tmem_slot + 1;
+  volatile uint32_t* peer_state = tmem_slot + 2;  // PAIR: the other CTA's fills and abort flag
+  uint32_t n_loads = 0;  // TMA stage fills issued (producer thread)
 
   if (PAIR) ptx::grid_launch_next();  // (of a last round's quarters)
   const uint32_t crank = PAIR || SPLIT ? ptx::cluster_ctarank() : 0u;
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
               ptx::tma_load_2d(a_dst, &tmap_a, &full[stage], kb * BK, m0);
               ptx::tma_load_2d(b_dst, &tmap_b, &full[stage], kb * BK, n0);
             }
+            ++n_loads;
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -631,16 +634,39 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
         }
       }
     }
-    if (!PACK && !SPLIT && lane == 0) ptx::bulk_wait_all();
   }
 
 done:
   __syncwarp();  // lanes idle during the producer / MMA loops rejoin lane 0
+  if (!PACK && !SPLIT && warp >= 4 && lane == 0) ptx::bulk_wait_all();
   ptx::tc_fence_before();
   __syncthreads();
-  if (*aborted) {  // read after the barrier: the same value in every thread
-    // the loads in flight may signal a barrier that can no longer complete
-    if (warp == 0 && lane == 0) ptx::spin_ns(1000000);
+  bool drain_it = *aborted != 0u;  // read after the barrier: the same value in every thread
+  // PAIR: the two tell each other what they issued; neither issues anything from here
+  // on, and unless there is something to drain neither uses the other's barriers or TMEM.
+  if (PAIR) {
+    if (warp == 0 && lane == 0)
+      ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(const_cast<uint32_t*>(peer_state)), crank ^ 1u),
+                          (n_loads << 1) | *aborted);
+    ptx::cluster_sync();
+    drain_it |= (*peer_state & 1u) != 0u;
+  }
+  if (drain_it) {
+    if (warp == 0 && lane == 0 && rank == 0) {
+      // the last fill of each stage: the fills went round the ring in order, so stage s
+      // got (n - s + STAGES - 1) / STAGES of them.  A pair's CTAs differ by one at
+      // most (a stage's next fill waits for MMAs that read both CTAs' last): where the
+      // other CTA's bytes will not come they are counted as arrived, where only its
+      // bytes are on their way they are all that is expected.
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t own = (n_loads + STAGES - 1 - s) / STAGES;
+        const uint32_t other = PAIR ? ((*peer_state >> 1) + STAGES - 1 - s) / STAGES : own;
+        if (own > other) ptx::mbar_complete_tx(&full[s], Cfg::STAGE_BYTES);
+        if (own < other) ptx::mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+        const uint32_t n_s = own > other ? own : other;
+        if (n_s > 0 && !ptx::mbar_wait(&full[s], (n_s - 1) & 1u)) break;
+      }
+    }
     if (warp == 1 && rank == 0 && ptx::elect_one_sync()) {
       ptx::tc_fence_after();
       // arrives once every MMA this thread issued is done
@@ -650,12 +676,11 @@ done:
     }
     __syncwarp();
     ptx::tc_fence_before();
-    __syncthreads();
+    if (PAIR) ptx::cluster_sync();
+    else __syncthreads();
   }
-  // PAIR: neither CTA's barriers or TMEM are used by the other from here on.
-  // SPLIT: every CTA's sums of the tile are in its shared memory.
-  if (PAIR || SPLIT) ptx::cluster_sync();
   if (SPLIT) {
+    ptx::cluster_sync();  // every CTA's sums of the tile are in its shared memory
     const TileAt at = tile_at<PAIR>(p, unit);
     const int left = p.M - at.m * BM, rows = left < BM ? left : BM;
     const uint32_t part = ptx::smem_u32(smem);

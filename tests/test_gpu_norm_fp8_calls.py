@@ -211,3 +211,42 @@ def test_quant_of_2_31_rows_or_columns(axis):
         assert (part.scale == scale[:, a // 128:-(-b // 128)]).all()
     del v, o, q, scale
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------- waits that run out
+
+
+FORMS = [(512, 1024, 2048, 1), (4, 1024, 2048, 128),   # a cluster per tile
+         (4, 8192, 512, 128),                          # the decode kernel
+         (300, 8192, 512, 128), (1000, 3200, 384, 1),  # a CTA per tile
+         (4096, 4096, 2048, 128), (4096, 4096, 2048, 1),  # pairs of CTAs
+         (2500, 2000, 1100, 128)]                      # and a last round of quarters
+
+
+@pytest.mark.parametrize("M,N,K,block", FORMS)
+def test_a_call_that_gives_up_drains_what_it_issued(M, N, K, block):
+    # bounds that run out at different places of the pipeline.  What is in flight then
+    # arrives, so that the call ends long before the second that each wait for it may
+    # take; the next call is right
+    g = _gen(M + N + K)
+    qa = tw.twell_quant_fp8(_randn(g, M, K))
+    qb = tw.twell_quant_fp8(_randn(g, N, K), block_rows=block)
+    want = tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gave_up = 0
+    for ns in (1, 5, 50, 200, 400, 700, 1000, 1500, 2000, 3000, 5000, 8000) * 3:
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        prev = tw.twell_gate_pack_wait_limit(ns)
+        try:
+            a.record()
+            tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale, status=st)
+            b.record()
+        finally:
+            tw.twell_gate_pack_wait_limit(prev)
+        again = tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale)
+        torch.cuda.synchronize()
+        assert a.elapsed_time(b) < 500
+        assert (again == want).all()
+        gave_up += int(st.item()) == tw.FLAG_TIMEOUT
+        st.zero_()
+    assert gave_up > 0
