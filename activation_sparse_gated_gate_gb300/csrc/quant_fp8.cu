@@ -137,8 +137,9 @@ template <typename T, bool VEC, bool SQUARE, bool TRANS>
 __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p, const bool wide_t) {
   constexpr int ROWS = SQUARE || TRANS ? 8 : 2;
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int64_t nbc = (static_cast<int64_t>(p.C) + 127) / 128,
-                nbr = (static_cast<int64_t>(p.R) + 127) / 128;
+  // (unsigned: a size within 127 of 2^31 rounds up past it)
+  const int64_t nbc = (static_cast<uint32_t>(p.C) + 127u) / 128u,
+                nbr = (static_cast<uint32_t>(p.R) + 127u) / 128u;
   const int bx = blockIdx.x % static_cast<unsigned>(nbc);  // the tile's columns and rows
   const int64_t by = blockIdx.x / static_cast<unsigned>(nbc);
   const int64_t r0 = (by * 16 + g) * ROWS;
