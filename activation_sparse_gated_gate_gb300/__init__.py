@@ -712,7 +712,7 @@ def twell_rms_norm(x, weight, residual=None, eps=1e-6, y=None, total=None, q=Non
         p_res, p_total = residual.data_ptr(), total.data_ptr()
     elif total is not None:
         raise ValueError("total is an output of the residual's addition: none is given")
-    if y is None and bf16 and (q is None or fp8):
+    if y is None and bf16:
         y = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
     if y is not None:
         ldy = _mat(y, _BF16, "y", dev, shape)[1]

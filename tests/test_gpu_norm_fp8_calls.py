@@ -250,3 +250,21 @@ def test_a_call_that_gives_up_drains_what_it_issued(M, N, K, block):
         gave_up += int(st.item()) == tw.FLAG_TIMEOUT
         st.zero_()
     assert gave_up > 0
+
+
+# --------------------------------------------------- outputs that the caller hands in
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_norm_allocates_y_when_asked_for_bf16(bf16, fp8):
+    # whether or not q and scale were given
+    x, w = _randn(_gen(51), 6, 256), torch.ones(256, device="cuda")
+    want = tw.twell_rms_norm(x, w, fp8=True)
+    q, scale = torch.empty((6, 256), dtype=E4M3, device="cuda"), torch.empty((6, 2), device="cuda")
+    o = tw.twell_rms_norm(x, w, q=q, scale=scale, bf16=bf16, fp8=fp8)
+    assert o.q is q and (q.float() == want.q.float()).all() and (scale == want.scale).all()
+    if bf16:
+        assert (o.y == want.y).all()
+    else:
+        assert o.y is None
