@@ -17,7 +17,8 @@ fp32 gradients.  The activation stream x is bf16 (its gradient too).
 
 ``AddRMSNormFunction`` is the residual addition and norm in front of an FFN
 (fused forward and backward), and ``Fp8LinearFunction`` a linear layer whose
-three products (y, dx, dW) run on e4m3 operands with block scales.
+three products (y, dx, dW) run on e4m3 operands with block scales.  Both refuse
+to be differentiated twice.
 """
 from __future__ import annotations
 
@@ -33,6 +34,27 @@ def _rows(g):
     a transposed one."""
     return g if g.stride(-1) == 1 and (g.shape[0] < 2 or g.stride(0) >= g.shape[1]) \
         else g.contiguous()
+
+
+class _Once(torch.autograd.Function):
+    """Gradients as they are, to be differentiated no further."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(None if g is None else g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("this function's gradient cannot be differentiated")
+
+
+def _once(*grads):
+    """What a backward returns.  Where it is itself being recorded (create_graph),
+    a derivative of it is refused, not left out."""
+    if not torch.is_grad_enabled():
+        return grads
+    g = next(g for g in grads if g is not None)
+    return _Once.apply(torch.empty(0, device=g.device, requires_grad=True), *grads)
 
 
 class AddRMSNormFunction(torch.autograd.Function):
@@ -55,7 +77,7 @@ class AddRMSNormFunction(torch.autograd.Function):
         if dtotal is not None:
             dtotal = _rows(dtotal)
         dx, dw = twell_rms_norm_bwd(total, weight, rstd, _rows(dy), dtotal=dtotal)
-        return (dx.to(ctx.types[0]), dw.to(ctx.types[1]), dx if ctx.added else None, None)
+        return _once(dx.to(ctx.types[0]), dw.to(ctx.types[1]), dx if ctx.added else None, None)
 
 
 class Fp8LinearFunction(torch.autograd.Function):
@@ -93,7 +115,7 @@ class Fp8LinearFunction(torch.autograd.Function):
                                  status=ctx.status) if T
                   else torch.zeros((N, K), dtype=torch.float32, device=dy.device))
             dw = dw.to(ctx.types[1])
-        return dx, dw, None
+        return _once(dx, dw, None)
 
 
 class Fp8Linear(torch.nn.Module):

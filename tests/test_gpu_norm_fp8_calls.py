@@ -5,7 +5,8 @@ import torch
 
 import activation_sparse_gated_gate_gb300 as tw
 from _gpu import ensure_built
-from activation_sparse_gated_gate_gb300.autograd import Fp8Linear, Fp8LinearFunction
+from activation_sparse_gated_gate_gb300.autograd import (AddRMSNormFunction, Fp8Linear,
+                                                         Fp8LinearFunction)
 from activation_sparse_gated_gate_gb300.block import Fp8GateFFN
 
 pytestmark = pytest.mark.gpu
@@ -268,3 +269,24 @@ def test_norm_allocates_y_when_asked_for_bf16(bf16, fp8):
         assert (o.y == want.y).all()
     else:
         assert o.y is None
+
+
+# --------------------------------------------------------------- second derivatives
+
+
+@pytest.mark.parametrize("which", ["norm", "add", "linear"])
+def test_a_second_derivative_is_refused(which):
+    # not left out: a penalty on a gradient would otherwise have no gradient itself
+    g = _gen(61)
+    x = _randn(g, 16, 128).requires_grad_(True)
+    w = torch.ones(128, device="cuda", requires_grad=True)
+    if which == "linear":
+        y = Fp8Linear(_randn(g, 256, 128))(x)
+    elif which == "add":
+        y = AddRMSNormFunction.apply(x, w, _randn(g, 16, 128), 1e-6)[0]
+    else:
+        y = AddRMSNormFunction.apply(x, w, None, 1e-6)
+    dx, = torch.autograd.grad(y.float().sum(), x, create_graph=True)
+    assert (dx == torch.autograd.grad(y.float().sum(), x, retain_graph=True)[0]).all()
+    with pytest.raises(RuntimeError, match="cannot be differentiated"):
+        (x.square().sum() + dx.square().sum()).backward()
