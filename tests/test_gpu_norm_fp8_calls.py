@@ -271,6 +271,74 @@ def test_norm_allocates_y_when_asked_for_bf16(bf16, fp8):
         assert o.y is None
 
 
+MARK = 0xA5
+
+
+def _inside(rows, cols, off, pitch):
+    """A [rows][cols] e4m3 view that starts `off` bytes into a marked buffer of that pitch,
+    and a function that tells whether a byte around it changed."""
+    buf = torch.full((rows * pitch + off + 64,), MARK, dtype=torch.uint8, device="cuda")
+    assert buf.data_ptr() % 128 == 0
+    view = buf[off:off + rows * pitch].view(rows, pitch)[:, :cols]
+
+    def changed():
+        inside = torch.zeros_like(buf, dtype=torch.bool)
+        inside[off:off + rows * pitch].view(rows, pitch)[:, :cols] = True
+        return bool((buf[~inside] != MARK).any())
+
+    return view.view(E4M3), changed
+
+
+def _same(a, b):
+    return bool((a.view(torch.uint8) == b.view(torch.uint8)).all())
+
+
+# start and pitch (beyond the columns) of the rows: on 1, 2, 4, 8 and 16 bytes
+PLACES = [(0, 0), (1, 3), (2, 2), (4, 4), (8, 0), (8, 8), (16, 5), (3, 16), (16, 16)]
+
+
+@pytest.mark.parametrize("off,more", PLACES)
+@pytest.mark.parametrize("R,C", [(5, 7), (37, 200), (130, 256), (300, 1001), (128, 392)])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_quant_into_rows_anywhere(off, more, R, C, block, dt):
+    x = _randn(_gen(R + C), R, C).to(dt)
+    want = tw.twell_quant_fp8(x, block_rows=block, transposed=True)
+    for rows, transposed in ((True, False), (False, True), (True, True)):
+        q, q_changed = _inside(R, C, off, C + more)
+        qt, qt_changed = _inside(C, R, off, R + more)
+        s, st = torch.empty_like(want.scale), torch.empty_like(want.scale_t)
+        o = tw.twell_quant_fp8(x, block_rows=block, rows=rows, transposed=transposed,
+                               out=tw.QuantFp8(q, s, qt, st))
+        if rows:
+            assert o.q.data_ptr() == q.data_ptr() and _same(q, want.q) and (s == want.scale).all()
+        if transposed:
+            assert _same(qt, want.qt) and (st == want.scale_t).all()
+        assert not q_changed() and not qt_changed()
+
+
+@pytest.mark.parametrize("off,more", PLACES)
+@pytest.mark.parametrize("T,D", [(1, 9), (5, 136), (37, 200), (64, 256), (9, 1001), (3, 8200)])
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_norm_into_e4m3_rows_anywhere(off, more, T, D, xt):
+    g = _gen(T + D)
+    x, r, w = _randn(g, T, D).to(xt), _randn(g, T, D), 1 + 0.1 * _randn(g, D)
+    want = tw.twell_rms_norm(x, w, residual=r, fp8=True)
+    q, changed = _inside(T, D, off, D + more)
+    scale = torch.empty_like(want.scale)
+    o = tw.twell_rms_norm(x, w, residual=r, q=q, scale=scale)
+    # (the row's sum is taken in another order where the rows are read element by element:
+    # y is off by (D / 2 + 8) 2^-24 either way, so e4m3 by a step where that crosses a tie)
+    tol = 2 * (D / 2 + 8) * 2.0 ** -24
+    assert ((o.scale - want.scale).abs() <= (tol + 2.0 ** -23) * want.scale).all()
+    a, b = q.float() * 1.0, want.q.float()
+    step = torch.maximum(b.abs(), a.abs()) * 2.0 ** -3
+    assert ((a - b).abs() <= torch.clamp(step, min=2.0 ** -9)).all()
+    assert ((a != b).float().mean() <= 0.01) or D < 100
+    assert (o.total == want.total).all()
+    assert not changed()
+
+
 # --------------------------------------------------------------- second derivatives
 
 
@@ -290,3 +358,30 @@ def test_a_second_derivative_is_refused(which):
     assert (dx == torch.autograd.grad(y.float().sum(), x, retain_graph=True)[0]).all()
     with pytest.raises(RuntimeError, match="cannot be differentiated"):
         (x.square().sum() + dx.square().sum()).backward()
+
+
+# -------------------------------------------- two launches, and the forms between
+
+
+@pytest.mark.parametrize("block", [1, 128])
+def test_a_product_of_two_launches_in_a_graph(block):
+    # the last round's quarters start as the launch before them leaves, in a graph too
+    g = _gen(71)
+    qa, qa2 = (tw.twell_quant_fp8(_randn(g, 2500, 1100)) for _ in range(2))
+    qb = tw.twell_quant_fp8(_randn(g, 2000, 1100), block_rows=block)
+    wants = [tw.twell_gemm_fp8(a.q, a.scale, qb.q, qb.scale) for a in (qa, qa2)]
+    a, s = tw.twell_quant_fp8(torch.zeros((2500, 1100), device="cuda"))[:2]
+    c, out = torch.empty_like(wants[0]), torch.empty_like(wants[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            c.zero_()
+            tw.twell_gemm_fp8(a, s, qb.q, qb.scale, out=c)
+            out.copy_(c)
+    for i in (0, 1, 0, 1):
+        a.view(torch.uint8).copy_((qa, qa2)[i].q.view(torch.uint8))
+        s.copy_((qa, qa2)[i].scale)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (out == wants[i]).all()
