@@ -1,12 +1,16 @@
 """What the norm and 8-bit calls do around their kernels: which tensors they refuse,
 whose status word they use, and the outputs that a caller hands in."""
+import numpy as np
 import pytest
 import torch
 
 import activation_sparse_gated_gate_gb300 as tw
-from _gpu import ensure_built
+import oracle
+from _gpu import assert_twell_equal, ensure_built, fetch_twell
+from activation_sparse_gated_gate_gb300 import autograd
 from activation_sparse_gated_gate_gb300.autograd import (AddRMSNormFunction, Fp8Linear,
-                                                         Fp8LinearFunction)
+                                                         Fp8LinearFunction, SparseFFNStack,
+                                                         SparseGatedFFNFunction)
 from activation_sparse_gated_gate_gb300.block import Fp8GateFFN
 
 pytestmark = pytest.mark.gpu
@@ -385,3 +389,92 @@ def test_a_product_of_two_launches_in_a_graph(block):
         graph.replay()
         torch.cuda.synchronize()
         assert (out == wants[i]).all()
+
+
+@pytest.mark.parametrize("tensor_cores", [True, False])
+def test_prenorm_stack_steps(tensor_cores, monkeypatch):
+    # what goes into and comes out of each layer's FFN, forward and backward, held against
+    # direct calls of the norm on the same values: bit for bit (the FFN functions have
+    # their own tests)
+    g = _gen(81)
+    T, D, F, C = 320, 128, 1024, 32
+    layers = [tuple((_randn(g, *s) * f).to(BF16) for s, f in (((F, D), D ** -0.5),) * 2
+                    + (((F, D), 0.2 * F ** -0.5),)) for _ in range(2)]
+    for wg, _, _ in layers:
+        wg[:, -1] = -1.5
+    norms = [1 + 0.05 * _randn(g, D) for _ in range(2)]
+    x = _randn(g, T, D)
+    x[:, -1] = 1.0
+    seen = []
+
+    class Seen:
+        @staticmethod
+        def apply(a, *rest):
+            at = {"a": a.detach()}
+            y = SparseGatedFFNFunction.apply(a, *rest)
+            at["y"] = y.detach()
+            a.register_hook(lambda d: at.__setitem__("da", d))
+            y.register_hook(lambda d: at.__setitem__("dy", d))
+            seen.append(at)
+            return y
+
+    monkeypatch.setattr(autograd, "SparseGatedFFNFunction", Seen)
+    args = {} if tensor_cores else {"tensor_cores": False}
+    stack = SparseFFNStack(layers, cap=C, max_dense=T, norms=norms, eps=1e-5, **args)
+    xr = x.clone().requires_grad_(True)
+    dout = _randn(g, T, D)
+    out = stack(xr)
+    out.backward(dout)
+    assert stack.status_flags() == 0 and len(seen) == 2 and stack.tc == tensor_cores
+
+    def no_bias(t):
+        t = t.clone()
+        t[:, -1] = 0.0
+        return t
+
+    w0, w1 = (n.detach() for n in stack.norms)
+    o0 = tw.twell_rms_norm(x, w0, eps=1e-5, rstd=True)
+    o1 = tw.twell_rms_norm(no_bias(seen[0]["y"]), w1, residual=x, eps=1e-5, rstd=True)
+    assert (seen[0]["a"] == o0.y).all() and (seen[1]["a"] == o1.y).all()
+    assert (out == o1.total + no_bias(seen[1]["y"])).all()
+    assert float(seen[0]["y"].abs().max()) > 0 and float(seen[1]["da"].abs().max()) > 0
+    assert (seen[1]["dy"] == no_bias(dout)).all()
+    dx1, dw1 = tw.twell_rms_norm_bwd(o1.total, w1, o1.rstd, seen[1]["da"], dtotal=dout)
+    assert (stack.norms[1].grad == dw1).all() and (seen[0]["dy"] == no_bias(dx1)).all()
+    dx0, dw0 = tw.twell_rms_norm_bwd(x, w0, o0.rstd, seen[0]["da"])
+    assert (stack.norms[0].grad == dw0).all() and (xr.grad == dx0 + dx1).all()
+    for p in (*stack.Wg, *stack.Wu, *stack.Wd):
+        assert float(p.grad.abs().max()) > 0
+
+
+# batches between a decode step and a prompt: either side of where the decode form's
+# columns for every K block end (64 tokens at 2048, 32 at 4096, 16 at 8192)
+@pytest.mark.parametrize("T,D,F", [
+    (17, 8192, 512), (16, 8192, 384), (32, 4096, 768), (33, 4096, 768), (64, 2048, 1024),
+    (65, 2048, 1024), (100, 4096, 512), (128, 2048, 2048), (129, 2304, 1152), (192, 2048, 1024),
+    (255, 2048, 1024), (512, 2304, 1152)])
+def test_gate_of_middle_batches(T, D, F):
+    # element by element: fp32 sums of exact products, off by (D + 8) 2 e sum |x w|
+    g = _gen(T + D)
+    x, w = _randn(g, T, D), _randn(g, F, D) / D ** 0.5
+    x[:, -1] = 1.0
+    w[:, -1] = -2.0                      # about 2 % active
+    qx, qw = tw.twell_quant_fp8(x), tw.twell_quant_fp8(w, block_rows=128)
+    h, z = tw.TwELL(T, F, 8), torch.empty((T, F), device="cuda")
+    tw.twell_gate_pack_fp8(qx.q, qx.scale, qw.q, qw.scale, h, z_debug=z)
+    a = qx.q.double() * qx.scale.double().repeat_interleave(128, 1)[:, :D]
+    b = qw.q.double() * qw.scale.double().repeat_interleave(128, 0)[:F].repeat_interleave(
+        128, 1)[:, :D]
+    tol = (D + 8) * 2 * 2.0 ** -24 * (a.abs() @ b.abs().t())
+    assert ((z.double() - a @ b.t()).abs() <= tol).all()
+    assert int(h.status.item()) == 0
+    assert_twell_equal(fetch_twell(h), oracle.twell_pack(z.cpu().numpy(), 128, 8))
+    act = (z > 0).cpu().numpy()
+    bits = h.block_bits.cpu().numpy().view(np.uint32)
+    for k in range((T + 127) // 128):
+        any_ = act[k * 128:(k + 1) * 128].any(0).reshape(-1, 32)
+        want = (any_.astype(np.uint64) << np.arange(32, dtype=np.uint64)).sum(1)
+        np.testing.assert_array_equal(bits[k].astype(np.uint64), want)
+    # and the general product of the same operands
+    c = tw.twell_gemm_fp8(qx.q, qx.scale, qw.q, qw.scale, dtype=F32)
+    assert ((c.double() - a @ b.t()).abs() <= tol).all()
