@@ -791,6 +791,23 @@ int split_for(const DeviceInfo& dev, int64_t tiles, int32_t num_kb) {
   return split;
 }
 
+// Whether few rows of a take the decode form: the tokens as the MMA's N, and K split
+// over a cluster of two CTAs for each 128 rows of b.  It is the faster where all its
+// clusters run at once: with the part's 76 a gate of 16 tokens, D 2048, takes 11.0
+// against 15.3 us, and a product 9.1 against 9.5; with 80 16.8 against 15.7, and 14.7
+// against 9.8.  And up to `most` rows, from where its epilogue, 16 of them a step,
+// outweighs what the split gains.  Gate, D 512, F 8192: 9.6 against 10.7 us at 128
+// tokens, 11.3 as either at 192, 12.8 against 10.4 at 256.  Product, N 8192: with K 512
+// 5.5 against 5.4 at 32 rows, 6.0 against 5.4 at 64; with K 1024 6.9 against 7.7 at 32;
+// with K 2048 8.5 against 9.3 for one row, 8.9 against 9.0 at 32, 9.6 against 9.5 at 64.
+// (In a graph, b not in L2.)
+constexpr int32_t kDecodeTokens = 128, kDecodeRows = 32;
+
+bool decode_form(const DeviceInfo& dev, int32_t M, int32_t N, int32_t K, int32_t most) {
+  return M <= most && 2 * ((static_cast<int64_t>(N) + 127) / 128) <= dev.sm_count &&
+         decode_fp8_supported(M, K);
+}
+
 // Operand checks shared by the entry points: e4m3 rows on 16-byte boundaries.
 bool operand_ok(const uint8_t* v, int64_t ld, int32_t K, const float* scale) {
   return v && scale && aligned16(v) && ld >= K && ld % 16 == 0 &&
@@ -872,10 +889,9 @@ extern "C" twell_status twell_gemm_fp8(const uint8_t* a, int64_t lda, const floa
   DeviceInfo dev;
   twell_status st;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
-  // Few rows: the tokens as the MMA's N and K split over two CTAs, unless the tiles
-  // are so few that larger clusters share K (at 16 rows: 7.5 against 8.9 us for
-  // N 8192, K 2048 with 64 tiles, but 15.9 against 9.1 for N 2048, K 8192 with 16).
-  if (b_block == 128 && decode_fp8_supported(M, K) &&
+  // Few rows: the decode form, unless the tiles are so few that larger clusters share
+  // K (16 rows, N 2048, K 8192 with 16 tiles: 15.9 against 9.1 us).
+  if (b_block == 128 && decode_form(dev, M, N, K, kDecodeRows) &&
       split_for<false>(dev,
                        (static_cast<int64_t>(M) + 127) / 128 * ((static_cast<int64_t>(N) + 127) / 128),
                        static_cast<int32_t>((static_cast<int64_t>(K) + 127) / 128)) < 4)
@@ -914,7 +930,7 @@ extern "C" twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, cons
   DeviceInfo dev;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (decode_fp8_supported(T, D))  // (it zeroes and stores all its counters and words itself)
+  if (decode_form(dev, T, F, D, kDecodeTokens))  // (it zeroes and stores all its counters and words itself)
     return launch_gate_decode_fp8(dev, xq, ldx, x_scale, wq, ldw, w_scale, T, D, F, out, z_debug,
                                   status_dev, gate_wait_ns(), s);
   if (!cuda_ok(cudaMemsetAsync(out->spill_n, 0, sizeof(int32_t), s))) return TWELL_ERR_CUDA;

@@ -478,3 +478,24 @@ def test_gate_of_middle_batches(T, D, F):
     # and the general product of the same operands
     c = tw.twell_gemm_fp8(qx.q, qx.scale, qw.q, qw.scale, dtype=F32)
     assert ((c.double() - a @ b.t()).abs() <= tol).all()
+
+
+# products and gates of few rows: either side of the decode form's rows (32, the gate's 128)
+# and of its 76 column tiles
+@pytest.mark.parametrize("M", [1, 16, 32, 33, 64])
+@pytest.mark.parametrize("N", [9728, 9729, 10240])
+@pytest.mark.parametrize("K", [300, 1024])
+def test_few_row_products_beside_the_decode_form(M, N, K):
+    qa, qb = _operands(_gen(M + N + K), M, N, K)
+    a = qa.q.double() * qa.scale.double().repeat_interleave(128, 1)[:, :K]
+    b = qb.q.double() * qb.scale.double().repeat_interleave(128, 0)[:N].repeat_interleave(
+        128, 1)[:, :K]
+    tol = (K + 8) * 2 * 2.0 ** -24 * (a.abs() @ b.abs().t())
+    c = tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale, dtype=F32)
+    assert ((c.double() - a @ b.t()).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T", [1, 128, 129])
+@pytest.mark.parametrize("F", [9728, 9856])
+def test_gates_beside_the_decode_form(T, F):
+    test_gate_of_middle_batches(T, 512, F)
