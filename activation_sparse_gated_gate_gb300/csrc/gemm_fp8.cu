@@ -108,7 +108,7 @@ struct Fp8Cfg {
   static constexpr int SETS = BN / COLS;
   static constexpr int EPI = 128 * SETS;        // epilogue threads
   static constexpr int BUFS = kTmemCols / BN;
-  static constexpr int STAGING = EPI * 128;     // 128 bytes per epilogue thread
+  static constexpr int STAGING = PACK ? 0 : EPI * 128;  // of C: 128 bytes per epilogue thread
   // scales of a round of K blocks, [K block][row], two rounds; rows padded so
   // that the lanes, along K blocks first, hit different banks
   static constexpr int ROUND = 8;
@@ -407,7 +407,6 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     // (47.9 against 44.8 us at 283 x 3424 x 15616).
     constexpr bool FRAG = PAIR && BROWS;
     const int row = FRAG ? q * 32 + (lane >> 2) : q * 32 + lane;
-    uint8_t* my_stage = staging + (threadIdx.x - 128) * 128;
     constexpr int kRound = Cfg::ROUND;
     int buf = 0, par = 0, stage = 0;
     const int& next = PAIR ? buf : stage;  // of tfull
@@ -539,8 +538,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
       if constexpr (PACK) {
         const int t = m_blk * BM + row;
         if (col0 < p.N)
-          pack_row_slice<true>(p.out, z, t, t < p.M, m_blk, col0 / TWELL_TILE, lane, row,
-                               my_stage);
+          pack_row_slice<true>(p.out, z, t, t < p.M, m_blk, col0 / TWELL_TILE, lane, row, nullptr);
       } else if constexpr (SPLIT) {
         // (every stage has been read: the last block's barrier has been seen)
 #pragma unroll
