@@ -67,8 +67,7 @@ constexpr int BM = 128;
 constexpr int BK = 128;             // e4m3 of a 128-byte row: one scale block
 constexpr int kPiece = 16;            // columns of a TMEM read
 constexpr int kTmemCols = 512;
-// K blocks from which a ragged last round is split; with packing
-constexpr int kSplitBlocks = 8, kSplitBlocksPack = 32;
+constexpr int kSplitBlocks = 8;       // K blocks from which a ragged last round is split
 // The pair kernel's 384 threads start with 168 registers each; its epilogue
 // threads take 224 and the others keep 56 (4 x 56 + 8 x 224 = 12 x 168).  (With
 // 208 and 88 nothing spills either, but the loop is scheduled less well: 403
@@ -818,7 +817,12 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
   p.num_kb = static_cast<int32_t>((static_cast<int64_t>(K) + BK - 1) / BK);
   const bool brows = !PACK && b_block == 1;
   // Pairs of CTAs on 256 x 256 tiles when they still give every SM work, tiles
-  // of 128 x 128 otherwise.
+  // of 128 x 128 otherwise.  Pairs against single CTAs, K 2048: 1024 x 4864 (76 tiles, the
+  // first with pairs) 13.2 against 13.5 us, with row scales 15.8 against 16.4, packed 19.6
+  // against 20.6; 1024 x 4608 (72) 13.3 against 13.7, and at 40 to 64 tiles pairs would gain
+  // 3 to 9 % (K 4096: 10 to 14 %), below 37 they lose to clusters over K (1536 x 1536: 12.4
+  // against 8.7).  A few tiles into a second round they lose, 1024 x 5120 (80) 20.3
+  // against 18.2, and from about 1536 x 5120 (120) they win: 20.6 against 22.6.
   const int64_t wide_m = (static_cast<int64_t>(p.M) + 255) / 256;
   const bool pair = 2 * wide_m * ((p.N + 255) / 256) >= dev.sm_count &&
                     (brows ? pair_ok<true, false>(dev) : pair_ok<false, PACK>(dev));
@@ -840,12 +844,12 @@ twell_status run(const DeviceInfo& dev, const uint8_t* a, int64_t lda, const uin
     // CTA, in a launch of its own that starts as the full rounds' CTAs leave, where K
     // is long enough to pay for it (8192 x 6144 x 1536 with 12 blocks 72.9 -> 72.3 us,
     // with 8 blocks there is no difference; started early, 8192 x 2560 x 4096 takes 71.4,
-    // else 73.5).  Packing quarters takes longer: gate 8192 x 1536 x 6144 with 12 blocks
-    // 95 us, whole 88.
+    // else 73.5).  Packed, gate 8192 x D x 6144: D 1536 86.4 -> 84.3 us, 4096 170 -> 165,
+    // 8192 317 -> 295; the most quarters at few blocks lose, 2500 x 1536 x 2560 24.3 -> 24.7.
     const int32_t pairs = dev.sm_count / 2;
     const int32_t rest = p.num_tiles % pairs;
-    const bool split = p.num_kb >= (PACK ? kSplitBlocksPack : kSplitBlocks) &&
-                       p.num_tiles > pairs && rest > 0 && 4 * rest <= dev.sm_count;
+    const bool split = p.num_kb >= kSplitBlocks && p.num_tiles > pairs && rest > 0 &&
+                       4 * rest <= dev.sm_count;
     GemmFp8Params q = p;
     q.num_tiles = split ? p.num_tiles - rest : p.num_tiles;
     st = brows ? launch<true, true, false, false>(dev, ma, mb, mc, q, s)

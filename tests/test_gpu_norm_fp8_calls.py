@@ -499,3 +499,9 @@ def test_few_row_products_beside_the_decode_form(M, N, K):
 @pytest.mark.parametrize("F", [9728, 9856])
 def test_gates_beside_the_decode_form(T, F):
     test_gate_of_middle_batches(T, 512, F)
+
+
+@pytest.mark.parametrize("T,D,F", [(2500, 1100, 2048), (2500, 1024, 2048), (2049, 1000, 2304)])
+def test_gates_with_a_ragged_last_round(T, D, F):
+    # 80 and 81 tiles of 256 x 256, from eight K blocks on with a last round of quarters
+    test_gate_of_middle_batches(T, D, F)
