@@ -414,6 +414,17 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
     const uint32_t taddr0 =
         tmem_base + static_cast<uint32_t>(set * COLS) + (static_cast<uint32_t>(q * 32) << 16);
     bool ready = false;  // the next block's barrier has been seen complete
+    // PACK, for a warp that gives up: its slices of this tile and of those it would have
+    // come to hold nothing, so that whoever reads the TwELL finds them empty
+    const auto leave_empty = [&](int tile) {
+      if constexpr (PACK) {
+        for (; tile < p.num_tiles; tile += units) {
+          const TileAt at = tile_at<PAIR>(p, tile);
+          const int t = (at.m + static_cast<int>(rank)) * BM + row, kt = at.n + set;
+          if (t < p.M && kt < p.out.n_t) p.out.cnt[static_cast<size_t>(t) * p.out.n_t + kt] = 0;
+        }
+      }
+    };
     for (int tile = unit; tile < p.num_tiles; tile += units) {
       f32x2 acc[COLS / 2];
 #pragma unroll
@@ -425,6 +436,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
             flag(p.status, TWELL_FLAG_TIMEOUT);
             *aborted = 1u;
           }
+          leave_empty(tile);
           goto done;
         }
         const float* as = a_sc + par * kRound * Cfg::A_PITCH + row;
@@ -440,6 +452,7 @@ __global__ void __launch_bounds__(Fp8Cfg<PAIR, BROWS, PACK>::THREADS, 1)
               flag(p.status, TWELL_FLAG_TIMEOUT);
               *aborted = 1u;
             }
+            leave_empty(tile);
             goto done;
           }
           ptx::tc_fence_after();

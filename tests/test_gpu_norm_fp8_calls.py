@@ -505,3 +505,50 @@ def test_gates_beside_the_decode_form(T, F):
 def test_gates_with_a_ragged_last_round(T, D, F):
     # 80 and 81 tiles of 256 x 256, from eight K blocks on with a last round of quarters
     test_gate_of_middle_batches(T, D, F)
+
+
+# ------------------------------------------------- a gate that gave up leaves no garbage
+
+
+def _gate_call(T, D, F, fp8):
+    g = _gen(T + D + F)
+    x, w = _randn(g, T, D), _randn(g, F, D) / D ** 0.5
+    x[:, -1] = 1.0
+    w[:, -1] = -1.0
+    if fp8:
+        qx, qw = tw.twell_quant_fp8(x), tw.twell_quant_fp8(w, block_rows=128)
+        return lambda h: tw.twell_gate_pack_fp8(qx.q, qx.scale, qw.q, qw.scale, h)
+    x, w = x.to(BF16), w.to(BF16)
+    return lambda h: tw.twell_gate_pack(x, w, h)
+
+
+def _counts_hold(call, T, F):
+    h = tw.TwELL(T, F, 8)
+    call(h)
+    good = h.cnt.clone()
+    assert int(h.status.item()) == 0
+    gave_up = 0
+    for ns in (1, 5, 100, 500, 1000, 2000, 4000, 8000):
+        h.cnt.fill_(255)        # what memory that was never written may hold
+        h.spill_slot.fill_(1 << 30)
+        h.status.zero_()
+        prev = tw.twell_gate_pack_wait_limit(ns)
+        try:
+            call(h)
+            torch.cuda.synchronize()
+        finally:
+            tw.twell_gate_pack_wait_limit(prev)
+        flags, n = int(h.status.item()), int(h.spill_n.item())
+        gave_up += flags == tw.FLAG_TIMEOUT
+        assert flags in (0, tw.FLAG_TIMEOUT)
+        assert ((h.cnt == good) | (h.cnt == 0)).all()
+        spilled = h.spill_slot[h.cnt.int() > 8]
+        assert ((spilled >= 0) & (spilled < n)).all()
+    assert gave_up > 0
+
+
+@pytest.mark.parametrize("T,D,F", [(16, 2048, 1024), (300, 2048, 1024), (4096, 512, 4096),
+                                   (2500, 2048, 2048)])
+def test_a_gate_that_gives_up_counts_only_what_it_packed(T, D, F):
+    # whoever reads the TwELL next finds the slices that were not packed empty
+    _counts_hold(_gate_call(T, D, F, True), T, F)
