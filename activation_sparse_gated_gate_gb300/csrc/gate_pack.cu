@@ -213,6 +213,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           flag(p.status, TWELL_FLAG_TIMEOUT);
           *aborted = 1u;
         }
+        // this warp's slices of this tile and of those it would have come to hold
+        // nothing, so that whoever reads the TwELL finds them empty
+        for (int rest = tile; rest < p.num_tiles; rest += gridDim.x) {
+          const int t = rest / p.num_n * BM + row;
+          const int kt0 = rest % p.num_n * (BN / TWELL_TILE);
+          for (int kt = kt0; kt < kt0 + BN / TWELL_TILE && kt < p.out.n_t && t < p.T; ++kt)
+            p.out.cnt[static_cast<size_t>(t) * p.out.n_t + kt] = 0;
+        }
         goto done;
       }
       ptx::tc_fence_after();

@@ -157,11 +157,12 @@ twell_status twell_ffn_decode(const uint16_t* x, const uint16_t* Wg_t, const uin
 
 /*
  * Bound, in nanoseconds, on each pipeline wait of the kernels launched by
- * later twell_gate_pack, twell_gate_pack_fp8 and twell_gemm_fp8 calls (process-wide; 0 restores the default of
- * 1e9 ns); returns the previous bound.  A wait that runs out sets
- * TWELL_FLAG_TIMEOUT; the kernel then waits (up to 1 s each) for the TMA
- * loads and MMAs it already issued, frees its tensor memory and returns, so
- * the context stays usable and the TwELL of that call is undefined.  Meant
+ * later twell_gate_pack, twell_gate_pack_fp8 and twell_gemm_fp8 calls
+ * (process-wide; 0 restores the default of 1e9 ns); returns the previous
+ * bound.  A wait that runs out sets TWELL_FLAG_TIMEOUT; the kernel then waits
+ * (up to 1 s each) for the TMA loads and MMAs it already issued, frees its
+ * tensor memory and returns, so the context stays usable.  The slices of the
+ * TwELL that were not packed are then empty (count 0).  Meant
  * for exercising that path (the paper has no counterpart); a bound of a
  * few nanoseconds makes every call time out.
  */

@@ -552,3 +552,9 @@ def _counts_hold(call, T, F):
 def test_a_gate_that_gives_up_counts_only_what_it_packed(T, D, F):
     # whoever reads the TwELL next finds the slices that were not packed empty
     _counts_hold(_gate_call(T, D, F, True), T, F)
+
+
+@pytest.mark.parametrize("T,D,F", [(16, 2048, 1024), (300, 2048, 1024), (200, 64, 1024),
+                                   (4096, 512, 4096)])
+def test_a_bf16_gate_that_gives_up_counts_only_what_it_packed(T, D, F):
+    _counts_hold(_gate_call(T, D, F, False), T, F)
