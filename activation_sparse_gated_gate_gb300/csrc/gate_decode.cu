@@ -39,8 +39,8 @@
 // 128-byte rows, and its MMAs go to N TMEM columns of their own (all of a CTA's
 // K blocks fit: that bounds the tokens this form takes); whoever reads a chunk's
 // sums adds the blocks' columns, scaled, in fp32.  Without PACK the sums are the
-// result, stored as a row of C per token (4 x 8192 x 2048: 7.2 us, 16.9 MB; 4.5 of it
-// are the prologue and the exchange).
+// result, stored as a row of C per token (4 x 8192 x 2048: 7.2 us with W in L2, 8.6 from
+// HBM, 16.9 MB; 4.5 of it are the prologue and the exchange).
 // Roles per CTA: warp 0 TMA producer, warp 1 TMEM allocation and MMA issue,
 // warps 2-9 epilogue (warp w reads TMEM lanes 32 (w mod 4) .. + 31).
 //

@@ -483,7 +483,8 @@ size_t twell_rms_norm_bwd_workspace(int32_t T, int32_t D);
  * elements, block_rows 1 (activations, gradients) or 128 (weights):
  *   amax = max(max |v| over the block, 2^-64),
  *   q = e4m3(v (448 / amax)) (nearest, ties to even),  scale = amax / 448,
- * so that v is about q scale.  A NaN becomes e4m3's NaN and does not enter
+ * so that v is about q scale.  448 / amax and its product with v are rounded to
+ * fp32: what is a tie in exact arithmetic only may go either way.  A NaN becomes e4m3's NaN and does not enter
  * the block's maximum; infinities give an infinite scale and NaN.
  *   src       [R][C] of `type`, rows ld elements apart
  *   q, scale  [R][C] (rows ldq bytes apart), [ceil(R/block_rows)][ceil(C/128)]
