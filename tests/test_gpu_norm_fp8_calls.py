@@ -558,3 +558,44 @@ def test_a_gate_that_gives_up_counts_only_what_it_packed(T, D, F):
                                    (4096, 512, 4096)])
 def test_a_bf16_gate_that_gives_up_counts_only_what_it_packed(T, D, F):
     _counts_hold(_gate_call(T, D, F, False), T, F)
+
+
+# ------------------------------------------------------- more than 2^31 elements
+
+
+def test_norm_of_more_than_2_31_elements():
+    # the last rows as by themselves
+    T, D = 270_000, 8192
+    x = torch.empty((T, D), dtype=BF16, device="cuda")
+    for a in range(0, T, 90_000):
+        x[a:a + 90_000] = torch.randn((90_000, D), generator=_gen(a), device="cuda", dtype=F32).to(BF16)
+    w = 1 + 0.1 * _randn(_gen(1), D)
+    o = tw.twell_rms_norm(x, w, residual=x, fp8=True, rstd=True)
+    dx, _ = tw.twell_rms_norm_bwd(o.total, w, o.rstd, o.y, dtotal=x)
+    for rows in (slice(0, 3), slice(262_140, 262_150), slice(T - 3, T)):
+        p = tw.twell_rms_norm(x[rows], w, residual=x[rows], fp8=True, rstd=True)
+        assert (o.y[rows] == p.y).all() and (o.total[rows] == p.total).all()
+        assert _same(o.q[rows], p.q) and (o.scale[rows] == p.scale).all()
+        d, _ = tw.twell_rms_norm_bwd(p.total, w, p.rstd, p.y, dtotal=x[rows])
+        assert (dx[rows] == d).all()
+    q = tw.twell_quant_fp8(x, transposed=True)
+    part = tw.twell_quant_fp8(x[T - 1000:])
+    assert _same(q.q[T - 1000:], part.q) and (q.scale[T - 1000:] == part.scale).all()
+    first = (T - 1000 + 127) // 128 * 128                       # whole blocks of 128 rows
+    part = tw.twell_quant_fp8(x[first:], rows=False, transposed=True)
+    assert _same(q.qt[:, first:], part.qt) and (q.scale_t[:, first // 128:] == part.scale_t).all()
+    del x, o, dx, q
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_product_of_more_than_2_31_elements(dt):
+    # one block of K: the sums are the same in every form
+    M, N, K = 68_000, 32_768, 128
+    qa, qb = _operands(_gen(91), M, N, K)
+    c = tw.twell_gemm_fp8(qa.q, qa.scale, qb.q, qb.scale, dtype=dt)
+    for rows in (slice(0, 300), slice(65_530, 65_560), slice(M - 200, M)):
+        p = tw.twell_gemm_fp8(qa.q[rows], qa.scale[rows], qb.q, qb.scale, dtype=dt)
+        assert (c[rows] == p).all()
+    del c
+    torch.cuda.empty_cache()
