@@ -31,6 +31,7 @@ __all__ = [
     "RmsNorm", "twell_rms_norm", "twell_rms_norm_bwd", "twell_rms_norm_bwd_workspace",
     "QuantFp8", "twell_quant_fp8", "twell_gemm_fp8", "twell_gate_pack_fp8", "status_word",
     "FP8_BLOCK",
+    "Int4", "twell_quant_int4", "twell_dequant_int4", "twell_gemv_int4", "INT4_BLOCK",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,6 +44,7 @@ FLAG_TIMEOUT = 4
 FLAG_RANGE = 8
 FLAG_BOUNDS = 16
 FP8_BLOCK = 128
+INT4_BLOCK = 128
 
 c_i32 = ctypes.c_int32
 c_i64 = ctypes.c_int64
@@ -67,6 +69,12 @@ class HybridStruct(ctypes.Structure):
         ("ell_val", c_ptr), ("ell_col", c_ptr), ("ell_cnt", c_ptr), ("dense_rows", c_ptr),
         ("dense_h", c_ptr),
     ]
+
+
+class Int4Struct(ctypes.Structure):
+    """Mirror of ``twell_int4_t``."""
+    _fields_ = [("rows", c_i64), ("K", c_i32), ("group", c_i32), ("code", c_ptr),
+                ("scale", c_ptr), ("zero", c_ptr)]
 
 
 class TwellError(RuntimeError):
@@ -118,6 +126,10 @@ _SIGNATURES = {
                                c_i32, c_ptr, c_i32, c_i64, c_ptr, c_ptr]),
     "twell_gate_pack_fp8": (c_i32, [c_ptr, c_i64, c_ptr, c_ptr, c_i64, c_ptr, c_i32, c_i32, c_i32,
                                     ctypes.POINTER(TwellStruct), c_ptr, c_ptr, c_ptr]),
+    "twell_quant_int4": (c_i32, [c_ptr, c_i32, c_i64, ctypes.POINTER(Int4Struct), c_ptr]),
+    "twell_dequant_int4": (c_i32, [ctypes.POINTER(Int4Struct), c_ptr, c_i32, c_i64, c_ptr]),
+    "twell_gemv_int4": (c_i32, [c_ptr, c_i64, ctypes.POINTER(Int4Struct), c_i32, c_ptr, c_i32,
+                                c_i64, c_ptr]),
     "twell_status_string": (ctypes.c_char_p, [c_i32]),
     "twell_gate_pack_wait_limit": (ctypes.c_uint64, [ctypes.c_uint64]),
     "twell_probe_fma": (c_i32, [c_i32, c_i32, c_ptr, ctypes.c_size_t,
@@ -949,4 +961,186 @@ def twell_gate_pack_fp8(xq, x_scale, wq, w_scale, out: TwELL, z_debug=None, stat
     _run("twell_gate_pack_fp8", dev, p_x, ldx, x_scale.data_ptr(), p_w, ldw, w_scale.data_ptr(),
          T, D, F, ctypes.byref(out.struct), p_z,
          _word(out.status if status is None else status, dev))
+    return out
+
+
+# ------------------------------------------- weights in 4 bits
+
+_U8 = {torch.uint8: 0}
+
+
+class Int4(NamedTuple):
+    """Weights [..., K] in 4 bits: (code - zero) * scale with a bf16 scale (and a zero
+    point, where ``zero`` is given: 8 otherwise) for each ``group`` columns of a row.
+    ``code`` [..., 64 ceil(K/128)] uint8, ``scale`` and ``zero`` (uint8) [..., G] with G
+    the groups of whole blocks of 128 columns; the order of the codes is in
+    ``include/twell.h``, and ``Int4.of_codes`` brings a checkpoint's codes into it."""
+    code: torch.Tensor
+    scale: torch.Tensor
+    zero: torch.Tensor | None
+    K: int
+    group: int
+
+    @property
+    def shape(self):
+        return (*self.code.shape[:-1], self.K)
+
+    @classmethod
+    def of_codes(cls, codes, scale, zero=None, group=128):
+        """From codes [..., K] (integers 0..15), scales [..., ceil(K/group)] and zero points
+        of the same shape: laid out once, as a checkpoint is loaded."""
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        *lead, K = codes.shape
+        n, nb = -(-K // group), -(-K // INT4_BLOCK)
+        if K < 1 or scale.shape != (*lead, n) or (zero is not None and zero.shape != scale.shape):
+            raise ValueError("codes are [..., K], scale and zero [..., ceil(K/group)]")
+        if codes.numel() and not 0 <= int(codes.min()) <= int(codes.max()) <= 15:
+            raise ValueError("codes must be 0..15")
+        if zero is not None and zero.numel() and not 0 <= int(zero.min()) <= int(zero.max()) <= 15:
+            raise ValueError("zero points must be 0..15")
+        full = torch.full((*lead, nb * INT4_BLOCK), 8, dtype=torch.uint8, device=codes.device)
+        full[..., :K] = codes
+        # column 32 i + 8 c + 2 n + o: (i, c, n, o) -> (c, o, i, n), two nibbles a byte
+        at = full.view(*lead, nb, 4, 4, 4, 2).movedim((-3, -1, -4, -2), (-4, -3, -2, -1))
+        code = (at[..., 0::2] | at[..., 1::2] << 4).reshape(*lead, nb * 64)
+
+        def held(v, fill, dtype):
+            out = torch.full((*lead, nb * (INT4_BLOCK // group)), fill, dtype=dtype,
+                             device=codes.device)
+            out[..., :n] = v
+            return out
+
+        return cls(code, held(scale, 0, torch.bfloat16),
+                   None if zero is None else held(zero, 8, torch.uint8), K, group)
+
+    def codes(self):
+        """The codes [..., K] in the columns' order (uint8)."""
+        lead, nb = self.code.shape[:-1], self.code.shape[-1] // 64
+        at = torch.stack((self.code & 15, self.code >> 4), -1).view(*lead, nb, 4, 2, 4, 4)
+        at = at.movedim((-4, -3, -2, -1), (-3, -1, -4, -2))
+        return at.reshape(*lead, nb * INT4_BLOCK)[..., :self.K].contiguous()
+
+
+def _int4(w, name, dev=None, lead=None):
+    """Check 4-bit weights; returns (descriptor, device)."""
+    try:
+        code, scale, zero, K, group = w
+        if dev is None:
+            dev = code.get_device()
+        nb = (K + 127) // 128
+        rows = code.shape[:-1]
+        held = (*rows, nb * (128 // group))
+        if (group in (32, 64, 128) and K > 0 and dev >= 0 and code.dtype is torch.uint8
+                and code.shape[-1] == 64 * nb and len(rows) > 0 and (lead is None or rows == lead)
+                and code.get_device() == dev == scale.get_device() and code.is_contiguous()
+                and scale.dtype is torch.bfloat16 and scale.shape == held
+                and scale.is_contiguous()
+                and (zero is None or (zero.dtype is torch.uint8 and zero.shape == held
+                                      and zero.get_device() == dev and zero.is_contiguous()))):
+            n = 1
+            for r in rows:
+                n *= r
+            return Int4Struct(n, K, group, code.data_ptr(), scale.data_ptr(),
+                              None if zero is None else zero.data_ptr()), dev
+    except (AttributeError, IndexError, TypeError, ValueError):
+        pass
+    if not isinstance(w, Int4):
+        raise TypeError(f"{name} must be an Int4")
+    if not isinstance(w.code, torch.Tensor) or not w.code.is_cuda:
+        raise TypeError(f"{name}'s code must be a CUDA tensor")
+    if w.group not in (32, 64, 128):
+        raise ValueError(f"{name}'s group must be 32, 64 or 128")
+    if not isinstance(w.K, int) or w.K < 1:
+        raise ValueError(f"{name}'s K must be a positive number of columns")
+    dev = w.code.get_device() if dev is None else dev
+    nb, rows = (w.K + 127) // 128, w.code.shape[:-1]
+    if len(rows) < 1 or (lead is not None and rows != lead):
+        raise ValueError(f"{name} is of {tuple(rows)} rows"
+                         + (f", not {tuple(lead)}" if lead is not None else ""))
+    held = (*rows, nb * (128 // w.group))
+    _vec(w.code, _U8, f"{name}'s code", dev, (*rows, 64 * nb))
+    _vec(w.scale, _BF16, f"{name}'s scale", dev, held)
+    if w.zero is not None:
+        _vec(w.zero, _U8, f"{name}'s zero", dev, held)
+    raise TypeError(f"{name} is not an Int4 of CUDA tensors")
+
+
+def twell_quant_int4(w, group=128, zero_points=False, out=None, stream=None) -> Int4:
+    """4-bit form of weights [..., K] (bf16 or fp32, rows contiguous; a matrix's rows may
+    be apart) with a bf16 scale for each ``group`` (32, 64 or 128) columns of a row, and
+    with ``zero_points`` an integer that stands for zero.  ``out``: an Int4 of an earlier
+    call of the same kind to write into."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_quant_int4(w, group, zero_points, out)
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    if not isinstance(w, torch.Tensor) or not w.is_cuda:
+        raise TypeError("w must be a CUDA tensor")
+    if w.dim() < 2 or w.shape[-1] < 1:
+        raise ValueError(f"w must be [..., K] with K >= 1, got {tuple(w.shape)}")
+    dev, lead, K = w.get_device(), w.shape[:-1], w.shape[-1]
+    if w.dim() == 2:
+        w_type, ld = _mat(w, _TYPES, "w", dev, w.shape)
+    else:
+        w_type, ld = _vec(w, _TYPES, "w", dev, w.shape), K
+    if out is None:
+        nb = -(-K // 128)
+        held = (*lead, nb * (128 // group))
+        out = Int4(torch.empty((*lead, 64 * nb), dtype=torch.uint8, device=w.device),
+                   torch.empty(held, dtype=torch.bfloat16, device=w.device),
+                   torch.empty(held, dtype=torch.uint8, device=w.device) if zero_points else None,
+                   K, group)
+    elif out.K != K or out.group != group or (out.zero is not None) != bool(zero_points):
+        raise ValueError("out is of another kind: K, group and zero points are the call's")
+    desc, _ = _int4(out, "out", dev, lead)
+    _run("twell_quant_int4", dev, w.data_ptr(), w_type, ld, ctypes.byref(desc))
+    return out
+
+
+def twell_dequant_int4(w: Int4, out=None, dtype=torch.bfloat16, stream=None):
+    """The values [..., K] that 4-bit weights stand for, in bf16 or fp32 (``dtype`` where
+    ``out`` is not given): the operand of a product of many rows."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_dequant_int4(w, out, dtype)
+    desc, dev = _int4(w, "w")
+    shape = (*w.code.shape[:-1], w.K)
+    ld = w.K
+    if out is None:
+        if dtype not in _TYPES:
+            raise TypeError(f"dtype must be bf16 or fp32, got {dtype}")
+        out = torch.empty(shape, dtype=dtype, device=w.code.device)
+        code = _TYPES[dtype]
+    elif len(shape) == 2:
+        code, ld = _mat(out, _TYPES, "out", dev, shape)
+    else:
+        code = _vec(out, _TYPES, "out", dev, shape)
+    _run("twell_dequant_int4", dev, ctypes.byref(desc), out.data_ptr(), code, ld)
+    return out
+
+
+def twell_gemv_int4(x, w: Int4, out=None, dtype=torch.bfloat16, stream=None):
+    """out [T][N] = x w^T for a few rows x [T][K] bf16 and 4-bit weights w [N][K], bf16 or
+    fp32 (``dtype`` where not given).  Every 64 rows of x read w once."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_gemv_int4(x, w, out, dtype)
+    dev, shape = _first(x, "x")
+    T, K = shape
+    ldx = _mat(x, _BF16, "x", dev, shape)[1]
+    desc, _ = _int4(w, "w", dev)
+    if len(w.code.shape) != 2 or w.K != K:
+        raise ValueError(f"w must be [N][{K}], got {w.shape}")
+    N = w.code.shape[0]
+    if out is None:
+        if dtype not in _TYPES:
+            raise TypeError(f"dtype must be bf16 or fp32, got {dtype}")
+        out = torch.empty((T, N), dtype=dtype, device=x.device)
+        y_type, ldy = _TYPES[dtype], N
+    else:
+        y_type, ldy = _mat(out, _TYPES, "out", dev, (T, N))
+    _run("twell_gemv_int4", dev, x.data_ptr(), ldx, ctypes.byref(desc), T, out.data_ptr(), y_type,
+         ldy)
     return out

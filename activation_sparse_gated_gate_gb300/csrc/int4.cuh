@@ -1,0 +1,89 @@
+// Weights in 4 bits with a scale (and a zero point) for each group of a row, and the
+// tensor-core products of a few rows of activations with them or with bf16 weights.
+//
+// A row of K weights is stored in blocks of 128 columns, 64 bytes each.  Column
+// 32 i + 8 c + 2 n + o of a block (i, c, n < 4, o < 2) is nibble n of the 16 bits at
+// byte 8 (2 c + o) + 2 i.  What this order is for:
+//   * lane c of four reads 16 bytes of a row and has the eight columns 8 c .. 8 c + 7 of
+//     every 32, so that the four lanes' share of an m16n8k16 product always lies in one
+//     group of 32, whatever the group's size, and the columns' order is the one of the
+//     activations as they lie in memory;
+//   * lane g of eight reads 8 bytes (or 4) of a row and has four columns of every 32: the
+//     transposed product (a sum over rows) has its 16 outputs in one group as well.
+// A 4-bit code becomes a bf16 without a conversion: 0x4300 | code is 128 + code, and
+// subtracting 128 + zero is exact.  Products of bf16 and such integers are exact in the
+// tensor core's fp32 sums; the group's scale multiplies the group's sum in fp32.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace twell {
+
+constexpr int kInt4Block = 128;  // columns of a stored block
+constexpr int kInt4Bytes = 64;   // its bytes
+
+// A matrix of 4-bit rows as the kernels see it.
+struct Int4View {
+  const uint8_t* code;
+  const uint16_t* scale;
+  const uint8_t* zero;  // optional
+  int64_t pitch;        // bytes of a row
+  int32_t held;         // groups of a row, those behind K of the last block included
+};
+
+inline Int4View view_of(const twell_int4_t& w) {
+  const int32_t nb = static_cast<int32_t>((static_cast<int64_t>(w.K) + kInt4Block - 1) / kInt4Block);
+  return Int4View{w.code, w.scale, w.zero, static_cast<int64_t>(nb) * kInt4Bytes,
+                  nb * (kInt4Block / w.group)};
+}
+
+// TWELL_OK if the descriptor may be used (its rows may be none).
+inline twell_status check_int4(const twell_int4_t* w) {
+  if (!w || w->rows < 0 || w->K < 1) return TWELL_ERR_INVALID;
+  if (w->group != 32 && w->group != 64 && w->group != 128) return TWELL_ERR_INVALID;
+  if (w->rows == 0) return TWELL_OK;
+  if (!w->code || !w->scale || !aligned16(w->code) ||
+      reinterpret_cast<uintptr_t>(w->scale) % 2 != 0)
+    return TWELL_ERR_INVALID;
+  return TWELL_OK;
+}
+
+// Reads of what is used once: weights pass the first cache by.
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  return __ldg(static_cast<const uint4*>(p));
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Of eight nibbles, those n and n + 4 (the halves' n-th) as bf16 less `bias`, which
+// holds 128 + zero in each half.
+__device__ __forceinline__ uint32_t nibbles(uint32_t p, int n, uint32_t bias) {
+  return sub_bf16x2(((p >> (4 * n)) & 0x000f000fu) | 0x43004300u, bias);
+}
+
+constexpr uint32_t kMiddle = 0x43084308u;  // the bias of codes without zero points
+
+// d += a b of a 16 x 16 and a 16 x 8 tile.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+}  // namespace twell

@@ -1,0 +1,385 @@
+// Quantisation of weights to 4 bits with a scale (and a zero point) for each group of 32,
+// 64 or 128 columns of a row, and the values that such weights stand for.
+//
+// Without zero points   s = bf16(max |v| / 7),  code = clamp(rint(v / s), -8, 7) + 8;
+// with them, lo = min(v, 0) and hi = max(v, 0) over the group,
+//   s = bf16((hi - lo) / 15),  z = clamp(rint(-lo / s), 0, 15),
+//   code = clamp(rint(v / s) + z, 0, 15).
+// rint is of the exact quotient, ties to even: v times 1 / s in fp32 gives a code that is
+// at most one off, and the remainder v - code s, exact in one fused operation, says
+// which (an IEEE division for each value would double the kernel's instructions).
+// The stored order is int4.cuh's.
+//
+// Bound by memory.  Half a warp takes a block of 128 columns of a row, 16 bytes (bf16)
+// or 32 a lane; a group's maximum is taken over its 4, 8 or 16 lanes; a lane's eight
+// codes are two runs of 16 bits, which a pair of lanes exchanges into words.  Rows off 16-byte
+// boundaries: a warp a block, lane l with columns l, l + 32, l + 64, l + 96.
+#include "common.cuh"
+#include "int4.cuh"
+#include "vec.cuh"
+
+namespace twell {
+namespace {
+
+constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer
+constexpr float kSmall = 7.88860905e-31f, kLift = 1.2676506e30f;  // 2^-100, 2^100
+
+struct Scale {
+  float s, inv, half;  // the scale (lifted where it is small), about 1 / s, s / 2
+  float zero;          // the zero point
+  uint16_t stored;
+  bool none;           // a scale of zero or NaN: every code is the zero point
+  bool small;
+};
+
+template <bool ZERO>
+__device__ __forceinline__ float code_of(float v, const Scale& k) {
+  const float t = fmaf(v, k.inv, kMagic);
+  float q = t - kMagic;
+  const float r = fmaf(-q, k.s, v);
+  if (fabsf(r) >= k.half && (fabsf(r) > k.half || (__float_as_uint(t) & 1u)))
+    q += copysignf(1.0f, r);
+  return ZERO ? fminf(fmaxf(q + k.zero, 0.0f), 15.0f) : fminf(fmaxf(q, -8.0f), 7.0f) + 8.0f;
+}
+
+// From a group's largest |v| (as its bits, above infinity's where there is a NaN), and its
+// least and largest value.
+template <bool ZERO>
+__device__ __forceinline__ Scale scale_of(uint32_t top, float lo, float hi) {
+  Scale k;
+  float s = ZERO ? (hi - lo) / 15.0f : __uint_as_float(top) / 7.0f;
+  uint16_t b;
+  narrow(s, b);
+  s = widen(b);
+  // a NaN, an infinity, or values whose scale is beyond bf16: the group is NaN
+  const bool bad = top >= 0x7f800000u || !(s < __uint_as_float(0x7f800000u));
+  k.stored = bad ? 0x7fc0u : b;
+  k.none = bad || s == 0.0f;
+  k.small = !k.none && s < kSmall;
+  k.s = k.small ? s * kLift : s;
+  k.inv = k.none ? 0.0f : 1.0f / k.s;
+  k.half = 0.5f * k.s;
+  k.zero = 8.0f;
+  if (ZERO && !k.none) {
+    Scale z = k;
+    z.zero = 0.0f;
+    k.zero = code_of<true>(k.small ? -lo * kLift : -lo, z);
+  }
+  return k;
+}
+
+// The code of a value as an integer.
+template <bool ZERO>
+__device__ __forceinline__ uint32_t quantise(float v, const Scale& k) {
+  if (k.none) return 8u;
+  const float q = code_of<ZERO>(k.small ? v * kLift : v, k);
+  return __float_as_uint(q + kMagic) & 15u;
+}
+
+struct QuantParams {
+  const void* src;
+  int64_t ld;
+  uint32_t rows, K, nb, items;  // items: rows * nb
+  uint8_t* code;
+  uint16_t* scale;
+  uint8_t* zero;
+};
+
+// G32: groups of 32 columns in a group.
+template <typename T, int G32, bool ZERO>
+__global__ void __launch_bounds__(256) quant_int4_kernel(const QuantParams p) {
+  constexpr int ITEMS = sizeof(T) == 2 ? 4 : 2;  // 64 bytes a thread in flight
+  const int l = threadIdx.x & 15, i = l >> 2, c = l & 3;
+  const uint32_t first = blockIdx.x * (16u * ITEMS) + (threadIdx.x >> 4);
+  float v[ITEMS][8];
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 16u * m;
+    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const uint32_t c0 = b * kInt4Block + 8u * l;
+    if (item < p.items && c0 < p.K) {
+      load8<true>(static_cast<const T*>(p.src) + static_cast<int64_t>(row) * p.ld + c0, 8, v[m]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[m][j] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 16u * m;
+    uint32_t top = 0u;
+    float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top = max(top, __float_as_uint(v[m][j]) & 0x7fffffffu);
+      if (ZERO) lo = fminf(lo, v[m][j]), hi = fmaxf(hi, v[m][j]);
+    }
+#pragma unroll
+    for (int o = 1; o < 4 * G32; o *= 2) {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (ZERO) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+    }
+    const Scale k = scale_of<ZERO>(top, lo, hi);
+    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const bool held = b * kInt4Block + 8u * l < p.K;  // (K is a multiple of 8 here)
+    uint32_t x = 0u;  // even columns in the low half, odd ones in the high
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x |= (held ? quantise<ZERO>(v[m][j], k) : 8u) << (4 * (j / 2) + 16 * (j % 2));
+    const uint32_t t = __shfl_xor_sync(0xffffffffu, x, 4);
+    const uint32_t w = i & 1 ? __byte_perm(t, x, 0x7632) : __byte_perm(x, t, 0x5410);
+    if (item >= p.items) continue;
+    // lane i of four: word 0 (even columns of i = 0, 1), 2 (odd), 1 (even of 2, 3), 3
+    reinterpret_cast<uint32_t*>(p.code + static_cast<int64_t>(item) * kInt4Bytes)
+        [4 * c + 2 * (i & 1) + (i >> 1)] = w;
+    if (l % (4 * G32) == 0) {
+      const int64_t at = static_cast<int64_t>(item) * (4 / G32) + l / (4 * G32);
+      p.scale[at] = held ? k.stored : static_cast<uint16_t>(0);
+      if (ZERO) p.zero[at] = held ? static_cast<uint8_t>(k.zero) : static_cast<uint8_t>(8);
+    }
+  }
+}
+
+// Any K and any pitch.
+template <typename T, int G32, bool ZERO>
+__global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams p) {
+  constexpr int ITEMS = 4;
+  const int l = threadIdx.x & 31;
+  const int n = (l >> 1) & 3, g = 2 * (l >> 3) + (l & 1);  // its nibble and its 8 bytes
+  const uint32_t first = blockIdx.x * (8u * ITEMS) + (threadIdx.x >> 5);
+  float v[ITEMS][4];
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 8u * m;
+    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const T* src = static_cast<const T*>(p.src) + static_cast<int64_t>(row) * p.ld;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t col = b * kInt4Block + 32u * i + l;
+      v[m][i] = item < p.items && col < p.K ? widen(src[col]) : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 8u * m;
+    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    uint32_t word[2] = {0u, 0u};
+#pragma unroll
+    for (int i0 = 0; i0 < 4; i0 += G32) {
+      uint32_t top = 0u;
+      float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+      for (int i = i0; i < i0 + G32; ++i) {
+        top = max(top, __float_as_uint(v[m][i]) & 0x7fffffffu);
+        if (ZERO) lo = fminf(lo, v[m][i]), hi = fmaxf(hi, v[m][i]);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (ZERO) {
+          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+      }
+      const Scale k = scale_of<ZERO>(top, lo, hi);
+#pragma unroll
+      for (int i = i0; i < i0 + G32; ++i) {
+        const bool held = b * kInt4Block + 32u * i + l < p.K;
+        const uint32_t q = held ? quantise<ZERO>(v[m][i], k) : 8u;
+        word[i / 2] |= q << (4 * n + 16 * (i % 2));
+      }
+      if (l == 0 && item < p.items) {
+        const int64_t at = static_cast<int64_t>(item) * (4 / G32) + i0 / G32;
+        const bool some = b * kInt4Block + 32u * i0 < p.K;
+        p.scale[at] = some ? k.stored : static_cast<uint16_t>(0);
+        if (ZERO) p.zero[at] = some ? static_cast<uint8_t>(k.zero) : static_cast<uint8_t>(8);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // the four lanes of the same 8 bytes
+      word[h] |= __shfl_xor_sync(0xffffffffu, word[h], 2);
+      word[h] |= __shfl_xor_sync(0xffffffffu, word[h], 4);
+    }
+    if (n == 0 && item < p.items)
+      *reinterpret_cast<uint2*>(p.code + static_cast<int64_t>(item) * kInt4Bytes + 8 * g) =
+          make_uint2(word[0], word[1]);
+  }
+}
+
+struct DequantParams {
+  Int4View w;
+  uint32_t rows, K, nb, items;
+  void* out;
+  int64_t ld;
+};
+
+__device__ __forceinline__ float value(uint32_t p, int n, float z) {
+  return static_cast<float>((p >> (4 * n)) & 15u) - z;
+}
+
+// A thread takes 16 bytes, the columns 8 c .. 8 c + 7 of each 32 of a block.
+template <typename T, int G32>
+__global__ void __launch_bounds__(256) dequant_int4_kernel(const DequantParams p) {
+  constexpr int ITEMS = 2;
+  const int c = threadIdx.x & 3;
+  const uint32_t first = blockIdx.x * (64u * ITEMS) + (threadIdx.x >> 2);
+  uint4 w[ITEMS];
+  uint16_t s[ITEMS][4 / G32];
+  uint8_t z[ITEMS][4 / G32];
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 64u * m;
+    if (item >= p.items) continue;
+    w[m] = ld_stream16(p.w.code + static_cast<int64_t>(item) * kInt4Bytes + 16 * c);
+#pragma unroll
+    for (int k = 0; k < 4 / G32; ++k) {
+      s[m][k] = __ldg(p.w.scale + static_cast<int64_t>(item) * (4 / G32) + k);
+      z[m][k] = p.w.zero ? __ldg(p.w.zero + static_cast<int64_t>(item) * (4 / G32) + k)
+                         : static_cast<uint8_t>(8);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 64u * m;
+    if (item >= p.items) continue;
+    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    T* out = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.ld;
+    const uint32_t even[2] = {w[m].x, w[m].y}, odd[2] = {w[m].z, w[m].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t col = b * kInt4Block + 32u * i + 8u * c;
+      const uint32_t e = even[i / 2] >> (16 * (i % 2)), o = odd[i / 2] >> (16 * (i % 2));
+      const float sc = widen(s[m][i / G32]), zf = static_cast<float>(z[m][i / G32]);
+      float f[8];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        f[2 * n] = value(e, n, zf) * sc, f[2 * n + 1] = value(o, n, zf) * sc;
+      if (col < p.K) store8<true>(out + col, 8, f);
+    }
+  }
+}
+
+template <typename T, int G32>
+__global__ void __launch_bounds__(256) dequant_int4_lanes_kernel(const DequantParams p) {
+  constexpr int ITEMS = 4;
+  const int l = threadIdx.x & 31;
+  const int n = (l >> 1) & 3, g = 2 * (l >> 3) + (l & 1);
+  const uint32_t first = blockIdx.x * (8u * ITEMS) + (threadIdx.x >> 5);
+  uint2 w[ITEMS];
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 8u * m;
+    w[m] = item < p.items ? __ldg(reinterpret_cast<const uint2*>(
+                                p.w.code + static_cast<int64_t>(item) * kInt4Bytes + 8 * g))
+                          : make_uint2(0u, 0u);
+  }
+#pragma unroll
+  for (int m = 0; m < ITEMS; ++m) {
+    const uint32_t item = first + 8u * m;
+    if (item >= p.items) continue;
+    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    T* out = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.ld;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t col = b * kInt4Block + 32u * i + l;
+      const int64_t at = static_cast<int64_t>(item) * (4 / G32) + i / G32;
+      const float sc = widen(__ldg(p.w.scale + at));
+      const float zf = p.w.zero ? static_cast<float>(__ldg(p.w.zero + at)) : 8.0f;
+      const float f = value((i < 2 ? w[m].x : w[m].y) >> (16 * (i % 2)), n, zf) * sc;
+      if (col < p.K) narrow(f, out[col]);
+    }
+  }
+}
+
+template <typename K, typename P>
+twell_status enqueue(K kernel, const P& p, uint32_t per_cta, cudaStream_t s) {
+  kernel<<<(p.items + per_cta - 1) / per_cta, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+template <typename T, int G32, bool ZERO>
+twell_status quant(const QuantParams& p, bool vec, cudaStream_t s) {
+  return vec ? enqueue(quant_int4_kernel<T, G32, ZERO>, p, sizeof(T) == 2 ? 64 : 32, s)
+             : enqueue(quant_int4_lanes_kernel<T, G32, ZERO>, p, 32, s);
+}
+
+template <typename T>
+twell_status quant(const QuantParams& p, int32_t group, bool vec, cudaStream_t s) {
+  if (p.zero)
+    return group == 32   ? quant<T, 1, true>(p, vec, s)
+           : group == 64 ? quant<T, 2, true>(p, vec, s)
+                         : quant<T, 4, true>(p, vec, s);
+  return group == 32   ? quant<T, 1, false>(p, vec, s)
+         : group == 64 ? quant<T, 2, false>(p, vec, s)
+                       : quant<T, 4, false>(p, vec, s);
+}
+
+template <typename T, int G32>
+twell_status dequant(const DequantParams& p, bool vec, cudaStream_t s) {
+  return vec ? enqueue(dequant_int4_kernel<T, G32>, p, 128, s)
+             : enqueue(dequant_int4_lanes_kernel<T, G32>, p, 32, s);
+}
+
+template <typename T>
+twell_status dequant(const DequantParams& p, int32_t group, bool vec, cudaStream_t s) {
+  return group == 32   ? dequant<T, 1>(p, vec, s)
+         : group == 64 ? dequant<T, 2>(p, vec, s)
+                       : dequant<T, 4>(p, vec, s);
+}
+
+// Blocks of the matrix, or 0 where there are more than the kernels index.
+uint32_t blocks_of(const twell_int4_t& w) {
+  const int64_t nb = (static_cast<int64_t>(w.K) + kInt4Block - 1) / kInt4Block;
+  return w.rows > 0x7fffffffLL / nb ? 0u : static_cast<uint32_t>(w.rows * nb);
+}
+
+}  // namespace
+}  // namespace twell
+
+extern "C" twell_status twell_quant_int4(const void* src, int32_t type, int64_t ld,
+                                         const twell_int4_t* out, void* stream) {
+  using namespace twell;
+  twell_status st = check_int4(out);
+  if (st != TWELL_OK) return st;
+  if (type != TWELL_BF16 && type != TWELL_F32) return TWELL_ERR_INVALID;
+  if (out->rows == 0) return TWELL_OK;
+  const int elem = type == TWELL_BF16 ? 2 : 4;
+  if (!src || reinterpret_cast<uintptr_t>(src) % elem != 0 || ld < out->K)
+    return TWELL_ERR_INVALID;
+  DeviceInfo dev;
+  if ((st = require_sm103(&dev)) != TWELL_OK) return st;
+  const uint32_t items = blocks_of(*out);
+  if (items == 0) return TWELL_ERR_UNSUPPORTED;
+  const uint32_t rows = static_cast<uint32_t>(out->rows);
+  const QuantParams p{src,       ld,         rows,       static_cast<uint32_t>(out->K),
+                      items / rows, items,   out->code,  out->scale, out->zero};
+  const bool vec = out->K % 8 == 0 && aligned16(src) && (ld * elem) % 16 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return type == TWELL_BF16 ? quant<uint16_t>(p, out->group, vec, s)
+                            : quant<float>(p, out->group, vec, s);
+}
+
+extern "C" twell_status twell_dequant_int4(const twell_int4_t* w, void* out, int32_t type,
+                                           int64_t ld, void* stream) {
+  using namespace twell;
+  twell_status st = check_int4(w);
+  if (st != TWELL_OK) return st;
+  if (type != TWELL_BF16 && type != TWELL_F32) return TWELL_ERR_INVALID;
+  if (w->rows == 0) return TWELL_OK;
+  const int elem = type == TWELL_BF16 ? 2 : 4;
+  if (!out || reinterpret_cast<uintptr_t>(out) % elem != 0 || ld < w->K) return TWELL_ERR_INVALID;
+  DeviceInfo dev;
+  if ((st = require_sm103(&dev)) != TWELL_OK) return st;
+  const uint32_t items = blocks_of(*w);
+  if (items == 0) return TWELL_ERR_UNSUPPORTED;
+  const uint32_t rows = static_cast<uint32_t>(w->rows);
+  const DequantParams p{view_of(*w), rows, static_cast<uint32_t>(w->K), items / rows, items,
+                        out,         ld};
+  const bool vec = w->K % 8 == 0 && aligned16(out) && (ld * elem) % 16 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return type == TWELL_BF16 ? dequant<uint16_t>(p, w->group, vec, s)
+                            : dequant<float>(p, w->group, vec, s);
+}

@@ -533,6 +533,63 @@ twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, const float* x_
                                  int32_t* status_dev, void* stream);
 
 /*
+ * Weights in 4 bits with a scale (and, where they are given, a zero point) for each
+ * group of 32, 64 or 128 columns of a row:
+ *   w[r][k] = (code[r][k] - zero[r][k/group]) scale[r][k/group],  code, zero in 0..15
+ * A row is stored in blocks of 128 columns, 64 bytes each: column 32 i + 8 c + 2 n + o
+ * of a block (i, c, n < 4, o < 2) is nibble n (from the lowest) of the 16 bits at byte
+ * 8 (2 c + o) + 2 i.  With nb = ceil(K/128) blocks and G = nb 128/group groups a row:
+ *   code   [rows][64 nb] bytes, 16-byte aligned
+ *   scale  [rows][G] bf16
+ *   zero   [rows][G] uint8 (values 0..15), or NULL: 8 everywhere
+ * What belongs to columns behind K is stored (codes 8, scales of whole groups 0, their
+ * zero points 8) but not used.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t K;
+  int32_t group;
+  uint8_t* code;
+  uint16_t* scale;
+  uint8_t* zero;
+} twell_int4_t;
+
+/*
+ * Quantisation into that form.  Without zero points (out->zero NULL):
+ *   scale = bf16(fl32(max |w| / 7)),  code = clamp(rint(w / scale), -8, 7) + 8
+ * with them, lo = min(0, w) and hi = max(0, w) over the group:
+ *   scale = bf16(fl32(fl32(hi - lo) / 15)),  zero = clamp(rint(-lo / scale), 0, 15),
+ *   code = clamp(rint(w / scale) + zero, 0, 15)
+ * rint is of the exact quotient, ties to even.  A group whose scale is 0 has codes (and
+ * zero points) of 8; one with a NaN, an infinity or a scale beyond bf16 gets a NaN
+ * as its scale.
+ *   src  [rows][K] of `type`, rows ld elements apart
+ * rows may be 0.  More than 2^31 - 1 blocks: TWELL_ERR_UNSUPPORTED.
+ */
+twell_status twell_quant_int4(const void* src, int32_t type, int64_t ld, const twell_int4_t* out,
+                              void* stream);
+
+/* The values of such weights: out [rows][K] of `type` (fp32 is exact, bf16 rounds once),
+ * rows ld elements apart; limits as above. */
+twell_status twell_dequant_int4(const twell_int4_t* w, void* out, int32_t type, int64_t ld,
+                                void* stream);
+
+/*
+ * Product of a few rows with such weights, y = x W^T:
+ *   y[t][n] = sum over groups g of scale[n][g] sum over k in g of (code - zero) x[t][k]
+ * Sums are fp32 and rounded once to y's type.
+ *   x  [T][K] bf16, rows ldx elements apart (on 16-byte boundaries with K % 8 == 0 they
+ *      are read 16 bytes at a time)
+ *   y  [T][w->rows] of y_type, rows ldy elements apart
+ * Any T: every 64 rows of x read W once, so that it is an operator for decode batches
+ * (twell_dequant_int4 gives the operand of a prompt's product).  T and w->rows may be 0.
+ * w->rows up to 2^31 - 1, T up to 2^22 - 64 (TWELL_ERR_UNSUPPORTED above).  Repeated calls
+ * agree bit for bit.
+ */
+twell_status twell_gemv_int4(const uint16_t* x, int64_t ldx, const twell_int4_t* w, int32_t T,
+                             void* y, int32_t y_type, int64_t ldy, void* stream);
+
+/*
  * FP32 FMA throughput probe (a measurement helper; the paper has no
  * counterpart).  Launches, on `stream`, one grid of two 512-thread CTAs per
  * SM in which every thread runs 16 independent register-resident chains
