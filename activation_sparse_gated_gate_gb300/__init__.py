@@ -32,6 +32,7 @@ __all__ = [
     "QuantFp8", "twell_quant_fp8", "twell_gemm_fp8", "twell_gate_pack_fp8", "status_word",
     "FP8_BLOCK",
     "Int4", "twell_quant_int4", "twell_dequant_int4", "twell_gemv_int4", "INT4_BLOCK",
+    "Moe", "twell_moe_decode", "twell_moe_decode_workspace",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -75,6 +76,13 @@ class Int4Struct(ctypes.Structure):
     """Mirror of ``twell_int4_t``."""
     _fields_ = [("rows", c_i64), ("K", c_i32), ("group", c_i32), ("code", c_ptr),
                 ("scale", c_ptr), ("zero", c_ptr)]
+
+
+class ExpertsStruct(ctypes.Structure):
+    """Mirror of ``twell_experts_t``."""
+    _fields_ = [("E", c_i32), ("F", c_i32), ("D", c_i32), ("Wg_t", c_ptr), ("Wu_t", c_ptr),
+                ("Wd", c_ptr), ("Wg4", ctypes.POINTER(Int4Struct)),
+                ("Wu4", ctypes.POINTER(Int4Struct)), ("Wd4", ctypes.POINTER(Int4Struct))]
 
 
 class TwellError(RuntimeError):
@@ -130,6 +138,10 @@ _SIGNATURES = {
     "twell_dequant_int4": (c_i32, [ctypes.POINTER(Int4Struct), c_ptr, c_i32, c_i64, c_ptr]),
     "twell_gemv_int4": (c_i32, [c_ptr, c_i64, ctypes.POINTER(Int4Struct), c_i32, c_ptr, c_i32,
                                 c_i64, c_ptr]),
+    "twell_moe_decode": (c_i32, [c_ptr, c_i32, c_ptr, c_i32, ctypes.POINTER(ExpertsStruct), c_i32,
+                                 c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_i32, c_ptr, ctypes.c_size_t,
+                                 c_ptr]),
+    "twell_moe_decode_workspace": (ctypes.c_size_t, [c_i32, c_i32, c_i32, c_i32, c_i32]),
     "twell_status_string": (ctypes.c_char_p, [c_i32]),
     "twell_gate_pack_wait_limit": (ctypes.c_uint64, [ctypes.c_uint64]),
     "twell_probe_fma": (c_i32, [c_i32, c_i32, c_ptr, ctypes.c_size_t,
@@ -1144,3 +1156,106 @@ def twell_gemv_int4(x, w: Int4, out=None, dtype=torch.bfloat16, stream=None):
     _run("twell_gemv_int4", dev, x.data_ptr(), ldx, ctypes.byref(desc), T, out.data_ptr(), y_type,
          ldy)
     return out
+
+
+# ------------------------------------------- mixture of experts
+
+_ACTS = {"relu": 0, "silu": 1}
+_I32 = {torch.int32: 0}
+
+
+class Moe(NamedTuple):
+    """What ``twell_moe_decode`` returns: y [T][D], and the choice of experts ids [T][k]
+    (int32) with its weights [T][k] (fp32)."""
+    y: torch.Tensor
+    ids: torch.Tensor
+    weights: torch.Tensor
+
+
+def twell_moe_decode_workspace(T: int, D: int, F: int, E: int, top_k: int) -> int:
+    return int(lib().twell_moe_decode_workspace(T, D, F, E, top_k))
+
+
+def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormalise=True,
+                     ids=None, weights=None, y=None, dtype=torch.float32, ws=None,
+                     stream=None) -> Moe:
+    """A mixture-of-experts layer for a few tokens: x [T][D] bf16, the router [E][D] (bf16
+    or fp32), and E gated FFNs Wg_t, Wu_t, Wd [E][F][D], all bf16 or all ``Int4`` of the same
+    group.  Each token goes to the ``top_k`` experts of its largest logits, weighted by
+    the softmax over those (``renormalise``) or over all; ``act`` is "relu" or "silu".
+
+    Without a router (None), ``ids`` [T][k] int32 and ``weights`` [T][k] fp32 are the caller's
+    choice; an id outside 0..E-1 is no expert (padding).  With one they are outputs,
+    allocated if not given.  y [T][D] fp32 or bf16 (``dtype`` where not given); ``ws`` is
+    the device workspace (``twell_moe_decode_workspace``, allocated if not given)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k, act, renormalise, ids,
+                                    weights, y, dtype, ws)
+    dev, shape = _first(x, "x")
+    T, D = shape
+    _vec(x, _BF16, "x", dev, shape)
+    if act not in _ACTS:
+        raise ValueError("act must be 'relu' or 'silu'")
+    experts = ExpertsStruct()
+    if isinstance(Wg_t, Int4):
+        lead = Wg_t.code.shape[:-1]
+        if len(lead) != 2:
+            raise ValueError("Wg_t must be [E][F][D]")
+        for w, name in ((Wg_t, "Wg_t"), (Wu_t, "Wu_t"), (Wd, "Wd")):
+            desc, _ = _int4(w, name, dev, lead)
+            if w.K != D or w.group != Wg_t.group:
+                raise ValueError(f"{name} must be of K {D} and group {Wg_t.group}, got {w.K} "
+                                 f"and {w.group}")
+            setattr(experts, name[:2] + "4", ctypes.pointer(desc))
+    else:
+        if not isinstance(Wg_t, torch.Tensor) or Wg_t.dim() != 3:
+            raise TypeError("Wg_t must be a tensor [E][F][D] or an Int4")
+        lead = Wg_t.shape[:2]
+        for w, name in ((Wg_t, "Wg_t"), (Wu_t, "Wu_t"), (Wd, "Wd")):
+            _vec(w, _BF16, name, dev, (*lead, D))
+            setattr(experts, name, w.data_ptr())
+    E, F = lead
+    experts.E, experts.F, experts.D = E, F, D
+    p_router, r_type = None, 0
+    if router is not None:
+        if top_k is None:
+            raise ValueError("top_k is needed with a router")
+        r_type = _vec(router, _TYPES, "router", dev, (E, D))
+        p_router = router.data_ptr()
+        if ids is None:
+            ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+        if weights is None:
+            weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+    elif ids is None or weights is None:
+        raise ValueError("without a router, ids and weights are needed")
+    elif top_k is None:
+        if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+            raise ValueError("ids must be [T][k]")
+        top_k = ids.shape[1]
+    _vec(ids, _I32, "ids", dev, (T, top_k))
+    _vec(weights, _F32, "weights", dev, (T, top_k))
+    if y is None:
+        if dtype not in _TYPES:
+            raise TypeError(f"dtype must be bf16 or fp32, got {dtype}")
+        y = torch.empty((T, D), dtype=dtype, device=x.device)
+        y_type = _TYPES[dtype]
+    else:
+        y_type = _vec(y, _TYPES, "y", dev, (T, D))
+    if ws is None:
+        if torch._C._cuda_getDevice() == dev:
+            need = twell_moe_decode_workspace(T, D, F, E, top_k)
+        else:
+            with torch.cuda.device(dev):
+                need = twell_moe_decode_workspace(T, D, F, E, top_k)
+        ws = _workspace(need, x.device)
+    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda:
+        raise TypeError("ws must be a CUDA tensor")
+    elif ws.get_device() != dev:
+        raise ValueError("ws is on another device")
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    _run("twell_moe_decode", dev, x.data_ptr(), T, p_router, r_type, ctypes.byref(experts), top_k,
+         _ACTS[act], 1 if renormalise else 0, ids.data_ptr(), weights.data_ptr(), y.data_ptr(),
+         y_type, ws.data_ptr(), ws.numel() * ws.element_size())
+    return Moe(y, ids, weights)

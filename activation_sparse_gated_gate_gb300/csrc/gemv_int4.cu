@@ -75,8 +75,7 @@ __global__ void __launch_bounds__(32 * WK * WR) gemv_int4_kernel(const GemvParam
 
   for (int b0 = wk; b0 < p.nb; b0 += WK * AHEAD) {
     uint4 raw[AHEAD][MT][2];
-    uint16_t sc[AHEAD][MT][2][GROUPS];
-    uint8_t ze[AHEAD][MT][2][GROUPS];
+    BlockScales<G32> sc[AHEAD][MT][2];
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
       const int b = b0 + a * WK;
@@ -95,12 +94,7 @@ __global__ void __launch_bounds__(32 * WK * WR) gemv_int4_kernel(const GemvParam
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int k = 0; k < GROUPS; ++k) {
-            const int64_t i = at[m][h] * p.w.held + b * GROUPS + k;
-            sc[a][m][h][k] = __ldg(p.w.scale + i);
-            ze[a][m][h][k] = p.w.zero ? __ldg(p.w.zero + i) : static_cast<uint8_t>(8);
-          }
+          sc[a][m][h].load(p.w, at[m][h] * p.w.held + b * GROUPS);
     }
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
@@ -113,7 +107,7 @@ __global__ void __launch_bounds__(32 * WK * WR) gemv_int4_kernel(const GemvParam
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t bias = 0x43004300u + ze[a][m][h][k] * 0x00010001u;
+            const uint32_t bias = sc[a][m][h].bias(k);
             const uint4 r = raw[a][m][h];
 #pragma unroll
             for (int q = 0; q < G32; ++q) {
@@ -146,7 +140,7 @@ __global__ void __launch_bounds__(32 * WK * WR) gemv_int4_kernel(const GemvParam
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              acc[m][n][j] = fmaf(widen(sc[a][m][j / 2][k]), part[m][j], acc[m][n][j]);
+              acc[m][n][j] = fmaf(sc[a][m][j / 2].scale(k), part[m][j], acc[m][n][j]);
         }
       }
     }

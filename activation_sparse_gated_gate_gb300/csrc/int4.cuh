@@ -45,8 +45,11 @@ inline twell_status check_int4(const twell_int4_t* w) {
   if (!w || w->rows < 0 || w->K < 1) return TWELL_ERR_INVALID;
   if (w->group != 32 && w->group != 64 && w->group != 128) return TWELL_ERR_INVALID;
   if (w->rows == 0) return TWELL_OK;
+  // a block's scales and zero points are read at once
+  const unsigned per = kInt4Block / w->group;
   if (!w->code || !w->scale || !aligned16(w->code) ||
-      reinterpret_cast<uintptr_t>(w->scale) % 2 != 0)
+      reinterpret_cast<uintptr_t>(w->scale) % (2 * per) != 0 ||
+      reinterpret_cast<uintptr_t>(w->zero) % per != 0)
     return TWELL_ERR_INVALID;
   return TWELL_OK;
 }
@@ -75,7 +78,33 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t p, int n, uint32_t bias) {
   return sub_bf16x2(((p >> (4 * n)) & 0x000f000fu) | 0x43004300u, bias);
 }
 
-constexpr uint32_t kMiddle = 0x43084308u;  // the bias of codes without zero points
+// Scales and zero points of a row's block, groups of 32 G32 columns.
+template <int G32>
+struct BlockScales {
+  uint32_t s[G32 == 1 ? 2 : 1];
+  uint32_t z;
+  // `at`: the index of the block's first group.
+  __device__ __forceinline__ void load(const Int4View& w, int64_t at) {
+    if constexpr (G32 == 1) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(w.scale + at));
+      s[0] = v.x, s[1] = v.y;
+      z = w.zero ? __ldg(reinterpret_cast<const uint32_t*>(w.zero + at)) : 0x08080808u;
+    } else if constexpr (G32 == 2) {
+      s[0] = __ldg(reinterpret_cast<const uint32_t*>(w.scale + at));
+      z = w.zero ? __ldg(reinterpret_cast<const uint16_t*>(w.zero + at)) : 0x0808u;
+    } else {
+      s[0] = __ldg(w.scale + at);
+      z = w.zero ? __ldg(w.zero + at) : 0x08u;
+    }
+  }
+  __device__ __forceinline__ float scale(int k) const {
+    return __uint_as_float(k & 1 ? s[k / 2] & 0xffff0000u : s[k / 2] << 16);
+  }
+  // 128 + zero as bf16, in both halves (a zero point above 15 is not one: its low bits)
+  __device__ __forceinline__ uint32_t bias(int k) const {
+    return 0x43004300u | ((z >> (8 * k)) & 15u) * 0x00010001u;
+  }
+};
 
 // d += a b of a 16 x 16 and a 16 x 8 tile.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,

@@ -589,6 +589,57 @@ twell_status twell_dequant_int4(const twell_int4_t* w, void* out, int32_t type, 
 twell_status twell_gemv_int4(const uint16_t* x, int64_t ldx, const twell_int4_t* w, int32_t T,
                              void* y, int32_t y_type, int64_t ldy, void* stream);
 
+/* Activations of twell_moe_decode's gates. */
+typedef enum {
+  TWELL_RELU = 0,
+  TWELL_SILU = 1
+} twell_activation;
+
+/*
+ * Experts of a mixture: E gated FFNs of F neurons over D features, neuron-major as
+ * everywhere ([E][F][D]): either three bf16 matrices, or three of 4 bits (rows = E F,
+ * K = D, the same group); the other three pointers NULL.
+ */
+typedef struct {
+  int32_t E, F, D;
+  const uint16_t* Wg_t;
+  const uint16_t* Wu_t;
+  const uint16_t* Wd;
+  const twell_int4_t* Wg4;
+  const twell_int4_t* Wu4;
+  const twell_int4_t* Wd4;
+} twell_experts_t;
+
+/*
+ * A mixture-of-experts layer for a few tokens, in two kernels:
+ *   logits = x router^T (fp32);  of each token the top_k largest, ties to the lowest
+ *   expert, in falling order;  weight = softmax over the chosen (renormalise != 0) or over
+ *   all E
+ *   y[t] = sum over the slots of weight sum_j a(x . Wg[e][j]) (x . Wu[e][j]) Wd[e][j]
+ * with a = ReLU (a neuron whose gate is not positive contributes nothing, whatever
+ * its other rows hold; where it is for no token of the expert they are not read) or SiLU.
+ *   x        [T][D] bf16
+ *   router   [E][D] of router_type, or NULL: ids and weights are given
+ *   ids      [T][top_k] int32, weights [T][top_k] fp32: the choice, written with a router
+ *            and read without one.  An id outside 0..E-1 is no expert (a padded row, an
+ *            expert elsewhere); an expert may stand in several slots of a token.  A token
+ *            without any gets y = 0
+ *   y        [T][D] of y_type
+ *   ws       twell_moe_decode_workspace(T, D, F, E, top_k) bytes, 16-byte aligned; calls
+ *            that may overlap have their own
+ * A NaN logit makes the token's weights NaN.  Sums and h are fp32 (h enters the last product
+ * in three bf16 parts, all of its bits).  Repeated calls agree bit for bit.
+ * D % 8 == 0, any F.  Limits (TWELL_ERR_UNSUPPORTED above): T 256, T top_k 2048, top_k 32,
+ * E 512, D 16384.  T may be 0.
+ */
+twell_status twell_moe_decode(const uint16_t* x, int32_t T, const void* router,
+                              int32_t router_type, const twell_experts_t* w, int32_t top_k,
+                              int32_t act, int32_t renormalise, int32_t* ids, float* weights,
+                              void* y, int32_t y_type, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of twell_moe_decode on the current device (0 on bad arguments). */
+size_t twell_moe_decode_workspace(int32_t T, int32_t D, int32_t F, int32_t E, int32_t top_k);
+
 /*
  * FP32 FMA throughput probe (a measurement helper; the paper has no
  * counterpart).  Launches, on `stream`, one grid of two 512-thread CTAs per
