@@ -97,6 +97,17 @@ struct BlockScales {
       z = w.zero ? __ldg(w.zero + at) : 0x08u;
     }
   }
+  __device__ __forceinline__ void clear() {
+    s[0] = 0u;
+    if constexpr (G32 == 1) s[1] = 0u;
+    z = 0u;
+  }
+  // Those that another lane has loaded.
+  __device__ __forceinline__ void from_lane(const BlockScales& o, int lane) {
+    s[0] = __shfl_sync(0xffffffffu, o.s[0], lane);
+    if constexpr (G32 == 1) s[1] = __shfl_sync(0xffffffffu, o.s[1], lane);
+    z = __shfl_sync(0xffffffffu, o.z, lane);
+  }
   __device__ __forceinline__ float scale(int k) const {
     return __uint_as_float(k & 1 ? s[k / 2] & 0xffff0000u : s[k / 2] << 16);
   }
