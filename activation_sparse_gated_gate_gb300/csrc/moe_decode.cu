@@ -1,26 +1,27 @@
 // A mixture-of-experts layer for a few tokens: the router's logits and choice, the chosen
-// experts' gated FFNs (bf16 or 4-bit weights) and their weighted sum, in two kernels.
+// experts' gated FFNs (bf16 or 4-bit weights) and their weighted sum.
 //
 //   logits = x W_r^T;  the k largest of a token (ties: the lowest expert), p = softmax
 //   y[t] = sum over the token's k slots of p sum_j a(x . Wg[e][j]) (x . Wu[e][j]) Wd[e][j]
 //
 // Bound by the stream of the chosen experts' weights, and at one token by the chain of
-// dependent steps behind it.  The first kernel computes the logits (a warp an expert
-// pair, eight tokens, fp32 FMAs: a choice must not hang on a tensor core's rounding).  In the second
-// every CTA makes the same choice from them, so that nothing waits for a third.  Then a cluster
-// of eight CTAs takes a part of an expert's neurons.  Each CTA computes the gate and up sums of its own
-// neurons for all the expert's tokens, writes h = a(gate) up into all CTAs' shared
-// memory, and after one cluster barrier sums h Wd over the cluster's neurons for its own
-// eighth of the D columns.  So no sum of D columns leaves the cluster before an expert's part is
-// complete: what goes through memory is a row of D for each (token, slot, part), read once
-// by whoever completes a token's columns (a counter for each token and eighth), in slot
-// order: results do not depend on the order in which clusters finish.
-//   With ReLU a neuron whose gate is not positive for any token is dropped after its gate
-// sum: its rows of Wu and Wd are not read.
-//   The sums over D run on mma.sync with 16 neurons as A and up to 8 NT tokens as B; the
-// sums over neurons with 16 columns of Wd as A (int4.cuh's order lets either way read whole
-// sectors) and h as B in three bf16 parts, whose sum is h's 24 bits: one part would cost
-// y 2^-9 of an element's size.
+// dependent steps behind it.  Three kernels, each launched while the one before runs:
+//   router   the logits: a warp an expert pair and eight tokens, in fp32 FMAs (a choice must not
+//            hang on a tensor core's rounding).  More tokens than eight: a fourth kernel
+//            makes the choice, a warp a token; of fewer every CTA of the next makes it
+//   neurons  the (token, slot) pairs sorted by expert into slabs of up to 8 NT; the slabs'
+//            neurons divided evenly among the CTAs; h = a(gate) up to memory.  With ReLU a
+//            neuron whose gate is not positive for any token of the slab is dropped after its
+//            gate sum: its rows of Wu and Wd are not read
+//   down     a CTA a slab, a tile of columns and a part of the neurons: h Wd, its warps on
+//            every eighth step of 16 neurons, and the token's sum by whoever completes a
+//            tile of it (a counter), in slot order: results do not depend on who it is
+// The sums over D run on mma.sync with 16 neurons as A and up to 8 NT pairs as B (rows.cuh);
+// those over neurons with 16 columns of Wd as A and h as B in three bf16 parts, whose
+// sum is h's 24 bits: one part would cost y 2^-9 of an element's size.
+//   A form in two kernels (clusters of 8 CTAs that exchanged h through shared memory and
+// summed their columns) took as long for a token and 407 us for 64 (4 bits) where this one
+// takes 209: its phases waited for one another.
 #include <atomic>
 
 #include "common.cuh"
@@ -32,7 +33,6 @@
 namespace twell {
 namespace {
 
-constexpr int kRanks = 8;        // CTAs of a cluster
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
 constexpr int kMaxExperts = 512, kMaxTokens = 256, kMaxPairs = 2048, kMaxTop = 32;
@@ -45,12 +45,14 @@ struct RouterParams {
   const void* w;
   int32_t T, D, E;
   float* logits;
-  int32_t* count;  // [T][kRanks], zeroed here for the experts' kernel
+  int32_t* count;  // counters of the down kernel, zeroed here
+  int32_t counters;
 };
 
 template <typename W, int EX, int TT>
 __global__ void __launch_bounds__(128) router_kernel(const RouterParams p) {
-  for (int i = blockIdx.x * 128 + threadIdx.x; i < p.T * kRanks; i += gridDim.x * 128)
+  ptx::grid_launch_next();
+  for (int i = blockIdx.x * 128 + threadIdx.x; i < p.counters; i += gridDim.x * 128)
     p.count[i] = 0;
   if (!p.w) return;
   const int lane = threadIdx.x & 31;
@@ -92,6 +94,18 @@ __global__ void __launch_bounds__(128) router_kernel(const RouterParams p) {
 
 // ------------------------------------------------------------------ experts
 
+// What the neurons kernel leaves for the down kernel, in the workspace: the slabs
+// (expert, first pair in the sorted list, pairs) and the list.
+struct Plan {
+  int32_t* n_slabs;
+  int4* slab;
+  int32_t* list;      // [T k] pairs, sorted by expert
+  int32_t* live;      // [T] slots that have an expert
+  uint16_t* masks;    // [slabs][units] ReLU: a bit for each active neuron of a unit of 16
+  void* h;            // [T k][16 units] by place in the list: fp32 (4-bit weights), or three
+                      // planes of bf16 whose sum it is
+};
+
 struct MoeParams {
   const uint16_t* x;
   int32_t T, D, F, E, k;
@@ -101,9 +115,10 @@ struct MoeParams {
   int32_t renormalise, act;
   const uint16_t* w[3];    // gate, up, down: bf16,
   Int4View q[3];           // or 4 bits
-  float* part;             // [T k][parts_cap + 1][D]
-  int32_t parts_cap;
-  int32_t* count;
+  Plan plan;
+  float* part;             // [T k][splits][D]
+  int32_t side;            // warps side by side on columns in the down kernel: 1, 2, 4 or 8
+  int32_t* count;          // [T][tiles]
   void* y;
   int32_t y_f32;
 };
@@ -137,52 +152,68 @@ __device__ __forceinline__ void mma_split(float (&d)[4], uint32_t a0, uint32_t a
   mma16816(d, a0, a1, a2, a3, b0[0], b1[0]);
 }
 
-// A step of the sums over neurons: 16 of them by a tile of columns.  Lane (g, c) has the
-// neurons 2 c, 2 c + 1, 2 c + 8, 2 c + 9 (row[i]; absent ones < 0), 16 bytes of bf16 each or 8 or 4 of
-// 4-bit codes, which it copies into its own part of a ring slot.  Of 4-bit rows lanes 0 to 15
-// also load the scales of one neuron each, a step or two ahead.
+// A step of the sums over neurons: 16 of them by a tile of columns.  Lane (g, c) uses the
+// neurons 2 c, 2 c + 1, 2 c + 8, 2 c + 9, 16 bytes of bf16 each or 8 of 4-bit codes.  The warp
+// copies them into a slot of its ring by whole lines (row_of(r): row of the r-th neuron, absent
+// ones < 0; lanes that are neighbours have neighbouring pieces), 16-byte pieces swizzled
+// so that the lanes' reads meet no bank twice.  Of 4-bit rows lanes 0 to 15 also load
+// the scales of one neuron each, a step or two ahead.
 struct Bf16Step {
   static constexpr int BYTES = 2 * kSlotBytes;
   struct Scales {
     __device__ __forceinline__ void load(const MoeParams&, int64_t, int) {}
   };
-  static __device__ __forceinline__ void copy(const MoeParams& p, const int64_t (&row)[4], int d0,
-                                              uint32_t slot) {
-    const int lane = threadIdx.x & 31, d = d0 + 8 * (lane >> 2);
+  // piece g of neuron r
+  static __device__ __forceinline__ uint32_t at(int r, int g) {
+    return 128 * r + 16 * (g ^ (r & 6));
+  }
+  template <typename R>
+  static __device__ __forceinline__ void copy(const MoeParams& p, R row_of, int d0, uint32_t slot) {
+    const int lane = threadIdx.x & 31, g = lane & 7, d = d0 + 8 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = row[i] >= 0 && d < p.D;
-      cp_async16_or_zero(slot + 512 * i + 16 * lane, p.w[2] + (in ? row[i] * p.D + d : 0), in);
+      const int r = 4 * i + (lane >> 3);
+      const int64_t row = row_of(r);
+      const bool in = row >= 0 && d < p.D;
+      cp_async16_or_zero(slot + at(r, g), p.w[2] + (in ? row * p.D + d : 0), in);
     }
   }
+  // h_of(i, half, n): part i of h of neurons 2 c, 2 c + 1 (half 0) or those 8 on
   template <int NT, typename H>
-  static __device__ __forceinline__ void add(uint32_t slot, const Scales&, int, H h_of, int nt,
+  static __device__ __forceinline__ void add(uint32_t slot, const Scales&, H h_of, int nt,
                                              bool three, float (&acc)[4][NT][4]) {
+    const int lane = threadIdx.x & 31;
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lds16(slot + 512 * i + 16 * (threadIdx.x & 31));
+    for (int i = 0; i < 4; ++i)
+      v[i] = lds16(slot + at(2 * (lane & 3) + (i & 1) + 8 * (i >> 1), lane >> 2));
     const uint32_t* v0 = &v[0].x;
     const uint32_t* v1 = &v[1].x;
     const uint32_t* v2 = &v[2].x;
     const uint32_t* v3 = &v[3].x;
+    uint32_t b0[NT][3], b1[NT][3];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n >= nt) break;
-      uint32_t b0[3], b1[3];
-      split(h_of(0, n), h_of(1, n), three, b0);
-      split(h_of(2, n), h_of(3, n), three, b1);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        mma_split(acc[q][n], __byte_perm(v0[q], v1[q], 0x5410), __byte_perm(v0[q], v1[q], 0x7632),
-                  __byte_perm(v2[q], v3[q], 0x5410), __byte_perm(v2[q], v3[q], 0x7632), three, b0,
-                  b1);
+      for (int i = 0; i < 3; ++i)
+        if (i < 2 || three) b0[n][i] = h_of(i, 0, n), b1[n][i] = h_of(i, 1, n);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t a0 = __byte_perm(v0[q], v1[q], 0x5410), a1 = __byte_perm(v0[q], v1[q], 0x7632),
+                     a2 = __byte_perm(v2[q], v3[q], 0x5410), a3 = __byte_perm(v2[q], v3[q], 0x7632);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= nt) break;
+        mma_split(acc[q][n], a0, a1, a2, a3, three, b0[n], b1[n]);
+      }
     }
   }
 };
-// SUB: 32s of columns, 4 (a block) or 2 (half of one).
-template <int G32, int SUB>
+template <int G32>
 struct FourStep {
-  static constexpr int BYTES = kSlotBytes * SUB / 4;
+  static constexpr int BYTES = kSlotBytes;
   typedef BlockScales<G32> One;
   struct Scales {
     One one;  // of neuron `lane & 15`
@@ -191,48 +222,41 @@ struct FourStep {
       if (row < 0) one.clear();  // (no product with a scale that is not finite)
     }
   };
-  static __device__ __forceinline__ void copy(const MoeParams& p, const int64_t (&row)[4], int d0,
-                                              uint32_t slot) {
-    const Int4View& q = p.q[2];
-    const int lane = threadIdx.x & 31;
-    const uint8_t* from = q.code + d0 / kInt4Block * kInt4Bytes + 8 * (lane >> 2) +
-                          (SUB == 2 ? 4 * (d0 / 64 % 2) : 0);
+  // 16-byte piece q of neuron r: even neurons in the slot's first half
+  static __device__ __forceinline__ uint32_t at(int r, int q) {
+    const int pos = (r >> 1) + 8 * (r & 1);
+    return 64 * pos + 16 * (q ^ (pos & 2));
+  }
+  template <typename R>
+  static __device__ __forceinline__ void copy(const MoeParams& p, R row_of, int d0, uint32_t slot) {
+    const Int4View& w = p.q[2];
+    const int lane = threadIdx.x & 31, q = lane & 3;
+    const uint8_t* from = w.code + d0 / kInt4Block * kInt4Bytes + 16 * q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = row[i] >= 0;
-      if constexpr (SUB == 4)
-        cp_async8_or_zero(slot + 256 * i + 8 * lane, from + (in ? row[i] * q.pitch : 0), in);
-      else
-        cp_async4_or_zero(slot + 128 * i + 4 * lane, from + (in ? row[i] * q.pitch : 0), in);
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const int64_t row = row_of(r);
+      cp_async16_or_zero(slot + at(r, q), from + (row >= 0 ? row * w.pitch : 0), row >= 0);
     }
   }
+  // h_of(i, n): h of the lane's neuron i
   template <int NT, typename H>
-  static __device__ __forceinline__ void add(uint32_t slot, const Scales& sc, int d0, H h_of, int nt,
-                                             bool three, float (&acc)[2 * SUB][NT][4]) {
+  static __device__ __forceinline__ void add(uint32_t slot, const Scales& sc, H h_of, int nt,
+                                             bool three, float (&acc)[8][NT][4]) {
     const int lane = threadIdx.x & 31, c = lane & 3;
-    uint32_t v[4][SUB / 2];
+    uint32_t v[4][2];
     One s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (SUB == 4)
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                     : "=r"(v[i][0]), "=r"(v[i][SUB / 2 - 1])
-                     : "r"(slot + 256 * i + 8 * lane)
-                     : "memory");
-      else
-        asm volatile("ld.shared.u32 %0, [%1];"
-                     : "=r"(v[i][0])
-                     : "r"(slot + 128 * i + 4 * lane)
-                     : "memory");
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(v[i][0]), "=r"(v[i][1])
+                   : "r"(slot + at(2 * c + (i & 1) + 8 * (i >> 1), lane >> 3) + (lane >> 2 & 1) * 8)
+                   : "memory");
       s[i].from_lane(sc.one, 2 * c + (i & 1) + 8 * (i >> 1));
-      if (SUB == 2 && d0 / 64 % 2) {  // the half's groups to the front
-        if constexpr (G32 == 1) s[i].s[0] = s[i].s[1], s[i].z >>= 16;
-        else if constexpr (G32 == 2) s[i].s[0] >>= 16, s[i].z >>= 8;
-      }
     }
     uint32_t b0[NT][3], b1[NT][3];
 #pragma unroll
-    for (int k = 0; k < SUB; ++k) {
+    for (int k = 0; k < 4; ++k) {
       const int gk = k / G32;
       if (k % G32 == 0) {
 #pragma unroll
@@ -266,8 +290,8 @@ struct FourStep {
 // 16 outputs is.
 struct Bf16 {
   static constexpr bool FOUR = false;
-  template <int TW>
-  using Step = Bf16Step;
+  static constexpr int COLS = 64;  // of a step's tile
+  typedef Bf16Step Step;
   template <int NT, int S, typename X>
   static __device__ __forceinline__ void rows(const MoeParams& p, const int (&mat)[2],
                                               const int64_t (&at)[2][2], int wk, int WK,
@@ -278,16 +302,16 @@ struct Bf16 {
     bf16_rows<2, NT, S>(from, p.D, wk, WK, ring, nt, x, acc);
   }
   static __device__ __forceinline__ int column(int q, int h, int g) { return 8 * g + 2 * q + h; }
-  // `width` columns (a multiple of 8) of a row of Wd towards the second cache.
-  static __device__ __forceinline__ void ahead(const MoeParams& p, int64_t row, int d0, int width) {
-    ptx::prefetch_l2_bulk(p.w[2] + row * p.D + d0, 2 * width);
+  // `n` rows of Wd towards the second cache.
+  static __device__ __forceinline__ void ahead(const MoeParams& p, int64_t row, int n) {
+    ptx::prefetch_l2_bulk(p.w[2] + row * p.D, 2u * n * p.D);
   }
 };
 template <int G>
 struct Four {
   static constexpr bool FOUR = true;
-  template <int TW>
-  using Step = FourStep<G, TW / 32>;
+  static constexpr int COLS = 128;
+  typedef FourStep<G> Step;
   template <int NT, int S, typename X>
   static __device__ __forceinline__ void rows(const MoeParams& p, const int (&mat)[2],
                                               const int64_t (&at)[2][2], int wk, int WK,
@@ -295,44 +319,17 @@ struct Four {
     const Int4View* const from[2] = {&p.q[mat[0]], &p.q[mat[1]]};
     int4_rows<G, 2, NT, S>(from, at, p.D, wk, WK, ring, nt, x, acc);
   }
-  static __device__ __forceinline__ void ahead(const MoeParams& p, int64_t row, int d0, int width) {
-    ptx::prefetch_l2_bulk(p.q[2].code + row * p.q[2].pitch + d0 / kInt4Block * kInt4Bytes,
-                          (width + kInt4Block - 1) / kInt4Block * kInt4Bytes);
+  static __device__ __forceinline__ void ahead(const MoeParams& p, int64_t row, int n) {
+    ptx::prefetch_l2_bulk(p.q[2].code + row * p.q[2].pitch, static_cast<uint32_t>(n * p.q[2].pitch));
   }
   static __device__ __forceinline__ int column(int q, int h, int g) {
     return 32 * (q >> 1) + 8 * (g >> 1) + 2 * (2 * (q & 1) + h) + (g & 1);
   }
 };
 
-template <int NT>
-struct Sizes {
-  static constexpr int SP = 8 * NT;              // pairs (token, slot) of an expert at a time
-  static constexpr int UR = NT <= 2 ? 4 : 2;     // units of 16 neurons of a CTA at a time
-  static constexpr int RM = 16 * UR;
-  static constexpr int SLOTS = kRanks * RM;
-  static constexpr int HS = SP + 4;              // floats between rows of h (no bank twice)
-  static constexpr int RING = 6;                 // KB of a warp's ring
-};
-
-// Columns of a step's tile of the sums over neurons.
-template <typename F, int NT>
-struct Tile {
-  static constexpr int COLS = F::FOUR && NT <= 2 ? 128 : 64;
-};
-
-struct Shared {
-  int32_t hcnt[kRanks];
-  int32_t n_slabs, n_act, total, n_rows;
-  int16_t act[64];               // active rows of this CTA's round
-  int32_t count[kMaxExperts];    // pairs of an expert
-  int32_t first[kMaxExperts];    // its first in the sorted list, below its first slab
-  int32_t live[kMaxTokens];      // rows of `part` that a token is the sum of
-  int32_t rows[128];             // those of the token that is being completed
-  uint8_t last[32];              // pairs whose token this CTA completes
-};
-
 // The k largest of a token's logits and their weights, by a warp: slot `lane` of them.
-// `key`: E words of shared memory of the warp's own.
+// `key`: E words of shared memory
+// of the warp's own.
 __device__ __forceinline__ void choose(const MoeParams& p, int t, uint32_t* key, int& chosen,
                                        float& weight) {
   const int lane = threadIdx.x & 31;
@@ -374,151 +371,131 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, uint32_t* key,
   if (nan) weight = __uint_as_float(0x7fc00000u);
 }
 
-template <typename F, int NT>
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2)
-    experts_kernel(const __grid_constant__ MoeParams p) {
-  typedef Sizes<NT> Z;
-  constexpr int SP = Z::SP, UR = Z::UR, RM = Z::RM, SLOTS = Z::SLOTS, HS = Z::HS;
-  constexpr int TW = Tile<F, NT>::COLS;
-  typedef typename F::template Step<TW> Step;
-  extern __shared__ __align__(16) uint8_t raw[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const int rank = static_cast<int>(ptx::cluster_ctarank());
-  const int cluster = blockIdx.x / kRanks;
-  const int P = p.T * p.k;
-  const int tiles = (p.D + TW - 1) / TW;              // of TW columns
-  const int per_rank = (tiles + kRanks - 1) / kRanks;
-  const int cols = TW * per_rank;
-  const int ystride = cols + 1;                       // (rows of a pair on other banks)
-  const int col0 = rank * cols;
-  const int my_tiles = max(0, min(per_rank, tiles - rank * per_rank));
-  const int width = max(0, min(cols, p.D - col0));    // a multiple of 8
+// More tokens than a CTA has warps: their choice, a warp a token.
+__global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant__ MoeParams p) {
+  __shared__ uint32_t key[kWarps][kMaxExperts];
+  ptx::grid_launch_next();
+  ptx::grid_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x * kWarps + warp;
+  if (t >= p.T) return;
+  int e = -1;
+  float w = 0.0f;
+  choose(p, t, key[warp], e, w);
+  if (lane < p.k) p.ids[t * p.k + lane] = e, p.weights[t * p.k + lane] = w;
+}
 
-  // Each warp's ring, which also holds what it hands to the others: its sums (`red`), the
-  // keys of its choice.
-  constexpr int RING = Z::RING * kSlotBytes;
+template <int NT>
+struct Sizes {
+  static constexpr int SP = 8 * NT;              // pairs (token, slot) of an expert at a time
+  static constexpr int UR = 4;                   // units of 16 neurons of a CTA at a time
+  static constexpr int RM = 16 * UR;
+  static constexpr int RING = 6 * kSlotBytes;    // of a warp, neurons kernel
+  static constexpr int CHUNK = 1024 / NT;        // neurons of h in shared memory
+  static constexpr int HS = CHUNK + 8;           // between pairs of it (no bank twice)
+  static constexpr int RING2 = 6 * kSlotBytes;   // of a warp, down kernel
+};
+
+template <typename F, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+    neurons_kernel(const __grid_constant__ MoeParams p) {
+  typedef Sizes<NT> Z;
+  constexpr int SP = Z::SP, UR = Z::UR, RM = Z::RM, RING = Z::RING;
+  extern __shared__ __align__(16) uint8_t raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
+  const int P = p.T * p.k;
+  // Each warp's ring, which also holds what it hands to the others: its sums, the keys of its
+  // choice.
   uint8_t* ring = raw + warp * RING;
-  float* hb = reinterpret_cast<float*>(raw + kWarps * RING);      // [SLOTS][HS]
-  int2* list = reinterpret_cast<int2*>(hb + SLOTS * HS);          // [SLOTS] (slot, neuron)
-  int32_t* hidx = reinterpret_cast<int32_t*>(list + SLOTS);       // [SLOTS]
-  float* zb = reinterpret_cast<float*>(hidx + SLOTS);             // [RM][SP + 1]
-  float* yacc = zb + RM * (SP + 1);                   // [SP][ystride]
-  float* pw = yacc + SP * ystride;                    // [P] (from an even word on)
-  int32_t* pid = reinterpret_cast<int32_t*>(pw + P);  // [P]
+  const uint32_t ring_at = ptx::smem_u32(ring);
+  int4* slab = reinterpret_cast<int4*>(raw + kWarps * RING);      // [E + P / SP]
+  float* zb = reinterpret_cast<float*>(slab + p.E + P / SP);      // [RM][SP + 1]
+  int32_t* count = reinterpret_cast<int32_t*>(zb + RM * (SP + 1));  // [E] pairs of an expert
+  int32_t* pid = count + p.E;                         // [P]
   int32_t* plist = pid + P;                           // [P] pairs by expert
   int32_t* place = plist + P;                         // [P] a pair's among its expert's
-  int2* slab = reinterpret_cast<int2*>(place + P);    // [E + P / SP]
-  __shared__ Shared sh;
-  const uint32_t ring_at = ptx::smem_u32(ring);
+  int32_t* live = place + P;                          // [T]
+  __shared__ int16_t act[RM];                         // active rows of this round
+  __shared__ int32_t sh_slabs, sh_act;
 
-  ptx::cluster_arrive_relaxed();  // this CTA's shared memory may be written
-  for (int i = tid; i < p.E; i += kThreads) sh.count[i] = 0;
-  for (int i = tid; i < p.T; i += kThreads) sh.live[i] = 0;
+  ptx::grid_launch_next();
+  for (int i = tid; i < p.E; i += kThreads) count[i] = 0;
+  for (int i = tid; i < p.T; i += kThreads) live[i] = 0;
   ptx::grid_wait();
-  ptx::cluster_wait();
 
-  // ---- the choice.  Of a few tokens every CTA makes it for itself, a token a warp; of more
-  // each warp of the cluster makes it for a token and tells the cluster's CTAs.
-  const bool alone = p.T <= kWarps;
-  if (p.logits) {
-#pragma unroll 1
-    for (int t = alone ? warp : rank + kRanks * warp; t < p.T; t += kRanks * kWarps) {
+  // ---- the choice (of a few tokens: every CTA for itself), and the pairs by expert
+  if (p.logits && p.T <= kWarps) {
+    if (warp < p.T) {
       int e = -1;
       float w = 0.0f;
-      __syncwarp();
-      choose(p, t, reinterpret_cast<uint32_t*>(ring), e, w);
-      const int at = t * p.k + lane;
+      choose(p, warp, reinterpret_cast<uint32_t*>(ring), e, w);
       if (lane < p.k) {
-        if (alone) {
-          pid[at] = e, pw[at] = w;
-        } else {
-#pragma unroll 1
-          for (int d = 0; d < kRanks; ++d) {
-            ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(pid + at), d), e);
-            ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(pw + at), d), __float_as_uint(w));
-          }
-        }
-        if (cluster == 0 && (!alone || rank == 0)) p.ids[at] = e, p.weights[at] = w;
+        const int at = warp * p.k + lane;
+        pid[at] = e;
+        if (blockIdx.x == 0) p.ids[at] = e, p.weights[at] = w;
       }
     }
   } else {
 #pragma unroll 1
     for (int i = tid; i < P; i += kThreads) {
-      const int e = p.ids[i];
+      const int e = __ldcg(p.ids + i);
       pid[i] = e >= 0 && e < p.E ? e : -1;
-      pw[i] = p.weights[i];
     }
   }
-  if (p.logits && !alone) {
-    ptx::cluster_arrive();
-    ptx::cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  ptx::cluster_arrive();  // (waited for before h is written to another CTA)
-
-  // The pairs sorted by expert, in order, and cut into slabs of at most SP pairs of one
-  // expert (slab[]: its expert and its first pair in the sorted list).
+  __syncthreads();
   if (warp == 0) {
 #pragma unroll 1
     for (int i0 = 0; i0 < P; i0 += 32) {
       const int e = i0 + lane < P ? pid[i0 + lane] : -1;
       const uint32_t same = __match_any_sync(0xffffffffu, e);
       const int before = __popc(same & ((1u << lane) - 1u));
-      if (e >= 0) place[i0 + lane] = sh.count[e] + before;
+      if (e >= 0) place[i0 + lane] = count[e] + before;
       __syncwarp();
-      if (e >= 0 && before == 0) sh.count[e] += __popc(same);
+      if (e >= 0 && before == 0) count[e] += __popc(same);
       __syncwarp();
     }
     int pairs = 0, slabs = 0;
 #pragma unroll 1
     for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int n = e0 + lane < p.E ? sh.count[e0 + lane] : 0;
-      int up = n | ((n + SP - 1) / SP) << 16, mine = up;  // both sums at once
+      const int n = e0 + lane < p.E ? count[e0 + lane] : 0;
+      const int mine = n | ((n + SP - 1) / SP) << 16;  // both sums at once
+      int up = mine;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
         const int v = __shfl_up_sync(0xffffffffu, up, o);
         if (lane >= o) up += v;
       }
       const int first = pairs + ((up - mine) & 0xffff), s = slabs + ((up - mine) >> 16);
-      if (e0 + lane < p.E) sh.first[e0 + lane] = first | s << 16;
+      if (e0 + lane < p.E) count[e0 + lane] = first;
 #pragma unroll 1
-      for (int q = 0; q < n; q += SP) slab[s + q / SP] = make_int2(e0 + lane, first + q);
+      for (int q = 0; q < n; q += SP)
+        slab[s + q / SP] = make_int4(e0 + lane, first + q, min(SP, n - q), 0);
       const int all = __shfl_sync(0xffffffffu, up, 31);
       pairs += all & 0xffff, slabs += all >> 16;
     }
-    if (lane == 0) sh.n_slabs = slabs;
+    if (lane == 0) sh_slabs = slabs;
   }
   __syncthreads();
-
-  // The slabs' units of 16 neurons in a row, U of them, are divided evenly among C
-  // clusters: cluster i has those from U i / C on.  A part is what one cluster has of one
-  // slab; a slab has at most parts_cap + 1 (C / slabs is at most parts_cap).
-  const uint32_t slabs = sh.n_slabs;
-  const uint32_t units = (p.F + 15u) / 16u;
-  const uint32_t U = units * slabs;
-  const uint32_t C = max(1u, min(min(gridDim.x / kRanks, U / kRanks), slabs * p.parts_cap));
-  const auto cluster_of = [&](uint32_t u) { return static_cast<int>(((u + 1u) * C - 1u) / U); };
-  const auto parts_of = [&](uint32_t s, int& first) {
-    first = cluster_of(s * units);
-    return cluster_of(s * units + units - 1u) - first + 1;
-  };
-  const auto slab_of = [&](int pair) {
-    return (sh.first[pid[pair]] >> 16) + place[pair] / SP;
-  };
 #pragma unroll 1
-  for (int i = tid; i < P; i += kThreads) {
-    if (pid[i] < 0) continue;
-    plist[(sh.first[pid[i]] & 0xffff) + place[i]] = i;
-    int first;
-    atomicAdd(&sh.live[i / p.k], parts_of(slab_of(i), first));
-  }
+  for (int i = tid; i < P; i += kThreads)
+    if (pid[i] >= 0) {
+      plist[count[pid[i]] + place[i]] = i;
+      atomicAdd(&live[i / p.k], 1);
+    }
   __syncthreads();
+  const int slabs = sh_slabs;
+  if (blockIdx.x == 0) {  // for the down kernel
+#pragma unroll 1
+    for (int i = tid; i < slabs; i += kThreads) p.plan.slab[i] = slab[i];
+#pragma unroll 1
+    for (int i = tid; i < P; i += kThreads) p.plan.list[i] = plist[i];
+#pragma unroll 1
+    for (int i = tid; i < p.T; i += kThreads) p.plan.live[i] = live[i];
+    if (tid == 0) *p.plan.n_slabs = slabs;
+  }
   // tokens without an expert
 #pragma unroll 1
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-    if (sh.live[t]) continue;
+    if (live[t]) continue;
 #pragma unroll 1
     for (int d = tid; d < p.D; d += kThreads) {
       const int64_t to = static_cast<int64_t>(t) * p.D + d;
@@ -527,425 +504,489 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2)
     }
   }
 
+  // ---- the slabs' units of 16 neurons in a row, divided evenly among the CTAs
   const bool silu = p.act == TWELL_SILU;
-  const bool three = p.y_f32 != 0;
-  const uint32_t u_last = cluster < C ? U * (cluster + 1) / C : 0u;
+  const uint32_t units = (p.F + 15u) / 16u, U = units * slabs, C = min(gridDim.x, U);
+  const uint32_t u_last = blockIdx.x < C ? U * (blockIdx.x + 1u) / C : 0u;
 #pragma unroll 1
-  for (uint32_t ub = cluster < C ? U * cluster / C : 0u; ub < u_last;) {
+  for (uint32_t ub = blockIdx.x < C ? U * blockIdx.x / C : 0u; ub < u_last;) {
     const uint32_t a = ub / units;
-    const int e = slab[a].x, s0 = slab[a].y;
-    const int ns = min(SP, (sh.first[e] & 0xffff) + sh.count[e] - s0);  // pairs of the slab
-    const int nt_used = (ns + 7) / 8;
+    const int e = slab[a].x, s0 = slab[a].y, ns = slab[a].z;
     const int u0 = ub - a * units;
-    const int nu = min(u_last - a * units, units) - u0;
-    int part;
-    parts_of(a, part);
-    part = cluster - part;
+    const int nu = min(min(u_last - a * units, units) - u0, static_cast<uint32_t>(UR));
     ub += nu;
-    const int rounds = ((nu + kRanks - 1) / kRanks + UR - 1) / UR;
-    const int r0 = u0 + nu * rank / kRanks, r1 = u0 + nu * (rank + 1) / kRanks;  // own units
+    const int nt_used = (ns + 7) / 8;
     const int64_t base = static_cast<int64_t>(e) * p.F;
-    {
-      const uint16_t* xt[NT];
+    const int j0 = u0 * 16, nj = min(nu * 16, p.F - j0);  // neurons of this round
+    const uint16_t* xt[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        xt[n] = p.x + static_cast<int64_t>(plist[s0 + min(8 * n + g, ns - 1)] / p.k) * p.D;
-      for (int i = tid; i < SP * ystride; i += kThreads) yacc[i] = 0.0f;
-#pragma unroll 1
-      for (int round = 0; round < rounds; ++round) {
-        const int ua = r0 + round * UR;
-        const int j0 = ua * 16;                                  // first neuron
-        const int nj = max(0, min(min(ua + UR, r1) * 16, p.F) - j0);  // neurons of this round
+    for (int n = 0; n < NT; ++n)
+      xt[n] = p.x + static_cast<int64_t>(plist[s0 + min(8 * n + g, ns - 1)] / p.k) * p.D;
+    // (their rows of Wd, which the next kernel reads whatever h is, on their way)
+    if (silu && tid == 0) F::ahead(p, base + j0, nj);
 
-        // (SiLU: the rows of Wd that the cluster's neurons of this round need, on their way)
-        if (silu && width > 0) {
+    // ---- gate and up sums (with ReLU the gate's, then up of the active neurons):
+    // `share` warps side by side on tiles of rows, the others on their columns
+    int n_act = silu ? nj : 0, share = 1;
+    // the sum of a tile's half m, row r of it, pair n
+    const auto sum_at = [&](int tile, int m, int r, int n) {
+      const int at =
+          (((m * NT + (n >> 3)) * 32 + (r & 7) * 4 + (n & 7) / 2) * 4) + (r >> 3) * 2 + (n & 1);
+      float v = 0.0f;
 #pragma unroll 1
-          for (int i = tid; i < SLOTS; i += kThreads) {
-            const int q = i / RM, first = (u0 + nu * q / kRanks + round * UR) * 16 + i % RM;
-            if (first < min((u0 + nu * (q + 1) / kRanks) * 16, p.F))
-              F::ahead(p, base + first, col0, width);
+      for (int w = tile; w < kWarps; w += share)
+        v += reinterpret_cast<const float*>(raw + w * RING)[at];
+      return v;
+    };
+#pragma unroll 1
+    for (int stage = 0;; ++stage) {
+      const int rows = stage ? n_act : nj;
+      // a warp's two tiles: the gate and up rows of the same 16 neurons, or 32 rows of one
+      const int n_tiles = silu ? (rows + 15) / 16 : (rows + 31) / 32;
+      share = n_tiles <= 2 ? n_tiles : 4;
+      const int tile = warp & (share - 1);
+      float acc[2][NT][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[m][n][j] = 0.0f;
+      if (tile < n_tiles) {
+        const int mat[2] = {stage, silu ? 1 : stage};
+        int64_t at[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = min((silu ? 16 * tile : 32 * tile + 16 * m) + 8 * h + g, rows - 1);
+            at[m][h] = base + j0 + (stage ? act[r] : r);
           }
-        }
-
-        // ---- gate and up sums (with ReLU the gate's, then up of the active neurons):
-        // `share` warps side by side on tiles of 16 rows, the others on their columns
-        int n_act = silu ? nj : 0, share = 1;
-        // the sum of a tile of pairs of tiles, its half m, row r of it, pair n
-        const auto sum_at = [&](int tile, int m, int r, int n) {
-          const int at = (((m * NT + (n >> 3)) * 32 + (r & 7) * 4 + (n & 7) / 2) * 4) +
-                         (r >> 3) * 2 + (n & 1);
-          float v = 0.0f;
-#pragma unroll 1
-          for (int w = tile; w < kWarps; w += share)
-            v += reinterpret_cast<const float*>(raw + w * RING)[at];
-          return v;
-        };
-#pragma unroll 1
-        for (int stage = 0; stage < (silu ? 1 : 2); ++stage) {
-          const int count = stage ? n_act : nj;
-          if (count == 0) break;
-          // a warp's two tiles: the gate and up rows of the same 16 neurons, or 32 rows of one
-          const int n_tiles = silu ? (count + 15) / 16 : (count + 31) / 32;
-          share = n_tiles <= 2 ? n_tiles : 4;
-          const int tile = warp & (share - 1);
-          float acc[2][NT][4];
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[m][n][j] = 0.0f;
-          const int mat[2] = {stage, silu ? 1 : stage};
-          const int row0 = silu ? 16 * tile : 32 * tile;
-          int64_t at[2][2];
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int r = min(row0 + (silu ? 0 : 16 * m) + 8 * h + g, count - 1);
-              at[m][h] = base + j0 + (stage ? sh.act[r] : r);
-            }
-          if (tile < n_tiles)
-            F::template rows<NT, Z::RING / 2>(
-                p, mat, at, warp / share, kWarps / share, ring_at, nt_used,
-                [&](int n, int k) { return ld16(xt[n] + min(k, p.D - 8)); }, acc);
-          __syncwarp();
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              reinterpret_cast<float4*>(ring)[(m * NT + n) * 32 + lane] =
-                  make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
-          __syncthreads();
-          if (silu || stage) break;
-#pragma unroll 1
-          for (int i = tid; i < nj * SP; i += kThreads) {
-            const int r = i / SP, n = i % SP;
-            if (n < ns) zb[r * (SP + 1) + n] = sum_at(r >> 5, (r >> 4) & 1, r & 15, n);
-          }
-          __syncthreads();
-          if (warp == 0) {
-            int n = 0;
-#pragma unroll 1
-            for (int q = lane; q - lane < nj; q += 32) {
-              bool on = false;
-              if (q < nj)
-#pragma unroll 1
-                for (int i = 0; i < ns; ++i) on |= !(zb[q * (SP + 1) + i] <= 0.0f);
-              const uint32_t m = __ballot_sync(0xffffffffu, on);
-              if (on) sh.act[n + __popc(m & ((1u << lane) - 1u))] = static_cast<int16_t>(q);
-              n += __popc(m);
-            }
-            if (lane == 0) sh.n_act = n;
-          }
-          __syncthreads();
-          n_act = sh.n_act;
-        }
-
-        // ---- h of the active neurons to all CTAs, once they are done with the last round's
-        ptx::cluster_wait();
-        {
-          const uint32_t to = ptx::smem_u32(hb + (rank * RM) * HS);
-#pragma unroll 1
-          for (int i = tid; i < n_act * (SP / 4); i += kThreads) {
-            const int r = i / (SP / 4), n4 = i % (SP / 4) * 4;
-            if (n4 >= 8 * nt_used) continue;
-            float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-            for (int n = n4; n < min(ns, n4 + 4); ++n) {
-              const float u = silu ? sum_at(r >> 4, 1, r & 15, n)
-                                   : sum_at(r >> 5, (r >> 4) & 1, r & 15, n);
-              const float z = silu ? sum_at(r >> 4, 0, r & 15, n) : zb[sh.act[r] * (SP + 1) + n];
-              const float v = silu ? z / (1.0f + expf(-z)) * u : z <= 0.0f ? 0.0f : z * u;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (n == n4 + j) h[j] = v;
-            }
-#pragma unroll
-            for (int d = 0; d < kRanks; ++d)
-              ptx::st_cluster_f32x4(ptx::mapa(to + 4u * (r * HS + n4), d),
-                                    make_float4(h[0], h[1], h[2], h[3]));
-          }
-          if (tid < n_act) {
-            const uint32_t ix = ptx::smem_u32(hidx + rank * RM + tid);
-            const uint32_t j = j0 + (silu ? tid : sh.act[tid]);
-#pragma unroll
-            for (int d = 0; d < kRanks; ++d) ptx::st_cluster_u32(ptx::mapa(ix, d), j);
-          }
-          if (tid < kRanks)
-            ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&sh.hcnt[rank]), tid), n_act);
-        }
-        ptx::cluster_arrive();
-        ptx::cluster_wait();
-
-        // ---- the cluster's neurons times Wd, this CTA's columns
-#pragma unroll 1
-        for (int i = tid; i < SLOTS; i += kThreads) {
-          const int q = i / RM, s = i % RM;
-          int before = 0, total = 0;
-#pragma unroll
-          for (int d = 0; d < kRanks; ++d) {
-            const int n = sh.hcnt[d];
-            before += d < q ? n : 0;
-            total += n;
-          }
-          if (s < sh.hcnt[q]) list[before + s] = make_int2(i, hidx[i]);
-          if (i == 0) sh.total = total;
-        }
-        __syncthreads();
-        const int total = sh.total;
-        const int steps = (total + 15) / 16;
-        const int side = min(kWarps, max(1, my_tiles));      // tiles side by side
-        const int NS = kWarps / side;                        // warps that share a tile's neurons
-        const int ct_w = warp % side, ns_w = warp / side;
-        const float* h0 = hb;
-#pragma unroll 1
-        for (int cb = 0; cb < my_tiles && steps > 0; cb += side) {
-          const int ct = cb + ct_w;
-          const bool on = ct < my_tiles && ns_w < NS;
-          constexpr int MT = TW / 16;
-          float acc[MT][NT][4];
-#pragma unroll
-          for (int q = 0; q < MT; ++q)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[q][n][j] = 0.0f;
-          if (on) {
-            constexpr int SB = RING / Step::BYTES;  // steps in the ring
-            const int d0 = col0 + TW * ct;
-            int put = 0, get = 0, st_put = ns_w;
-            const auto issue = [&] {
-              int64_t row[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int s = 16 * st_put + 2 * c + (i & 1) + 8 * (i >> 1);
-                row[i] = s < total ? base + list[s].y : -1;
-              }
-              Step::copy(p, row, d0, ring_at + put * Step::BYTES);
-              cp_async_commit_group();
-              st_put += NS;
-              put = put + 1 == SB ? 0 : put + 1;
-            };
-            const auto scales = [&](int st, typename Step::Scales& s) {
-              const int i = 16 * st + (lane & 15);
-              s.load(p, i < total ? base + list[i].y : -1, d0);
-            };
-            typename Step::Scales s_now, s_next, s_then;
-            scales(ns_w, s_now);
-            scales(ns_w + NS, s_next);
-#pragma unroll 1
-            for (int i = 0; i < SB - 1; ++i) issue();
-#pragma unroll 1
-            for (int st = ns_w; st < steps; st += NS) {
-              issue();
-              scales(st + 2 * NS, s_then);
-              int slot[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int s = 16 * st + 2 * c + (i & 1) + 8 * (i >> 1);
-                slot[i] = s < total ? list[s].x : -1;
-              }
-              cp_async_wait_for<SB - 1>();
-              Step::template add<NT>(
-                  ring_at + get * Step::BYTES, s_now, d0,
-                  [&](int i, int n) {
-                    return slot[i] >= 0 ? h0[slot[i] * HS + 8 * n + g] : 0.0f;
-                  },
-                  nt_used, three, acc);
-              get = get + 1 == SB ? 0 : get + 1;
-              s_now = s_next, s_next = s_then;
-            }
-            cp_async_wait_for<0>();
-          }
-#pragma unroll 1
-          for (int turn = 0; turn < NS; ++turn) {
-            if (on && ns_w == turn) {
-#pragma unroll
-              for (int q = 0; q < MT; ++q) {
-                float* to[NT][4];
-                float v[NT][4];  // (all loads before the stores, which might alias them)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const int pair = 8 * n + 2 * c + (j & 1);
-                    to[n][j] = yacc + pair * ystride + TW * ct + F::column(q, j / 2, g);
-                    v[n][j] = *to[n][j];
-                  }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) *to[n][j] = v[n][j] + acc[q][n][j];
-              }
-            }
-            __syncthreads();
-          }
-        }
-        ptx::cluster_arrive();
+        F::template rows<NT, RING / (2 * kSlotBytes)>(
+            p, mat, at, warp / share, kWarps / share, ring_at, nt_used,
+            [&](int n, int k) { return ld16(xt[n] + min(k, p.D - 8)); }, acc);
       }
-      // ---- the slab's rows of this part, and the tokens that they complete
+      __syncwarp();
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          reinterpret_cast<float4*>(ring)[(m * NT + n) * 32 + lane] =
+              make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
       __syncthreads();
+      if (silu || stage) break;
 #pragma unroll 1
-      for (int i = tid; i < ns * (width / 4); i += kThreads) {
-        const int n = i / (width / 4), d = i % (width / 4) * 4;
-        const int pair = plist[s0 + n];
-        const float w = pw[pair];
-        const float* v = yacc + n * ystride + d;
-        __stcg(reinterpret_cast<float4*>(
-                   p.part + (static_cast<int64_t>(pair) * (p.parts_cap + 1) + part) * p.D + col0 +
-                   d),
-               make_float4(v[0] * w, v[1] * w, v[2] * w, v[3] * w));
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid < ns) {
-        const int t = plist[s0 + tid] / p.k;
-        sh.last[tid] =
-            width > 0 && atomicAdd(p.count + t * kRanks + rank, 1) + 1 == sh.live[t];
+      for (int i = tid; i < nj * SP; i += kThreads) {
+        const int r = i / SP, n = i % SP;
+        if (n < ns) zb[r * (SP + 1) + n] = sum_at(r >> 5, (r >> 4) & 1, r & 15, n);
       }
       __syncthreads();
+      if (warp == 0) {
+        int n = 0;
 #pragma unroll 1
-      for (int n = 0; n < ns; ++n) {
-        if (!sh.last[n]) continue;
-        __threadfence();
-        const int t = plist[s0 + n] / p.k;
-        if (warp == 0) {  // the token's rows of `part`, by slot and part
-          const int pair = t * p.k + lane;
-          int first, mine = lane < p.k && pid[pair] >= 0 ? parts_of(slab_of(pair), first) : 0;
-          int upto = mine;
-#pragma unroll
-          for (int o = 1; o < 32; o *= 2) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-          }
+        for (int q = lane; q - lane < nj; q += 32) {
+          bool on = false;
+          if (q < nj)
 #pragma unroll 1
-          for (int q = 0; q < mine; ++q)
-            sh.rows[upto - mine + q] = pair * (p.parts_cap + 1) + q;
-          if (lane == 31) sh.n_rows = upto;
+            for (int i = 0; i < ns; ++i) on |= !(zb[q * (SP + 1) + i] <= 0.0f);
+          const uint32_t m = __ballot_sync(0xffffffffu, on);
+          if (on) act[n + __popc(m & ((1u << lane) - 1u))] = static_cast<int16_t>(q);
+          n += __popc(m);
+          const int u = u0 + q / 16;
+          if ((lane & 15) == 0 && q < nj)
+            p.plan.masks[static_cast<int64_t>(a) * units + u] = static_cast<uint16_t>(m >> lane);
         }
-        __syncthreads();
-        // four groups of threads have every fourth row each
-        float4* quarter = reinterpret_cast<float4*>(raw);
-        const int at = tid & 63, gr = tid >> 6, n_rows = sh.n_rows;
-#pragma unroll 1
-        for (int d = 4 * at; d - 4 * at < width; d += 256) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (d < width) {
-#pragma unroll 8
-            for (int r = gr; r < n_rows; r += 4) {
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(
-                  p.part + static_cast<int64_t>(sh.rows[r]) * p.D + col0 + d));
-              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
-          }
-          quarter[gr * 64 + at] = v;
-          __syncthreads();
-          if (gr == 0 && d < width) {
-#pragma unroll
-            for (int i = 1; i < 4; ++i) {
-              const float4 o = quarter[i * 64 + at];
-              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
-            const float f[4] = {v.x, v.y, v.z, v.w};
-            const int64_t to = static_cast<int64_t>(t) * p.D + col0 + d;
-            if (p.y_f32) store4(static_cast<float*>(p.y) + to, f);
-            else store4(static_cast<uint16_t*>(p.y) + to, f);
-          }
-          __syncthreads();
-        }
+        if (lane == 0) sh_act = n;
       }
       __syncthreads();
+      n_act = sh_act;
+      if (n_act == 0) break;
     }
+
+    // ---- h (of neurons behind F: 0)
+    const int rows = silu ? nu * 16 : n_act;
+#pragma unroll 1
+    for (int i = tid; i < ns * RM; i += kThreads) {
+      const int n = i / RM, r = i % RM;
+      if (r >= rows) continue;
+      float h = 0.0f;
+      int j = r;
+      if (silu) {
+        if (r < nj) {
+          const float z = sum_at(r >> 4, 0, r & 15, n);
+          h = z / (1.0f + expf(-z)) * sum_at(r >> 4, 1, r & 15, n);
+        }
+      } else {
+        j = act[r];
+        const float z = zb[j * (SP + 1) + n];
+        h = z <= 0.0f ? 0.0f : z * sum_at(r >> 5, (r >> 4) & 1, r & 15, n);
+      }
+      const int64_t at = static_cast<int64_t>(s0 + n) * (16 * units) + j0 + j;
+      if constexpr (F::FOUR) {
+        static_cast<float*>(p.plan.h)[at] = h;
+      } else {
+        uint32_t o[3];
+        split(h, 0.0f, p.y_f32 != 0, o);
+        uint16_t* to = static_cast<uint16_t*>(p.plan.h) + at;
+        const int64_t plane = static_cast<int64_t>(P) * (16 * units);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) to[q * plane] = static_cast<uint16_t>(o[q]);
+      }
+    }
+    __syncthreads();
   }
-  ptx::cluster_wait();  // (nobody leaves while another CTA may still write to it)
+}
+
+template <typename F, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+    down_kernel(const __grid_constant__ MoeParams p) {
+  typedef Sizes<NT> Z;
+  typedef typename F::Step Step;
+  constexpr int SP = Z::SP, CHUNK = Z::CHUNK, HS = Z::HS, TW = F::COLS, MT = TW / 16;
+  constexpr int SB = Z::RING2 / Step::BYTES;  // steps in a warp's ring
+  extern __shared__ __align__(16) uint8_t raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int WC = p.side, WN = kWarps / WC, CW = TW * WC;  // (WC a power of two)
+  const int wc = warp & (WC - 1), wn = warp / WC;
+  // The rings and h ([SP][HS] fp32, or three planes of bf16); at the end the warps' sums
+  // [warp][NT MT 4][32].
+  const uint32_t ring_at = ptx::smem_u32(raw + warp * Z::RING2);
+  uint8_t* hs = raw + kWarps * Z::RING2;
+  float* red = reinterpret_cast<float*>(raw);
+  __shared__ int16_t list[CHUNK];  // ReLU: the chunk's active neurons
+  __shared__ int32_t sh_n, sh_done, done[SP], pairs[SP], expect[SP];
+  __shared__ float share[SP];
+  __shared__ uint8_t in[SP][kMaxTop];
+
+  const int a = blockIdx.z, part = blockIdx.y, splits = gridDim.y, ct = blockIdx.x;
+  const int tiles = gridDim.x, units = (p.F + 15) / 16, d0 = CW * ct + TW * wc;
+  const int ub = static_cast<int>(static_cast<int64_t>(units) * part / splits),
+            ue = static_cast<int>(static_cast<int64_t>(units) * (part + 1) / splits);
+  const bool three = p.y_f32 != 0, relu = p.act == TWELL_RELU;
+  ptx::grid_wait();
+  // (reads that depend on one another are few: under load each waits behind all that is
+  // on its way)
+  const int slabs = __ldcg(p.plan.n_slabs);
+  const int4 sl = __ldcg(p.plan.slab + a);
+  const uint16_t* masks = p.plan.masks + static_cast<int64_t>(a) * units;
+  constexpr int PER = CHUNK / 16 / 32;  // units of a chunk that a lane of warp 0 compacts
+  uint32_t mask[PER];
+  const auto load_masks = [&](int u0) {
+    const int nu = min(CHUNK / 16, ue - u0);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int q = PER * lane + i;
+      mask[i] = q < nu ? __ldcg(masks + u0 + q) : 0u;
+    }
+  };
+  if (relu && warp == 0) load_masks(ub);
+  if (a >= slabs) return;
+  const int e = sl.x, s0 = sl.y, ns = sl.z, nt_used = (ns + 7) / 8;
+  const int64_t base = static_cast<int64_t>(e) * p.F;
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int q = 0; q < MT; ++q)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[q][n][j] = 0.0f;
+#pragma unroll 1
+  for (int u0 = ub; u0 < ue; u0 += CHUNK / 16) {
+    const int nu = min(CHUNK / 16, ue - u0), whole = min(16 * nu, p.F - 16 * u0);
+    int total = whole;
+    if (relu) {  // compact
+      if (warp == 0) {
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mine += __popc(mask[i]);
+        int up = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int v = __shfl_up_sync(0xffffffffu, up, o);
+          if (lane >= o) up += v;
+        }
+        int at = up - mine;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll 1
+          for (uint32_t m = mask[i]; m; m &= m - 1)
+            list[at++] = static_cast<int16_t>(16 * (PER * lane + i) + __ffs(m) - 1);
+        if (lane == 31) sh_n = up;
+        if (u0 + CHUNK / 16 < ue) load_masks(u0 + CHUNK / 16);
+      }
+      __syncthreads();
+      total = sh_n;
+    }
+    // (else the list is 0, 1, 2 ..., and h is there for whole steps)
+    const bool some = total < whole || (relu && whole % 16);
+    const int steps = (total + 15) / 16;
+    const int64_t row0 = base + 16 * u0;
+    const auto neuron = [&](int s) { return some ? list[s] : s; };
+
+    // h of the chunk, its places up to a whole step 0 (of absent pairs: anything, each
+    // pair is a column of its own)
+    const int64_t pitch = 16 * static_cast<int64_t>(units);  // of a pair's h
+    const int planes = F::FOUR ? 1 : three ? 3 : 2;
+    constexpr int BYTES = F::FOUR ? 4 : 2, EACH = 16 / BYTES;
+    const uint8_t* from =
+        static_cast<const uint8_t*>(p.plan.h) + BYTES * (s0 * pitch + 16 * u0);
+    const int64_t plane = BYTES * pitch * p.T * p.k;
+    const uint32_t to = ptx::smem_u32(hs);
+    if (!some) {
+      const int pieces = 16 / EACH * steps;
+#pragma unroll 1
+      for (int q = 0; q < planes; ++q)
+#pragma unroll 1
+        for (int n = 0; n < ns; ++n)
+#pragma unroll 1
+          for (int s = tid; s < pieces; s += kThreads)
+            cp_async16_or_zero(to + BYTES * (q * SP + n) * HS + 16 * s,
+                               from + q * plane + BYTES * (n * pitch) + 16 * s, true);
+    } else {
+#pragma unroll 1
+      for (int s = tid; s < 16 * steps; s += kThreads) {
+        const bool on = s < total;
+        const int j = on ? list[s] : 0;
+        if constexpr (F::FOUR) {
+#pragma unroll 1
+          for (int n = 0; n < ns; ++n)
+            cp_async4_or_zero(to + 4 * (n * HS + s), from + 4 * (n * pitch + j), on);
+        } else {
+          uint16_t* at = reinterpret_cast<uint16_t*>(hs) + s;
+#pragma unroll 1
+          for (int q = 0; q < planes; ++q)
+#pragma unroll 8
+            for (int n = 0; n < ns; ++n)
+              at[(q * SP + n) * HS] =
+                  on ? __ldcg(reinterpret_cast<const uint16_t*>(from + q * plane) + n * pitch + j)
+                     : 0;
+        }
+      }
+    }
+    cp_async_commit_group();
+
+    int put = 0, get = 0, st_put = wn;
+    const auto issue = [&] {
+      Step::copy(
+          p,
+          [&](int r) -> int64_t {
+            const int s = 16 * st_put + r;
+            return s < total && d0 < p.D ? row0 + neuron(s) : -1;
+          },
+          d0, ring_at + put * Step::BYTES);
+      cp_async_commit_group();
+      st_put += WN;
+      put = put + 1 == SB ? 0 : put + 1;
+    };
+    const auto scales = [&](int st, typename Step::Scales& s) {
+      const int i = 16 * st + (lane & 15);
+      s.load(p, i < total && d0 < p.D ? row0 + neuron(i) : -1, d0);
+    };
+    typename Step::Scales s_now, s_next, s_then;
+#pragma unroll 1
+    for (int i = 0; i < SB - 1; ++i) issue();
+    scales(wn, s_now);
+    scales(wn + WN, s_next);
+    if (u0 == ub) {  // what the end needs
+      if (tid < ns) {
+        const int pair = __ldcg(p.plan.list + s0 + tid);
+        pairs[tid] = pair;
+        expect[tid] = __ldcg(p.plan.live + pair / p.k) * splits;
+        share[tid] = __ldcg(p.weights + pair);
+      }
+    }
+    cp_async_wait_for<SB - 1>();
+    __syncthreads();
+#pragma unroll 1
+    for (int st = wn; st < steps; st += WN) {
+      issue();
+      scales(st + 2 * WN, s_then);
+      cp_async_wait_for<SB - 1>();
+      __syncwarp();
+      if constexpr (F::FOUR) {
+        const float* h0 = reinterpret_cast<const float*>(hs) + g * HS + 16 * st + 2 * c;
+        Step::template add<NT>(
+            ring_at + get * Step::BYTES, s_now,
+            [&](int i, int n) { return h0[8 * n * HS + (i & 1) + 8 * (i >> 1)]; }, nt_used, three,
+            acc);
+      } else {
+        const uint16_t* h0 = reinterpret_cast<const uint16_t*>(hs) + g * HS + 16 * st + 2 * c;
+        Step::template add<NT>(
+            ring_at + get * Step::BYTES, s_now,
+            [&](int i, int half, int n) {
+              return *reinterpret_cast<const uint32_t*>(h0 + (i * SP + 8 * n) * HS + 8 * half);
+            },
+            nt_used, three, acc);
+      }
+      __syncwarp();  // (the next copy but SB - 2 goes where this step was)
+      get = get + 1 == SB ? 0 : get + 1;
+      s_now = s_next, s_next = s_then;
+    }
+    cp_async_wait_for<0>();
+    __syncthreads();
+  }
+
+  // ---- the warps' sums, then the token's where this part completes it
+  constexpr int VALUES = MT * NT * 4 * 32;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        red[warp * VALUES + ((n * MT + q) * 4 + j) * 32 + lane] = acc[q][n][j];
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < WC * nt_used * (MT * 128); i += kThreads) {
+    const int w0 = i / (nt_used * (MT * 128)), at = i % (nt_used * (MT * 128));
+    const int l = at & 31, j = (at >> 5) & 3, q = (at >> 7) % MT, n = (at >> 7) / MT;
+    const int pair = 8 * n + 2 * (l & 3) + (j & 1);
+    const int d = CW * ct + TW * w0 + F::column(q, j / 2, l >> 2);
+    if (pair >= ns || d >= p.D) continue;
+    float v = 0.0f;
+#pragma unroll 1
+    for (int w = w0; w < kWarps; w += WC) v += red[w * VALUES + at];
+    __stcg(p.part + (static_cast<int64_t>(pairs[pair]) * splits + part) * p.D + d,
+           v * share[pair]);
+  }
+  __threadfence();
+  __syncthreads();
+  if (warp == 0) {
+    bool last = false;
+    int t = 0;
+    if (lane < ns) {
+      t = pairs[lane] / p.k;
+      last = atomicAdd(p.count + static_cast<int64_t>(t) * tiles + ct, 1) + 1 == expect[lane];
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, last);
+    if (last) done[__popc(m & ((1u << lane) - 1u))] = t;
+    if (lane == 0) sh_done = __popc(m);
+  }
+  __syncthreads();
+  const int n_done = sh_done;
+  if (n_done == 0) return;
+  __threadfence();
+#pragma unroll 1
+  for (int i = tid; i < n_done * p.k; i += kThreads) {  // the slots that have an expert
+    const int id = __ldcg(p.ids + static_cast<int64_t>(done[i / p.k]) * p.k + i % p.k);
+    in[i / p.k][i % p.k] = id >= 0 && id < p.E;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < n_done * (CW / 4); i += kThreads) {
+    const int o = i / (CW / 4), t = done[o], d = CW * ct + i % (CW / 4) * 4;
+    if (d >= p.D) continue;
+    const float* from = p.part + static_cast<int64_t>(t) * p.k * splits * p.D + d;
+    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int q = 0; q < splits; ++q) {
+#pragma unroll 8
+      for (int s = 0; s < p.k; ++s) {
+        if (!in[o][s]) continue;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(
+            from + (static_cast<int64_t>(s) * splits + q) * p.D));
+        f[0] += v.x, f[1] += v.y, f[2] += v.z, f[3] += v.w;
+      }
+    }
+    const int64_t to = static_cast<int64_t>(t) * p.D + d;
+    if (p.y_f32) store4(static_cast<float*>(p.y) + to, f);
+    else store4(static_cast<uint16_t*>(p.y) + to, f);
+  }
 }
 
 // -------------------------------------------------------------------- host
 
-struct Layout {
-  size_t logits, count, part, total;
-  int32_t parts_cap;
-};
+// Tiles of eight pairs that an expert's weights are read once for: all of them where there
+// are eight tokens at most (an expert with more than a slab reads its weights again, from
+// the second cache).
+int pair_tiles(int32_t T) { return T <= 8 ? 1 : 2; }
 
-// Clusters of the experts' kernel at the most: two CTAs on each SM.
-int clusters_of(const DeviceInfo& dev) {
-  const int n = dev.sm_count * 2 / kRanks;
-  return n < 80 ? n : 80;  // (a token is the sum of at most that many rows and top_k more)
+// The down kernel: warps side by side on columns, tiles of a CTA's columns, slabs at the most,
+// and parts of a slab's neurons.  The widest CTAs that still give every SM one (a CTA
+// loads h, waits for a chain of small reads and takes part in the tokens' sums
+// whatever it has to do); neurons are divided where CTAs of one warp's width leave SMs
+// without two, into parts of 128 neurons at least.
+struct Down {
+  int32_t side, tiles, slabs, splits;
+};
+Down down_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t E, int32_t k,
+             bool four) {
+  const int nt = pair_tiles(T), tw = four ? 128 : 64, P = T * k;
+  Down o;
+  o.slabs = (P < E ? P : E) + P / (8 * nt);
+  if (o.slabs > P) o.slabs = P;
+  for (o.side = kWarps;; o.side /= 2) {
+    o.tiles = (D + o.side * tw - 1) / (o.side * tw);
+    if (o.side == 1 || o.tiles * o.slabs >= 4 * dev.sm_count) break;
+  }
+  const int fill = 2 * dev.sm_count / (o.tiles * o.slabs), most = (F + 15) / 16 / 8;
+  o.splits = most < fill ? most : fill;
+  o.splits = o.splits < 1 ? 1 : o.splits > 8 ? 8 : o.splits;
+  return o;
 }
-constexpr size_t kTwoCtas = 107 * 1024;  // dynamic shared memory that leaves room for two
+
+struct Layout {
+  size_t logits, count, slab, list, live, masks, h, part, total;
+  int32_t counters;
+};
 
 Layout layout_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t E, int32_t k) {
   Layout l;
-  const int C = clusters_of(dev);
-  // clusters an expert is divided among on average at the most: a unit of 16 neurons for
-  // each CTA, and no more than leave every slot of a token one
-  const int by_units = (F + 16 * kRanks - 1) / (16 * kRanks);
-  l.parts_cap = by_units < C / k ? by_units : C / k;
-  if (l.parts_cap < 1) l.parts_cap = 1;
-  const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  l.logits = 0;
-  l.count = up(sizeof(float) * T * E);
-  l.part = l.count + up(sizeof(int32_t) * T * kRanks);
-  l.total = l.part + sizeof(float) * T * k * (l.parts_cap + 1) * D;
+  const size_t P = static_cast<size_t>(T) * k, units = (static_cast<size_t>(F) + 15) / 16;
+  const Down a = down_of(dev, T, D, F, E, k, false), b = down_of(dev, T, D, F, E, k, true);
+  const size_t slabs = a.slabs,
+               splits = a.splits > b.splits ? a.splits : b.splits;
+  l.counters = T * (a.tiles > b.tiles ? a.tiles : b.tiles);
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  l.logits = take(4 * static_cast<size_t>(T) * E);
+  l.count = take(4 * static_cast<size_t>(l.counters));
+  l.slab = take(16 * (slabs + 1));  // (the first: how many)
+  l.list = take(4 * P);
+  l.live = take(4 * static_cast<size_t>(T));
+  l.masks = take(2 * slabs * units);
+  l.h = take(6 * P * 16 * units);
+  l.part = take(4 * P * splits * D);
+  l.total = at;
   return l;
 }
 
 template <typename F, int NT>
-size_t shared_bytes(int32_t D, int32_t E, int32_t P) {
+twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) {
   typedef Sizes<NT> Z;
-  constexpr int TW = Tile<F, NT>::COLS;
-  const size_t cols = TW * (((D + TW - 1) / TW + kRanks - 1) / kRanks);
-  return kWarps * Z::RING * kSlotBytes +
-         4 * (Z::SLOTS * Z::HS + 3 * Z::SLOTS + Z::RM * (Z::SP + 1) + Z::SP * (cols + 1) +
-              4 * P + 2 * (E + P / Z::SP));
-}
-
-template <typename F, int NT>
-twell_status launch_experts(const MoeParams& p, const DeviceInfo& dev, cudaStream_t s) {
-  static std::atomic<uint64_t> set{0};
-  static DeviceValue resident[2];
+  static std::atomic<uint64_t> set[2] = {{0}, {0}};
   const int limit = dev.max_smem_optin - 8192;
-  const int64_t pairs = static_cast<int64_t>(p.T) * p.k;
-  const size_t smem = shared_bytes<F, NT>(p.D, p.E, static_cast<int32_t>(pairs));
-  cudaLaunchConfig_t cfg =
-      launch_config(dim3(kRanks * clusters_of(dev)), dim3(kThreads), smem, s);
-  // as many clusters as run at once: with two CTAs on an SM, or one where its shared
-  // memory holds no more
-  const bool big = smem > kTwoCtas;
-  const int most = resident[big].get(dev, [&]() -> int {
-    int n = 0;
-    cudaLaunchConfig_t ask = cfg;
-    ask.dynamicSmemBytes = big ? limit : kTwoCtas;
-    if (!cuda_ok(cudaFuncSetAttribute(reinterpret_cast<const void*>(experts_kernel<F, NT>),
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, limit)) ||
-        !cuda_ok(cudaOccupancyMaxActiveClusters(&n, experts_kernel<F, NT>, &ask)))
-      return -1;
-    return n;
-  });
-  if (most < 0) return TWELL_ERR_CUDA;
-  const int64_t units = ((pairs < p.E ? pairs : p.E) + pairs / Sizes<NT>::SP) *
-                        ((static_cast<int64_t>(p.F) + 15) / 16);
-  int64_t clusters = units / kRanks;  // one unit a CTA at the least
-  if (clusters > most) clusters = most;
-  if (clusters > clusters_of(dev)) clusters = clusters_of(dev);
-  if (clusters < 1) clusters = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kRanks));
+  const int64_t P = static_cast<int64_t>(p.T) * p.k;
+  const Down o = down_of(dev, p.T, p.D, p.F, p.E, p.k, F::FOUR);
+  p.side = o.side;
+  const int64_t units = o.slabs * ((static_cast<int64_t>(p.F) + 15) / 16);
+  const int most = 2 * dev.sm_count;
   cudaLaunchAttribute attr = overlapped();
+  size_t smem = kWarps * Z::RING + 16 * (p.E + P / Z::SP) +
+                4 * (Z::RM * (Z::SP + 1) + p.E + 3 * P + p.T);
+  cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>(units < most ? units : most)),
+                                         dim3(kThreads), smem, s);
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return launch_large(experts_kernel<F, NT>, limit, cfg, dev, set, p);
+  twell_status st = launch_large(neurons_kernel<F, NT>, limit, cfg, dev, set[0], p);
+  if (st != TWELL_OK) return st;
+  const size_t rings = kWarps * Z::RING2 + (F::FOUR ? 4 : 6) * Z::SP * Z::HS;
+  const size_t sums = 4 * kWarps * (F::COLS / 16) * NT * 4 * 32;
+  cfg = launch_config(dim3(o.tiles, o.splits, o.slabs), dim3(kThreads),
+                      rings > sums ? rings : sums, s);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return launch_large(down_kernel<F, NT>, limit, cfg, dev, set[1], p);
 }
 
 template <typename F>
 twell_status launch_experts(const MoeParams& p, const DeviceInfo& dev, cudaStream_t s) {
-  // tiles of eight pairs that an expert's weights are read once for: all its tokens
-  // where they are eight at most, else by the pairs an expert has on average (one with
-  // more reads its weights again, from the second cache); h and the sums of a slab's columns
-  // are held in shared memory, which bounds them for wide rows
-  const int64_t mean = static_cast<int64_t>(p.T) * p.k / p.E;
-  if (p.T <= 8 || p.D > 8192) return launch_experts<F, 1>(p, dev, s);
-  return mean <= 12 ? launch_experts<F, 2>(p, dev, s) : launch_experts<F, 4>(p, dev, s);
+  return pair_tiles(p.T) == 1 ? launch_experts<F, 1>(p, dev, s) : launch_experts<F, 2>(p, dev, s);
 }
 
 bool sizes_ok(int32_t T, int32_t D, int32_t F, int32_t E, int32_t k) {
@@ -955,9 +996,9 @@ bool within_limits(int32_t T, int32_t D, int32_t E, int32_t k) {
   return T <= kMaxTokens && D <= kMaxWidth && E <= kMaxExperts && k <= kMaxTop &&
          static_cast<int64_t>(T) * k <= kMaxPairs;
 }
-// (units of 16 neurons of every slab of eight pairs, times the clusters, are counted in 32 bits)
+// (units of 16 neurons of every slab of eight pairs, times the CTAs, are counted in 32 bits)
 bool neurons_ok(int32_t F, int32_t E) {
-  return static_cast<int64_t>(E + kMaxPairs / 8) * ((static_cast<int64_t>(F) + 15) / 16) <= 1 << 25;
+  return static_cast<int64_t>(E + kMaxPairs / 8) * ((static_cast<int64_t>(F) + 15) / 16) <= 1 << 23;
 }
 
 }  // namespace
@@ -1016,7 +1057,7 @@ extern "C" twell_status twell_moe_decode(const uint16_t* x, int32_t T, const voi
   int32_t* count = reinterpret_cast<int32_t*>(base + l.count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-  const RouterParams r{x, router, T, D, E, logits, count};
+  const RouterParams r{x, router, T, D, E, logits, count, l.counters};
   const int64_t jobs = !router  ? 1
                        : T == 1 ? E
                                 : static_cast<int64_t>((E + 1) / 2) * ((T + 7) / 8);
@@ -1036,10 +1077,22 @@ extern "C" twell_status twell_moe_decode(const uint16_t* x, int32_t T, const voi
   p.logits = router ? logits : nullptr;
   p.ids = ids, p.weights = weights;
   p.renormalise = renormalise, p.act = act;
+  p.plan.n_slabs = reinterpret_cast<int32_t*>(base + l.slab);
+  p.plan.slab = reinterpret_cast<int4*>(base + l.slab) + 1;
+  p.plan.list = reinterpret_cast<int32_t*>(base + l.list);
+  p.plan.live = reinterpret_cast<int32_t*>(base + l.live);
+  p.plan.masks = reinterpret_cast<uint16_t*>(base + l.masks);
+  p.plan.h = reinterpret_cast<float*>(base + l.h);
   p.part = reinterpret_cast<float*>(base + l.part);
-  p.parts_cap = l.parts_cap;
   p.count = count;
   p.y = y, p.y_f32 = y_type == TWELL_F32;
+  if (router && T > kWarps) {
+    cudaLaunchConfig_t cfg = launch_config(dim3((T + kWarps - 1) / kWarps), dim3(kThreads), 0, s);
+    cudaLaunchAttribute attr = overlapped();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (!cuda_ok(cudaLaunchKernelEx(&cfg, choose_kernel, p))) return TWELL_ERR_CUDA;
+  }
   if (!four) {
     p.w[0] = w->Wg_t, p.w[1] = w->Wu_t, p.w[2] = w->Wd;
     return launch_experts<Bf16>(p, dev, s);
