@@ -1135,7 +1135,7 @@ def twell_dequant_int4(w: Int4, out=None, dtype=torch.bfloat16, stream=None):
 
 def twell_gemv_int4(x, w: Int4, out=None, dtype=torch.bfloat16, stream=None):
     """out [T][N] = x w^T for a few rows x [T][K] bf16 and 4-bit weights w [N][K], bf16 or
-    fp32 (``dtype`` where not given).  Every 64 rows of x read w once."""
+    fp32 (``dtype`` where not given).  Every 32 rows of x read w once."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return twell_gemv_int4(x, w, out, dtype)

@@ -4,14 +4,18 @@
 // What a 4-bit weight costs apart from its half byte decides whether the stream is kept
 // up: 13.5e12 weights a second leave a thread 2.7 issue slots a weight.  So the products run
 // on the tensor cores even for a single row: an m16n8k16 takes 16 rows of W by 16 columns as
-// its A operand, eight tokens as B, and unpacking is 1.5 instructions a weight (int4.cuh).
-// mma.sync and not tcgen05: its operands come from registers, where the codes are
-// unpacked anyway, and its rate is far above what the stream needs at these T.
-//
-// A warp takes MT tiles of 16 rows and every WK-th block of 128 columns; lane (g, c) = (lane
-// / 4, lane % 4) reads 16 bytes of rows g and g + 8 of a tile, a row's four lanes a block of
-// it.  The group's sums are scaled in fp32.  The WK warps of the same rows add up through shared
-// memory in a fixed tree; WR row sets share a CTA and x through the first cache.
+// its A operand, eight rows of x as B.  mma.sync and not tcgen05: its operands come from
+// registers, where the codes are unpacked anyway, and its rate (measured: 8 cycles a warp) is
+// above what the stream needs at these T.  What bounds it is the integer pipe: shifts,
+// logic and byte permutations issue every other cycle, so that unpacking (8 of them for 8
+// weights, 4 bf16 subtractions beside) takes 2 of the 2.7 cycles.  So the loop does little
+// else: codes and scales go to registers, a step while the last one is used, at fixed
+// offsets from one pointer a row, and bounds are looked at once a block.
+// A CTA takes 16 rows of W, its 2 to 16 warps an equal part of the blocks of 128 columns
+// each; their sums meet in shared memory, in a fixed order.  More than 32 rows of x are taken 32
+// at a time, each reading W again (from the second cache).
+#include <type_traits>
+
 #include "common.cuh"
 #include "int4.cuh"
 #include "vec.cuh"
@@ -29,174 +33,185 @@ struct GemvParams {
   int32_t y_f32;
 };
 
-template <int MT, int NT, int WK, int WR, int G32, bool XV>
-__global__ void __launch_bounds__(32 * WK * WR) gemv_int4_kernel(const GemvParams p) {
-  constexpr int GROUPS = 4 / G32;             // of a block
-  constexpr int AHEAD = MT == 1 ? 4 : 2;      // blocks of codes in registers
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wk = warp % WK, wr = warp / WK;
-  const int g = lane >> 2, c = lane & 3;
-  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * WR + wr) * (16 * MT);
-  const int t0 = blockIdx.y * (8 * NT);
-  int64_t at[MT][2];  // this lane's rows (those behind the last repeat it)
+constexpr int kMaxWarps = 16;
+
+// Rows 8 t + g of x from column 8 c on: load(t, i, left) gives this lane's columns of the i-th
+// 32 behind the place that advance() moves, of `left` that there are.  Aligned rows, read 16
+// bytes at a time (K is a multiple of 8),
+template <int NT>
+struct Rows16 {
+  const uint16_t* p[NT];
+  __device__ __forceinline__ uint4 load(int t, int i, int left) const {
+    return 32 * i < left ? ld16(p[t] + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void advance(int k) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int t = 0; t < NT; ++t) p[t] += k;
+  }
+};
+// or any rows.
+template <int NT>
+struct RowsAny {
+  const uint16_t* p[NT];
+  __device__ __forceinline__ uint4 load(int t, int i, int left) const {
+    uint32_t u[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (32 * i + j < left)
+        u[j / 2] |= static_cast<uint32_t>(__ldg(p[t] + 32 * i + j)) << (16 * (j % 2));
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __device__ __forceinline__ void advance(int k) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) p[t] += k;
+  }
+};
+
+template <int NT, int G32, bool XV>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1)
+    gemv_int4_kernel(const __grid_constant__ GemvParams p) {
+  constexpr int GROUPS = 4 / G32;  // of a block
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int warps = blockDim.x / 32;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int t0 = blockIdx.y * (8 * NT), nt = min(NT, (p.T - t0 + 7) / 8);
+  // this warp's blocks, and where its rows and x stand for them (rows behind the last
+  // repeat it)
+  const int b0 = static_cast<int>(static_cast<int64_t>(p.nb) * warp / warps),
+            b1 = static_cast<int>(static_cast<int64_t>(p.nb) * (warp + 1) / warps);
+  const uint8_t* code[2];
+  const uint16_t* scale[2];
+  const uint8_t* zero[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = min(row0 + 8 * h + g, static_cast<int64_t>(p.N - 1));
+    code[h] = p.w.code + r * p.w.pitch + b0 * kInt4Bytes + 16 * c;
+    scale[h] = p.w.scale + r * p.w.held + b0 * GROUPS;
+    zero[h] = p.w.zero ? p.w.zero + r * p.w.held + b0 * GROUPS : nullptr;
+  }
+  typename std::conditional<XV, Rows16<NT>, RowsAny<NT>>::type x;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    x.p[n] = p.x + static_cast<int64_t>(min(t0 + 8 * n + g, p.T - 1)) * p.ldx + b0 * kInt4Block +
+             8 * c;
+
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+
+  uint4 now[2], next[2];
+  BlockScales<G32> s_now[2], s_next[2];
+  const auto fetch = [&] {  // the block where the pointers stand
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t r = row0 + 16 * m + 8 * h + g;
-      at[m][h] = r < p.N ? r : p.N - 1;
+      next[h] = ld_stream16(code[h]);
+      s_next[h].load(scale[h], p.w.zero ? zero[h] : nullptr);
+      code[h] += kInt4Bytes;
+      scale[h] += GROUPS;
+      zero[h] += GROUPS;
     }
-  const uint16_t* xt[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-    xt[n] = t0 + 8 * n + g < p.T ? p.x + static_cast<int64_t>(t0 + 8 * n + g) * p.ldx : nullptr;
-
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][n][j] = 0.0f;
-
-  const auto load_x = [&](const uint16_t* row, int k) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (XV) {
-      if (row && k < p.K) v = ld16(row + k);
-    } else if (row) {
-      uint32_t u[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (k + j < p.K) u[j / 2] |= static_cast<uint32_t>(__ldg(row + k + j)) << (16 * (j % 2));
-      v = make_uint4(u[0], u[1], u[2], u[3]);
-    }
-    return v;
   };
-
-  for (int b0 = wk; b0 < p.nb; b0 += WK * AHEAD) {
-    uint4 raw[AHEAD][MT][2];
-    BlockScales<G32> sc[AHEAD][MT][2];
+  if (b0 < b1) fetch();
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      const int b = b0 + a * WK;
-      if (b >= p.nb) break;
+    for (int h = 0; h < 2; ++h) now[h] = next[h], s_now[h] = s_next[h];
+    if (b + 1 < b1) fetch();
+    const int left = p.K - b * kInt4Block - 8 * c;  // columns before K
+    // (a block's rows of x at once, or 32 columns' where they would not fit in registers)
+    constexpr int HELD = NT <= 2 ? 4 : 1;
+    uint4 u[HELD][NT];
+    const auto load_x = [&](int q) {
+      if (left + 8 * c >= kInt4Block) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int t = 0; t < NT; ++t)
+          if (t < nt) u[q % HELD][t] = x.load(t, q, kInt4Block);
+      } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          raw[a][m][h] = ld_stream16(p.w.code + at[m][h] * p.w.pitch + b * kInt4Bytes + 16 * c);
+        for (int t = 0; t < NT; ++t)
+          if (t < nt) u[q % HELD][t] = x.load(t, q, left);
+      }
+    };
+    if (HELD == 4) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) load_x(q);
     }
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      const int b = b0 + a * WK;
-      if (b >= p.nb) break;
+    for (int k = 0; k < GROUPS; ++k) {
+      float part[NT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          sc[a][m][h].load(p.w, at[m][h] * p.w.held + b * GROUPS);
-    }
+        for (int j = 0; j < 4; ++j) part[t][j] = 0.0f;
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      const int b = b0 + a * WK;
-      if (b >= p.nb) break;
+      for (int q = k * G32; q < (k + 1) * G32; ++q) {
+        if (HELD == 1) load_x(q);
+        uint32_t v[2][4];
 #pragma unroll
-      for (int k = 0; k < GROUPS; ++k) {
-        uint32_t w[MT][G32][2][4];  // bf16 pairs of rows g, g + 8
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t bias = s_now[h].bias(k);
+          const uint4 r = now[h];
+          const uint32_t pr = q < 2 ? __byte_perm(r.x, r.z, q & 1 ? 0x7632 : 0x5410)
+                                    : __byte_perm(r.y, r.w, q & 1 ? 0x7632 : 0x5410);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int z = 0; z < 4; ++z) v[h][z] = nibbles(pr, z, bias);
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t bias = sc[a][m][h].bias(k);
-            const uint4 r = raw[a][m][h];
-#pragma unroll
-            for (int q = 0; q < G32; ++q) {
-              const int i = k * G32 + q;
-              const uint32_t pr = i < 2 ? __byte_perm(r.x, r.z, i & 1 ? 0x7632 : 0x5410)
-                                        : __byte_perm(r.y, r.w, i & 1 ? 0x7632 : 0x5410);
-#pragma unroll
-              for (int n = 0; n < 4; ++n) w[m][q][h][n] = nibbles(pr, n, bias);
-            }
-          }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float part[MT][4];
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[m][j] = 0.0f;
-#pragma unroll
-          for (int q = 0; q < G32; ++q) {
-            const uint4 x = load_x(xt[n], b * kInt4Block + 32 * (k * G32 + q) + 8 * c);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma16816(part[m], w[m][q][0][0], w[m][q][1][0], w[m][q][0][1], w[m][q][1][1], x.x,
-                       x.y);
-              mma16816(part[m], w[m][q][0][2], w[m][q][1][2], w[m][q][0][3], w[m][q][1][3], x.z,
-                       x.w);
-            }
-          }
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              acc[m][n][j] = fmaf(sc[a][m][j / 2].scale(k), part[m][j], acc[m][n][j]);
+        for (int t = 0; t < NT; ++t) {
+          if (t >= nt) break;
+          const uint4 o = u[q % HELD][t];
+          mma16816(part[t], v[0][0], v[1][0], v[0][1], v[1][1], o.x, o.y);
+          mma16816(part[t], v[0][2], v[1][2], v[0][3], v[1][3], o.z, o.w);
         }
       }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (t >= nt) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[t][j] = fmaf(s_now[j / 2].scale(k), part[t][j], acc[t][j]);
+      }
     }
+    x.advance(kInt4Block);
   }
 
-  // the WK warps of the same rows, halves onto halves
-  if constexpr (WK > 1) {
-    __shared__ float4 sum[WK / 2][WR][MT][NT][32];
-#pragma unroll
-    for (int half = WK / 2; half > 0; half /= 2) {
-      if (half < WK / 2) __syncthreads();
-      if (wk >= half && wk < 2 * half) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            sum[wk - half][wr][m][n][lane] =
-                make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
-      }
-      __syncthreads();
-      if (wk < half) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float4 o = sum[wk][wr][m][n][lane];
-            acc[m][n][0] += o.x, acc[m][n][1] += o.y, acc[m][n][2] += o.z, acc[m][n][3] += o.w;
-          }
-      }
-    }
-  }
-  if (wk != 0) return;
+  // the warps' sums
+  extern __shared__ float sum[];  // [warps][NT 4][32]
+  constexpr int VALUES = NT * 128;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t0 + 8 * n + 2 * c + (j & 1);
-        const int64_t r = row0 + 16 * m + 8 * (j >> 1) + g;
-        if (t >= p.T || r >= p.N) continue;
-        const int64_t to = static_cast<int64_t>(t) * p.ldy + r;
-        if (p.y_f32) static_cast<float*>(p.y)[to] = acc[m][n][j];
-        else narrow(acc[m][n][j], static_cast<uint16_t*>(p.y)[to]);
-      }
+    for (int j = 0; j < 4; ++j) sum[warp * VALUES + (n * 4 + j) * 32 + lane] = acc[n][j];
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < 16 * min(8 * nt, p.T - t0); i += blockDim.x) {
+    const int r = i % 16, t = i / 16;
+    const int from = ((t >> 3) * 4 + (r >> 3) * 2 + (t & 1)) * 32 + (r & 7) * 4 + (t >> 1 & 3);
+    float v = 0.0f;
+#pragma unroll 4
+    for (int q = 0; q < warps; ++q) v += sum[q * VALUES + from];
+    if (row0 + r >= p.N) continue;
+    const int64_t to = static_cast<int64_t>(t0 + t) * p.ldy + row0 + r;
+    if (p.y_f32) static_cast<float*>(p.y)[to] = v;
+    else narrow(v, static_cast<uint16_t*>(p.y)[to]);
+  }
 }
 
-template <int MT, int NT, int WK, int WR>
-twell_status launch(const GemvParams& p, int32_t group, bool xv, cudaStream_t s) {
-  const int64_t rows = 16 * MT * WR;
-  const dim3 grid(static_cast<unsigned>((p.N + rows - 1) / rows),
+template <int NT>
+twell_status launch(const GemvParams& p, int32_t group, bool xv, int sms, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.N + 15LL) / 16),
                   static_cast<unsigned>((static_cast<int64_t>(p.T) + 8 * NT - 1) / (8 * NT)));
-  const dim3 block(32 * WK * WR);
-#define TWELL_GO(G32)                                                              \
-  (xv ? gemv_int4_kernel<MT, NT, WK, WR, G32, true><<<grid, block, 0, s>>>(p)      \
-      : gemv_int4_kernel<MT, NT, WK, WR, G32, false><<<grid, block, 0, s>>>(p))
+  // as many warps as run at once (20 an SM): what a warp does once takes as long as one or
+  // two blocks do
+  const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y;
+  int warps = kMaxWarps;
+  while (warps > 2 && (warps > p.nb || warps * ctas > 20 * sms)) warps /= 2;
+  const size_t smem = warps * NT * 512;
+#define TWELL_GO(G32)                                                      \
+  (xv ? gemv_int4_kernel<NT, G32, true><<<grid, 32 * warps, smem, s>>>(p)  \
+      : gemv_int4_kernel<NT, G32, false><<<grid, 32 * warps, smem, s>>>(p))
   if (group == 32) TWELL_GO(1);
   else if (group == 64) TWELL_GO(2);
   else TWELL_GO(4);
@@ -218,7 +233,7 @@ extern "C" twell_status twell_gemv_int4(const uint16_t* x, int64_t ldx, const tw
   if (!x || !y || ldx < w->K || ldy < w->rows || reinterpret_cast<uintptr_t>(x) % 2 != 0 ||
       reinterpret_cast<uintptr_t>(y) % (y_type == TWELL_BF16 ? 2 : 4) != 0)
     return TWELL_ERR_INVALID;
-  if (w->rows > 0x7fffffffLL || T > (1 << 22) - 64) return TWELL_ERR_UNSUPPORTED;
+  if (w->rows > 0x7fffffffLL || T > (1 << 20)) return TWELL_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   const Int4View v = view_of(*w);
@@ -226,8 +241,7 @@ extern "C" twell_status twell_gemv_int4(const uint16_t* x, int64_t ldx, const tw
                      static_cast<int32_t>(v.pitch / kInt4Bytes), y, ldy, y_type == TWELL_F32};
   const bool xv = w->K % 8 == 0 && aligned16(x) && ldx % 8 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T <= 8) return launch<1, 1, 8, 1>(p, w->group, xv, s);
-  if (T <= 16) return launch<1, 2, 8, 1>(p, w->group, xv, s);
-  if (T <= 32) return launch<2, 4, 4, 2>(p, w->group, xv, s);
-  return launch<2, 8, 4, 2>(p, w->group, xv, s);
+  if (T <= 8) return launch<1>(p, w->group, xv, dev.sm_count, s);
+  if (T <= 16) return launch<2>(p, w->group, xv, dev.sm_count, s);
+  return launch<4>(p, w->group, xv, dev.sm_count, s);
 }

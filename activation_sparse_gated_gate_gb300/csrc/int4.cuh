@@ -83,19 +83,22 @@ template <int G32>
 struct BlockScales {
   uint32_t s[G32 == 1 ? 2 : 1];
   uint32_t z;
-  // `at`: the index of the block's first group.
-  __device__ __forceinline__ void load(const Int4View& w, int64_t at) {
+  // From the block's first scale and zero point (NULL: 8).
+  __device__ __forceinline__ void load(const uint16_t* scale, const uint8_t* zero) {
     if constexpr (G32 == 1) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(w.scale + at));
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(scale));
       s[0] = v.x, s[1] = v.y;
-      z = w.zero ? __ldg(reinterpret_cast<const uint32_t*>(w.zero + at)) : 0x08080808u;
+      z = zero ? __ldg(reinterpret_cast<const uint32_t*>(zero)) : 0x08080808u;
     } else if constexpr (G32 == 2) {
-      s[0] = __ldg(reinterpret_cast<const uint32_t*>(w.scale + at));
-      z = w.zero ? __ldg(reinterpret_cast<const uint16_t*>(w.zero + at)) : 0x0808u;
+      s[0] = __ldg(reinterpret_cast<const uint32_t*>(scale));
+      z = zero ? __ldg(reinterpret_cast<const uint16_t*>(zero)) : 0x0808u;
     } else {
-      s[0] = __ldg(w.scale + at);
-      z = w.zero ? __ldg(w.zero + at) : 0x08u;
+      s[0] = __ldg(scale);
+      z = zero ? __ldg(zero) : 0x08u;
     }
+  }
+  __device__ __forceinline__ void load(const Int4View& w, int64_t at) {
+    load(w.scale + at, w.zero ? w.zero + at : nullptr);
   }
   __device__ __forceinline__ void clear() {
     s[0] = 0u;
@@ -111,9 +114,10 @@ struct BlockScales {
   __device__ __forceinline__ float scale(int k) const {
     return __uint_as_float(k & 1 ? s[k / 2] & 0xffff0000u : s[k / 2] << 16);
   }
-  // 128 + zero as bf16, in both halves (a zero point above 15 is not one: its low bits)
+  // 128 + zero as bf16, in both halves (zero points are below 16)
   __device__ __forceinline__ uint32_t bias(int k) const {
-    return 0x43004300u | ((z >> (8 * k)) & 15u) * 0x00010001u;
+    const uint32_t b = G32 == 4 ? z : (z >> (8 * k)) & 255u;
+    return b * 0x00010001u + 0x43004300u;
   }
 };
 

@@ -7,7 +7,11 @@
 //   code = clamp(rint(v / s) + z, 0, 15).
 // rint is of the exact quotient, ties to even: v times 1 / s in fp32 gives a code that is
 // at most one off, and the remainder v - code s, exact in one fused operation, says
-// which (an IEEE division for each value would double the kernel's instructions).
+// whether it is (an IEEE division for each value would double the kernel's instructions):
+// eight values whose remainders are all below s / 2 have their codes, others are looked at
+// one by one.  Of bf16 values, where one in some hundred is a tie, the remainder gives the
+// quotient itself to its last bit, and no quotient of two 8-bit numbers is so near a
+// tie without being one.
 // The stored order is int4.cuh's.
 //
 // Bound by memory.  Half a warp takes a block of 128 columns of a row, 16 bytes (bf16)
@@ -47,7 +51,14 @@ __device__ __forceinline__ float code_of(float v, const Scale& k) {
 template <bool ZERO>
 __device__ __forceinline__ Scale scale_of(uint32_t top, float lo, float hi) {
   Scale k;
-  float s = ZERO ? (hi - lo) / 15.0f : __uint_as_float(top) / 7.0f;
+  // a / 7 or a / 15, rounded as the division is: a quotient that is an ulp or two off,
+  // corrected once by its exact remainder times the rounded reciprocal (Markstein 1990); where
+  // the remainder might be subnormal, the division itself
+  constexpr float D = ZERO ? 15.0f : 7.0f, Y = 1.0f / D;
+  const float a = ZERO ? hi - lo : __uint_as_float(top);
+  const float near = a * Y;
+  float s = fmaf(fmaf(-near, D, a), Y, near);
+  if (a < kSmall * 1024.0f) s = a / D;
   uint16_t b;
   narrow(s, b);
   s = widen(b);
@@ -57,7 +68,7 @@ __device__ __forceinline__ Scale scale_of(uint32_t top, float lo, float hi) {
   k.none = bad || s == 0.0f;
   k.small = !k.none && s < kSmall;
   k.s = k.small ? s * kLift : s;
-  k.inv = k.none ? 0.0f : 1.0f / k.s;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(k.inv) : "f"(k.s));  // (an ulp does not matter)
   k.half = 0.5f * k.s;
   k.zero = 8.0f;
   if (ZERO && !k.none) {
@@ -68,21 +79,150 @@ __device__ __forceinline__ Scale scale_of(uint32_t top, float lo, float hi) {
   return k;
 }
 
-// The code of a value as an integer.
-template <bool ZERO>
-__device__ __forceinline__ uint32_t quantise(float v, const Scale& k) {
-  if (k.none) return 8u;
-  const float q = code_of<ZERO>(k.small ? v * kLift : v, k);
-  return __float_as_uint(q + kMagic) & 15u;
+// The codes of N values, the j-th at nibble `order` has it.  A code is the low end of the
+// bits of 1.5 2^23 + code, so that the codes are put together by multiply-adds of these bits (one
+// a value, where masks and shifts would be three on the slower integer pipe); what the
+// constant adds up to is known.
+template <bool ZERO, bool BF16, int N>
+__device__ __forceinline__ uint32_t quantise(const float (&v)[N], const Scale& k,
+                                             const int (&order)[N]) {
+  static_assert(N == 8 || N == 1, "a word, or one code");
+  constexpr uint32_t ONES = N == 8 ? 0x11111111u : 1u;
+  if (k.none) return 8u * ONES;
+  uint32_t x = 0u;
+  float worst = 0.0f;
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) {
+    const float w = v[order[i]];
+    float t;
+    if (BF16) {
+      const float near = w * k.inv;
+      t = fmaf(fmaf(-near, k.s, w), k.inv, near) + kMagic;
+    } else {
+      t = fmaf(w, k.inv, kMagic);
+      worst = fmaxf(worst, fabsf(fmaf(kMagic - t, k.s, w)));
+    }
+    if (ZERO) t = fminf(t, kMagic + 15.0f - k.zero);
+    x = x * 16u + __float_as_uint(t);
+  }
+  // (a scale that rounding has not left far from the group's extent keeps the others in range)
+  if ((BF16 || worst < k.half) && !k.small)
+    return x + (static_cast<uint32_t>(k.zero) - 0x4b400000u) * ONES;
+  x = 0u;
+#pragma unroll 1
+  for (int i = N - 1; i >= 0; --i) {
+    float w = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (i == j) w = v[order[j]];
+    x = x * 16u + (__float_as_uint(code_of<ZERO>(k.small ? w * kLift : w, k) + kMagic) & 15u);
+  }
+  return x;
+}
+
+// Division of a number below 2^31 by a divisor that the host knows.
+struct Divisor {
+  uint32_t d, m, shift;
+};
+Divisor divisor(uint32_t d) {
+  uint32_t l = 0;
+  while (l < 31 && (1ull << l) < d) ++l;
+  return Divisor{d, static_cast<uint32_t>((1ull << (31 + l)) / d + 1), l};
+}
+__device__ __forceinline__ uint32_t over(uint32_t n, const Divisor& v) {
+  return v.d == 1 ? n : __umulhi(n, v.m) >> (v.shift - 1);
 }
 
 struct QuantParams {
   const void* src;
   int64_t ld;
-  uint32_t rows, K, nb, items;  // items: rows * nb
+  uint32_t rows, K, items;  // items: blocks, nb a row
+  Divisor nb;
   uint8_t* code;
   uint16_t* scale;
   uint8_t* zero;
+};
+
+// Eight values as they were loaded, and over LANES lanes the largest |v| (its bits; a NaN is
+// above all) and the least and largest value.
+template <typename T>
+struct Eight;
+
+template <>
+struct Eight<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p, bool have) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (have) load8<true>(p, 8, v);
+  }
+  __device__ __forceinline__ float get(int j) const { return v[j]; }
+  template <bool ZERO, int LANES>
+  __device__ __forceinline__ void extent(uint32_t& top, float& lo, float& hi) const {
+    top = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+      if (ZERO) lo = fminf(lo, v[j]), hi = fmaxf(hi, v[j]);
+    }
+#pragma unroll
+    for (int o = 1; o < LANES; o *= 2) {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (ZERO) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <>
+struct Eight<uint16_t> {
+  uint32_t v[4];
+  __device__ __forceinline__ void load(const uint16_t* p, bool have) {
+    const uint4 a = have ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return __uint_as_float(j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16);
+  }
+  template <bool ZERO, int LANES>
+  __device__ __forceinline__ void extent(uint32_t& top, float& lo, float& hi) const {
+    // two columns at a time; a NaN stays one
+    uint32_t t = 0u, least = 0u, most = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (ZERO) least = min_nan_bf16x2(least, v[j]), most = max_nan_bf16x2(most, v[j]);
+      else t = max_nan_bf16x2(t, v[j] & 0x7fff7fffu);
+    }
+#pragma unroll
+    for (int o = 1; o < LANES; o *= 2) {
+      if (ZERO) {
+        least = min_nan_bf16x2(least, __shfl_xor_sync(0xffffffffu, least, o));
+        most = max_nan_bf16x2(most, __shfl_xor_sync(0xffffffffu, most, o));
+      } else {
+        t = max_nan_bf16x2(t, __shfl_xor_sync(0xffffffffu, t, o));
+      }
+    }
+    if (ZERO) {
+      least = min_nan_bf16x2(least, least >> 16), most = max_nan_bf16x2(most, most >> 16);
+      lo = __uint_as_float(least << 16), hi = __uint_as_float(most << 16);
+      top = max(__float_as_uint(lo) & 0x7fffffffu, __float_as_uint(hi) & 0x7fffffffu);
+    } else {
+      top = max_nan_bf16x2(t, t >> 16) << 16;
+    }
+  }
 };
 
 // G32: groups of 32 columns in a group.
@@ -91,44 +231,30 @@ __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantParams p) {
   constexpr int ITEMS = sizeof(T) == 2 ? 4 : 2;  // 64 bytes a thread in flight
   const int l = threadIdx.x & 15, i = l >> 2, c = l & 3;
   const uint32_t first = blockIdx.x * (16u * ITEMS) + (threadIdx.x >> 4);
-  float v[ITEMS][8];
+  Eight<T> raw[ITEMS];
 #pragma unroll
   for (int m = 0; m < ITEMS; ++m) {
     const uint32_t item = first + 16u * m;
-    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const uint32_t row = over(item, p.nb), b = item - row * p.nb.d;
     const uint32_t c0 = b * kInt4Block + 8u * l;
-    if (item < p.items && c0 < p.K) {
-      load8<true>(static_cast<const T*>(p.src) + static_cast<int64_t>(row) * p.ld + c0, 8, v[m]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[m][j] = 0.0f;
-    }
+    raw[m].load(static_cast<const T*>(p.src) + static_cast<int64_t>(row) * p.ld + c0,
+                item < p.items && c0 < p.K);
   }
 #pragma unroll
   for (int m = 0; m < ITEMS; ++m) {
     const uint32_t item = first + 16u * m;
-    uint32_t top = 0u;
+    uint32_t top;
     float lo = 0.0f, hi = 0.0f;
+    raw[m].template extent<ZERO, 4 * G32>(top, lo, hi);
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      top = max(top, __float_as_uint(v[m][j]) & 0x7fffffffu);
-      if (ZERO) lo = fminf(lo, v[m][j]), hi = fmaxf(hi, v[m][j]);
-    }
-#pragma unroll
-    for (int o = 1; o < 4 * G32; o *= 2) {
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (ZERO) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      }
-    }
+    for (int j = 0; j < 8; ++j) v[j] = raw[m].get(j);
     const Scale k = scale_of<ZERO>(top, lo, hi);
-    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const uint32_t row = over(item, p.nb), b = item - row * p.nb.d;
     const bool held = b * kInt4Block + 8u * l < p.K;  // (K is a multiple of 8 here)
-    uint32_t x = 0u;  // even columns in the low half, odd ones in the high
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      x |= (held ? quantise<ZERO>(v[m][j], k) : 8u) << (4 * (j / 2) + 16 * (j % 2));
+    // even columns in the low half, odd ones in the high
+    const int order[8] = {0, 2, 4, 6, 1, 3, 5, 7};
+    const uint32_t x = held ? quantise<ZERO, sizeof(T) == 2>(v, k, order) : 0x88888888u;
     const uint32_t t = __shfl_xor_sync(0xffffffffu, x, 4);
     const uint32_t w = i & 1 ? __byte_perm(t, x, 0x7632) : __byte_perm(x, t, 0x5410);
     if (item >= p.items) continue;
@@ -146,7 +272,7 @@ __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantParams p) {
 // Any K and any pitch.
 template <typename T, int G32, bool ZERO>
 __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams p) {
-  constexpr int ITEMS = 4;
+  constexpr int ITEMS = 2;
   const int l = threadIdx.x & 31;
   const int n = (l >> 1) & 3, g = 2 * (l >> 3) + (l & 1);  // its nibble and its 8 bytes
   const uint32_t first = blockIdx.x * (8u * ITEMS) + (threadIdx.x >> 5);
@@ -154,7 +280,7 @@ __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams
 #pragma unroll
   for (int m = 0; m < ITEMS; ++m) {
     const uint32_t item = first + 8u * m;
-    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const uint32_t row = over(item, p.nb), b = item - row * p.nb.d;
     const T* src = static_cast<const T*>(p.src) + static_cast<int64_t>(row) * p.ld;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -165,7 +291,7 @@ __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams
 #pragma unroll
   for (int m = 0; m < ITEMS; ++m) {
     const uint32_t item = first + 8u * m;
-    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const uint32_t row = over(item, p.nb), b = item - row * p.nb.d;
     uint32_t word[2] = {0u, 0u};
 #pragma unroll
     for (int i0 = 0; i0 < 4; i0 += G32) {
@@ -188,7 +314,9 @@ __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams
 #pragma unroll
       for (int i = i0; i < i0 + G32; ++i) {
         const bool held = b * kInt4Block + 32u * i + l < p.K;
-        const uint32_t q = held ? quantise<ZERO>(v[m][i], k) : 8u;
+        const float one[1] = {v[m][i]};
+        const int order[1] = {0};
+        const uint32_t q = held ? quantise<ZERO, sizeof(T) == 2>(one, k, order) & 15u : 8u;
         word[i / 2] |= q << (4 * n + 16 * (i % 2));
       }
       if (l == 0 && item < p.items) {
@@ -211,14 +339,34 @@ __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams
 
 struct DequantParams {
   Int4View w;
-  uint32_t rows, K, nb, items;
+  uint32_t rows, K, items;
+  Divisor nb;
   void* out;
   int64_t ld;
 };
 
-__device__ __forceinline__ float value(uint32_t p, int n, float z) {
-  return static_cast<float>((p >> (4 * n)) & 15u) - z;
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
+
+// Nibble n of the low half as a float less the zero point, times the scale: the nibble is
+// taken where it stands, as 2^23 + code 16^n, so that nothing is shifted or converted (code - zero
+// and its products with the scale are exact).
+struct Scaled {
+  float minus[4], times[4];  // 2^23 + zero 16^n, scale / 16^n
+  __device__ __forceinline__ Scaled(float zero, float scale) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      minus[n] = fmaf(zero, static_cast<float>(1 << (4 * n)), 8388608.0f);
+      times[n] = scale * (1.0f / static_cast<float>(1 << (4 * n)));
+    }
+  }
+  __device__ __forceinline__ float of(uint32_t p, int n) const {
+    return (__uint_as_float((p & (15u << (4 * n))) | 0x4b000000u) - minus[n]) * times[n];
+  }
+};
 
 // A thread takes 16 bytes, the columns 8 c .. 8 c + 7 of each 32 of a block.
 template <typename T, int G32>
@@ -245,19 +393,30 @@ __global__ void __launch_bounds__(256) dequant_int4_kernel(const DequantParams p
   for (int m = 0; m < ITEMS; ++m) {
     const uint32_t item = first + 64u * m;
     if (item >= p.items) continue;
-    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const uint32_t row = over(item, p.nb), b = item - row * p.nb.d;
     T* out = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.ld;
-    const uint32_t even[2] = {w[m].x, w[m].y}, odd[2] = {w[m].z, w[m].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t col = b * kInt4Block + 32u * i + 8u * c;
-      const uint32_t e = even[i / 2] >> (16 * (i % 2)), o = odd[i / 2] >> (16 * (i % 2));
-      const float sc = widen(s[m][i / G32]), zf = static_cast<float>(z[m][i / G32]);
-      float f[8];
+      const uint32_t e = i < 2 ? w[m].x : w[m].y, o = i < 2 ? w[m].z : w[m].w;
+      if (col >= p.K) continue;
+      if constexpr (sizeof(T) == 2) {  // two at a time, rounded once by the product
+        const uint32_t both = __byte_perm(e, o, i & 1 ? 0x7632 : 0x5410);
+        const uint32_t bias = z[m][i / G32] * 0x00010001u + 0x43004300u,
+                       sc = s[m][i / G32] * 0x00010001u;
+        *reinterpret_cast<uint4*>(out + col) =
+            make_uint4(mul_bf16x2(nibbles(both, 0, bias), sc), mul_bf16x2(nibbles(both, 1, bias), sc),
+                       mul_bf16x2(nibbles(both, 2, bias), sc), mul_bf16x2(nibbles(both, 3, bias), sc));
+      } else {
+        const Scaled k(static_cast<float>(z[m][i / G32]), widen(s[m][i / G32]));
+        float f[8];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        f[2 * n] = value(e, n, zf) * sc, f[2 * n + 1] = value(o, n, zf) * sc;
-      if (col < p.K) store8<true>(out + col, 8, f);
+        for (int n = 0; n < 4; ++n) {
+          f[2 * n] = k.of(i & 1 ? e >> 16 : e, n);
+          f[2 * n + 1] = k.of(i & 1 ? o >> 16 : o, n);
+        }
+        store8<true>(out + col, 8, f);
+      }
     }
   }
 }
@@ -280,7 +439,7 @@ __global__ void __launch_bounds__(256) dequant_int4_lanes_kernel(const DequantPa
   for (int m = 0; m < ITEMS; ++m) {
     const uint32_t item = first + 8u * m;
     if (item >= p.items) continue;
-    const uint32_t row = item / p.nb, b = item - row * p.nb;
+    const uint32_t row = over(item, p.nb), b = item - row * p.nb.d;
     T* out = static_cast<T*>(p.out) + static_cast<int64_t>(row) * p.ld;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -288,7 +447,8 @@ __global__ void __launch_bounds__(256) dequant_int4_lanes_kernel(const DequantPa
       const int64_t at = static_cast<int64_t>(item) * (4 / G32) + i / G32;
       const float sc = widen(__ldg(p.w.scale + at));
       const float zf = p.w.zero ? static_cast<float>(__ldg(p.w.zero + at)) : 8.0f;
-      const float f = value((i < 2 ? w[m].x : w[m].y) >> (16 * (i % 2)), n, zf) * sc;
+      const uint32_t q = ((i < 2 ? w[m].x : w[m].y) >> (16 * (i % 2) + 4 * n)) & 15u;
+      const float f = (__uint_as_float(q | 0x4b000000u) - (8388608.0f + zf)) * sc;
       if (col < p.K) narrow(f, out[col]);
     }
   }
@@ -303,7 +463,7 @@ twell_status enqueue(K kernel, const P& p, uint32_t per_cta, cudaStream_t s) {
 template <typename T, int G32, bool ZERO>
 twell_status quant(const QuantParams& p, bool vec, cudaStream_t s) {
   return vec ? enqueue(quant_int4_kernel<T, G32, ZERO>, p, sizeof(T) == 2 ? 64 : 32, s)
-             : enqueue(quant_int4_lanes_kernel<T, G32, ZERO>, p, 32, s);
+             : enqueue(quant_int4_lanes_kernel<T, G32, ZERO>, p, 16, s);
 }
 
 template <typename T>
@@ -354,8 +514,8 @@ extern "C" twell_status twell_quant_int4(const void* src, int32_t type, int64_t 
   const uint32_t items = blocks_of(*out);
   if (items == 0) return TWELL_ERR_UNSUPPORTED;
   const uint32_t rows = static_cast<uint32_t>(out->rows);
-  const QuantParams p{src,       ld,         rows,       static_cast<uint32_t>(out->K),
-                      items / rows, items,   out->code,  out->scale, out->zero};
+  const QuantParams p{src,   ld,        rows,       static_cast<uint32_t>(out->K),
+                      items, divisor(items / rows), out->code, out->scale, out->zero};
   const bool vec = out->K % 8 == 0 && aligned16(src) && (ld * elem) % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return type == TWELL_BF16 ? quant<uint16_t>(p, out->group, vec, s)
@@ -376,7 +536,7 @@ extern "C" twell_status twell_dequant_int4(const twell_int4_t* w, void* out, int
   const uint32_t items = blocks_of(*w);
   if (items == 0) return TWELL_ERR_UNSUPPORTED;
   const uint32_t rows = static_cast<uint32_t>(w->rows);
-  const DequantParams p{view_of(*w), rows, static_cast<uint32_t>(w->K), items / rows, items,
+  const DequantParams p{view_of(*w), rows, static_cast<uint32_t>(w->K), items, divisor(items / rows),
                         out,         ld};
   const bool vec = w->K % 8 == 0 && aligned16(out) && (ld * elem) % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

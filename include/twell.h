@@ -581,9 +581,9 @@ twell_status twell_dequant_int4(const twell_int4_t* w, void* out, int32_t type, 
  *   x  [T][K] bf16, rows ldx elements apart (on 16-byte boundaries with K % 8 == 0 they
  *      are read 16 bytes at a time)
  *   y  [T][w->rows] of y_type, rows ldy elements apart
- * Any T: every 64 rows of x read W once, so that it is an operator for decode batches
+ * Any T: every 32 rows of x read W once, so that it is an operator for decode batches
  * (twell_dequant_int4 gives the operand of a prompt's product).  T and w->rows may be 0.
- * w->rows up to 2^31 - 1, T up to 2^22 - 64 (TWELL_ERR_UNSUPPORTED above).  Repeated calls
+ * w->rows up to 2^31 - 1, T up to 2^20 (TWELL_ERR_UNSUPPORTED above).  Repeated calls
  * agree bit for bit.
  */
 twell_status twell_gemv_int4(const uint16_t* x, int64_t ldx, const twell_int4_t* w, int32_t T,
