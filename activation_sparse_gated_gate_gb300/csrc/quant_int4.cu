@@ -269,10 +269,29 @@ __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantParams p) {
   }
 }
 
+// op over the warp of each of N values a lane: the lanes halve the values between them as
+// long as there are several, so that lane l ends with value l N / 32.
+template <int N, typename V, typename Op>
+__device__ __forceinline__ V over_warp(V (&x)[N], Op op) {
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2, o /= 2) {
+    const bool upper = (threadIdx.x & o) != 0;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const V away = upper ? x[k] : x[k + n], mine = upper ? x[k + n] : x[k];
+      x[k] = op(mine, __shfl_xor_sync(0xffffffffu, away, o));
+    }
+  }
+#pragma unroll
+  for (; o > 0; o /= 2) x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
+  return x[0];
+}
+
 // Any K and any pitch.
 template <typename T, int G32, bool ZERO>
 __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams p) {
-  constexpr int ITEMS = 2;
+  constexpr int ITEMS = 2, GROUPS = 4 / G32;
   const int l = threadIdx.x & 31;
   const int n = (l >> 1) & 3, g = 2 * (l >> 3) + (l & 1);  // its nibble and its 8 bytes
   const uint32_t first = blockIdx.x * (8u * ITEMS) + (threadIdx.x >> 5);
@@ -292,38 +311,52 @@ __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams
   for (int m = 0; m < ITEMS; ++m) {
     const uint32_t item = first + 8u * m;
     const uint32_t row = over(item, p.nb), b = item - row * p.nb.d;
+    uint32_t top[GROUPS];
+    float lo[GROUPS], hi[GROUPS];
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      top[k] = 0u, lo[k] = hi[k] = 0.0f;
+#pragma unroll
+      for (int i = k * G32; i < (k + 1) * G32; ++i) {
+        top[k] = max(top[k], __float_as_uint(v[m][i]) & 0x7fffffffu);
+        if (ZERO) lo[k] = fminf(lo[k], v[m][i]), hi[k] = fmaxf(hi[k], v[m][i]);
+      }
+    }
+    const uint32_t t = over_warp(top, [](uint32_t a, uint32_t c) { return max(a, c); });
+    float least = 0.0f, most = 0.0f;
+    if (ZERO) {
+      least = over_warp(lo, [](float a, float c) { return fminf(a, c); });
+      most = over_warp(hi, [](float a, float c) { return fmaxf(a, c); });
+    }
+    // each lane the scale of one group
+    const int mine = l / (32 / GROUPS);
+    const Scale own = scale_of<ZERO>(t, least, most);
+    if (l % (32 / GROUPS) == 0 && item < p.items) {
+      const int64_t at = static_cast<int64_t>(item) * GROUPS + mine;
+      const bool some = b * kInt4Block + 32u * G32 * mine < p.K;
+      p.scale[at] = some ? own.stored : static_cast<uint16_t>(0);
+      if (ZERO) p.zero[at] = some ? static_cast<uint8_t>(own.zero) : static_cast<uint8_t>(8);
+    }
+    const uint32_t bits =
+        static_cast<uint32_t>(own.zero) | (own.none ? 32u : 0u) | (own.small ? 64u : 0u);
     uint32_t word[2] = {0u, 0u};
 #pragma unroll
-    for (int i0 = 0; i0 < 4; i0 += G32) {
-      uint32_t top = 0u;
-      float lo = 0.0f, hi = 0.0f;
+    for (int k = 0; k < GROUPS; ++k) {
+      const int from = k * (32 / GROUPS);
+      Scale sc;
+      sc.s = __shfl_sync(0xffffffffu, own.s, from);
+      sc.inv = __shfl_sync(0xffffffffu, own.inv, from);
+      const uint32_t f = __shfl_sync(0xffffffffu, bits, from);
+      sc.half = 0.5f * sc.s;
+      sc.zero = static_cast<float>(f & 15u);
+      sc.none = f & 32u, sc.small = f & 64u;
 #pragma unroll
-      for (int i = i0; i < i0 + G32; ++i) {
-        top = max(top, __float_as_uint(v[m][i]) & 0x7fffffffu);
-        if (ZERO) lo = fminf(lo, v[m][i]), hi = fmaxf(hi, v[m][i]);
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (ZERO) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-      }
-      const Scale k = scale_of<ZERO>(top, lo, hi);
-#pragma unroll
-      for (int i = i0; i < i0 + G32; ++i) {
+      for (int i = k * G32; i < (k + 1) * G32; ++i) {
         const bool held = b * kInt4Block + 32u * i + l < p.K;
         const float one[1] = {v[m][i]};
         const int order[1] = {0};
-        const uint32_t q = held ? quantise<ZERO, sizeof(T) == 2>(one, k, order) & 15u : 8u;
+        const uint32_t q = held ? quantise<ZERO, sizeof(T) == 2>(one, sc, order) & 15u : 8u;
         word[i / 2] |= q << (4 * n + 16 * (i % 2));
-      }
-      if (l == 0 && item < p.items) {
-        const int64_t at = static_cast<int64_t>(item) * (4 / G32) + i0 / G32;
-        const bool some = b * kInt4Block + 32u * i0 < p.K;
-        p.scale[at] = some ? k.stored : static_cast<uint16_t>(0);
-        if (ZERO) p.zero[at] = some ? static_cast<uint8_t>(k.zero) : static_cast<uint8_t>(8);
       }
     }
 #pragma unroll
