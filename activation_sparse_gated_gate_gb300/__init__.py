@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -72,19 +73,6 @@ class HybridStruct(ctypes.Structure):
     ]
 
 
-class Int4Struct(ctypes.Structure):
-    """Mirror of ``twell_int4_t``."""
-    _fields_ = [("rows", c_i64), ("K", c_i32), ("group", c_i32), ("code", c_ptr),
-                ("scale", c_ptr), ("zero", c_ptr)]
-
-
-class ExpertsStruct(ctypes.Structure):
-    """Mirror of ``twell_experts_t``."""
-    _fields_ = [("E", c_i32), ("F", c_i32), ("D", c_i32), ("Wg_t", c_ptr), ("Wu_t", c_ptr),
-                ("Wd", c_ptr), ("Wg4", ctypes.POINTER(Int4Struct)),
-                ("Wu4", ctypes.POINTER(Int4Struct)), ("Wd4", ctypes.POINTER(Int4Struct))]
-
-
 class TwellError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -134,13 +122,11 @@ _SIGNATURES = {
                                c_i32, c_ptr, c_i32, c_i64, c_ptr, c_ptr]),
     "twell_gate_pack_fp8": (c_i32, [c_ptr, c_i64, c_ptr, c_ptr, c_i64, c_ptr, c_i32, c_i32, c_i32,
                                     ctypes.POINTER(TwellStruct), c_ptr, c_ptr, c_ptr]),
-    "twell_quant_int4": (c_i32, [c_ptr, c_i32, c_i64, ctypes.POINTER(Int4Struct), c_ptr]),
-    "twell_dequant_int4": (c_i32, [ctypes.POINTER(Int4Struct), c_ptr, c_i32, c_i64, c_ptr]),
-    "twell_gemv_int4": (c_i32, [c_ptr, c_i64, ctypes.POINTER(Int4Struct), c_i32, c_ptr, c_i32,
-                                c_i64, c_ptr]),
-    "twell_moe_decode": (c_i32, [c_ptr, c_i32, c_ptr, c_i32, ctypes.POINTER(ExpertsStruct), c_i32,
-                                 c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_i32, c_ptr, ctypes.c_size_t,
-                                 c_ptr]),
+    "twell_quant_int4": (c_i32, [c_ptr, c_i32, c_i64, c_ptr, c_ptr]),
+    "twell_dequant_int4": (c_i32, [c_ptr, c_ptr, c_i32, c_i64, c_ptr]),
+    "twell_gemv_int4": (c_i32, [c_ptr, c_i64, c_ptr, c_i32, c_ptr, c_i32, c_i64, c_ptr]),
+    "twell_moe_decode": (c_i32, [c_ptr, c_i32, c_ptr, c_i32, c_ptr, c_i32, c_i32, c_i32, c_ptr,
+                                 c_ptr, c_ptr, c_i32, c_ptr, ctypes.c_size_t, c_ptr]),
     "twell_moe_decode_workspace": (ctypes.c_size_t, [c_i32, c_i32, c_i32, c_i32, c_i32]),
     "twell_status_string": (ctypes.c_char_p, [c_i32]),
     "twell_gate_pack_wait_limit": (ctypes.c_uint64, [ctypes.c_uint64]),
@@ -1034,28 +1020,33 @@ class Int4(NamedTuple):
         return at.reshape(*lead, nb * INT4_BLOCK)[..., :self.K].contiguous()
 
 
+# ``twell_int4_t`` and ``twell_experts_t`` as bytes: a call's descriptors are written at once
+_INT4 = struct.Struct("qiiPPP")
+_EXPERTS = struct.Struct("iii4xPPPPPP")
+
+
 def _int4(w, name, dev=None, lead=None):
-    """Check 4-bit weights; returns (descriptor, device)."""
+    """Check 4-bit weights; returns (the descriptor's fields, device)."""
     try:
         code, scale, zero, K, group = w
         if dev is None:
             dev = code.get_device()
         nb = (K + 127) // 128
-        rows = code.shape[:-1]
+        shape = code.shape
+        rows = shape[:-1]
         held = (*rows, nb * (128 // group))
         if (group in (32, 64, 128) and K > 0 and dev >= 0 and code.dtype is torch.uint8
-                and code.shape[-1] == 64 * nb and len(rows) > 0 and (lead is None or rows == lead)
+                and shape[-1] == 64 * nb and rows and (lead is None or rows == lead)
                 and code.get_device() == dev == scale.get_device() and code.is_contiguous()
                 and scale.dtype is torch.bfloat16 and scale.shape == held
-                and scale.is_contiguous()
-                and (zero is None or (zero.dtype is torch.uint8 and zero.shape == held
-                                      and zero.get_device() == dev and zero.is_contiguous()))):
-            n = 1
-            for r in rows:
-                n *= r
-            return Int4Struct(n, K, group, code.data_ptr(), scale.data_ptr(),
-                              None if zero is None else zero.data_ptr()), dev
-    except (AttributeError, IndexError, TypeError, ValueError):
+                and scale.is_contiguous()):
+            n = rows[0] if len(rows) == 1 else rows.numel()
+            if zero is None:
+                return (n, K, group, code.data_ptr(), scale.data_ptr(), 0), dev
+            if (zero.dtype is torch.uint8 and zero.shape == held and zero.get_device() == dev
+                    and zero.is_contiguous()):
+                return (n, K, group, code.data_ptr(), scale.data_ptr(), zero.data_ptr()), dev
+    except (AttributeError, IndexError, TypeError, ValueError, ZeroDivisionError):
         pass
     if not isinstance(w, Int4):
         raise TypeError(f"{name} must be an Int4")
@@ -1107,7 +1098,7 @@ def twell_quant_int4(w, group=128, zero_points=False, out=None, stream=None) -> 
     elif out.K != K or out.group != group or (out.zero is not None) != bool(zero_points):
         raise ValueError("out is of another kind: K, group and zero points are the call's")
     desc, _ = _int4(out, "out", dev, lead)
-    _run("twell_quant_int4", dev, w.data_ptr(), w_type, ld, ctypes.byref(desc))
+    _run("twell_quant_int4", dev, w.data_ptr(), w_type, ld, _INT4.pack(*desc))
     return out
 
 
@@ -1129,7 +1120,7 @@ def twell_dequant_int4(w: Int4, out=None, dtype=torch.bfloat16, stream=None):
         code, ld = _mat(out, _TYPES, "out", dev, shape)
     else:
         code = _vec(out, _TYPES, "out", dev, shape)
-    _run("twell_dequant_int4", dev, ctypes.byref(desc), out.data_ptr(), code, ld)
+    _run("twell_dequant_int4", dev, _INT4.pack(*desc), out.data_ptr(), code, ld)
     return out
 
 
@@ -1153,7 +1144,7 @@ def twell_gemv_int4(x, w: Int4, out=None, dtype=torch.bfloat16, stream=None):
         y_type, ldy = _TYPES[dtype], N
     else:
         y_type, ldy = _mat(out, _TYPES, "out", dev, (T, N))
-    _run("twell_gemv_int4", dev, x.data_ptr(), ldx, ctypes.byref(desc), T, out.data_ptr(), y_type,
+    _run("twell_gemv_int4", dev, x.data_ptr(), ldx, _INT4.pack(*desc), T, out.data_ptr(), y_type,
          ldy)
     return out
 
@@ -1161,6 +1152,7 @@ def twell_gemv_int4(x, w: Int4, out=None, dtype=torch.bfloat16, stream=None):
 # ------------------------------------------- mixture of experts
 
 _ACTS = {"relu": 0, "silu": 1}
+_MOE_WS = {}  # bytes of workspace by device and sizes
 _I32 = {torch.int32: 0}
 
 
@@ -1197,26 +1189,31 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
     _vec(x, _BF16, "x", dev, shape)
     if act not in _ACTS:
         raise ValueError("act must be 'relu' or 'silu'")
-    experts = ExpertsStruct()
+    buf = ctypes.create_string_buffer(_EXPERTS.size + 3 * _INT4.size)
+    p_experts = ctypes.addressof(buf)
     if isinstance(Wg_t, Int4):
         lead = Wg_t.code.shape[:-1]
         if len(lead) != 2:
             raise ValueError("Wg_t must be [E][F][D]")
+        at = _EXPERTS.size
         for w, name in ((Wg_t, "Wg_t"), (Wu_t, "Wu_t"), (Wd, "Wd")):
             desc, _ = _int4(w, name, dev, lead)
             if w.K != D or w.group != Wg_t.group:
                 raise ValueError(f"{name} must be of K {D} and group {Wg_t.group}, got {w.K} "
                                  f"and {w.group}")
-            setattr(experts, name[:2] + "4", ctypes.pointer(desc))
+            _INT4.pack_into(buf, at, *desc)
+            at += _INT4.size
+        E, F = lead
+        p_q = p_experts + _EXPERTS.size
+        _EXPERTS.pack_into(buf, 0, E, F, D, 0, 0, 0, p_q, p_q + _INT4.size, p_q + 2 * _INT4.size)
     else:
         if not isinstance(Wg_t, torch.Tensor) or Wg_t.dim() != 3:
             raise TypeError("Wg_t must be a tensor [E][F][D] or an Int4")
-        lead = Wg_t.shape[:2]
+        E, F, _ = shape_w = (*Wg_t.shape[:2], D)
         for w, name in ((Wg_t, "Wg_t"), (Wu_t, "Wu_t"), (Wd, "Wd")):
-            _vec(w, _BF16, name, dev, (*lead, D))
-            setattr(experts, name, w.data_ptr())
-    E, F = lead
-    experts.E, experts.F, experts.D = E, F, D
+            _vec(w, _BF16, name, dev, shape_w)
+        _EXPERTS.pack_into(buf, 0, E, F, D, Wg_t.data_ptr(), Wu_t.data_ptr(), Wd.data_ptr(), 0, 0,
+                           0)
     p_router, r_type = None, 0
     if router is not None:
         if top_k is None:
@@ -1243,11 +1240,13 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
     else:
         y_type = _vec(y, _TYPES, "y", dev, (T, D))
     if ws is None:
-        if torch._C._cuda_getDevice() == dev:
-            need = twell_moe_decode_workspace(T, D, F, E, top_k)
-        else:
+        need = _MOE_WS.get((dev, T, D, F, E, top_k))
+        if need is None:
             with torch.cuda.device(dev):
                 need = twell_moe_decode_workspace(T, D, F, E, top_k)
+            if len(_MOE_WS) >= 256:
+                _MOE_WS.clear()
+            _MOE_WS[(dev, T, D, F, E, top_k)] = need
         ws = _workspace(need, x.device)
     elif not isinstance(ws, torch.Tensor) or not ws.is_cuda:
         raise TypeError("ws must be a CUDA tensor")
@@ -1255,7 +1254,7 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
         raise ValueError("ws is on another device")
     elif not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
-    _run("twell_moe_decode", dev, x.data_ptr(), T, p_router, r_type, ctypes.byref(experts), top_k,
-         _ACTS[act], 1 if renormalise else 0, ids.data_ptr(), weights.data_ptr(), y.data_ptr(),
+    _run("twell_moe_decode", dev, x.data_ptr(), T, p_router, r_type, p_experts, top_k, _ACTS[act],
+         1 if renormalise else 0, ids.data_ptr(), weights.data_ptr(), y.data_ptr(),
          y_type, ws.data_ptr(), ws.numel() * ws.element_size())
     return Moe(y, ids, weights)
