@@ -327,67 +327,85 @@ struct Four {
   }
 };
 
-// The k largest of a token's logits and their weights, by a warp: slot `lane` of them.
-// `key`: E words of shared memory
-// of the warp's own.
-__device__ __forceinline__ void choose(const MoeParams& p, int t, uint32_t* key, int& chosen,
-                                       float& weight) {
+// The k largest of a token's logits and their weights, by a warp: slot `lane` of them.  EJ: 32s
+// of experts in a lane's registers.
+template <int EJ>
+__device__ __forceinline__ void choose(const MoeParams& p, int t, int& chosen, float& weight) {
   const int lane = threadIdx.x & 31;
   const float* logits = p.logits + static_cast<int64_t>(t) * p.E;
   const auto float_of = [](uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
   };
   bool nan = false;
-  uint32_t best = 0u;  // keys are ordered as the logits are; 1: NaN, 0: taken
-#pragma unroll 1
-  for (int e = lane; e < p.E; e += 32) {
-    const float v = __ldcg(logits + e) + 0.0f;  // (adding zero makes one zero of two)
-    const uint32_t b = __float_as_uint(v);
-    const bool bad = v != v;
-    nan |= bad;
-    key[e] = bad ? 1u : b & 0x80000000u ? ~b : b | 0x80000000u;
-    best = max(best, key[e]);
+  uint32_t key[EJ], best = 0u;  // ordered as the logits are; 1: NaN, 0: taken or none
+#pragma unroll
+  for (int j = 0; j < EJ; ++j) {
+    const int e = 32 * j + lane;
+    key[j] = 0u;
+    if (e < p.E) {
+      const float v = __ldcg(logits + e) + 0.0f;  // (adding zero makes one zero of two)
+      const uint32_t b = __float_as_uint(v);
+      const bool bad = v != v;
+      nan |= bad;
+      key[j] = bad ? 1u : b & 0x80000000u ? ~b : b | 0x80000000u;
+    }
+    best = max(best, key[j]);
   }
   nan = __any_sync(0xffffffffu, nan);
-  const float top = float_of(__reduce_max_sync(0xffffffffu, best));
-  float sum = 0.0f, mine = 0.0f;
-  if (!p.renormalise)
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) sum += expf(float_of(key[e]) - top);
+  float top = 0.0f, sum = 0.0f, mine = 0.0f;
 #pragma unroll 1
   for (int s = 0; s < p.k; ++s) {
-    best = 0u;
-    int at = 0x7fffffff;
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32)
-      if (key[e] > best) best = key[e], at = e;
     const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-    const int e = __reduce_min_sync(0xffffffffu, best == most ? at : 0x7fffffff);
+    if (s == 0) {
+      top = float_of(most);
+      if (!p.renormalise)
+#pragma unroll
+        for (int j = 0; j < EJ; ++j)
+          if (32 * j + lane < p.E) sum += expf(float_of(key[j]) - top);
+    }
+    // the lowest expert that has it is taken
+    int at = 0x7fffffff;
+    if (best == most)
+#pragma unroll
+      for (int j = EJ - 1; j >= 0; --j)
+        if (key[j] == most) at = 32 * j + lane;
+    const int e = __reduce_min_sync(0xffffffffu, at);
     if (lane == s) chosen = e, mine = float_of(most);
-    if ((e & 31) == lane) key[e] = 0u;
+    if (at == e) {
+      best = 0u;
+#pragma unroll
+      for (int j = 0; j < EJ; ++j) {
+        if (32 * j + lane == e) key[j] = 0u;
+        best = max(best, key[j]);
+      }
+    }
   }
   weight = lane < p.k ? expf(mine - top) : 0.0f;
   weight /= warp_sum(p.renormalise ? weight : sum);
   if (nan) weight = __uint_as_float(0x7fc00000u);
 }
+__device__ __forceinline__ void choose(const MoeParams& p, int t, int& chosen, float& weight) {
+  if (p.E <= 64) choose<2>(p, t, chosen, weight);
+  else if (p.E <= 128) choose<4>(p, t, chosen, weight);
+  else choose<kMaxExperts / 32>(p, t, chosen, weight);
+}
 
 // More tokens than a CTA has warps: their choice, a warp a token.
 __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant__ MoeParams p) {
-  __shared__ uint32_t key[kWarps][kMaxExperts];
   ptx::grid_launch_next();
   ptx::grid_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x * kWarps + warp;
   if (t >= p.T) return;
   int e = -1;
   float w = 0.0f;
-  choose(p, t, key[warp], e, w);
+  choose(p, t, e, w);
   if (lane < p.k) p.ids[t * p.k + lane] = e, p.weights[t * p.k + lane] = w;
 }
 
 template <int NT>
 struct Sizes {
   static constexpr int SP = 8 * NT;              // pairs (token, slot) of an expert at a time
-  static constexpr int UR = 4;                   // units of 16 neurons of a CTA at a time
+  static constexpr int UR = 8;                   // units of 16 neurons of a CTA at a time
   static constexpr int RM = 16 * UR;
   static constexpr int RING = 6 * kSlotBytes;    // of a warp, neurons kernel
   static constexpr int CHUNK = 1024 / NT;        // neurons of h in shared memory
@@ -403,8 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ __align__(16) uint8_t raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int P = p.T * p.k;
-  // Each warp's ring, which also holds what it hands to the others: its sums, the keys of its
-  // choice.
+  // Each warp's ring, which also holds the sums that it hands to the others.
   uint8_t* ring = raw + warp * RING;
   const uint32_t ring_at = ptx::smem_u32(ring);
   int4* slab = reinterpret_cast<int4*>(raw + kWarps * RING);      // [E + P / SP]
@@ -427,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp < p.T) {
       int e = -1;
       float w = 0.0f;
-      choose(p, warp, reinterpret_cast<uint32_t*>(ring), e, w);
+      choose(p, warp, e, w);
       if (lane < p.k) {
         const int at = warp * p.k + lane;
         pid[at] = e;
@@ -543,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int rows = stage ? n_act : nj;
       // a warp's two tiles: the gate and up rows of the same 16 neurons, or 32 rows of one
       const int n_tiles = silu ? (rows + 15) / 16 : (rows + 31) / 32;
-      share = n_tiles <= 2 ? n_tiles : 4;
+      share = n_tiles <= 2 ? n_tiles : n_tiles <= 4 ? 4 : 8;
       const int tile = warp & (share - 1);
       float acc[2][NT][4];
 #pragma unroll
@@ -903,22 +920,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 int pair_tiles(int32_t T) { return T <= 8 ? 1 : 2; }
 
 // The down kernel: warps side by side on columns, tiles of a CTA's columns, slabs at the most,
-// and parts of a slab's neurons.  The widest CTAs that still give every SM one (a CTA
-// loads h, waits for a chain of small reads and takes part in the tokens' sums
-// whatever it has to do); neurons are divided where CTAs of one warp's width leave SMs
-// without two, into parts of 128 neurons at least.
+// and parts of a slab's neurons.  The widest CTAs that still give every SM four, so that
+// an SM's last ones leave little of it idle (64 tokens, 4 bits: 223 us, 312 with one); or one
+// where few tokens with a ReLU leave a CTA little to do beside its chain of small reads and
+// the tokens' sums (8 tokens, 2 % active: 67 us, 69 with four).  Neurons are divided where
+// CTAs of one warp's width leave SMs without two, into parts of 128 neurons at least.
 struct Down {
   int32_t side, tiles, slabs, splits;
 };
 Down down_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t E, int32_t k,
-             bool four) {
+             bool four, bool relu) {
   const int nt = pair_tiles(T), tw = four ? 128 : 64, P = T * k;
+  const int want = relu && nt == 1 ? dev.sm_count : 4 * dev.sm_count;
   Down o;
   o.slabs = (P < E ? P : E) + P / (8 * nt);
   if (o.slabs > P) o.slabs = P;
   for (o.side = kWarps;; o.side /= 2) {
     o.tiles = (D + o.side * tw - 1) / (o.side * tw);
-    if (o.side == 1 || o.tiles * o.slabs >= 4 * dev.sm_count) break;
+    if (o.side == 1 || o.tiles * o.slabs >= want) break;
   }
   const int fill = 2 * dev.sm_count / (o.tiles * o.slabs), most = (F + 15) / 16 / 8;
   o.splits = most < fill ? most : fill;
@@ -934,10 +953,14 @@ struct Layout {
 Layout layout_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t E, int32_t k) {
   Layout l;
   const size_t P = static_cast<size_t>(T) * k, units = (static_cast<size_t>(F) + 15) / 16;
-  const Down a = down_of(dev, T, D, F, E, k, false), b = down_of(dev, T, D, F, E, k, true);
-  const size_t slabs = a.slabs,
-               splits = a.splits > b.splits ? a.splits : b.splits;
-  l.counters = T * (a.tiles > b.tiles ? a.tiles : b.tiles);
+  size_t slabs = 0, splits = 0, tiles = 0;  // of whichever form asks for most
+  for (int form = 0; form < 4; ++form) {
+    const Down o = down_of(dev, T, D, F, E, k, form & 1, form & 2);
+    slabs = slabs > static_cast<size_t>(o.slabs) ? slabs : o.slabs;
+    splits = splits > static_cast<size_t>(o.splits) ? splits : o.splits;
+    tiles = tiles > static_cast<size_t>(o.tiles) ? tiles : o.tiles;
+  }
+  l.counters = static_cast<int32_t>(T * tiles);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -962,7 +985,7 @@ twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) 
   static std::atomic<uint64_t> set[2] = {{0}, {0}};
   const int limit = dev.max_smem_optin - 8192;
   const int64_t P = static_cast<int64_t>(p.T) * p.k;
-  const Down o = down_of(dev, p.T, p.D, p.F, p.E, p.k, F::FOUR);
+  const Down o = down_of(dev, p.T, p.D, p.F, p.E, p.k, F::FOUR, p.act == TWELL_RELU);
   p.side = o.side;
   const int64_t units = o.slabs * ((static_cast<int64_t>(p.F) + 15) / 16);
   const int most = 2 * dev.sm_count;
