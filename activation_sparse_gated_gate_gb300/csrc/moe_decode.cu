@@ -302,10 +302,6 @@ struct Bf16 {
     bf16_rows<2, NT, S>(from, p.D, wk, WK, ring, nt, x, acc);
   }
   static __device__ __forceinline__ int column(int q, int h, int g) { return 8 * g + 2 * q + h; }
-  // `n` rows of Wd towards the second cache.
-  static __device__ __forceinline__ void ahead(const MoeParams& p, int64_t row, int n) {
-    ptx::prefetch_l2_bulk(p.w[2] + row * p.D, 2u * n * p.D);
-  }
 };
 template <int G>
 struct Four {
@@ -318,9 +314,6 @@ struct Four {
                                               uint32_t ring, int nt, X x, float (&acc)[2][NT][4]) {
     const Int4View* const from[2] = {&p.q[mat[0]], &p.q[mat[1]]};
     int4_rows<G, 2, NT, S>(from, at, p.D, wk, WK, ring, nt, x, acc);
-  }
-  static __device__ __forceinline__ void ahead(const MoeParams& p, int64_t row, int n) {
-    ptx::prefetch_l2_bulk(p.q[2].code + row * p.q[2].pitch, static_cast<uint32_t>(n * p.q[2].pitch));
   }
   static __device__ __forceinline__ int column(int q, int h, int g) {
     return 32 * (q >> 1) + 8 * (g >> 1) + 2 * (2 * (q & 1) + h) + (g & 1);
@@ -539,8 +532,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       xt[n] = p.x + static_cast<int64_t>(plist[s0 + min(8 * n + g, ns - 1)] / p.k) * p.D;
-    // (their rows of Wd, which the next kernel reads whatever h is, on their way)
-    if (silu && tid == 0) F::ahead(p, base + j0, nj);
 
     // ---- gate and up sums (with ReLU the gate's, then up of the active neurons):
     // `share` warps side by side on tiles of rows, the others on their columns
@@ -1051,6 +1042,7 @@ extern "C" twell_status twell_moe_decode(const uint16_t* x, int32_t T, const voi
     return TWELL_ERR_INVALID;
   const bool four = w->Wg4 != nullptr;
   const int32_t D = w->D, F = w->F, E = w->E;
+  if (four && (w->Wg_t || w->Wu_t || w->Wd)) return TWELL_ERR_INVALID;
   if (four) {
     const twell_int4_t* m[3] = {w->Wg4, w->Wu4, w->Wd4};
     for (const twell_int4_t* q : m) {
@@ -1059,7 +1051,6 @@ extern "C" twell_status twell_moe_decode(const uint16_t* x, int32_t T, const voi
       if (q->rows != static_cast<int64_t>(E) * F || q->K != D || q->group != m[0]->group)
         return TWELL_ERR_INVALID;
     }
-    if (w->Wg_t || w->Wu_t || w->Wd) return TWELL_ERR_INVALID;
   } else if (w->Wu4 || w->Wd4 || !w->Wg_t || !w->Wu_t || !w->Wd || !aligned16(w->Wg_t) ||
              !aligned16(w->Wu_t) || !aligned16(w->Wd)) {
     return TWELL_ERR_INVALID;

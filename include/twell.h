@@ -542,6 +542,7 @@ twell_status twell_gate_pack_fp8(const uint8_t* xq, int64_t ldx, const float* x_
  *   code   [rows][64 nb] bytes, 16-byte aligned
  *   scale  [rows][G] bf16
  *   zero   [rows][G] uint8 (values 0..15), or NULL: 8 everywhere
+ * scale and zero aligned to what a block has of them (8, 4 or 2 and 4, 2 or 1 bytes).
  * What belongs to columns behind K is stored (codes 8, scales of whole groups 0, their
  * zero points 8) but not used.
  */
@@ -611,13 +612,14 @@ typedef struct {
 } twell_experts_t;
 
 /*
- * A mixture-of-experts layer for a few tokens, in two kernels:
+ * A mixture-of-experts layer for a few tokens:
  *   logits = x router^T (fp32);  of each token the top_k largest, ties to the lowest
  *   expert, in falling order;  weight = softmax over the chosen (renormalise != 0) or over
  *   all E
  *   y[t] = sum over the slots of weight sum_j a(x . Wg[e][j]) (x . Wu[e][j]) Wd[e][j]
- * with a = ReLU (a neuron whose gate is not positive contributes nothing, whatever
- * its other rows hold; where it is for no token of the expert they are not read) or SiLU.
+ * with a = SiLU or ReLU (a neuron whose gate is not positive for a token contributes nothing
+ * to it, whatever its row of Wu holds; its rows of Wu and Wd are not read where that is so
+ * for all of the expert's tokens).
  *   x        [T][D] bf16
  *   router   [E][D] of router_type, or NULL: ids and weights are given
  *   ids      [T][top_k] int32, weights [T][top_k] fp32: the choice, written with a router
@@ -628,9 +630,11 @@ typedef struct {
  *   ws       twell_moe_decode_workspace(T, D, F, E, top_k) bytes, 16-byte aligned; calls
  *            that may overlap have their own
  * A NaN logit makes the token's weights NaN.  Sums and h are fp32 (h enters the last product
- * in three bf16 parts, all of its bits).  Repeated calls agree bit for bit.
+ * in three bf16 parts, all of its bits, or in two, 16 bits, where y is bf16).  Repeated calls
+ * agree bit for bit; a token's y may differ in its last bits with the tokens beside it, which
+ * decide how sums are divided.
  * D % 8 == 0, any F.  Limits (TWELL_ERR_UNSUPPORTED above): T 256, T top_k 2048, top_k 32,
- * E 512, D 16384.  T may be 0.
+ * E 512, D 16384, (E + 256) ceil(F/16) 2^23.  T may be 0.
  */
 twell_status twell_moe_decode(const uint16_t* x, int32_t T, const void* router,
                               int32_t router_type, const twell_experts_t* w, int32_t top_k,

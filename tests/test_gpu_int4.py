@@ -237,3 +237,66 @@ def test_gemv_streams_and_graph():
     x.copy_(weights(4, 512, 3, torch.bfloat16))
     graph.replay()
     assert torch.equal(out, tw.twell_gemv_int4(x, q))
+
+
+def test_refusals():
+    w = torch.randn((6, 64), device="cuda")
+    q = tw.twell_quant_int4(w, group=32, zero_points=True)
+    x = torch.randn((2, 64), device="cuda").to(torch.bfloat16)
+
+    def bad(error, f, *a, **k):
+        with pytest.raises(error):
+            f(*a, **k)
+
+    bad(TypeError, tw.twell_quant_int4, w.half())
+    bad(TypeError, tw.twell_quant_int4, w.cpu())
+    bad(ValueError, tw.twell_quant_int4, w[0])
+    bad(ValueError, tw.twell_quant_int4, w.t())
+    bad(ValueError, tw.twell_quant_int4, w[:, :0])
+    bad(ValueError, tw.twell_quant_int4, w, group=16)
+    bad(ValueError, tw.twell_quant_int4, w, group=64, out=q)
+    bad(ValueError, tw.twell_quant_int4, w, group=32, out=q)
+    bad(ValueError, tw.twell_quant_int4, w[:5], group=32, zero_points=True, out=q)
+    bad(ValueError, tw.twell_quant_int4, w.view(2, 3, 64)[:, :2], group=32)
+    bad(TypeError, tw.twell_dequant_int4, w)
+    bad(TypeError, tw.twell_dequant_int4, q, dtype=torch.float16)
+    bad(ValueError, tw.twell_dequant_int4, q, out=torch.empty((6, 63), device="cuda"))
+    bad(TypeError, tw.twell_gemv_int4, x.float(), q)
+    bad(TypeError, tw.twell_gemv_int4, x, w)
+    bad(ValueError, tw.twell_gemv_int4, x[:, :32], q)
+    bad(ValueError, tw.twell_gemv_int4, x[0], q)
+    bad(ValueError, tw.twell_gemv_int4, x, tw.twell_quant_int4(w.view(2, 3, 64), group=32))
+    bad(TypeError, tw.twell_gemv_int4, x, q, dtype=torch.float16)
+    bad(ValueError, tw.twell_gemv_int4, x, q, out=torch.empty((2, 5), device="cuda"))
+    bad(ValueError, tw.twell_gemv_int4, x, q._replace(scale=q.scale[:, :1]))
+    bad(TypeError, tw.twell_gemv_int4, x, q._replace(scale=q.scale.float()))
+    bad(TypeError, tw.twell_gemv_int4, x, q._replace(zero=q.zero.int()))
+    bad(ValueError, tw.twell_gemv_int4, x, q._replace(code=q.code[:, :32]))
+    bad(ValueError, tw.twell_gemv_int4, x, q._replace(group=20))
+    bad(TypeError, tw.twell_gemv_int4, x, q._replace(code=q.code.cpu()))
+    held = torch.empty((6 * 64 + 8,), dtype=torch.uint8, device="cuda")
+    bad(tw.TwellError, tw.twell_gemv_int4, x, q._replace(code=held[8:].view(6, 64)))
+    assert tw.twell_gemv_int4(x, q).isfinite().all()
+
+
+def test_more_than_2_31_bytes():
+    """Rows behind 2^31 bytes of codes and 2^31 elements of values."""
+    N, K = 70000, 65536
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("needs 24 GB")
+    w = torch.zeros((N, K), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w[-40:] = torch.randn((40, K), generator=g, device="cuda").to(torch.bfloat16)
+    q = tw.twell_quant_int4(w, group=64)
+    last = tw.twell_quant_int4(w[-40:].contiguous(), group=64)
+    assert torch.equal(q.code[-40:], last.code) and torch.equal(q.scale[-40:], last.scale)
+    x = torch.randn((3, K), generator=g, device="cuda").to(torch.bfloat16)
+    y = tw.twell_gemv_int4(x, q, dtype=torch.float32)
+    del w
+    check_gemv(x, last, torch.float32)
+    ref = tw.twell_gemv_int4(x, last, dtype=torch.float32)
+    assert torch.allclose(y[:, -40:], ref, rtol=1e-5, atol=1e-5 * float(ref.abs().max()))
+    assert not y[:, :-40].any()
+    v = tw.twell_dequant_int4(q)
+    assert torch.equal(v[-40:], tw.twell_dequant_int4(last)) and not v[:1000].any()

@@ -300,3 +300,85 @@ def test_no_tokens():
     r, w = layer(4, 16, 64, 16)
     o = tw.twell_moe_decode(tokens(0, 64), r, *w, top_k=2)
     assert o.y.shape == (0, 64) and o.ids.shape == (0, 2)
+
+
+# ------------------------------------------- refusals of the binding
+
+
+def test_refusals():
+    r, w = layer(4, 32, 64, 16)
+    x = tokens(3, 64)
+    four = [tw.twell_quant_int4(v, group=32) for v in w]
+    ids = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    weights = torch.ones((3, 2), device="cuda")
+
+    def bad(error, *a, **k):
+        with pytest.raises(error):
+            tw.twell_moe_decode(*a, **k)
+
+    bad(TypeError, x.float(), r, *w, top_k=2)
+    bad(ValueError, x[:, :32], r, *w, top_k=2)
+    bad(ValueError, tokens(6, 64)[::2], r, *w, top_k=2)
+    bad(ValueError, x, r, *w)
+    bad(ValueError, x, r, *w, top_k=2, act="gelu")
+    bad(ValueError, x, r[:3], *w, top_k=2)
+    bad(TypeError, x, r.half(), *w, top_k=2)
+    bad(TypeError, x, r.cpu(), *w, top_k=2)
+    bad(ValueError, x, r, w[0], w[1], w[2][:3], top_k=2)
+    bad(TypeError, x, r, w[0], w[1], w[2].float(), top_k=2)
+    bad(TypeError, x, r, w[0][0], w[1], w[2], top_k=2)
+    bad(TypeError, x, r, four[0], w[1], four[2], top_k=2)
+    bad(TypeError, x, r, w[0], four[1], w[2], top_k=2)
+    bad(ValueError, x, r, four[0], four[1], tw.twell_quant_int4(w[2], group=64), top_k=2)
+    bad(ValueError, x, r, four[0], four[1], tw.twell_quant_int4(w[2][:, :16].contiguous(),
+                                                                 group=32), top_k=2)
+    bad(ValueError, x, None, *w, ids=ids)
+    bad(ValueError, x, None, *w, weights=weights)
+    bad(TypeError, x, None, *w, ids=ids.long(), weights=weights)
+    bad(ValueError, x, None, *w, ids=ids[:2], weights=weights)
+    bad(ValueError, x, None, *w, ids=ids, weights=weights[:, :1])
+    bad(ValueError, x, r, *w, top_k=2, ids=ids[:, :1].contiguous())
+    bad(TypeError, x, r, *w, top_k=2, dtype=torch.float16)
+    bad(ValueError, x, r, *w, top_k=2, y=torch.empty((3, 32), device="cuda"))
+    bad(TypeError, x, r, *w, top_k=2, ws=torch.empty((1 << 20,)))
+    bad(tw.TwellError, x, r, *w, top_k=2, ws=torch.empty((64,), dtype=torch.uint8, device="cuda"))
+    bad(tw.TwellError, x, r, *w, top_k=5)
+    many = tokens(257, 64)
+    bad(tw.TwellError, many, r, *w, top_k=2)
+    odd = layer(2, 8, 60, 16)
+    bad(tw.TwellError, tokens(2, 60), odd[0], *odd[1], top_k=1)
+    held = torch.empty((4 * 32 * 64 + 4,), dtype=torch.bfloat16, device="cuda")
+    off = held[4:].view(4, 32, 64)   # rows off 16-byte boundaries
+    bad(tw.TwellError, x, r, off, w[1], w[2], top_k=2)
+    y = tw.twell_moe_decode(x, r, *w, top_k=2).y
+    assert y.isfinite().all()        # the context is as it was
+
+
+def test_more_than_2_31_elements():
+    """Experts behind 2^31 elements, in both forms."""
+    E, F, D = 36, 15000, 4096
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = tokens(3, D)
+    w = [torch.zeros((E, F, D), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    last = [torch.randn((F, D), generator=g, device="cuda") / D ** 0.5 for _ in range(3)]
+    for a, b in zip(w, last):
+        a[E - 1] = b
+    ids = torch.full((3, 1), E - 1, dtype=torch.int32, device="cuda")
+    one = torch.zeros_like(ids)
+    weights = torch.ones((3, 1), device="cuda")
+    small = [v[E - 1:].contiguous() for v in w]
+    # (a single expert's products are divided as one of many are: the same bits)
+    y = tw.twell_moe_decode(x, None, *w, ids=ids, weights=weights).y
+    ref = tw.twell_moe_decode(x, None, *small, ids=one, weights=weights)
+    assert y.any() and torch.allclose(y, ref.y, rtol=1e-5, atol=1e-5 * float(ref.y.abs().max()))
+    four = []
+    for i in range(3):
+        four.append(tw.twell_quant_int4(w[i]))
+        w[i] = None
+    y = tw.twell_moe_decode(x, None, *four, ids=ids, weights=weights).y
+    small = [tw.Int4(q.code[E - 1:].clone(), q.scale[E - 1:].clone(), None, D, 128) for q in four]
+    ref = tw.twell_moe_decode(x, None, *small, ids=one, weights=weights)
+    assert y.any() and torch.allclose(y, ref.y, rtol=1e-5, atol=1e-5 * float(ref.y.abs().max()))
