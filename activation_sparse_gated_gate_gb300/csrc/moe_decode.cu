@@ -926,6 +926,7 @@ Down down_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t E, 
   Down o;
   o.slabs = (P < E ? P : E) + P / (8 * nt);
   if (o.slabs > P) o.slabs = P;
+  if (o.slabs < 1) o.slabs = 1;  // (no tokens)
   for (o.side = kWarps;; o.side /= 2) {
     o.tiles = (D + o.side * tw - 1) / (o.side * tw);
     if (o.side == 1 || o.tiles * o.slabs >= want) break;
@@ -1025,7 +1026,14 @@ extern "C" size_t twell_moe_decode_workspace(int32_t T, int32_t D, int32_t F, in
     return 0;
   DeviceInfo dev;
   if (!current_device(&dev)) return 0;
-  return layout_of(dev, T, D, F, E, top_k).total;
+  // A layout may need more than that of a larger batch, whose neurons are in fewer parts: the
+  // workspace is enough for any up to T.
+  size_t most = 0;
+  for (int32_t t = 0; t <= T; ++t) {
+    const size_t total = layout_of(dev, t, D, F, E, top_k).total;
+    most = most > total ? most : total;
+  }
+  return most;
 }
 
 extern "C" twell_status twell_moe_decode(const uint16_t* x, int32_t T, const void* router,

@@ -641,7 +641,8 @@ twell_status twell_moe_decode(const uint16_t* x, int32_t T, const void* router,
                               int32_t act, int32_t renormalise, int32_t* ids, float* weights,
                               void* y, int32_t y_type, void* ws, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace of twell_moe_decode on the current device (0 on bad arguments). */
+/* Bytes of workspace of twell_moe_decode on the current device (0 on bad arguments), enough
+ * for T tokens and for any fewer. */
 size_t twell_moe_decode_workspace(int32_t T, int32_t D, int32_t F, int32_t E, int32_t top_k);
 
 /*

@@ -302,6 +302,20 @@ def test_no_tokens():
     assert o.y.shape == (0, 64) and o.ids.shape == (0, 2)
 
 
+def test_workspace_of_the_largest_batch():
+    """One workspace for a loop whose batch shrinks, though fewer tokens are divided into more
+    parts: 15 tokens and one expert are one slab in 8 parts, 16 may be two slabs in 4."""
+    D, F, E, k = 2048, 1200, 1, 1
+    sizes = [tw.twell_moe_decode_workspace(T, D, F, E, k) for T in range(41)]
+    assert sizes == sorted(sizes) and sizes[1] > 0
+    ws = torch.full((sizes[16],), 255, dtype=torch.uint8, device="cuda")
+    r, w = layer(E, F, D, 16, seed=2)
+    x = tokens(16, D)
+    for T in (16, 15, 9, 8, 1, 0):
+        o = tw.twell_moe_decode(x[:T], r, *w, top_k=k, ws=ws)
+        assert torch.equal(o.y, tw.twell_moe_decode(x[:T], r, *w, top_k=k).y)
+
+
 # ------------------------------------------- refusals of the binding
 
 
