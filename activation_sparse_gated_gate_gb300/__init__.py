@@ -1035,7 +1035,8 @@ def _int4(w, name, dev=None, lead=None):
         shape = code.shape
         rows = shape[:-1]
         held = (*rows, nb * (128 // group))
-        if (group in (32, 64, 128) and K > 0 and dev >= 0 and code.dtype is torch.uint8
+        if (isinstance(w, Int4) and group in (32, 64, 128) and isinstance(K, int) and K > 0
+                and dev >= 0 and code.dtype is torch.uint8
                 and shape[-1] == 64 * nb and rows and (lead is None or rows == lead)
                 and code.get_device() == dev == scale.get_device() and code.is_contiguous()
                 and scale.dtype is torch.bfloat16 and scale.shape == held
@@ -1095,6 +1096,8 @@ def twell_quant_int4(w, group=128, zero_points=False, out=None, stream=None) -> 
                    torch.empty(held, dtype=torch.bfloat16, device=w.device),
                    torch.empty(held, dtype=torch.uint8, device=w.device) if zero_points else None,
                    K, group)
+    elif not isinstance(out, Int4):
+        raise TypeError("out must be an Int4")
     elif out.K != K or out.group != group or (out.zero is not None) != bool(zero_points):
         raise ValueError("out is of another kind: K, group and zero points are the call's")
     desc, _ = _int4(out, "out", dev, lead)

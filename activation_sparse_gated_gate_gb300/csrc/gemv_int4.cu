@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     const int64_t r = min(row0 + 8 * h + g, static_cast<int64_t>(p.N - 1));
     code[h] = p.w.code + r * p.w.pitch + b0 * kInt4Bytes + 16 * c;
     scale[h] = p.w.scale + r * p.w.held + b0 * GROUPS;
-    zero[h] = p.w.zero ? p.w.zero + r * p.w.held + b0 * GROUPS : nullptr;
+    // (without zero points it is never read)
+    zero[h] = (p.w.zero ? p.w.zero : p.w.code) + r * p.w.held + b0 * GROUPS;
   }
   typename std::conditional<XV, Rows16<NT>, RowsAny<NT>>::type x;
 #pragma unroll

@@ -274,6 +274,10 @@ def test_refusals():
     bad(ValueError, tw.twell_gemv_int4, x, q._replace(code=q.code[:, :32]))
     bad(ValueError, tw.twell_gemv_int4, x, q._replace(group=20))
     bad(TypeError, tw.twell_gemv_int4, x, q._replace(code=q.code.cpu()))
+    bad(TypeError, tw.twell_gemv_int4, x, tuple(q))
+    bad(TypeError, tw.twell_dequant_int4, tuple(q))
+    bad(TypeError, tw.twell_quant_int4, w, group=32, zero_points=True, out=tuple(q))
+    bad(ValueError, tw.twell_gemv_int4, x, q._replace(K=64.0))
     held = torch.empty((6 * 64 + 8,), dtype=torch.uint8, device="cuda")
     bad(tw.TwellError, tw.twell_gemv_int4, x, q._replace(code=held[8:].view(6, 64)))
     assert tw.twell_gemv_int4(x, q).isfinite().all()
