@@ -107,12 +107,17 @@ struct BlockScales {
   }
   // Those that another lane has loaded.
   __device__ __forceinline__ void from_lane(const BlockScales& o, int lane) {
+    if constexpr (G32 == 4) {  // both in one word (the scale is its low half)
+      s[0] = __shfl_sync(0xffffffffu, o.s[0] | o.z << 16, lane);
+      z = s[0] >> 16;
+      return;
+    }
     s[0] = __shfl_sync(0xffffffffu, o.s[0], lane);
     if constexpr (G32 == 1) s[1] = __shfl_sync(0xffffffffu, o.s[1], lane);
     z = __shfl_sync(0xffffffffu, o.z, lane);
   }
   __device__ __forceinline__ float scale(int k) const {
-    return __uint_as_float(k & 1 ? s[k / 2] & 0xffff0000u : s[k / 2] << 16);
+    return __uint_as_float(k & 1 ? s[k / 2] & 0xffff0000u : s[k / 2] << 16);  // (k = 0 of 128)
   }
   // 128 + zero as bf16, in both halves (zero points are below 16)
   __device__ __forceinline__ uint32_t bias(int k) const {

@@ -49,25 +49,23 @@ struct RouterParams {
   int32_t counters;
 };
 
+// The logits of EX experts for TT tokens: its four warps take every fourth 256 columns.
 template <typename W, int EX, int TT>
 __global__ void __launch_bounds__(128) router_kernel(const RouterParams p) {
+  constexpr int N = EX * TT;
   ptx::grid_launch_next();
   for (int i = blockIdx.x * 128 + threadIdx.x; i < p.counters; i += gridDim.x * 128)
     p.count[i] = 0;
   if (!p.w) return;
-  const int lane = threadIdx.x & 31;
-  const int eg = (p.E + EX - 1) / EX, tg = (p.T + TT - 1) / TT;
-  const int job = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (job >= eg * tg) return;
-  const int e0 = job % eg * EX, t0 = job / eg * TT;
-  float acc[EX][TT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int eg = (p.E + EX - 1) / EX;
+  const int e0 = blockIdx.x % eg * EX, t0 = blockIdx.x / eg * TT;
+  float acc[N];
 #pragma unroll
-  for (int e = 0; e < EX; ++e)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[e][t] = 0.0f;
+  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
   const W* w = static_cast<const W*>(p.w);
-#pragma unroll(EX* TT == 1 ? 4 : 1)
-  for (int k = 8 * lane; k < p.D; k += 256) {
+#pragma unroll(N == 1 ? 2 : 1)
+  for (int k = 256 * warp + 8 * lane; k < p.D; k += 1024) {
     float wf[EX][8];
 #pragma unroll
     for (int e = 0; e < EX; ++e)
@@ -79,17 +77,18 @@ __global__ void __launch_bounds__(128) router_kernel(const RouterParams p) {
 #pragma unroll
       for (int e = 0; e < EX; ++e)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[e][t] = fmaf(wf[e][j], xf[j], acc[e][t]);
+        for (int j = 0; j < 8; ++j)
+          acc[e * TT + t] = fmaf(wf[e][j], xf[j], acc[e * TT + t]);
     }
   }
-#pragma unroll
-  for (int e = 0; e < EX; ++e)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const float v = warp_sum(acc[e][t]);
-      if (lane == 0 && e0 + e < p.E && t0 + t < p.T)
-        p.logits[static_cast<int64_t>(t0 + t) * p.E + e0 + e] = v;
-    }
+  __shared__ float sum[4][N];
+  const float v = over_warp(acc, [](float a, float b) { return a + b; });
+  if (lane % (32 / N) == 0) sum[warp][lane / (32 / N)] = v;
+  __syncthreads();
+  const int e = e0 + threadIdx.x / TT, t = t0 + threadIdx.x % TT;
+  if (threadIdx.x < N && e < p.E && t < p.T)
+    p.logits[static_cast<int64_t>(t) * p.E + e] = sum[0][threadIdx.x] + sum[1][threadIdx.x] +
+                                                  sum[2][threadIdx.x] + sum[3][threadIdx.x];
 }
 
 // ------------------------------------------------------------------ experts
@@ -102,8 +101,10 @@ struct Plan {
   int32_t* list;      // [T k] pairs, sorted by expert
   int32_t* live;      // [T] slots that have an expert
   uint16_t* masks;    // [slabs][units] ReLU: a bit for each active neuron of a unit of 16
-  void* h;            // [T k][16 units] by place in the list: fp32 (4-bit weights), or three
-                      // planes of bf16 whose sum it is
+  // h of each eight pairs of a slab, one after the other ([tile][16 units][8]): fp32 (4-bit
+  // weights), or three planes of bf16 whose sum it is, `plane` elements apart
+  void* h;
+  int64_t plane;
 };
 
 struct MoeParams {
@@ -123,17 +124,22 @@ struct MoeParams {
   int32_t y_f32;
 };
 
-// What is left of a value behind its upper half (nothing of an infinity).
+// Where a slab's h begins, in tiles of eight pairs (each slab's last may not be whole).
+__host__ __device__ inline int64_t first_tile(int slab, int pair) {
+  return (pair + 7 * static_cast<int64_t>(slab)) / 8;
+}
+
+// What is left of a value behind its upper half.
 __device__ __forceinline__ float behind(float a) {
-  const float hi = __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-  return fabsf(a) == __uint_as_float(0x7f800000u) ? 0.0f : a - hi;
+  return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
 }
 
 // Two values as three bf16 each, whose sum they are (to their 24 bits).  Two hold 16 bits:
 // enough where y is rounded to bf16.
 __device__ __forceinline__ void split(float a, float b, bool three, uint32_t (&o)[3]) {
   o[0] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-  a = behind(a), b = behind(b);
+  const float inf = __uint_as_float(0x7f800000u);
+  a = fabsf(a) == inf ? 0.0f : behind(a), b = fabsf(b) == inf ? 0.0f : behind(b);
   o[2] = 0u;
   if (three) {
     o[1] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
@@ -152,6 +158,29 @@ __device__ __forceinline__ void mma_split(float (&d)[4], uint32_t a0, uint32_t a
   mma16816(d, a0, a1, a2, a3, b0[0], b1[0]);
 }
 
+__device__ __forceinline__ uint64_t offset(int row, int64_t pitch) {
+  return static_cast<uint64_t>(static_cast<uint32_t>(row)) * static_cast<uint32_t>(pitch);
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+// 8 x 8 tiles of bf16, transposed: rows of 16 bytes at the addresses of lanes 0 to 7, 8 to 15 ...
+__device__ __forceinline__ void ldmatrix_x2_t(uint32_t at, uint32_t& a, uint32_t& b) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+               : "=r"(a), "=r"(b)
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c,
+                                              uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(at)
+               : "memory");
+}
+
 // A step of the sums over neurons: 16 of them by a tile of columns.  Lane (g, c) uses the
 // neurons 2 c, 2 c + 1, 2 c + 8, 2 c + 9, 16 bytes of bf16 each or 8 of 4-bit codes.  The warp
 // copies them into a slot of its ring by whole lines (row_of(r): row of the r-th neuron, absent
@@ -161,27 +190,29 @@ __device__ __forceinline__ void mma_split(float (&d)[4], uint32_t a0, uint32_t a
 struct Bf16Step {
   static constexpr int BYTES = 2 * kSlotBytes;
   struct Scales {
-    __device__ __forceinline__ void load(const MoeParams&, int64_t, int) {}
+    __device__ __forceinline__ void load(const MoeParams&, int64_t, int, int) {}
   };
   // piece g of neuron r
   static __device__ __forceinline__ uint32_t at(int r, int g) {
     return 128 * r + 16 * (g ^ (r & 6));
   }
   template <typename R>
-  static __device__ __forceinline__ void copy(const MoeParams& p, R row_of, int d0, uint32_t slot) {
+  static __device__ __forceinline__ void copy(const MoeParams& p, int64_t base, R row_of, int d0,
+                                              uint32_t slot) {
     const int lane = threadIdx.x & 31, g = lane & 7, d = d0 + 8 * g;
+    const uint16_t* from = p.w[2] + base * p.D + d;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      const int64_t row = row_of(r);
+      const int r = 4 * i + (lane >> 3), row = row_of(r);
       const bool in = row >= 0 && d < p.D;
-      cp_async16_or_zero(slot + at(r, g), p.w[2] + (in ? row * p.D + d : 0), in);
+      cp_async16_or_zero(slot + at(r, g), in ? from + offset(row, p.D) : p.w[2], in);
     }
   }
-  // h_of(i, half, n): part i of h of neurons 2 c, 2 c + 1 (half 0) or those 8 on
-  template <int NT, typename H>
-  static __device__ __forceinline__ void add(uint32_t slot, const Scales&, H h_of, int nt,
-                                             bool three, float (&acc)[4][NT][4]) {
+  // h of a chunk in shared memory: [part][tile][neuron][8 pairs] of bf16
+  static constexpr int H_ROW = 16;
+  template <int NT, int CHUNK>
+  static __device__ __forceinline__ void add(uint32_t slot, const Scales&, uint32_t hs, int st,
+                                             int nt, bool three, float (&acc)[4][NT][4]) {
     const int lane = threadIdx.x & 31;
     uint4 v[4];
 #pragma unroll
@@ -195,9 +226,10 @@ struct Bf16Step {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n >= nt) break;
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < 2 || three) b0[n][i] = h_of(i, 0, n), b1[n][i] = h_of(i, 1, n);
+      // (lanes 16 to 31: the rows of the second part)
+      const uint32_t from = hs + ((lane >> 4) * NT * CHUNK + n * CHUNK + 16 * st + (lane & 15)) * H_ROW;
+      ldmatrix_x4_t(from, b0[n][0], b1[n][0], b0[n][1], b1[n][1]);
+      if (three) ldmatrix_x2_t(from + 2 * NT * CHUNK * H_ROW, b0[n][2], b1[n][2]);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -217,33 +249,41 @@ struct FourStep {
   typedef BlockScales<G32> One;
   struct Scales {
     One one;  // of neuron `lane & 15`
-    __device__ __forceinline__ void load(const MoeParams& p, int64_t row, int d0) {
-      one.load(p.q[2], (row >= 0 ? row : 0) * p.q[2].held + d0 / kInt4Block * (4 / G32));
+    __device__ __forceinline__ void load(const MoeParams& p, int64_t base, int row, int d0) {
+      one.load(p.q[2], base * p.q[2].held + offset(max(row, 0), p.q[2].held) +
+                           d0 / kInt4Block * (4 / G32));
       if (row < 0) one.clear();  // (no product with a scale that is not finite)
     }
   };
+  // where a neuron's h is: those of the four lanes of a quarter warp in different banks
+  static __device__ __forceinline__ int place(int r) { return r ^ (r >> 2 & 1); }
   // 16-byte piece q of neuron r: even neurons in the slot's first half
   static __device__ __forceinline__ uint32_t at(int r, int q) {
     const int pos = (r >> 1) + 8 * (r & 1);
     return 64 * pos + 16 * (q ^ (pos & 2));
   }
   template <typename R>
-  static __device__ __forceinline__ void copy(const MoeParams& p, R row_of, int d0, uint32_t slot) {
+  static __device__ __forceinline__ void copy(const MoeParams& p, int64_t base, R row_of, int d0,
+                                              uint32_t slot) {
     const Int4View& w = p.q[2];
     const int lane = threadIdx.x & 31, q = lane & 3;
-    const uint8_t* from = w.code + d0 / kInt4Block * kInt4Bytes + 16 * q;
+    const uint8_t* from = w.code + base * w.pitch + d0 / kInt4Block * kInt4Bytes + 16 * q;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      const int64_t row = row_of(r);
-      cp_async16_or_zero(slot + at(r, q), from + (row >= 0 ? row * w.pitch : 0), row >= 0);
+      const int r = 8 * i + (lane >> 2), row = row_of(r);
+      cp_async16_or_zero(slot + at(r, q), row >= 0 ? from + offset(row, w.pitch) : w.code, row >= 0);
     }
   }
-  // h_of(i, n): h of the lane's neuron i
-  template <int NT, typename H>
-  static __device__ __forceinline__ void add(uint32_t slot, const Scales& sc, H h_of, int nt,
-                                             bool three, float (&acc)[8][NT][4]) {
+  // h of a chunk in shared memory: [tile][place(neuron)][8 pairs] of fp32
+  static constexpr int H_ROW = 32;
+  template <int NT, int CHUNK>
+  static __device__ __forceinline__ void add(uint32_t slot, const Scales& sc, uint32_t hs, int st,
+                                             int nt, bool three, float (&acc)[8][NT][4]) {
     const int lane = threadIdx.x & 31, c = lane & 3;
+    const uint32_t h0 = hs + 16 * st * H_ROW + (lane >> 2) * 4;
+    const auto h_of = [&](int i, int n) {
+      return lds_f32(h0 + (n * CHUNK + place(2 * c + (i & 1)) + 8 * (i >> 1)) * H_ROW);
+    };
     uint32_t v[4][2];
     One s[4];
 #pragma unroll
@@ -400,9 +440,9 @@ struct Sizes {
   static constexpr int SP = 8 * NT;              // pairs (token, slot) of an expert at a time
   static constexpr int UR = 8;                   // units of 16 neurons of a CTA at a time
   static constexpr int RM = 16 * UR;
+  static constexpr int ZP = NT == 1 ? 8 : 24;    // between neurons' gate sums (no bank twice)
   static constexpr int RING = 6 * kSlotBytes;    // of a warp, neurons kernel
   static constexpr int CHUNK = 1024 / NT;        // neurons of h in shared memory
-  static constexpr int HS = CHUNK + 8;           // between pairs of it (no bank twice)
   static constexpr int RING2 = 6 * kSlotBytes;   // of a warp, down kernel
 };
 
@@ -410,7 +450,7 @@ template <typename F, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     neurons_kernel(const __grid_constant__ MoeParams p) {
   typedef Sizes<NT> Z;
-  constexpr int SP = Z::SP, UR = Z::UR, RM = Z::RM, RING = Z::RING;
+  constexpr int SP = Z::SP, UR = Z::UR, RM = Z::RM, RING = Z::RING, ZP = Z::ZP;
   extern __shared__ __align__(16) uint8_t raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int P = p.T * p.k;
@@ -418,14 +458,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* ring = raw + warp * RING;
   const uint32_t ring_at = ptx::smem_u32(ring);
   int4* slab = reinterpret_cast<int4*>(raw + kWarps * RING);      // [E + P / SP]
-  float* zb = reinterpret_cast<float*>(slab + p.E + P / SP);      // [RM][SP + 1]
-  int32_t* count = reinterpret_cast<int32_t*>(zb + RM * (SP + 1));  // [E] pairs of an expert
+  float* zb = reinterpret_cast<float*>(slab + p.E + P / SP);      // [RM][ZP] gate sums (ReLU)
+  int32_t* count = reinterpret_cast<int32_t*>(zb + RM * ZP);      // [E] pairs of an expert
   int32_t* pid = count + p.E;                         // [P]
   int32_t* plist = pid + P;                           // [P] pairs by expert
   int32_t* place = plist + P;                         // [P] a pair's among its expert's
   int32_t* live = place + P;                          // [T]
   __shared__ int16_t act[RM];                         // active rows of this round
-  __shared__ int32_t sh_slabs, sh_act;
+  __shared__ uint32_t sh_mask[kWarps];                // those of a unit
+  __shared__ int32_t sh_slabs;
 
   ptx::grid_launch_next();
   for (int i = tid; i < p.E; i += kThreads) count[i] = 0;
@@ -536,14 +577,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- gate and up sums (with ReLU the gate's, then up of the active neurons):
     // `share` warps side by side on tiles of rows, the others on their columns
     int n_act = silu ? nj : 0, share = 1;
-    // the sum of a tile's half m, row r of it, pair n
-    const auto sum_at = [&](int tile, int m, int r, int n) {
-      const int at =
-          (((m * NT + (n >> 3)) * 32 + (r & 7) * 4 + (n & 7) / 2) * 4) + (r >> 3) * 2 + (n & 1);
-      float v = 0.0f;
-#pragma unroll 1
-      for (int w = tile; w < kWarps; w += share)
-        v += reinterpret_cast<const float*>(raw + w * RING)[at];
+    // The sum of a tile's half m for the eight pairs n: rows g and g + 8 (x, y and z, w) of
+    // its 16, pairs 2 c and 2 c + 1.  Warp w looks after the w-th 16 rows.
+    const int c = lane & 3;
+    const auto sum_of = [&](int tile, int m, int n) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+      for (int w = tile; w < kWarps; w += share) {
+        const float4 u = reinterpret_cast<const float4*>(raw + w * RING)[(m * NT + n) * 32 + lane];
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
       return v;
     };
 #pragma unroll 1
@@ -583,62 +626,84 @@ __global__ void __launch_bounds__(kThreads, 2)
               make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
       __syncthreads();
       if (silu || stage) break;
-#pragma unroll 1
-      for (int i = tid; i < nj * SP; i += kThreads) {
-        const int r = i / SP, n = i % SP;
-        if (n < ns) zb[r * (SP + 1) + n] = sum_at(r >> 5, (r >> 4) & 1, r & 15, n);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        int n = 0;
-#pragma unroll 1
-        for (int q = lane; q - lane < nj; q += 32) {
-          bool on = false;
-          if (q < nj)
-#pragma unroll 1
-            for (int i = 0; i < ns; ++i) on |= !(zb[q * (SP + 1) + i] <= 0.0f);
-          const uint32_t m = __ballot_sync(0xffffffffu, on);
-          if (on) act[n + __popc(m & ((1u << lane) - 1u))] = static_cast<int16_t>(q);
-          n += __popc(m);
-          const int u = u0 + q / 16;
-          if ((lane & 15) == 0 && q < nj)
-            p.plan.masks[static_cast<int64_t>(a) * units + u] = static_cast<uint16_t>(m >> lane);
+      uint32_t mask = 0u;
+      if (16 * warp < nj) {
+        bool lo = false, hi = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n >= nt_used) break;
+          const float4 z = sum_of(warp >> 1, warp & 1, n);
+          const bool one = 8 * n + 2 * c < ns, two = 8 * n + 2 * c + 1 < ns;
+          lo |= (one && !(z.x <= 0.0f)) || (two && !(z.y <= 0.0f));
+          hi |= (one && !(z.z <= 0.0f)) || (two && !(z.w <= 0.0f));
+          float2* to = reinterpret_cast<float2*>(zb + (16 * warp + g) * ZP + 8 * n + 2 * c);
+          to[0] = make_float2(z.x, z.y);
+          to[8 * ZP / 2] = make_float2(z.z, z.w);
         }
-        if (lane == 0) sh_act = n;
+        // (ballots: the four lanes of a row beside one another)
+        const uint32_t b_lo = __ballot_sync(0xffffffffu, lo), b_hi = __ballot_sync(0xffffffffu, hi);
+        const uint32_t of = (lane & 8 ? b_hi : b_lo) >> (4 * (lane & 7)) & 15u;
+        mask = __ballot_sync(0xffffffffu, lane < 16 && 16 * warp + lane < nj && of != 0u);
+        if (lane == 0)
+          p.plan.masks[static_cast<int64_t>(a) * units + u0 + warp] = static_cast<uint16_t>(mask);
+      }
+      if (lane == 0) sh_mask[warp] = mask;
+      __syncthreads();
+      n_act = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w == warp && (mask >> lane & 1u))
+          act[n_act + __popc(mask & ((1u << lane) - 1u))] = static_cast<int16_t>(16 * warp + lane);
+        n_act += __popc(sh_mask[w]);
       }
       __syncthreads();
-      n_act = sh_act;
       if (n_act == 0) break;
     }
 
-    // ---- h (of neurons behind F: 0)
-    const int rows = silu ? nu * 16 : n_act;
-#pragma unroll 1
-    for (int i = tid; i < ns * RM; i += kThreads) {
-      const int n = i / RM, r = i % RM;
-      if (r >= rows) continue;
-      float h = 0.0f;
-      int j = r;
-      if (silu) {
-        if (r < nj) {
-          const float z = sum_at(r >> 4, 0, r & 15, n);
-          h = z / (1.0f + expf(-z)) * sum_at(r >> 4, 1, r & 15, n);
-        }
-      } else {
-        j = act[r];
-        const float z = zb[j * (SP + 1) + n];
-        h = z <= 0.0f ? 0.0f : z * sum_at(r >> 5, (r >> 4) & 1, r & 15, n);
-      }
-      const int64_t at = static_cast<int64_t>(s0 + n) * (16 * units) + j0 + j;
-      if constexpr (F::FOUR) {
-        static_cast<float*>(p.plan.h)[at] = h;
-      } else {
-        uint32_t o[3];
-        split(h, 0.0f, p.y_f32 != 0, o);
-        uint16_t* to = static_cast<uint16_t*>(p.plan.h) + at;
-        const int64_t plane = static_cast<int64_t>(P) * (16 * units);
+    // ---- h
+    const int rows = silu ? nj : n_act;
+    if (16 * warp < rows) {
+      const int r[2] = {16 * warp + g, 16 * warp + g + 8};
+      int j[2];
 #pragma unroll
-        for (int q = 0; q < 3; ++q) to[q * plane] = static_cast<uint16_t>(o[q]);
+      for (int i = 0; i < 2; ++i) j[i] = silu || r[i] >= rows ? min(r[i], nj - 1) : act[r[i]];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= nt_used) break;
+        float z[4], h[4];
+        if (silu) {
+          const float4 s = sum_of(warp, 0, n), v = sum_of(warp, 1, n);
+          z[0] = s.x, z[1] = s.y, z[2] = s.z, z[3] = s.w;
+          h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] *= z[i] / (1.0f + expf(-z[i]));
+        } else {
+          const float4 v = sum_of(warp >> 1, warp & 1, n);
+          h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            z[i] = zb[j[i >> 1] * ZP + 8 * n + 2 * c + (i & 1)];
+            h[i] = z[i] <= 0.0f ? 0.0f : z[i] * h[i];
+          }
+        }
+        if (8 * n + 2 * c >= ns) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (r[i] >= rows) continue;
+          const int64_t at =
+              ((first_tile(a, s0) + n) * (16 * units) + (j0 + j[i])) * 8 + 2 * c;
+          if constexpr (F::FOUR) {
+            *reinterpret_cast<float2*>(static_cast<float*>(p.plan.h) + at) =
+                make_float2(h[2 * i], h[2 * i + 1]);
+          } else {
+            uint32_t o[3];
+            split(h[2 * i], h[2 * i + 1], p.y_f32 != 0, o);
+            uint16_t* to = static_cast<uint16_t*>(p.plan.h) + at;
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+              if (q < 2 || p.y_f32) *reinterpret_cast<uint32_t*>(to + q * p.plan.plane) = o[q];
+          }
+        }
       }
     }
     __syncthreads();
@@ -650,17 +715,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     down_kernel(const __grid_constant__ MoeParams p) {
   typedef Sizes<NT> Z;
   typedef typename F::Step Step;
-  constexpr int SP = Z::SP, CHUNK = Z::CHUNK, HS = Z::HS, TW = F::COLS, MT = TW / 16;
+  constexpr int SP = Z::SP, CHUNK = Z::CHUNK, TW = F::COLS, MT = TW / 16, HR = Step::H_ROW;
   constexpr int SB = Z::RING2 / Step::BYTES;  // steps in a warp's ring
   extern __shared__ __align__(16) uint8_t raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, c = lane & 3;
   const int WC = p.side, WN = kWarps / WC, CW = TW * WC;  // (WC a power of two)
   const int wc = warp & (WC - 1), wn = warp / WC;
-  // The rings and h ([SP][HS] fp32, or three planes of bf16); at the end the warps' sums
-  // [warp][NT MT 4][32].
+  // The rings and h of a chunk; at the end the warps' sums [warp][NT MT 4][32].
   const uint32_t ring_at = ptx::smem_u32(raw + warp * Z::RING2);
-  uint8_t* hs = raw + kWarps * Z::RING2;
+  const uint32_t hs = ptx::smem_u32(raw + kWarps * Z::RING2);
   float* red = reinterpret_cast<float*>(raw);
   __shared__ int16_t list[CHUNK];  // ReLU: the chunk's active neurons
   __shared__ int32_t sh_n, sh_done, done[SP], pairs[SP], expect[SP];
@@ -726,49 +789,33 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
       total = sh_n;
     }
-    // (else the list is 0, 1, 2 ..., and h is there for whole steps)
-    const bool some = total < whole || (relu && whole % 16);
+    const bool some = total < whole;  // (else the list is 0, 1, 2 ...)
     const int steps = (total + 15) / 16;
     const int64_t row0 = base + 16 * u0;
     const auto neuron = [&](int s) { return some ? list[s] : s; };
 
-    // h of the chunk, its places up to a whole step 0 (of absent pairs: anything, each
-    // pair is a column of its own)
-    const int64_t pitch = 16 * static_cast<int64_t>(units);  // of a pair's h
-    const int planes = F::FOUR ? 1 : three ? 3 : 2;
-    constexpr int BYTES = F::FOUR ? 4 : 2, EACH = 16 / BYTES;
+    // h of the chunk, up to a whole step (of absent pairs: anything, each pair is a column of
+    // its own)
+    const int64_t tile = static_cast<int64_t>(16 * units) * HR;
     const uint8_t* from =
-        static_cast<const uint8_t*>(p.plan.h) + BYTES * (s0 * pitch + 16 * u0);
-    const int64_t plane = BYTES * pitch * p.T * p.k;
-    const uint32_t to = ptx::smem_u32(hs);
-    if (!some) {
-      const int pieces = 16 / EACH * steps;
+        static_cast<const uint8_t*>(p.plan.h) + first_tile(a, s0) * tile + 16 * u0 * HR;
 #pragma unroll 1
-      for (int q = 0; q < planes; ++q)
-#pragma unroll 1
-        for (int n = 0; n < ns; ++n)
-#pragma unroll 1
-          for (int s = tid; s < pieces; s += kThreads)
-            cp_async16_or_zero(to + BYTES * (q * SP + n) * HS + 16 * s,
-                               from + q * plane + BYTES * (n * pitch) + 16 * s, true);
-    } else {
-#pragma unroll 1
-      for (int s = tid; s < 16 * steps; s += kThreads) {
-        const bool on = s < total;
-        const int j = on ? list[s] : 0;
+    for (int s = tid; s < 16 * steps; s += kThreads) {
+      const bool on = s < total;
+      const uint8_t* src = from + (on ? neuron(s) : 0) * HR;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= nt_used) break;
         if constexpr (F::FOUR) {
-#pragma unroll 1
-          for (int n = 0; n < ns; ++n)
-            cp_async4_or_zero(to + 4 * (n * HS + s), from + 4 * (n * pitch + j), on);
+          const uint32_t to = hs + (n * CHUNK + Step::place(s)) * HR;
+          cp_async16_or_zero(to, src + n * tile, on);
+          if (8 * n + 4 < ns) cp_async16_or_zero(to + 16, src + n * tile + 16, on);
         } else {
-          uint16_t* at = reinterpret_cast<uint16_t*>(hs) + s;
-#pragma unroll 1
-          for (int q = 0; q < planes; ++q)
-#pragma unroll 8
-            for (int n = 0; n < ns; ++n)
-              at[(q * SP + n) * HS] =
-                  on ? __ldcg(reinterpret_cast<const uint16_t*>(from + q * plane) + n * pitch + j)
-                     : 0;
+          const uint32_t to = hs + (n * CHUNK + s) * HR;
+#pragma unroll
+          for (int q = 0; q < 3; ++q)
+            if (q < 2 || three)
+              cp_async16_or_zero(to + q * NT * CHUNK * HR, src + n * tile + q * 2 * p.plan.plane, on);
         }
       }
     }
@@ -777,10 +824,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     int put = 0, get = 0, st_put = wn;
     const auto issue = [&] {
       Step::copy(
-          p,
-          [&](int r) -> int64_t {
+          p, row0,
+          [&](int r) {
             const int s = 16 * st_put + r;
-            return s < total && d0 < p.D ? row0 + neuron(s) : -1;
+            return s < total && d0 < p.D ? neuron(s) : -1;
           },
           d0, ring_at + put * Step::BYTES);
       cp_async_commit_group();
@@ -789,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     const auto scales = [&](int st, typename Step::Scales& s) {
       const int i = 16 * st + (lane & 15);
-      s.load(p, i < total && d0 < p.D ? row0 + neuron(i) : -1, d0);
+      s.load(p, row0, i < total && d0 < p.D ? neuron(i) : -1, d0 < p.D ? d0 : 0);
     };
     typename Step::Scales s_now, s_next, s_then;
 #pragma unroll 1
@@ -812,21 +859,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       scales(st + 2 * WN, s_then);
       cp_async_wait_for<SB - 1>();
       __syncwarp();
-      if constexpr (F::FOUR) {
-        const float* h0 = reinterpret_cast<const float*>(hs) + g * HS + 16 * st + 2 * c;
-        Step::template add<NT>(
-            ring_at + get * Step::BYTES, s_now,
-            [&](int i, int n) { return h0[8 * n * HS + (i & 1) + 8 * (i >> 1)]; }, nt_used, three,
-            acc);
-      } else {
-        const uint16_t* h0 = reinterpret_cast<const uint16_t*>(hs) + g * HS + 16 * st + 2 * c;
-        Step::template add<NT>(
-            ring_at + get * Step::BYTES, s_now,
-            [&](int i, int half, int n) {
-              return *reinterpret_cast<const uint32_t*>(h0 + (i * SP + 8 * n) * HS + 8 * half);
-            },
-            nt_used, three, acc);
-      }
+      Step::template add<NT, CHUNK>(ring_at + get * Step::BYTES, s_now, hs, st, nt_used, three, acc);
       __syncwarp();  // (the next copy but SB - 2 goes where this step was)
       get = get + 1 == SB ? 0 : get + 1;
       s_now = s_next, s_next = s_then;
@@ -939,6 +972,7 @@ Down down_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t E, 
 
 struct Layout {
   size_t logits, count, slab, list, live, masks, h, part, total;
+  int64_t plane;
   int32_t counters;
 };
 
@@ -965,7 +999,9 @@ Layout layout_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t
   l.list = take(4 * P);
   l.live = take(4 * static_cast<size_t>(T));
   l.masks = take(2 * slabs * units);
-  l.h = take(6 * P * 16 * units);
+  l.plane = static_cast<int64_t>(first_tile(static_cast<int>(slabs), static_cast<int>(P)) + 1) *
+            16 * units * 8;
+  l.h = take(6 * static_cast<size_t>(l.plane));
   l.part = take(4 * P * splits * D);
   l.total = at;
   return l;
@@ -983,14 +1019,15 @@ twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) 
   const int most = 2 * dev.sm_count;
   cudaLaunchAttribute attr = overlapped();
   size_t smem = kWarps * Z::RING + 16 * (p.E + P / Z::SP) +
-                4 * (Z::RM * (Z::SP + 1) + p.E + 3 * P + p.T);
+                4 * (Z::RM * Z::ZP + p.E + 3 * P + p.T);
   cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>(units < most ? units : most)),
                                          dim3(kThreads), smem, s);
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   twell_status st = launch_large(neurons_kernel<F, NT>, limit, cfg, dev, set[0], p);
   if (st != TWELL_OK) return st;
-  const size_t rings = kWarps * Z::RING2 + (F::FOUR ? 4 : 6) * Z::SP * Z::HS;
+  const size_t rings =
+      kWarps * Z::RING2 + (F::FOUR ? 1 : p.y_f32 ? 3 : 2) * NT * Z::CHUNK * F::Step::H_ROW;
   const size_t sums = 4 * kWarps * (F::COLS / 16) * NT * 4 * 32;
   cfg = launch_config(dim3(o.tiles, o.splits, o.slabs), dim3(kThreads),
                       rings > sums ? rings : sums, s);
@@ -1080,10 +1117,7 @@ extern "C" twell_status twell_moe_decode(const uint16_t* x, int32_t T, const voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
   const RouterParams r{x, router, T, D, E, logits, count, l.counters};
-  const int64_t jobs = !router  ? 1
-                       : T == 1 ? E
-                                : static_cast<int64_t>((E + 1) / 2) * ((T + 7) / 8);
-  const unsigned grid = static_cast<unsigned>((jobs + 3) / 4);
+  const unsigned grid = !router ? 1u : T == 1 ? E : (E + 1) / 2 * ((T + 7) / 8);
   if (router_type == TWELL_F32 && router) {
     if (T == 1) router_kernel<float, 1, 1><<<grid, 128, 0, s>>>(r);
     else router_kernel<float, 2, 8><<<grid, 128, 0, s>>>(r);
@@ -1104,7 +1138,8 @@ extern "C" twell_status twell_moe_decode(const uint16_t* x, int32_t T, const voi
   p.plan.list = reinterpret_cast<int32_t*>(base + l.list);
   p.plan.live = reinterpret_cast<int32_t*>(base + l.live);
   p.plan.masks = reinterpret_cast<uint16_t*>(base + l.masks);
-  p.plan.h = reinterpret_cast<float*>(base + l.h);
+  p.plan.h = base + l.h;
+  p.plan.plane = l.plane;
   p.part = reinterpret_cast<float*>(base + l.part);
   p.count = count;
   p.y = y, p.y_f32 = y_type == TWELL_F32;

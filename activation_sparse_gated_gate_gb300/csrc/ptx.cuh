@@ -520,12 +520,6 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_f32x4(uint32_t cluster_addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x),
-               "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
-
 // Arrive, where `pred` holds, on a barrier of the cluster (a mapa address) without
 // ordering this thread's other memory accesses (a release would wait for them):
 // for barriers that hand over TMEM, whose loads tcgen05.wait::ld has already

@@ -269,25 +269,6 @@ __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantParams p) {
   }
 }
 
-// op over the warp of each of N values a lane: the lanes halve the values between them as
-// long as there are several, so that lane l ends with value l N / 32.
-template <int N, typename V, typename Op>
-__device__ __forceinline__ V over_warp(V (&x)[N], Op op) {
-  int o = 16;
-#pragma unroll
-  for (int n = N / 2; n > 0; n /= 2, o /= 2) {
-    const bool upper = (threadIdx.x & o) != 0;
-#pragma unroll
-    for (int k = 0; k < n; ++k) {
-      const V away = upper ? x[k] : x[k + n], mine = upper ? x[k + n] : x[k];
-      x[k] = op(mine, __shfl_xor_sync(0xffffffffu, away, o));
-    }
-  }
-#pragma unroll
-  for (; o > 0; o /= 2) x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
-  return x[0];
-}
-
 // Any K and any pitch.
 template <typename T, int G32, bool ZERO>
 __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams p) {

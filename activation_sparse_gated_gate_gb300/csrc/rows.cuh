@@ -7,9 +7,7 @@
 // and g + 8, its share c of the columns; lane = 4 g + c), so that a copy is waited for by the thread
 // that made it and by nobody else.  A slot holds 128 columns of 4-bit rows or 32 of bf16,
 // 1 KB a tile either way.  The loops are kept rolled: a decode step runs each instruction a
-// few times only, and code fetched from memory costs more than what it does (the first
-// version of the experts' kernel, 200 KB of unrolled code, took 35 us where this one
-// takes 12).
+// few times only, and code fetched from memory may cost more than what it does.
 #pragma once
 
 #include "common.cuh"
@@ -32,16 +30,6 @@ __device__ __forceinline__ void cp_async_commit_group() {
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool have) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(have ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async8_or_zero(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-               "r"(have ? 8 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(have ? 4 : 0)
                : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
