@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int warps = blockDim.x / 32;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const int t0 = blockIdx.y * (8 * NT), nt = min(NT, (p.T - t0 + 7) / 8);
+  const int t0 = blockIdx.y * (8 * NT);
   // this warp's blocks, and where its rows and x stand for them (rows behind the last
   // repeat it)
   const int b0 = static_cast<int>(static_cast<int64_t>(p.nb) * warp / warps),
@@ -128,11 +128,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       if (left + 8 * c >= kInt4Block) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          if (t < nt) u[q % HELD][t] = x.load(t, q, kInt4Block);
+          u[q % HELD][t] = x.load(t, q, kInt4Block);
       } else {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          if (t < nt) u[q % HELD][t] = x.load(t, q, left);
+          u[q % HELD][t] = x.load(t, q, left);
       }
     };
     if (HELD == 4) {
@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          if (t >= nt) break;
           const uint4 o = u[q % HELD][t];
           mma16816(part[t], v[0][0], v[1][0], v[0][1], v[1][1], o.x, o.y);
           mma16816(part[t], v[0][2], v[1][2], v[0][3], v[1][3], o.z, o.w);
@@ -169,7 +168,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if (t >= nt) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           acc[t][j] = fmaf(s_now[j / 2].scale(k), part[t][j], acc[t][j]);
@@ -187,7 +185,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     for (int j = 0; j < 4; ++j) sum[warp * VALUES + (n * 4 + j) * 32 + lane] = acc[n][j];
   __syncthreads();
 #pragma unroll 1
-  for (int i = tid; i < 16 * min(8 * nt, p.T - t0); i += blockDim.x) {
+  for (int i = tid; i < 16 * min(8 * NT, p.T - t0); i += blockDim.x) {
     const int r = i % 16, t = i / 16;
     const int from = ((t >> 3) * 4 + (r >> 3) * 2 + (t & 1)) * 32 + (r & 7) * 4 + (t >> 1 & 3);
     float v = 0.0f;

@@ -23,6 +23,7 @@
 // summed their columns) took as long for a token and 407 us for 64 (4 bits) where this one
 // takes 209: its phases waited for one another.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "int4.cuh"
@@ -32,6 +33,11 @@
 
 namespace twell {
 namespace {
+
+template <int N>
+using Count = std::integral_constant<int, N>;
+template <bool B>
+using Truth = std::integral_constant<bool, B>;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__(128) router_kernel(const RouterParams p) {
 // ------------------------------------------------------------------ experts
 
 // What the neurons kernel leaves for the down kernel, in the workspace: the slabs
-// (expert, first pair in the sorted list, pairs) and the list.
+// (expert, first pair in the sorted list, pairs, first tile of h) and the list.
 struct Plan {
   int32_t* n_slabs;
   int4* slab;
@@ -124,11 +130,6 @@ struct MoeParams {
   int32_t y_f32;
 };
 
-// Where a slab's h begins, in tiles of eight pairs (each slab's last may not be whole).
-__host__ __device__ inline int64_t first_tile(int slab, int pair) {
-  return (pair + 7 * static_cast<int64_t>(slab)) / 8;
-}
-
 // What is left of a value behind its upper half.
 __device__ __forceinline__ float behind(float a) {
   return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
@@ -136,12 +137,12 @@ __device__ __forceinline__ float behind(float a) {
 
 // Two values as three bf16 each, whose sum they are (to their 24 bits).  Two hold 16 bits:
 // enough where y is rounded to bf16.
-__device__ __forceinline__ void split(float a, float b, bool three, uint32_t (&o)[3]) {
+template <bool THREE>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&o)[3]) {
   o[0] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
   const float inf = __uint_as_float(0x7f800000u);
   a = fabsf(a) == inf ? 0.0f : behind(a), b = fabsf(b) == inf ? 0.0f : behind(b);
-  o[2] = 0u;
-  if (three) {
+  if constexpr (THREE) {
     o[1] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
     o[2] = bf16x2(behind(a), behind(b));
   } else {
@@ -150,10 +151,11 @@ __device__ __forceinline__ void split(float a, float b, bool three, uint32_t (&o
 }
 
 // d += a times the values that b0, b1 are split into, the small ones first.
+template <bool THREE>
 __device__ __forceinline__ void mma_split(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, bool three, const uint32_t (&b0)[3],
+                                          uint32_t a3, const uint32_t (&b0)[3],
                                           const uint32_t (&b1)[3]) {
-  if (three) mma16816(d, a0, a1, a2, a3, b0[2], b1[2]);
+  if constexpr (THREE) mma16816(d, a0, a1, a2, a3, b0[2], b1[2]);
   mma16816(d, a0, a1, a2, a3, b0[1], b1[1]);
   mma16816(d, a0, a1, a2, a3, b0[0], b1[0]);
 }
@@ -210,9 +212,9 @@ struct Bf16Step {
   }
   // h of a chunk in shared memory: [part][tile][neuron][8 pairs] of bf16
   static constexpr int H_ROW = 16;
-  template <int NT, int CHUNK>
+  template <int NU, int NT, int CHUNK, bool THREE>
   static __device__ __forceinline__ void add(uint32_t slot, const Scales&, uint32_t hs, int st,
-                                             int nt, bool three, float (&acc)[4][NT][4]) {
+                                             float (&acc)[4][NT][4]) {
     const int lane = threadIdx.x & 31;
     uint4 v[4];
 #pragma unroll
@@ -222,23 +224,21 @@ struct Bf16Step {
     const uint32_t* v1 = &v[1].x;
     const uint32_t* v2 = &v[2].x;
     const uint32_t* v3 = &v[3].x;
-    uint32_t b0[NT][3], b1[NT][3];
+    uint32_t b0[NU][3], b1[NU][3];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n >= nt) break;
+    for (int n = 0; n < NU; ++n) {
       // (lanes 16 to 31: the rows of the second part)
       const uint32_t from = hs + ((lane >> 4) * NT * CHUNK + n * CHUNK + 16 * st + (lane & 15)) * H_ROW;
       ldmatrix_x4_t(from, b0[n][0], b1[n][0], b0[n][1], b1[n][1]);
-      if (three) ldmatrix_x2_t(from + 2 * NT * CHUNK * H_ROW, b0[n][2], b1[n][2]);
+      if constexpr (THREE) ldmatrix_x2_t(from + 2 * NT * CHUNK * H_ROW, b0[n][2], b1[n][2]);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint32_t a0 = __byte_perm(v0[q], v1[q], 0x5410), a1 = __byte_perm(v0[q], v1[q], 0x7632),
                      a2 = __byte_perm(v2[q], v3[q], 0x5410), a3 = __byte_perm(v2[q], v3[q], 0x7632);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n >= nt) break;
-        mma_split(acc[q][n], a0, a1, a2, a3, three, b0[n], b1[n]);
+      for (int n = 0; n < NU; ++n) {
+        mma_split<THREE>(acc[q][n], a0, a1, a2, a3, b0[n], b1[n]);
       }
     }
   }
@@ -276,9 +276,9 @@ struct FourStep {
   }
   // h of a chunk in shared memory: [tile][place(neuron)][8 pairs] of fp32
   static constexpr int H_ROW = 32;
-  template <int NT, int CHUNK>
+  template <int NU, int NT, int CHUNK, bool THREE>
   static __device__ __forceinline__ void add(uint32_t slot, const Scales& sc, uint32_t hs, int st,
-                                             int nt, bool three, float (&acc)[8][NT][4]) {
+                                             float (&acc)[8][NT][4]) {
     const int lane = threadIdx.x & 31, c = lane & 3;
     const uint32_t h0 = hs + 16 * st * H_ROW + (lane >> 2) * 4;
     const auto h_of = [&](int i, int n) {
@@ -294,16 +294,15 @@ struct FourStep {
                    : "memory");
       s[i].from_lane(sc.one, 2 * c + (i & 1) + 8 * (i >> 1));
     }
-    uint32_t b0[NT][3], b1[NT][3];
+    uint32_t b0[NU][3], b1[NU][3];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int gk = k / G32;
       if (k % G32 == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n >= nt) break;
-          split(h_of(0, n) * s[0].scale(gk), h_of(1, n) * s[1].scale(gk), three, b0[n]);
-          split(h_of(2, n) * s[2].scale(gk), h_of(3, n) * s[3].scale(gk), three, b1[n]);
+        for (int n = 0; n < NU; ++n) {
+          split<THREE>(h_of(0, n) * s[0].scale(gk), h_of(1, n) * s[1].scale(gk), b0[n]);
+          split<THREE>(h_of(2, n) * s[2].scale(gk), h_of(3, n) * s[3].scale(gk), b1[n]);
         }
       }
       const uint32_t sel = k & 1 ? 0x7632 : 0x5410;
@@ -316,9 +315,8 @@ struct FourStep {
         const uint32_t a0 = nibbles(p01, 2 * q, z01), a1 = nibbles(p01, 2 * q + 1, z01),
                        a2 = nibbles(p23, 2 * q, z23), a3 = nibbles(p23, 2 * q + 1, z23);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n >= nt) break;
-          mma_split(acc[2 * k + q][n], a0, a1, a2, a3, three, b0[n], b1[n]);
+        for (int n = 0; n < NU; ++n) {
+          mma_split<THREE>(acc[2 * k + q][n], a0, a1, a2, a3, b0[n], b1[n]);
         }
       }
     }
@@ -334,12 +332,12 @@ struct Bf16 {
   typedef Bf16Step Step;
   template <int NT, int S, typename X>
   static __device__ __forceinline__ void rows(const MoeParams& p, const int (&mat)[2],
-                                              const int64_t (&at)[2][2], int wk, int WK,
+                                              const int64_t (&at)[2][2], int b0, int b1,
                                               uint32_t ring, int nt, X x, float (&acc)[2][NT][4]) {
     const uint16_t* const from[2][2] = {
         {p.w[mat[0]] + at[0][0] * p.D, p.w[mat[0]] + at[0][1] * p.D},
         {p.w[mat[1]] + at[1][0] * p.D, p.w[mat[1]] + at[1][1] * p.D}};
-    bf16_rows<2, NT, S>(from, p.D, wk, WK, ring, nt, x, acc);
+    bf16_rows<2, NT, S>(from, p.D, b0, b1, ring, nt, x, acc);
   }
   static __device__ __forceinline__ int column(int q, int h, int g) { return 8 * g + 2 * q + h; }
 };
@@ -350,10 +348,11 @@ struct Four {
   typedef FourStep<G> Step;
   template <int NT, int S, typename X>
   static __device__ __forceinline__ void rows(const MoeParams& p, const int (&mat)[2],
-                                              const int64_t (&at)[2][2], int wk, int WK,
+                                              const int64_t (&at)[2][2], int b0, int b1,
                                               uint32_t ring, int nt, X x, float (&acc)[2][NT][4]) {
     const Int4View* const from[2] = {&p.q[mat[0]], &p.q[mat[1]]};
-    int4_rows<G, 2, NT, S>(from, at, p.D, wk, WK, ring, nt, x, acc);
+    if (NT > 1 && nt == 1) int4_rows<G, 2, 1, NT, S>(from, at, p.D, b0, b1, ring, x, acc);
+    else int4_rows<G, 2, NT, NT, S>(from, at, p.D, b0, b1, ring, x, acc);
   }
   static __device__ __forceinline__ int column(int q, int h, int g) {
     return 32 * (q >> 1) + 8 * (g >> 1) + 2 * (2 * (q & 1) + h) + (g & 1);
@@ -435,13 +434,15 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
   if (lane < p.k) p.ids[t * p.k + lane] = e, p.weights[t * p.k + lane] = w;
 }
 
-template <int NT>
+template <bool FOUR, int NT>
 struct Sizes {
   static constexpr int SP = 8 * NT;              // pairs (token, slot) of an expert at a time
   static constexpr int UR = 8;                   // units of 16 neurons of a CTA at a time
   static constexpr int RM = 16 * UR;
   static constexpr int ZP = NT == 1 ? 8 : 24;    // between neurons' gate sums (no bank twice)
-  static constexpr int RING = 6 * kSlotBytes;    // of a warp, neurons kernel
+  // of a warp, neurons kernel (4-bit rows, bound by instructions, want no more on its way: 64
+  // tokens 166 us, 169 with 6)
+  static constexpr int RING = (FOUR ? 4 : 6) * kSlotBytes;
   static constexpr int CHUNK = 1024 / NT;        // neurons of h in shared memory
   static constexpr int RING2 = 6 * kSlotBytes;   // of a warp, down kernel
 };
@@ -449,15 +450,19 @@ struct Sizes {
 template <typename F, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     neurons_kernel(const __grid_constant__ MoeParams p) {
-  typedef Sizes<NT> Z;
+  typedef Sizes<F::FOUR, NT> Z;
   constexpr int SP = Z::SP, UR = Z::UR, RM = Z::RM, RING = Z::RING, ZP = Z::ZP;
   extern __shared__ __align__(16) uint8_t raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int P = p.T * p.k;
-  // Each warp's ring, which also holds the sums that it hands to the others.
+  // Each warp's ring, which also holds the sums that it hands to the others (those of a
+  // first of two tiles: `firsts`).
   uint8_t* ring = raw + warp * RING;
   const uint32_t ring_at = ptx::smem_u32(ring);
-  int4* slab = reinterpret_cast<int4*>(raw + kWarps * RING);      // [E + P / SP]
+  constexpr int FIRST = 1024 * NT;
+  static_assert(FIRST <= RING, "a warp's sums");
+  uint8_t* firsts = raw + kWarps * RING;
+  int4* slab = reinterpret_cast<int4*>(firsts + kWarps * FIRST);  // [E + P / SP]
   float* zb = reinterpret_cast<float*>(slab + p.E + P / SP);      // [RM][ZP] gate sums (ReLU)
   int32_t* count = reinterpret_cast<int32_t*>(zb + RM * ZP);      // [E] pairs of an expert
   int32_t* pid = count + p.E;                         // [P]
@@ -504,25 +509,36 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (e >= 0 && before == 0) count[e] += __popc(same);
       __syncwarp();
     }
-    int pairs = 0, slabs = 0;
+    // the slabs; of two tiles, those that need both first (what is left for the end is short)
+    const auto both = [](int n) { return NT == 1 ? (n + SP - 1) / SP : n / SP + (n % SP > SP / 2); };
+    int full = 0;
+    if (NT > 1) {
+#pragma unroll 1
+      for (int e = lane; e < p.E; e += 32) full += both(count[e]);
+      full = __reduce_add_sync(0xffffffffu, full);
+    }
+    int sums = 0;  // of pairs, full slabs (from bit 12) and others (from bit 20)
 #pragma unroll 1
     for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int n = e0 + lane < p.E ? count[e0 + lane] : 0;
-      const int mine = n | ((n + SP - 1) / SP) << 16;  // both sums at once
+      const int e = e0 + lane, n = e < p.E ? count[e] : 0;
+      const int f = both(n), o = n > f * SP;
+      const int mine = n | f << 12 | o << 20;
       int up = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o) up += v;
+      for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, up, d);
+        if (lane >= d) up += v;
       }
-      const int first = pairs + ((up - mine) & 0xffff), s = slabs + ((up - mine) >> 16);
-      if (e0 + lane < p.E) count[e0 + lane] = first;
+      const int before = sums + up - mine;
+      const int first = before & 0xfff, af = NT == 1 ? before >> 12 : before >> 12 & 0xff, ao = full + (before >> 20);
+      if (e < p.E) count[e] = first;
 #pragma unroll 1
-      for (int q = 0; q < n; q += SP)
-        slab[s + q / SP] = make_int4(e0 + lane, first + q, min(SP, n - q), 0);
-      const int all = __shfl_sync(0xffffffffu, up, 31);
-      pairs += all & 0xffff, slabs += all >> 16;
+      for (int q = 0; q < f; ++q)
+        slab[af + q] = make_int4(e, first + q * SP, min(SP, n - q * SP), NT * (af + q));
+      if (o) slab[ao] = make_int4(e, first + f * SP, n - f * SP, NT * full + ao - full);
+      sums += __shfl_sync(0xffffffffu, up, 31);
     }
+    const int slabs = NT == 1 ? sums >> 12 : full + (sums >> 20);
     if (lane == 0) sh_slabs = slabs;
   }
   __syncthreads();
@@ -562,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
   for (uint32_t ub = blockIdx.x < C ? U * blockIdx.x / C : 0u; ub < u_last;) {
     const uint32_t a = ub / units;
-    const int e = slab[a].x, s0 = slab[a].y, ns = slab[a].z;
+    const int e = slab[a].x, s0 = slab[a].y, ns = slab[a].z, tile0 = slab[a].w;
     const int u0 = ub - a * units;
     const int nu = min(min(u_last - a * units, units) - u0, static_cast<uint32_t>(UR));
     ub += nu;
@@ -574,17 +590,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int n = 0; n < NT; ++n)
       xt[n] = p.x + static_cast<int64_t>(plist[s0 + min(8 * n + g, ns - 1)] / p.k) * p.D;
 
-    // ---- gate and up sums (with ReLU the gate's, then up of the active neurons):
-    // `share` warps side by side on tiles of rows, the others on their columns
-    int n_act = silu ? nj : 0, share = 1;
+    // ---- gate and up sums (with ReLU the gate's, then up of the active neurons): tiles of
+    // two times 16 rows, their blocks of 128 columns divided evenly among the warps
+    int n_act = silu ? nj : 0, n_tiles = 1, jobs = 0;
+    const int nb = (p.D + kInt4Block - 1) / kInt4Block, c = lane & 3;
     // The sum of a tile's half m for the eight pairs n: rows g and g + 8 (x, y and z, w) of
     // its 16, pairs 2 c and 2 c + 1.  Warp w looks after the w-th 16 rows.
-    const int c = lane & 3;
     const auto sum_of = [&](int tile, int m, int n) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 2
-      for (int w = tile; w < kWarps; w += share) {
-        const float4 u = reinterpret_cast<const float4*>(raw + w * RING)[(m * NT + n) * 32 + lane];
+      for (int w = kWarps * tile / n_tiles; w * n_tiles < kWarps * (tile + 1); ++w) {
+        const int from = jobs * w / kWarps, to = jobs * (w + 1) / kWarps;
+        if (from == to || from >= (tile + 1) * nb || to <= tile * nb) continue;
+        const uint8_t* at = to > (tile + 1) * nb ? firsts + w * FIRST : raw + w * RING;
+        const float4 u = reinterpret_cast<const float4*>(at)[(m * NT + n) * 32 + lane];
         v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
       }
       return v;
@@ -593,17 +612,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int stage = 0;; ++stage) {
       const int rows = stage ? n_act : nj;
       // a warp's two tiles: the gate and up rows of the same 16 neurons, or 32 rows of one
-      const int n_tiles = silu ? (rows + 15) / 16 : (rows + 31) / 32;
-      share = n_tiles <= 2 ? n_tiles : n_tiles <= 4 ? 4 : 8;
-      const int tile = warp & (share - 1);
-      float acc[2][NT][4];
+      n_tiles = silu ? (rows + 15) / 16 : (rows + 31) / 32;
+      jobs = n_tiles * nb;
+      // (a warp's share may be the end of a tile and the beginning of the next)
+      const int last = jobs * (warp + 1) / kWarps;
+#pragma unroll 1
+      for (int job = jobs * warp / kWarps; job < last;) {
+        const int tile = job / nb, b0 = job - tile * nb, b1 = min(nb, b0 + last - job);
+        job += b1 - b0;
+        float acc[2][NT][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[m][n][j] = 0.0f;
-      if (tile < n_tiles) {
+            for (int j = 0; j < 4; ++j) acc[m][n][j] = 0.0f;
         const int mat[2] = {stage, silu ? 1 : stage};
         int64_t at[2][2];
 #pragma unroll
@@ -614,16 +637,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             at[m][h] = base + j0 + (stage ? act[r] : r);
           }
         F::template rows<NT, RING / (2 * kSlotBytes)>(
-            p, mat, at, warp / share, kWarps / share, ring_at, nt_used,
+            p, mat, at, b0, b1, ring_at, nt_used,
             [&](int n, int k) { return ld16(xt[n] + min(k, p.D - 8)); }, acc);
+        __syncwarp();
+        float4* to = reinterpret_cast<float4*>(job < last ? firsts + warp * FIRST : ring);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            to[(m * NT + n) * 32 + lane] =
+                make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
       }
-      __syncwarp();
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          reinterpret_cast<float4*>(ring)[(m * NT + n) * 32 + lane] =
-              make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
       __syncthreads();
       if (silu || stage) break;
       uint32_t mask = 0u;
@@ -691,13 +715,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 2; ++i) {
           if (r[i] >= rows) continue;
           const int64_t at =
-              ((first_tile(a, s0) + n) * (16 * units) + (j0 + j[i])) * 8 + 2 * c;
+              (static_cast<int64_t>(tile0 + n) * (16 * units) + (j0 + j[i])) * 8 + 2 * c;
           if constexpr (F::FOUR) {
             *reinterpret_cast<float2*>(static_cast<float*>(p.plan.h) + at) =
                 make_float2(h[2 * i], h[2 * i + 1]);
           } else {
             uint32_t o[3];
-            split(h[2 * i], h[2 * i + 1], p.y_f32 != 0, o);
+            if (p.y_f32) split<true>(h[2 * i], h[2 * i + 1], o);
+            else split<false>(h[2 * i], h[2 * i + 1], o);
             uint16_t* to = static_cast<uint16_t*>(p.plan.h) + at;
 #pragma unroll
             for (int q = 0; q < 3; ++q)
@@ -713,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <typename F, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     down_kernel(const __grid_constant__ MoeParams p) {
-  typedef Sizes<NT> Z;
+  typedef Sizes<F::FOUR, NT> Z;
   typedef typename F::Step Step;
   constexpr int SP = Z::SP, CHUNK = Z::CHUNK, TW = F::COLS, MT = TW / 16, HR = Step::H_ROW;
   constexpr int SB = Z::RING2 / Step::BYTES;  // steps in a warp's ring
@@ -798,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // its own)
     const int64_t tile = static_cast<int64_t>(16 * units) * HR;
     const uint8_t* from =
-        static_cast<const uint8_t*>(p.plan.h) + first_tile(a, s0) * tile + 16 * u0 * HR;
+        static_cast<const uint8_t*>(p.plan.h) + sl.w * tile + 16 * u0 * HR;
 #pragma unroll 1
     for (int s = tid; s < 16 * steps; s += kThreads) {
       const bool on = s < total;
@@ -853,16 +878,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     cp_async_wait_for<SB - 1>();
     __syncthreads();
+    // (for the tiles of pairs and parts of h that there are: a test for each would cost as much
+    // as what it leaves out)
+    const auto run = [&](auto used, auto f32) {
 #pragma unroll 1
-    for (int st = wn; st < steps; st += WN) {
-      issue();
-      scales(st + 2 * WN, s_then);
-      cp_async_wait_for<SB - 1>();
-      __syncwarp();
-      Step::template add<NT, CHUNK>(ring_at + get * Step::BYTES, s_now, hs, st, nt_used, three, acc);
-      __syncwarp();  // (the next copy but SB - 2 goes where this step was)
-      get = get + 1 == SB ? 0 : get + 1;
-      s_now = s_next, s_next = s_then;
+      for (int st = wn; st < steps; st += WN) {
+        issue();
+        scales(st + 2 * WN, s_then);
+        cp_async_wait_for<SB - 1>();
+        __syncwarp();
+        Step::template add<decltype(used)::value, NT, CHUNK, decltype(f32)::value>(
+            ring_at + get * Step::BYTES, s_now, hs, st, acc);
+        __syncwarp();  // (the next copy but SB - 2 goes where this step was)
+        get = get + 1 == SB ? 0 : get + 1;
+        s_now = s_next, s_next = s_then;
+      }
+    };
+    if (NT > 1 && nt_used == 1) {
+      if (three) run(Count<1>(), Truth<true>());
+      else run(Count<1>(), Truth<false>());
+    } else {
+      if (three) run(Count<NT>(), Truth<true>());
+      else run(Count<NT>(), Truth<false>());
     }
     cp_async_wait_for<0>();
     __syncthreads();
@@ -999,8 +1036,7 @@ Layout layout_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t
   l.list = take(4 * P);
   l.live = take(4 * static_cast<size_t>(T));
   l.masks = take(2 * slabs * units);
-  l.plane = static_cast<int64_t>(first_tile(static_cast<int>(slabs), static_cast<int>(P)) + 1) *
-            16 * units * 8;
+  l.plane = static_cast<int64_t>((P + 7 * slabs) / 8 * 16 * units * 8);
   l.h = take(6 * static_cast<size_t>(l.plane));
   l.part = take(4 * P * splits * D);
   l.total = at;
@@ -1009,7 +1045,7 @@ Layout layout_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t
 
 template <typename F, int NT>
 twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) {
-  typedef Sizes<NT> Z;
+  typedef Sizes<F::FOUR, NT> Z;
   static std::atomic<uint64_t> set[2] = {{0}, {0}};
   const int limit = dev.max_smem_optin - 8192;
   const int64_t P = static_cast<int64_t>(p.T) * p.k;
@@ -1018,7 +1054,7 @@ twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) 
   const int64_t units = o.slabs * ((static_cast<int64_t>(p.F) + 15) / 16);
   const int most = 2 * dev.sm_count;
   cudaLaunchAttribute attr = overlapped();
-  size_t smem = kWarps * Z::RING + 16 * (p.E + P / Z::SP) +
+  size_t smem = kWarps * (Z::RING + 1024 * NT) + 16 * (p.E + P / Z::SP) +
                 4 * (Z::RM * Z::ZP + p.E + 3 * P + p.T);
   cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>(units < most ? units : most)),
                                          dim3(kThreads), smem, s);

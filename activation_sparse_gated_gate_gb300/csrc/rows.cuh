@@ -62,41 +62,39 @@ struct Ahead {
   }
 };
 
-// acc[m][t] += row tile m times activations t, over the blocks of 128 columns wk, wk + WK, ...
-// of K.  at[m][h]: this lane's rows of bf16 (g + 8 h of tile m); nt tiles of activations are
+// acc[m][t] += row tile m times activations t, over the blocks b0 to b1 of 128 columns, of K.
+// at[m][h]: this lane's rows of bf16 (g + 8 h of tile m); nt tiles of activations are
 // used.  A sum of 32 columns is taken by the tensor core and added in fp32: its own additions
 // truncate, and a long chain of them would be felt in an fp32 result.
 template <int MT, int NT, int S, typename X>
-__device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], int K, int wk, int WK,
+__device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], int K, int b0, int b1,
                                           uint32_t ring, int nt, X x, float (&acc)[MT][NT][4]) {
   constexpr int DIST = Ahead<NT>::DIST, SLOT = MT * kSlotBytes;
   const int lane = threadIdx.x & 31, c8 = 8 * (lane & 3);
-  const int nb = (K + kInt4Block - 1) / kInt4Block;
   const uint32_t mine = ring + 16 * lane;
-  int put = 0, get = 0, k_put = wk * kInt4Block + c8;
-  // the next piece of 32 columns (`ends`: the last of a block)
-  const auto issue = [&](bool ends) {
-    const bool in = k_put < K;
+  int put = 0, get = 0, k_put = b0 * kInt4Block + c8;
+  const int k_end = min(K, b1 * kInt4Block);
+  const auto issue = [&] {  // the next 32 columns
+    const bool in = k_put < k_end;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         cp_async16_or_zero(mine + put * SLOT + (2 * m + h) * 512, at[m][h] + (in ? k_put : 0), in);
     cp_async_commit_group();
-    k_put += ends ? WK * kInt4Block - 96 : 32;
+    k_put += 32;
     put = put + 1 == S ? 0 : put + 1;
   };
-  static_assert(S - 1 <= 4, "the first fills are of one block");
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i == 3);
+  for (int i = 0; i < S - 1; ++i) issue();
   Ahead<NT> b;
 #pragma unroll
-  for (int i = 0; i < DIST; ++i) b.load(i, wk * kInt4Block + 32 * i + c8, nt, x);
+  for (int i = 0; i < DIST; ++i) b.load(i, b0 * kInt4Block + 32 * i + c8, nt, x);
 #pragma unroll 1
-  for (int blk = wk; blk < nb; blk += WK) {
+  for (int blk = b0; blk < b1; ++blk) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      issue((i + S - 1) % 4 == 3);
+      issue();
       cp_async_wait_for<S - 1>();
       uint4 u[MT], v[MT];
 #pragma unroll
@@ -119,32 +117,33 @@ __device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], in
           for (int j = 0; j < 4; ++j) acc[m][t][j] += part[j];
         }
       }
-      const int q = i + DIST;
-      b.load(i % DIST, (blk + (q >= 4 ? WK : 0)) * kInt4Block + 32 * (q % 4) + c8, nt, x);
+      b.load(i % DIST, blk * kInt4Block + 32 * (i + DIST) + c8, nt, x);
     }
   }
   cp_async_wait_for<0>();
 }
 
-// The same of 4-bit rows; at[m][h]: the indexes of this lane's rows in w[m].  The four lanes of a row
+// The same of 4-bit rows; at[m][h]: the indexes of this lane's rows in w[m]; of the sums'
+// HELD tiles of activations the first NT are used (what a test for each tile costs is felt
+// here, where instructions bound the loop: 64 tokens, 205 us of the layer with, 184 without).  The four lanes of a row
 // have the scales of four blocks between them, the next four on their way.
-template <int G32, int MT, int NT, int S, typename X>
+template <int G32, int MT, int NT, int HELD, int S, typename X>
 __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
-                                          const int64_t (&at)[MT][2], int K, int wk, int WK,
-                                          uint32_t ring, int nt, X x, float (&acc)[MT][NT][4]) {
+                                          const int64_t (&at)[MT][2], int K, int b0, int b1,
+                                          uint32_t ring, X x, float (&acc)[MT][HELD][4]) {
   constexpr int GROUPS = 4 / G32, DIST = Ahead<NT>::DIST, SLOT = MT * kSlotBytes;
   const int lane = threadIdx.x & 31, c = lane & 3;
   const int nb = (K + kInt4Block - 1) / kInt4Block;
-  const int n = (nb - wk + WK - 1) / WK;
+  const int n = b1 - b0;
   const uint32_t mine = ring + 16 * lane;
   const uint8_t* code[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) code[m][h] = w[m]->code + at[m][h] * w[m]->pitch + 16 * c;
-  int put = 0, get = 0, b_put = wk;
+  int put = 0, get = 0, b_put = b0;
   const auto issue = [&] {
-    if (b_put < nb) {
+    if (b_put < b1) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -153,7 +152,7 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
                              code[m][h] + b_put * kInt4Bytes, true);
     }
     cp_async_commit_group();
-    b_put += WK;
+    ++b_put;
     put = put + 1 == S ? 0 : put + 1;
   };
   BlockScales<G32> next[MT][2];
@@ -162,15 +161,15 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        next[m][h].load(*w[m], at[m][h] * w[m]->held + min(wk + (i + c) * WK, nb - 1) * GROUPS);
+        next[m][h].load(*w[m], at[m][h] * w[m]->held + min(b0 + i + c, nb - 1) * GROUPS);
   };
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) issue();
   if (n > 0) scales(0);
   Ahead<NT> b;
 #pragma unroll
-  for (int i = 0; i < DIST; ++i) b.load(i, wk * kInt4Block + 32 * i + 8 * c, nt, x);
-  int blk = wk;
+  for (int i = 0; i < DIST; ++i) b.load(i, b0 * kInt4Block + 32 * i + 8 * c, NT, x);
+  int blk = b0;
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += 4) {
     BlockScales<G32> four[MT][2];
@@ -179,7 +178,7 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
     if (i0 + 4 < n) scales(i0 + 4);
     const int last = min(4, n - i0);
 #pragma unroll 1
-    for (int i = 0; i < last; ++i, blk += WK) {
+    for (int i = 0; i < last; ++i, ++blk) {
       issue();
       BlockScales<G32> sc[MT][2];
 #pragma unroll
@@ -221,21 +220,18 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            if (t >= nt) break;
-            const uint4 u = b.v[q % DIST][t];
+                const uint4 u = b.v[q % DIST][t];
             mma16816(part[m][t], v[0][0], v[1][0], v[0][1], v[1][1], u.x, u.y);
             mma16816(part[m][t], v[0][2], v[1][2], v[0][3], v[1][3], u.z, u.w);
           }
         }
-        const int f = q + DIST;
-        b.load(q % DIST, (blk + (f >= 4 ? WK : 0)) * kInt4Block + 32 * (f % 4) + 8 * c, nt, x);
+        b.load(q % DIST, blk * kInt4Block + 32 * (q + DIST) + 8 * c, NT, x);
         if (q % G32 == G32 - 1) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              if (t >= nt) break;
-#pragma unroll
+      #pragma unroll
               for (int j = 0; j < 4; ++j)
                 acc[m][t][j] = fmaf(sc[m][j / 2].scale(k), part[m][t][j], acc[m][t][j]);
             }
