@@ -4,24 +4,31 @@
 //   logits = x W_r^T;  the k largest of a token (ties: the lowest expert), p = softmax
 //   y[t] = sum over the token's k slots of p sum_j a(x . Wg[e][j]) (x . Wu[e][j]) Wd[e][j]
 //
-// Bound by the stream of the chosen experts' weights, and at one token by the chain of
-// dependent steps behind it.  Three kernels, each launched while the one before runs:
-//   router   the logits: a warp an expert pair and eight tokens, in fp32 FMAs (a choice must not
-//            hang on a tensor core's rounding).  More tokens than eight: a fourth kernel
-//            makes the choice, a warp a token; of fewer every CTA of the next makes it
+// Three kernels, each launched while the one before runs:
+//   router   the logits in fp32 FMAs (a choice must not hang on a tensor core's rounding).  More
+//            tokens than eight: a fourth kernel makes the choice, a warp a token; of fewer
+//            every CTA of the next makes it (a launch costs 2 us, the choice 3 in either)
 //   neurons  the (token, slot) pairs sorted by expert into slabs of up to 8 NT; the slabs'
-//            neurons divided evenly among the CTAs; h = a(gate) up to memory.  With ReLU a
-//            neuron whose gate is not positive for any token of the slab is dropped after its
-//            gate sum: its rows of Wu and Wd are not read
+//            neurons divided evenly among the CTAs, a CTA's columns among its warps; h = a(gate) up
+//            to memory.  With ReLU a neuron whose gate is not positive for any token of the
+//            slab is dropped after its gate sum: its rows of Wu and Wd are not read
 //   down     a CTA a slab, a tile of columns and a part of the neurons: h Wd, its warps on
 //            every eighth step of 16 neurons, and the token's sum by whoever completes a
 //            tile of it (a counter), in slot order: results do not depend on who it is
 // The sums over D run on mma.sync with 16 neurons as A and up to 8 NT pairs as B (rows.cuh);
 // those over neurons with 16 columns of Wd as A and h as B in three bf16 parts, whose
-// sum is h's 24 bits: one part would cost y 2^-9 of an element's size.
+// sum is h's 24 bits: one part would cost y 2^-9 of an element's size.  mma.sync and not tcgen05:
+// 4-bit codes are unpacked in registers, where its operands come from, and eight to sixteen
+// pairs of an expert leave the tensor pipe idle either way (17 to 25 % of its cycles).
+//   What bounds it (E = 64, D = 2048, F = 1024, 8 experts a token, weights from memory):
+//   * one token: the chain of launches, dependent reads and barriers, 26 us in bf16 with
+//     1 % of the neurons active (34 MB read, 5 us of the stream), 28 in 4 bits with all
+//   * 64 tokens, bf16: the stream, 805 MB in 180 to 186 us (4.4 TB/s; neurons 4.8, down 3.8)
+//   * 64 tokens, 4 bits: instructions, 5 a weight for unpacking, split parts and addresses with
+//     registers for 16 warps an SM, which issue in half of the cycles: 166 us
 //   A form in two kernels (clusters of 8 CTAs that exchanged h through shared memory and
-// summed their columns) took as long for a token and 407 us for 64 (4 bits) where this one
-// takes 209: its phases waited for one another.
+// summed their columns) took as long for a token and 364 us (bf16) and 407 (4 bits) for 64: its
+// phases waited for one another.
 #include <atomic>
 #include <type_traits>
 
@@ -323,9 +330,9 @@ struct FourStep {
   }
 };
 
-// The two forms of weights: the sums over the columns of two tiles of rows (at[m][h]: this
-// lane's of matrix mat[m]), the step above, and the column of a tile that row (h, g) (g of the upper or lower eight) of its q-th
-// 16 outputs is.
+// The two forms of weights: the sums over the blocks b0 to b1 of two tiles of rows (at[m][h]:
+// this lane's of matrix mat[m]), the step above, and the column of a tile that row g of the
+// upper (h = 0) or lower eight of its q-th 16 outputs is.
 struct Bf16 {
   static constexpr bool FOUR = false;
   static constexpr int COLS = 64;  // of a step's tile
@@ -530,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane >= d) up += v;
       }
       const int before = sums + up - mine;
-      const int first = before & 0xfff, af = NT == 1 ? before >> 12 : before >> 12 & 0xff, ao = full + (before >> 20);
+      const int first = before & 0xfff, af = NT == 1 ? before >> 12 : before >> 12 & 0xff,
+                ao = full + (before >> 20);
       if (e < p.E) count[e] = first;
 #pragma unroll 1
       for (int q = 0; q < f; ++q)
@@ -975,31 +983,30 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // -------------------------------------------------------------------- host
 
-// Tiles of eight pairs that an expert's weights are read once for: all of them where there
-// are eight tokens at most (an expert with more than a slab reads its weights again, from
-// the second cache).
-int pair_tiles(int32_t T) { return T <= 8 ? 1 : 2; }
+// Tiles of eight pairs that an expert's weights are read once for: two where most experts
+// have more than one tile's (an expert with more than a slab reads its weights again, from the
+// second cache).  4 bits, E = 64, 8 experts a token: 32 tokens 112 us with one and 123 with two,
+// 48 119 and 135, 64 192 and 166; bf16 169 and 170, 177 and 179, 222 and 187.
+int pair_tiles(int32_t T, int32_t E, int32_t k) { return T <= 8 || T * k < 7 * E ? 1 : 2; }
 
 // The down kernel: warps side by side on columns, tiles of a CTA's columns, slabs at the most,
 // and parts of a slab's neurons.  The widest CTAs that still give every SM four, so that
-// an SM's last ones leave little of it idle (64 tokens, 4 bits: 223 us, 312 with one); or one
-// where few tokens with a ReLU leave a CTA little to do beside its chain of small reads and
-// the tokens' sums (8 tokens, 2 % active: 67 us, 69 with four).  Neurons are divided where
-// CTAs of one warp's width leave SMs without two, into parts of 128 neurons at least.
+// an SM's last ones leave little of it idle (64 tokens, 4 bits: 166 us, 172 with two, 239 with
+// one, 177 with eight; bf16 187, 191, 192, 197).  Neurons are divided where CTAs of one
+// warp's width leave SMs without two, into parts of 128 neurons at least.
 struct Down {
   int32_t side, tiles, slabs, splits;
 };
 Down down_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t E, int32_t k,
-             bool four, bool relu) {
-  const int nt = pair_tiles(T), tw = four ? 128 : 64, P = T * k;
-  const int want = relu && nt == 1 ? dev.sm_count : 4 * dev.sm_count;
+             bool four) {
+  const int nt = pair_tiles(T, E, k), tw = four ? 128 : 64, P = T * k;
   Down o;
   o.slabs = (P < E ? P : E) + P / (8 * nt);
   if (o.slabs > P) o.slabs = P;
   if (o.slabs < 1) o.slabs = 1;  // (no tokens)
   for (o.side = kWarps;; o.side /= 2) {
     o.tiles = (D + o.side * tw - 1) / (o.side * tw);
-    if (o.side == 1 || o.tiles * o.slabs >= want) break;
+    if (o.side == 1 || o.tiles * o.slabs >= 4 * dev.sm_count) break;
   }
   const int fill = 2 * dev.sm_count / (o.tiles * o.slabs), most = (F + 15) / 16 / 8;
   o.splits = most < fill ? most : fill;
@@ -1017,8 +1024,8 @@ Layout layout_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t
   Layout l;
   const size_t P = static_cast<size_t>(T) * k, units = (static_cast<size_t>(F) + 15) / 16;
   size_t slabs = 0, splits = 0, tiles = 0;  // of whichever form asks for most
-  for (int form = 0; form < 4; ++form) {
-    const Down o = down_of(dev, T, D, F, E, k, form & 1, form & 2);
+  for (int four = 0; four < 2; ++four) {
+    const Down o = down_of(dev, T, D, F, E, k, four);
     slabs = slabs > static_cast<size_t>(o.slabs) ? slabs : o.slabs;
     splits = splits > static_cast<size_t>(o.splits) ? splits : o.splits;
     tiles = tiles > static_cast<size_t>(o.tiles) ? tiles : o.tiles;
@@ -1049,7 +1056,7 @@ twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) 
   static std::atomic<uint64_t> set[2] = {{0}, {0}};
   const int limit = dev.max_smem_optin - 8192;
   const int64_t P = static_cast<int64_t>(p.T) * p.k;
-  const Down o = down_of(dev, p.T, p.D, p.F, p.E, p.k, F::FOUR, p.act == TWELL_RELU);
+  const Down o = down_of(dev, p.T, p.D, p.F, p.E, p.k, F::FOUR);
   p.side = o.side;
   const int64_t units = o.slabs * ((static_cast<int64_t>(p.F) + 15) / 16);
   const int most = 2 * dev.sm_count;
@@ -1074,7 +1081,8 @@ twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) 
 
 template <typename F>
 twell_status launch_experts(const MoeParams& p, const DeviceInfo& dev, cudaStream_t s) {
-  return pair_tiles(p.T) == 1 ? launch_experts<F, 1>(p, dev, s) : launch_experts<F, 2>(p, dev, s);
+  return pair_tiles(p.T, p.E, p.k) == 1 ? launch_experts<F, 1>(p, dev, s)
+                                        : launch_experts<F, 2>(p, dev, s);
 }
 
 bool sizes_ok(int32_t T, int32_t D, int32_t F, int32_t E, int32_t k) {

@@ -123,10 +123,10 @@ __device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], in
   cp_async_wait_for<0>();
 }
 
-// The same of 4-bit rows; at[m][h]: the indexes of this lane's rows in w[m]; of the sums'
-// HELD tiles of activations the first NT are used (what a test for each tile costs is felt
-// here, where instructions bound the loop: 64 tokens, 205 us of the layer with, 184 without).  The four lanes of a row
-// have the scales of four blocks between them, the next four on their way.
+// The same of 4-bit rows; at[m][h]: the indexes of this lane's rows in w[m].  Of the sums'
+// HELD tiles of activations the first NT are used: instructions bound this loop, and a test
+// for each tile cost a layer of 64 tokens 196 us instead of 169 (with those of its other sums).
+// The four lanes of a row have the scales of four blocks between them, the next four on their way.
 template <int G32, int MT, int NT, int HELD, int S, typename X>
 __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
                                           const int64_t (&at)[MT][2], int K, int b0, int b1,

@@ -140,6 +140,20 @@ def test_sparse_gates(T, E, k, F, D, density, bits):
     check_y(o, x, w, "relu", wt, dw)
 
 
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("act,density", [("relu", 0.5), ("relu", 0.03), ("silu", 0.5)])
+@pytest.mark.parametrize("T,E,k", [(8, 32, 8), (64, 16, 2)])
+def test_many_neurons(T, E, k, act, density, bits):
+    """More than a round of neurons a block: tiles whose columns several warps divide unevenly,
+    slabs that begin within a block's share, chunks of h."""
+    F, D = 2100, 520
+    r, w = layer(E, F, D, bits, seed=12, density=density, group=64)
+    x = tokens(T, D)
+    o = tw.twell_moe_decode(x, r, *w, top_k=k, act=act)
+    wt, dw = check_choice(o, x, r, k, True)
+    check_y(o, x, w, act, wt, dw)
+
+
 @pytest.mark.parametrize("bits,T,D", [(16, 2, 16384), (4, 12, 8200), (16, 12, 8192), (4, 1, 9000)])
 def test_wide(bits, T, D):
     r, w = layer(3, 24, D, bits, seed=5, group=32)
