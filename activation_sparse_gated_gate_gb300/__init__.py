@@ -1090,17 +1090,21 @@ def twell_quant_int4(w, group=128, zero_points=False, out=None, stream=None) -> 
     else:
         w_type, ld = _vec(w, _TYPES, "w", dev, w.shape), K
     if out is None:
-        nb = -(-K // 128)
+        nb, device, zero = -(-K // 128), w.device, None
         held = (*lead, nb * (128 // group))
-        out = Int4(torch.empty((*lead, 64 * nb), dtype=torch.uint8, device=w.device),
-                   torch.empty(held, dtype=torch.bfloat16, device=w.device),
-                   torch.empty(held, dtype=torch.uint8, device=w.device) if zero_points else None,
-                   K, group)
+        code = torch.empty((*lead, 64 * nb), dtype=torch.uint8, device=device)
+        scale = torch.empty(held, dtype=torch.bfloat16, device=device)
+        if zero_points:
+            zero = torch.empty(held, dtype=torch.uint8, device=device)
+        out = Int4(code, scale, zero, K, group)
+        desc = (lead.numel(), K, group, code.data_ptr(), scale.data_ptr(),
+                zero.data_ptr() if zero_points else 0)
     elif not isinstance(out, Int4):
         raise TypeError("out must be an Int4")
     elif out.K != K or out.group != group or (out.zero is not None) != bool(zero_points):
         raise ValueError("out is of another kind: K, group and zero points are the call's")
-    desc, _ = _int4(out, "out", dev, lead)
+    else:
+        desc, _ = _int4(out, "out", dev, lead)
     _run("twell_quant_int4", dev, w.data_ptr(), w_type, ld, _INT4.pack(*desc))
     return out
 
@@ -1223,18 +1227,20 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
             raise ValueError("top_k is needed with a router")
         r_type = _vec(router, _TYPES, "router", dev, (E, D))
         p_router = router.data_ptr()
-        if ids is None:
-            ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
-        if weights is None:
-            weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
     elif ids is None or weights is None:
         raise ValueError("without a router, ids and weights are needed")
     elif top_k is None:
         if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
             raise ValueError("ids must be [T][k]")
         top_k = ids.shape[1]
-    _vec(ids, _I32, "ids", dev, (T, top_k))
-    _vec(weights, _F32, "weights", dev, (T, top_k))
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+    else:
+        _vec(ids, _I32, "ids", dev, (T, top_k))
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+    else:
+        _vec(weights, _F32, "weights", dev, (T, top_k))
     if y is None:
         if dtype not in _TYPES:
             raise TypeError(f"dtype must be bf16 or fp32, got {dtype}")
