@@ -117,27 +117,27 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       zero[h] += GROUPS;
     }
   };
+  // A block's rows of x at once, or where they would not fit in registers, those of 32 columns
+  // while the 32 before are used.
+  constexpr int HELD = NT <= 2 ? 4 : 2;
+  uint4 u[HELD][NT];
+  int left = p.K - b0 * kInt4Block - 8 * c;  // columns before K
+  const auto load_x = [&](int q) {
+    if (left + 8 * c >= (q < 4 ? kInt4Block : kInt4Block + 32)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) u[q % HELD][t] = x.load(t, q, 2 * kInt4Block);
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) u[q % HELD][t] = x.load(t, q, left);
+    }
+  };
   if (b0 < b1) fetch();
+  if (HELD == 2) load_x(0);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) now[h] = next[h], s_now[h] = s_next[h];
     if (b + 1 < b1) fetch();
-    const int left = p.K - b * kInt4Block - 8 * c;  // columns before K
-    // (a block's rows of x at once, or 32 columns' where they would not fit in registers)
-    constexpr int HELD = NT <= 2 ? 4 : 1;
-    uint4 u[HELD][NT];
-    const auto load_x = [&](int q) {
-      if (left + 8 * c >= kInt4Block) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          u[q % HELD][t] = x.load(t, q, kInt4Block);
-      } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          u[q % HELD][t] = x.load(t, q, left);
-      }
-    };
     if (HELD == 4) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) load_x(q);
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
         for (int j = 0; j < 4; ++j) part[t][j] = 0.0f;
 #pragma unroll
       for (int q = k * G32; q < (k + 1) * G32; ++q) {
-        if (HELD == 1) load_x(q);
+        if (HELD == 2) load_x(q + 1);
         uint32_t v[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       }
     }
     x.advance(kInt4Block);
+    left -= kInt4Block;
   }
 
   // the warps' sums
