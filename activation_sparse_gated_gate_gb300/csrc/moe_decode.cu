@@ -1043,7 +1043,9 @@ Layout layout_of(const DeviceInfo& dev, int32_t T, int32_t D, int32_t F, int32_t
   l.list = take(4 * P);
   l.live = take(4 * static_cast<size_t>(T));
   l.masks = take(2 * slabs * units);
-  l.plane = static_cast<int64_t>((P + 7 * slabs) / 8 * 16 * units * 8);
+  // (tiles: an expert's last may not be whole)
+  const size_t used = P < static_cast<size_t>(E) ? P : E;
+  l.plane = static_cast<int64_t>((P + 7 * used) / 8 * 16 * units * 8);
   l.h = take(6 * static_cast<size_t>(l.plane));
   l.part = take(4 * P * splits * D);
   l.total = at;

@@ -619,7 +619,7 @@ typedef struct {
  *   y[t] = sum over the slots of weight sum_j a(x . Wg[e][j]) (x . Wu[e][j]) Wd[e][j]
  * with a = SiLU or ReLU (a neuron whose gate is not positive for a token contributes nothing
  * to it, whatever its row of Wu holds; its rows of Wu and Wd are not read where that is so
- * for all of the expert's tokens).
+ * for all of the expert's tokens, and where it is not, its row of Wd enters times 0).
  *   x        [T][D] bf16
  *   router   [E][D] of router_type, or NULL: ids and weights are given
  *   ids      [T][top_k] int32, weights [T][top_k] fp32: the choice, written with a router

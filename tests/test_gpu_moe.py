@@ -330,6 +330,23 @@ def test_workspace_of_the_largest_batch():
         assert torch.equal(o.y, tw.twell_moe_decode(x[:T], r, *w, top_k=k).y)
 
 
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("T,E,k", [(1, 64, 8), (8, 64, 8), (8, 3, 3), (9, 200, 1), (64, 16, 2),
+                                   (256, 30, 8), (256, 500, 8)])
+def test_stays_within_its_workspace(T, E, k, bits):
+    D, F = 136, 50
+    r, w = layer(E, F, D, bits, seed=6, group=32)
+    x = tokens(T, D)
+    need = tw.twell_moe_decode_workspace(T, D, F, E, k)
+    buf = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    for act in ("relu", "silu"):
+        o = tw.twell_moe_decode(x, r, *w, top_k=k, act=act, ws=buf[:need])
+        assert torch.equal(o.y, tw.twell_moe_decode(x, r, *w, top_k=k, act=act).y)
+    one = torch.zeros((T, k), dtype=torch.int32, device="cuda")   # all with one expert
+    tw.twell_moe_decode(x, None, *w, ids=one, weights=o.weights, ws=buf[:need])
+    assert (buf[need:] == 171).all()
+
+
 # ------------------------------------------- refusals of the binding
 
 
