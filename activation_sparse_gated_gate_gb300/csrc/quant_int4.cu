@@ -9,12 +9,13 @@
 // at most one off, and the remainder v - code s, exact in one fused operation, says
 // whether it is (an IEEE division for each value would double the kernel's instructions):
 // eight values whose remainders are all below s / 2 have their codes, others are looked at
-// one by one.  Of bf16 values, where one in some hundred is a tie, the remainder gives the
-// quotient itself to its last bit, and no quotient of two 8-bit numbers is so near a
-// tie without being one.
+// one by one.  Of bf16 values one in some hundred is a tie, but a quotient of two 8-bit numbers
+// that is none is 2^-9 or more away from any (2 v - (2 q + 1) s is a multiple of the last place of
+// one of them): rounded to multiples of 2^-11 first, ties are exact and others stay where
+// they are.
 // The stored order is int4.cuh's.
 //
-// Bound by memory (8192 x 2048 bf16 and back in two launches, 76 MB: 17.7 us, 4.3 TB/s) and
+// Bound by memory (8192 x 2048 bf16 and back in two launches, 76 MB: 16.5 us, 4.6 TB/s) and
 // of ragged rows by instructions (1001 x 1999 with zero points and back: 10.8 us).  Half a
 // warp takes a block of 128 columns of a row, 16 bytes (bf16) or 32 a lane; a group's maximum is taken over its 4, 8 or 16 lanes; a lane's eight
 // codes are two runs of 16 bits, which a pair of lanes exchanges into words.  Rows off 16-byte
@@ -27,6 +28,7 @@ namespace twell {
 namespace {
 
 constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer
+constexpr float kSnap = 6144.0f;       // 1.5 2^12: the nearest multiple of 2^-11
 constexpr float kSmall = 7.88860905e-31f, kLift = 1.2676506e30f;  // 2^-100, 2^100
 
 struct Scale {
@@ -97,8 +99,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&v)[N], const Scale& k
     const float w = v[order[i]];
     float t;
     if (BF16) {
-      const float near = w * k.inv;
-      t = fmaf(fmaf(-near, k.s, w), k.inv, near) + kMagic;
+      t = fmaf(w, k.inv, kSnap) + (kMagic - kSnap);
     } else {
       t = fmaf(w, k.inv, kMagic);
       worst = fmaxf(worst, fabsf(fmaf(kMagic - t, k.s, w)));
