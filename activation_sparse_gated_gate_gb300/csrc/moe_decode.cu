@@ -192,29 +192,34 @@ __device__ __forceinline__ void ldmatrix_x4_t(uint32_t at, uint32_t& a, uint32_t
 
 // A step of the sums over neurons: 16 of them by a tile of columns.  Lane (g, c) uses the
 // neurons 2 c, 2 c + 1, 2 c + 8, 2 c + 9, 16 bytes of bf16 each or 8 of 4-bit codes.  The warp
-// copies them into a slot of its ring by whole lines (row_of(r): row of the r-th neuron, absent
-// ones < 0; lanes that are neighbours have neighbouring pieces), 16-byte pieces swizzled
-// so that the lanes' reads meet no bank twice.  Of 4-bit rows lanes 0 to 15 also load
-// the scales of one neuron each, a step or two ahead.
+// copies them into a slot of its ring by whole lines (row_of(r): row of the r-th neuron; lanes that
+// are neighbours have neighbouring pieces), 16-byte pieces swizzled so that the lanes' reads
+// meet no bank twice.  Of 4-bit rows lanes 0 to 15 also load the scales of one neuron each, a
+// step or two ahead.  Neurons behind the last repeat it with an h of 0, columns behind D repeat
+// some of the row and are left out at the end.
 struct Bf16Step {
   static constexpr int BYTES = 2 * kSlotBytes;
+  // where the warp's columns begin in row `base`
+  struct Origin {
+    const uint16_t* w;
+    __device__ __forceinline__ Origin(const MoeParams& p, int64_t base, int d0)
+        : w(p.w[2] + base * p.D + min(d0 + 8 * static_cast<int>(threadIdx.x & 7), p.D - 8)) {}
+  };
   struct Scales {
-    __device__ __forceinline__ void load(const MoeParams&, int64_t, int, int) {}
+    __device__ __forceinline__ void load(const MoeParams&, const Origin&, int) {}
   };
   // piece g of neuron r
   static __device__ __forceinline__ uint32_t at(int r, int g) {
     return 128 * r + 16 * (g ^ (r & 6));
   }
   template <typename R>
-  static __device__ __forceinline__ void copy(const MoeParams& p, int64_t base, R row_of, int d0,
+  static __device__ __forceinline__ void copy(const MoeParams& p, const Origin& o, R row_of,
                                               uint32_t slot) {
-    const int lane = threadIdx.x & 31, g = lane & 7, d = d0 + 8 * g;
-    const uint16_t* from = p.w[2] + base * p.D + d;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 4 * i + (lane >> 3), row = row_of(r);
-      const bool in = row >= 0 && d < p.D;
-      cp_async16_or_zero(slot + at(r, g), in ? from + offset(row, p.D) : p.w[2], in);
+      const int r = 4 * i + (lane >> 3);
+      ptx::cp_async<16>(slot + at(r, lane & 7), o.w + offset(row_of(r), p.D));
     }
   }
   // h of a chunk in shared memory: [part][tile][neuron][8 pairs] of bf16
@@ -254,12 +259,24 @@ template <int G32>
 struct FourStep {
   static constexpr int BYTES = kSlotBytes;
   typedef BlockScales<G32> One;
+  struct Origin {
+    const uint8_t* code;
+    const uint16_t* scale;
+    const uint8_t* zero;
+    __device__ __forceinline__ Origin(const MoeParams& p, int64_t base, int d0) {
+      const Int4View& w = p.q[2];
+      const int block = d0 < p.D ? d0 / kInt4Block : 0;
+      code = w.code + base * w.pitch + block * kInt4Bytes + 16 * (threadIdx.x & 3);
+      const int64_t at = base * w.held + block * (4 / G32);
+      scale = w.scale + at;
+      zero = (w.zero ? w.zero : w.code) + at;
+    }
+  };
   struct Scales {
     One one;  // of neuron `lane & 15`
-    __device__ __forceinline__ void load(const MoeParams& p, int64_t base, int row, int d0) {
-      one.load(p.q[2], base * p.q[2].held + offset(max(row, 0), p.q[2].held) +
-                           d0 / kInt4Block * (4 / G32));
-      if (row < 0) one.clear();  // (no product with a scale that is not finite)
+    __device__ __forceinline__ void load(const MoeParams& p, const Origin& o, int row) {
+      const uint64_t at = offset(row, p.q[2].held);
+      one.load(o.scale + at, p.q[2].zero ? o.zero + at : nullptr);
     }
   };
   // where a neuron's h is: those of the four lanes of a quarter warp in different banks
@@ -270,15 +287,13 @@ struct FourStep {
     return 64 * pos + 16 * (q ^ (pos & 2));
   }
   template <typename R>
-  static __device__ __forceinline__ void copy(const MoeParams& p, int64_t base, R row_of, int d0,
+  static __device__ __forceinline__ void copy(const MoeParams& p, const Origin& o, R row_of,
                                               uint32_t slot) {
-    const Int4View& w = p.q[2];
-    const int lane = threadIdx.x & 31, q = lane & 3;
-    const uint8_t* from = w.code + base * w.pitch + d0 / kInt4Block * kInt4Bytes + 16 * q;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = 8 * i + (lane >> 2), row = row_of(r);
-      cp_async16_or_zero(slot + at(r, q), row >= 0 ? from + offset(row, w.pitch) : w.code, row >= 0);
+      const int r = 8 * i + (lane >> 2);
+      ptx::cp_async<16>(slot + at(r, lane & 3), o.code + offset(row_of(r), p.q[2].pitch));
     }
   }
   // h of a chunk in shared memory: [tile][place(neuron)][8 pairs] of fp32
@@ -331,8 +346,8 @@ struct FourStep {
 };
 
 // The two forms of weights: the sums over the blocks b0 to b1 of two tiles of rows (at[m][h]:
-// this lane's of matrix mat[m]), the step above, and the column of a tile that row g of the
-// upper (h = 0) or lower eight of its q-th 16 outputs is.
+// this lane's of matrix mat[m]), the step above, and where in a warp's sums of eight pairs
+// ([16 outputs q][2 h + pair & 1][4 g + pair / 2]; row g + 8 h of the q-th 16) columns are.
 struct Bf16 {
   static constexpr bool FOUR = false;
   static constexpr int COLS = 64;  // of a step's tile
@@ -346,7 +361,10 @@ struct Bf16 {
         {p.w[mat[1]] + at[1][0] * p.D, p.w[mat[1]] + at[1][1] * p.D}};
     bf16_rows<2, NT, S>(from, p.D, b0, b1, ring, nt, x, acc);
   }
-  static __device__ __forceinline__ int column(int q, int h, int g) { return 8 * g + 2 * q + h; }
+  // the t-th four columns, the first of them of pair 0, and how far on the others are
+  static __device__ __forceinline__ int columns(int t) { return 8 * (t & 7) + 4 * (t >> 3); }
+  static __device__ __forceinline__ int first_of(int t) { return 256 * (t >> 3) + 4 * (t & 7); }
+  static __device__ __forceinline__ int next(int j) { return 64 * j; }
 };
 template <int G>
 struct Four {
@@ -361,9 +379,11 @@ struct Four {
     if (NT > 1 && nt == 1) int4_rows<G, 2, 1, NT, S>(from, at, p.D, b0, b1, ring, x, acc);
     else int4_rows<G, 2, NT, NT, S>(from, at, p.D, b0, b1, ring, x, acc);
   }
-  static __device__ __forceinline__ int column(int q, int h, int g) {
-    return 32 * (q >> 1) + 8 * (g >> 1) + 2 * (2 * (q & 1) + h) + (g & 1);
+  static __device__ __forceinline__ int columns(int t) {
+    return 32 * (t >> 3) + 8 * (t & 3) + (t & 4);
   }
+  static __device__ __forceinline__ int first_of(int t) { return 128 * (t >> 2) + 8 * (t & 3); }
+  static __device__ __forceinline__ int next(int j) { return 64 * (j >> 1) + 4 * (j & 1); }
 };
 
 // The k largest of a token's logits and their weights, by a warp: slot `lane` of them.  EJ: 32s
@@ -826,6 +846,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int steps = (total + 15) / 16;
     const int64_t row0 = base + 16 * u0;
     const auto neuron = [&](int s) { return some ? list[s] : s; };
+    const auto first = [&] {  // what the end needs
+      if (u0 == ub && tid < ns) {
+        const int pair = __ldcg(p.plan.list + s0 + tid);
+        pairs[tid] = pair;
+        expect[tid] = __ldcg(p.plan.live + pair / p.k) * splits;
+        share[tid] = __ldcg(p.weights + pair);
+      }
+    };
+    if (total == 0) {
+      first();
+      __syncthreads();
+      continue;
+    }
 
     // h of the chunk, up to a whole step (of absent pairs: anything, each pair is a column of
     // its own)
@@ -841,50 +874,40 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (n >= nt_used) break;
         if constexpr (F::FOUR) {
           const uint32_t to = hs + (n * CHUNK + Step::place(s)) * HR;
-          cp_async16_or_zero(to, src + n * tile, on);
-          if (8 * n + 4 < ns) cp_async16_or_zero(to + 16, src + n * tile + 16, on);
+          ptx::cp_async16(to, src + n * tile, on ? 16 : 0);
+          if (8 * n + 4 < ns) ptx::cp_async16(to + 16, src + n * tile + 16, on ? 16 : 0);
         } else {
           const uint32_t to = hs + (n * CHUNK + s) * HR;
 #pragma unroll
           for (int q = 0; q < 3; ++q)
             if (q < 2 || three)
-              cp_async16_or_zero(to + q * NT * CHUNK * HR, src + n * tile + q * 2 * p.plan.plane, on);
+              ptx::cp_async16(to + q * NT * CHUNK * HR, src + n * tile + q * 2 * p.plan.plane, on ? 16 : 0);
         }
       }
     }
-    cp_async_commit_group();
+    ptx::cp_async_commit();
 
     int put = 0, get = 0, st_put = wn;
+    const typename Step::Origin origin(p, row0, d0);
     const auto issue = [&] {
-      Step::copy(
-          p, row0,
-          [&](int r) {
-            const int s = 16 * st_put + r;
-            return s < total && d0 < p.D ? neuron(s) : -1;
-          },
-          d0, ring_at + put * Step::BYTES);
-      cp_async_commit_group();
+      if (st_put < steps)
+        Step::copy(
+            p, origin, [&](int r) { return neuron(min(16 * st_put + r, total - 1)); },
+            ring_at + put * Step::BYTES);
+      ptx::cp_async_commit();
       st_put += WN;
       put = put + 1 == SB ? 0 : put + 1;
     };
     const auto scales = [&](int st, typename Step::Scales& s) {
-      const int i = 16 * st + (lane & 15);
-      s.load(p, row0, i < total && d0 < p.D ? neuron(i) : -1, d0 < p.D ? d0 : 0);
+      if (st < steps) s.load(p, origin, neuron(min(16 * st + (lane & 15), total - 1)));
     };
     typename Step::Scales s_now, s_next, s_then;
 #pragma unroll 1
     for (int i = 0; i < SB - 1; ++i) issue();
     scales(wn, s_now);
     scales(wn + WN, s_next);
-    if (u0 == ub) {  // what the end needs
-      if (tid < ns) {
-        const int pair = __ldcg(p.plan.list + s0 + tid);
-        pairs[tid] = pair;
-        expect[tid] = __ldcg(p.plan.live + pair / p.k) * splits;
-        share[tid] = __ldcg(p.weights + pair);
-      }
-    }
-    cp_async_wait_for<SB - 1>();
+    first();
+    ptx::cp_async_wait<SB - 1>();
     __syncthreads();
     // (for the tiles of pairs and parts of h that there are: a test for each would cost as much
     // as what it leaves out)
@@ -893,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int st = wn; st < steps; st += WN) {
         issue();
         scales(st + 2 * WN, s_then);
-        cp_async_wait_for<SB - 1>();
+        ptx::cp_async_wait<SB - 1>();
         __syncwarp();
         Step::template add<decltype(used)::value, NT, CHUNK, decltype(f32)::value>(
             ring_at + get * Step::BYTES, s_now, hs, st, acc);
@@ -909,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (three) run(Count<NT>(), Truth<true>());
       else run(Count<NT>(), Truth<false>());
     }
-    cp_async_wait_for<0>();
+    ptx::cp_async_wait<0>();
     __syncthreads();
   }
 
@@ -923,18 +946,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int j = 0; j < 4; ++j)
         red[warp * VALUES + ((n * MT + q) * 4 + j) * 32 + lane] = acc[q][n][j];
   __syncthreads();
+  constexpr int QUADS = 2 * TW;  // fours of columns of eight pairs
 #pragma unroll 1
-  for (int i = tid; i < WC * nt_used * (MT * 128); i += kThreads) {
-    const int w0 = i / (nt_used * (MT * 128)), at = i % (nt_used * (MT * 128));
-    const int l = at & 31, j = (at >> 5) & 3, q = (at >> 7) % MT, n = (at >> 7) / MT;
-    const int pair = 8 * n + 2 * (l & 3) + (j & 1);
-    const int d = CW * ct + TW * w0 + F::column(q, j / 2, l >> 2);
+  for (int i = tid; i < WC * nt_used * QUADS; i += kThreads) {
+    const int w0 = i / QUADS & (WC - 1), n = i >= WC * QUADS, t = i % QUADS / 8;
+    const int pair = 8 * n + i % 8, d = CW * ct + TW * w0 + F::columns(t);
     if (pair >= ns || d >= p.D) continue;
-    float v = 0.0f;
-#pragma unroll 1
-    for (int w = w0; w < kWarps; w += WC) v += red[w * VALUES + at];
-    __stcg(p.part + (static_cast<int64_t>(pairs[pair]) * splits + part) * p.D + d,
-           v * share[pair]);
+    const float* at = red + w0 * VALUES + n * (MT * 128) + F::first_of(t) + 32 * (i & 1) + (i >> 1 & 3);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+    for (int w = w0; w < kWarps; w += WC, at += WC * VALUES)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += at[F::next(j)];
+    const float a = share[pair];
+    __stcg(reinterpret_cast<float4*>(
+               p.part + (static_cast<int64_t>(pairs[pair]) * splits + part) * p.D + d),
+           make_float4(v[0] * a, v[1] * a, v[2] * a, v[3] * a));
   }
   __threadfence();
   __syncthreads();

@@ -19,19 +19,6 @@ namespace twell {
 
 constexpr int kSlotBytes = 1024;  // 16 rows of a block of 128 columns in 4 bits, or of 32 in bf16
 
-template <int N>
-__device__ __forceinline__ void cp_async_wait_for() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit_group() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// 16 bytes past the first cache, zeros without `have`.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(have ? 16 : 0)
-               : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -80,8 +67,8 @@ __device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], in
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        cp_async16_or_zero(mine + put * SLOT + (2 * m + h) * 512, at[m][h] + (in ? k_put : 0), in);
-    cp_async_commit_group();
+        ptx::cp_async16(mine + put * SLOT + (2 * m + h) * 512, at[m][h] + (in ? k_put : 0), in ? 16 : 0);
+    ptx::cp_async_commit();
     k_put += 32;
     put = put + 1 == S ? 0 : put + 1;
   };
@@ -95,7 +82,7 @@ __device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       issue();
-      cp_async_wait_for<S - 1>();
+      ptx::cp_async_wait<S - 1>();
       uint4 u[MT], v[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -120,7 +107,7 @@ __device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], in
       b.load(i % DIST, blk * kInt4Block + 32 * (i + DIST) + c8, nt, x);
     }
   }
-  cp_async_wait_for<0>();
+  ptx::cp_async_wait<0>();
 }
 
 // The same of 4-bit rows; at[m][h]: the indexes of this lane's rows in w[m].  Of the sums'
@@ -148,10 +135,10 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          cp_async16_or_zero(mine + put * SLOT + (2 * m + h) * 512,
-                             code[m][h] + b_put * kInt4Bytes, true);
+          ptx::cp_async<16>(mine + put * SLOT + (2 * m + h) * 512,
+                             code[m][h] + b_put * kInt4Bytes);
     }
-    cp_async_commit_group();
+    ptx::cp_async_commit();
     ++b_put;
     put = put + 1 == S ? 0 : put + 1;
   };
@@ -185,7 +172,7 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) sc[m][h].from_lane(four[m][h], (lane & 28) + i);
-      cp_async_wait_for<S - 1>();
+      ptx::cp_async_wait<S - 1>();
       uint4 raw[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -239,7 +226,7 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
       }
     }
   }
-  cp_async_wait_for<0>();
+  ptx::cp_async_wait<0>();
 }
 
 }  // namespace twell
