@@ -104,7 +104,8 @@ __device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], in
           for (int j = 0; j < 4; ++j) acc[m][t][j] += part[j];
         }
       }
-      b.load(i % DIST, blk * kInt4Block + 32 * (i + DIST) + c8, nt, x);
+      if (i + DIST < 4 || blk + 1 < b1)
+        b.load(i % DIST, blk * kInt4Block + 32 * (i + DIST) + c8, nt, x);
     }
   }
   ptx::cp_async_wait<0>();
@@ -212,7 +213,8 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
             mma16816(part[m][t], v[0][2], v[1][2], v[0][3], v[1][3], u.z, u.w);
           }
         }
-        b.load(q % DIST, blk * kInt4Block + 32 * (q + DIST) + 8 * c, NT, x);
+        if (q + DIST < 4 || blk + 1 < b1)
+          b.load(q % DIST, blk * kInt4Block + 32 * (q + DIST) + 8 * c, NT, x);
         if (q % G32 == G32 - 1) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
