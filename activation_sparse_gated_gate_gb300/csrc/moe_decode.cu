@@ -21,11 +21,11 @@
 // 4-bit codes are unpacked in registers, where its operands come from, and eight to sixteen
 // pairs of an expert leave the tensor pipe idle either way (17 to 25 % of its cycles).
 //   What bounds it (E = 64, D = 2048, F = 1024, 8 experts a token, weights from memory):
-//   * one token: the chain of launches, dependent reads and barriers, 26 us in bf16 with
-//     1 % of the neurons active (34 MB read, 5 us of the stream), 28 in 4 bits with all
-//   * 64 tokens, bf16: the stream, 805 MB in 180 to 186 us (4.4 TB/s; neurons 4.8, down 3.8)
-//   * 64 tokens, 4 bits: instructions, 5 a weight for unpacking, split parts and addresses with
-//     registers for 16 warps an SM, which issue in half of the cycles: 166 us
+//   * one token: the chain of launches, dependent reads and barriers, 25 us in bf16 with
+//     1 % of the neurons active (34 MB read, 5 us of the stream), 26 in 4 bits with all
+//   * 64 tokens, bf16: the stream, 805 MB in 175 to 182 us (4.5 TB/s; neurons 4.6, down 4.2)
+//   * 64 tokens, 4 bits: instructions, 4 to 7 a weight for unpacking, split parts and addresses, with
+//     registers for 16 warps an SM, which issue in half of the cycles: 156 us
 //   A form in two kernels (clusters of 8 CTAs that exchanged h through shared memory and
 // summed their columns) took as long for a token and 364 us (bf16) and 407 (4 bits) for 64: its
 // phases waited for one another.
@@ -1020,7 +1020,8 @@ int pair_tiles(int32_t T, int32_t E, int32_t k) { return T <= 8 || T * k < 7 * E
 // and parts of a slab's neurons.  The widest CTAs that still give every SM four, so that
 // an SM's last ones leave little of it idle (64 tokens, 4 bits: 166 us, 172 with two, 239 with
 // one, 177 with eight; bf16 187, 191, 192, 197).  Neurons are divided where CTAs of one
-// warp's width leave SMs without two, into parts of 128 neurons at least.
+// warp's width leave SMs without two, into parts of 128 neurons at least (a token, 4 bits:
+// 26.2 us, 29.3 where they are divided for one an SM, 30.6 for four).
 struct Down {
   int32_t side, tiles, slabs, splits;
 };
