@@ -23,7 +23,7 @@
 //   What bounds it (E = 64, D = 2048, F = 1024, 8 experts a token, weights from memory):
 //   * one token: the chain of launches, dependent reads and barriers, 25 us in bf16 with
 //     1 % of the neurons active (34 MB read, 5 us of the stream), 26 in 4 bits with all
-//   * 64 tokens, bf16: the stream, 805 MB in 175 to 182 us (4.5 TB/s; neurons 4.6, down 4.2)
+//   * 64 tokens, bf16: the stream, 805 MB in 170 us (4.75 TB/s; neurons 4.9, down 4.2)
 //   * 64 tokens, 4 bits: instructions, 4 to 7 a weight for unpacking, split parts and addresses, with
 //     registers for 16 warps an SM, which issue in half of the cycles: 156 us
 //   A form in two kernels (clusters of 8 CTAs that exchanged h through shared memory and

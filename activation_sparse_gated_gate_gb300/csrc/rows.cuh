@@ -19,6 +19,14 @@ namespace twell {
 
 constexpr int kSlotBytes = 1024;  // 16 rows of a block of 128 columns in 4 bits, or of 32 in bf16
 
+// As ptx::cp_async16, with the rest of the 256 bytes on its way to the second cache: for a
+// stream of rows whose neighbouring pieces come next (64 tokens in bf16: 175 us of the layer
+// without, 170 with; of 4-bit rows it makes no difference).
+__device__ __forceinline__ void cp_async16_ahead(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -67,7 +75,8 @@ __device__ __forceinline__ void bf16_rows(const uint16_t* const (&at)[MT][2], in
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        ptx::cp_async16(mine + put * SLOT + (2 * m + h) * 512, at[m][h] + (in ? k_put : 0), in ? 16 : 0);
+        cp_async16_ahead(mine + put * SLOT + (2 * m + h) * 512, at[m][h] + (in ? k_put : 0),
+                         in ? 16 : 0);
     ptx::cp_async_commit();
     k_put += 32;
     put = put + 1 == S ? 0 : put + 1;
