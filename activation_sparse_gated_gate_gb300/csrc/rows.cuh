@@ -38,12 +38,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 
 // The activations of a row tile's product: B operands of 32 columns each, loaded DIST pieces of
 // 32 ahead of their use (a load from the second cache takes longer than a piece does).
-// x(t, k) loads columns k .. k + 7 of activation 8 t + g; k is clamped to the last eight by
-// `top`, and what lies behind K is masked where a block is not whole.  Activations that are
+// x(t, k) loads columns k .. k + 7 of activation 8 t + g (it clamps k to the last eight there
+// are); what lies behind K is masked where a block is not whole.  Activations that are
 // absent may hold anything: a column of B is a column of the result and nothing else.
 template <int NT>
 struct Ahead {
-  static constexpr int DIST = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+  static constexpr int DIST = NT == 1 ? 4 : 2;
   uint4 v[DIST][NT];
   template <typename X>
   __device__ __forceinline__ void load(int at, int k, int nt, X x) {
