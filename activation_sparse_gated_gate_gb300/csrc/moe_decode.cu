@@ -25,7 +25,7 @@
 //     1 % of the neurons active (34 MB read, 5 us of the stream), 26 in 4 bits with all
 //   * 64 tokens, bf16: the stream, 805 MB in 170 us (4.75 TB/s; neurons 4.9, down 4.2)
 //   * 64 tokens, 4 bits: instructions, 4 to 7 a weight for unpacking, split parts and addresses, with
-//     registers for 16 warps an SM, which issue in half of the cycles: 156 us
+//     registers for 16 warps an SM, which issue in half of the cycles: 150 us
 //   A form in two kernels (clusters of 8 CTAs that exchanged h through shared memory and
 // summed their columns) took as long for a token and 364 us (bf16) and 407 (4 bits) for 64: its
 // phases waited for one another.
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   int32_t* live = place + P;                          // [T]
   __shared__ int16_t act[RM];                         // active rows of this round
   __shared__ uint32_t sh_mask[kWarps];                // those of a unit
-  __shared__ int32_t sh_slabs;
+  __shared__ int32_t sh_slabs, sh_full;
 
   ptx::grid_launch_next();
   for (int i = tid; i < p.E; i += kThreads) count[i] = 0;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       sums += __shfl_sync(0xffffffffu, up, 31);
     }
     const int slabs = NT == 1 ? sums >> 12 : full + (sums >> 20);
-    if (lane == 0) sh_slabs = slabs;
+    if (lane == 0) sh_slabs = slabs, sh_full = NT == 1 ? slabs : full;
   }
   __syncthreads();
 #pragma unroll 1
@@ -602,9 +602,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- the slabs' units of 16 neurons in a row, divided evenly among the CTAs
   const bool silu = p.act == TWELL_SILU;
   const uint32_t units = (p.F + 15u) / 16u, U = units * slabs, C = min(gridDim.x, U);
-  const uint32_t u_last = blockIdx.x < C ? U * (blockIdx.x + 1u) / C : 0u;
+  const auto first_unit = [&](uint32_t i) {  // of CTA i
+    // what a unit of a slab of two tiles costs, and of one (4 bits, 64 tokens: 149 us, 156 where
+    // both count the same; bf16 170 and 172)
+    constexpr uint32_t FULL = F::FOUR ? 4 : 8, OTHER = F::FOUR ? 3 : 7;
+    const uint32_t full = units * sh_full, all = full * FULL + (U - full) * OTHER;
+    const uint32_t at = static_cast<uint32_t>(static_cast<uint64_t>(all) * i / C);
+    return at <= full * FULL ? at / FULL : full + (at - full * FULL) / OTHER;
+  };
+  const uint32_t u_last = blockIdx.x < C ? first_unit(blockIdx.x + 1u) : 0u;
 #pragma unroll 1
-  for (uint32_t ub = blockIdx.x < C ? U * blockIdx.x / C : 0u; ub < u_last;) {
+  for (uint32_t ub = blockIdx.x < C ? first_unit(blockIdx.x) : 0u; ub < u_last;) {
     const uint32_t a = ub / units;
     const int e = slab[a].x, s0 = slab[a].y, ns = slab[a].z, tile0 = slab[a].w;
     const int u0 = ub - a * units;
