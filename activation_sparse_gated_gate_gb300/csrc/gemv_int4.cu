@@ -16,7 +16,8 @@
 // at a time, each reading W again (from the second cache).  All 8 NT rows are computed, whether x
 // has them or repeats its last: a test for each tile cost 64 x 9216 x 2304 10 % of its time.
 //   Measured, weights from memory: 1 x 8192 x 2048 5.6 us (8.7 MB, 1.5 TB/s; a kernel that only
-// reads them 2.8 to 4.7), 5 x 2048 x 8192 6.8, 64 x 9216 x 2304 17.2.
+// reads them 2.8 to 4.7), 5 x 2048 x 8192 6.9, 64 x 9216 x 2304 16.2, 1 x 32768 x 8192 42.6
+// (3.3 TB/s).
 #include <type_traits>
 
 #include "common.cuh"
@@ -206,11 +207,23 @@ template <int NT>
 twell_status launch(const GemvParams& p, int32_t group, bool xv, int sms, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.N + 15LL) / 16),
                   static_cast<unsigned>((static_cast<int64_t>(p.T) + 8 * NT - 1) / (8 * NT)));
-  // as many warps as run at once (20 an SM): what a warp does once takes as long as one or
-  // two blocks do (8192 x 2048: 4 warps a CTA 5.8 us, 8 6.2; 2048 x 8192: 16 6.4, 8 7.4)
+  // As many warps as run at once (20 an SM; 16 where more than eight rows of x take the
+  // registers): what a warp does once takes as long as one or two blocks do (8192 x 2048: 4
+  // warps a CTA 5.8 us, 8 6.2; 2048 x 8192: 16 6.4, 8 7.4; 16 rows, 11000 x 4096: 2 15.7, 4 17.9).
+  // CTAs that run one after the other are better shorter, up to eight rows with 4 warps at
+  // least (32768 x 8192: 42 us, 50 with 2; 12288 x 4096 12.1 and 13.9), of more rows with 4
+  // where that leaves clearly less of the last round idle (32 rows, 20000 x 4096: 40 us, 49
+  // with 2; 12288 x 4096, one round: 27 and 23).
   const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y;
+  const int most = (NT == 1 ? 20 : 16) * sms, least = NT == 1 && p.nb >= 8 ? 4 : 2;
   int warps = kMaxWarps;
-  while (warps > 2 && (warps > p.nb || warps * ctas > 20 * sms)) warps /= 2;
+  while (warps > least && (warps > p.nb || warps * ctas > most)) warps /= 2;
+  if (NT > 1 && warps == 2 && p.nb >= 8 && ctas > 8 * sms) {
+    const auto busy = [&](int64_t at_once) {  // percent, of the rounds
+      return 100 * ctas / ((ctas + at_once - 1) / at_once * at_once);
+    };
+    if (busy(4 * sms) > busy(8 * sms) + 10) warps = 4;
+  }
   const size_t smem = warps * NT * 512;
 #define TWELL_GO(G32)                                                      \
   (xv ? gemv_int4_kernel<NT, G32, true><<<grid, 32 * warps, smem, s>>>(p)  \

@@ -25,7 +25,7 @@
 //     1 % of the neurons active (34 MB read, 5 us of the stream), 26 in 4 bits with all
 //   * 64 tokens, bf16: the stream, 805 MB in 170 us (4.75 TB/s; neurons 4.9, down 4.2)
 //   * 64 tokens, 4 bits: instructions, 4 to 7 a weight for unpacking, split parts and addresses, with
-//     registers for 16 warps an SM, which issue in half of the cycles: 150 us
+//     registers for 16 warps an SM, which issue in half of the cycles: 145 us
 //   A form in two kernels (clusters of 8 CTAs that exchanged h through shared memory and
 // summed their columns) took as long for a token and 364 us (bf16) and 407 (4 bits) for 64: its
 // phases waited for one another.

@@ -186,6 +186,15 @@ def test_gemv(T, N, K, group, zero_points):
     check_gemv(x, q, torch.bfloat16)
 
 
+@pytest.mark.parametrize("T,N", [(1, 8001), (2, 30007), (9, 30007), (16, 20000), (20, 8001),
+                                 (33, 20000)])
+def test_gemv_many_rows(T, N):
+    """Few warps share K, blocks run one after the other."""
+    K = 1100
+    q = tw.twell_quant_int4(weights(N, K, N).cuda(), group=128)
+    check_gemv(weights(T, K, 3, torch.bfloat16).cuda(), q, torch.float32)
+
+
 @pytest.mark.parametrize("K,off,pitch", [(256, 0, 264), (256, 8, 264), (256, 1, 260), (250, 2, 252)])
 @pytest.mark.parametrize("T", [1, 12, 40])
 def test_gemv_strided(T, K, off, pitch):
