@@ -43,8 +43,6 @@ namespace {
 
 template <int N>
 using Count = std::integral_constant<int, N>;
-template <bool B>
-using Truth = std::integral_constant<bool, B>;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
@@ -142,27 +140,20 @@ __device__ __forceinline__ float behind(float a) {
   return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u);
 }
 
-// Two values as three bf16 each, whose sum they are (to their 24 bits).  Two hold 16 bits:
-// enough where y is rounded to bf16.
-template <bool THREE>
+// Two values as three bf16 each, whose sum they are (to their 24 bits).
 __device__ __forceinline__ void split(float a, float b, uint32_t (&o)[3]) {
   o[0] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
   const float inf = __uint_as_float(0x7f800000u);
   a = fabsf(a) == inf ? 0.0f : behind(a), b = fabsf(b) == inf ? 0.0f : behind(b);
-  if constexpr (THREE) {
-    o[1] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-    o[2] = bf16x2(behind(a), behind(b));
-  } else {
-    o[1] = bf16x2(a, b);
-  }
+  o[1] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  o[2] = bf16x2(behind(a), behind(b));
 }
 
 // d += a times the values that b0, b1 are split into, the small ones first.
-template <bool THREE>
 __device__ __forceinline__ void mma_split(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, const uint32_t (&b0)[3],
                                           const uint32_t (&b1)[3]) {
-  if constexpr (THREE) mma16816(d, a0, a1, a2, a3, b0[2], b1[2]);
+  mma16816(d, a0, a1, a2, a3, b0[2], b1[2]);
   mma16816(d, a0, a1, a2, a3, b0[1], b1[1]);
   mma16816(d, a0, a1, a2, a3, b0[0], b1[0]);
 }
@@ -224,7 +215,7 @@ struct Bf16Step {
   }
   // h of a chunk in shared memory: [part][tile][neuron][8 pairs] of bf16
   static constexpr int H_ROW = 16;
-  template <int NU, int NT, int CHUNK, bool THREE>
+  template <int NU, int NT, int CHUNK>
   static __device__ __forceinline__ void add(uint32_t slot, const Scales&, uint32_t hs, int st,
                                              float (&acc)[4][NT][4]) {
     const int lane = threadIdx.x & 31;
@@ -242,7 +233,7 @@ struct Bf16Step {
       // (lanes 16 to 31: the rows of the second part)
       const uint32_t from = hs + ((lane >> 4) * NT * CHUNK + n * CHUNK + 16 * st + (lane & 15)) * H_ROW;
       ldmatrix_x4_t(from, b0[n][0], b1[n][0], b0[n][1], b1[n][1]);
-      if constexpr (THREE) ldmatrix_x2_t(from + 2 * NT * CHUNK * H_ROW, b0[n][2], b1[n][2]);
+      ldmatrix_x2_t(from + 2 * NT * CHUNK * H_ROW, b0[n][2], b1[n][2]);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -250,7 +241,7 @@ struct Bf16Step {
                      a2 = __byte_perm(v2[q], v3[q], 0x5410), a3 = __byte_perm(v2[q], v3[q], 0x7632);
 #pragma unroll
       for (int n = 0; n < NU; ++n) {
-        mma_split<THREE>(acc[q][n], a0, a1, a2, a3, b0[n], b1[n]);
+        mma_split(acc[q][n], a0, a1, a2, a3, b0[n], b1[n]);
       }
     }
   }
@@ -298,7 +289,7 @@ struct FourStep {
   }
   // h of a chunk in shared memory: [tile][place(neuron)][8 pairs] of fp32
   static constexpr int H_ROW = 32;
-  template <int NU, int NT, int CHUNK, bool THREE>
+  template <int NU, int NT, int CHUNK>
   static __device__ __forceinline__ void add(uint32_t slot, const Scales& sc, uint32_t hs, int st,
                                              float (&acc)[8][NT][4]) {
     const int lane = threadIdx.x & 31, c = lane & 3;
@@ -323,8 +314,8 @@ struct FourStep {
       if (k % G32 == 0) {
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
-          split<THREE>(h_of(0, n) * s[0].scale(gk), h_of(1, n) * s[1].scale(gk), b0[n]);
-          split<THREE>(h_of(2, n) * s[2].scale(gk), h_of(3, n) * s[3].scale(gk), b1[n]);
+          split(h_of(0, n) * s[0].scale(gk), h_of(1, n) * s[1].scale(gk), b0[n]);
+          split(h_of(2, n) * s[2].scale(gk), h_of(3, n) * s[3].scale(gk), b1[n]);
         }
       }
       const uint32_t sel = k & 1 ? 0x7632 : 0x5410;
@@ -338,7 +329,7 @@ struct FourStep {
                        a2 = nibbles(p23, 2 * q, z23), a3 = nibbles(p23, 2 * q + 1, z23);
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
-          mma_split<THREE>(acc[2 * k + q][n], a0, a1, a2, a3, b0[n], b1[n]);
+          mma_split(acc[2 * k + q][n], a0, a1, a2, a3, b0[n], b1[n]);
         }
       }
     }
@@ -759,12 +750,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 make_float2(h[2 * i], h[2 * i + 1]);
           } else {
             uint32_t o[3];
-            if (p.y_f32) split<true>(h[2 * i], h[2 * i + 1], o);
-            else split<false>(h[2 * i], h[2 * i + 1], o);
+            split(h[2 * i], h[2 * i + 1], o);
             uint16_t* to = static_cast<uint16_t*>(p.plan.h) + at;
 #pragma unroll
             for (int q = 0; q < 3; ++q)
-              if (q < 2 || p.y_f32) *reinterpret_cast<uint32_t*>(to + q * p.plan.plane) = o[q];
+              *reinterpret_cast<uint32_t*>(to + q * p.plan.plane) = o[q];
           }
         }
       }
@@ -797,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tiles = gridDim.x, units = (p.F + 15) / 16, d0 = CW * ct + TW * wc;
   const int ub = static_cast<int>(static_cast<int64_t>(units) * part / splits),
             ue = static_cast<int>(static_cast<int64_t>(units) * (part + 1) / splits);
-  const bool three = p.y_f32 != 0, relu = p.act == TWELL_RELU;
+  const bool relu = p.act == TWELL_RELU;
   ptx::grid_wait();
   // (reads that depend on one another are few: under load each waits behind all that is
   // on its way)
@@ -890,8 +880,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint32_t to = hs + (n * CHUNK + s) * HR;
 #pragma unroll
           for (int q = 0; q < 3; ++q)
-            if (q < 2 || three)
-              ptx::cp_async16(to + q * NT * CHUNK * HR, src + n * tile + q * 2 * p.plan.plane, on ? 16 : 0);
+            ptx::cp_async16(to + q * NT * CHUNK * HR, src + n * tile + q * 2 * p.plan.plane,
+                            on ? 16 : 0);
         }
       }
     }
@@ -919,29 +909,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     first();
     ptx::cp_async_wait<SB - 1>();
     __syncthreads();
-    // (for the tiles of pairs and parts of h that there are: a test for each would cost as much
-    // as what it leaves out)
-    const auto run = [&](auto used, auto f32) {
+    // (for the tiles of pairs that there are: a test for each would cost as much as what it
+    // leaves out)
+    const auto run = [&](auto used) {
 #pragma unroll 1
       for (int st = wn; st < steps; st += WN) {
         issue();
         scales(st + 2 * WN, s_then);
         ptx::cp_async_wait<SB - 1>();
         __syncwarp();
-        Step::template add<decltype(used)::value, NT, CHUNK, decltype(f32)::value>(
+        Step::template add<decltype(used)::value, NT, CHUNK>(
             ring_at + get * Step::BYTES, s_now, hs, st, acc);
         __syncwarp();  // (the next copy but SB - 2 goes where this step was)
         get = get + 1 == SB ? 0 : get + 1;
         s_now = s_next, s_next = s_then;
       }
     };
-    if (NT > 1 && nt_used == 1) {
-      if (three) run(Count<1>(), Truth<true>());
-      else run(Count<1>(), Truth<false>());
-    } else {
-      if (three) run(Count<NT>(), Truth<true>());
-      else run(Count<NT>(), Truth<false>());
-    }
+    if (NT > 1 && nt_used == 1) run(Count<1>());
+    else run(Count<NT>());
     ptx::cp_async_wait<0>();
     __syncthreads();
   }
@@ -1110,7 +1095,7 @@ twell_status launch_experts(MoeParams p, const DeviceInfo& dev, cudaStream_t s) 
   twell_status st = launch_large(neurons_kernel<F, NT>, limit, cfg, dev, set[0], p);
   if (st != TWELL_OK) return st;
   const size_t rings =
-      kWarps * Z::RING2 + (F::FOUR ? 1 : p.y_f32 ? 3 : 2) * NT * Z::CHUNK * F::Step::H_ROW;
+      kWarps * Z::RING2 + (F::FOUR ? 1 : 3) * NT * Z::CHUNK * F::Step::H_ROW;
   const size_t sums = 4 * kWarps * (F::COLS / 16) * NT * 4 * 32;
   cfg = launch_config(dim3(o.tiles, o.splits, o.slabs), dim3(kThreads),
                       rings > sums ? rings : sums, s);

@@ -630,8 +630,8 @@ typedef struct {
  *   ws       twell_moe_decode_workspace(T, D, F, E, top_k) bytes, 16-byte aligned; calls
  *            that may overlap have their own
  * A NaN logit makes the token's weights NaN.  Sums and h are fp32 (h enters the last product
- * in three bf16 parts, all of its bits, or in two, 16 bits, where y is bf16).  Repeated calls
- * agree bit for bit; a token's y may differ in its last bits with the tokens beside it, which
+ * in three bf16 parts, all of its bits); y_type decides how y is rounded and nothing else.
+ * Repeated calls agree bit for bit; a token's y may differ in its last bits with the tokens beside it, which
  * decide how sums are divided.
  * D % 8 == 0, any F.  Limits (TWELL_ERR_UNSUPPORTED above): T 256, T top_k 2048, top_k 32,
  * E 512, D 16384, (E + 256) ceil(F/16) 2^23.  T may be 0.
