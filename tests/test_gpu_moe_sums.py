@@ -61,3 +61,48 @@ def test_bf16_is_the_rounded_fp32(T, E, k, F, D, act, bits):
     a = tw.twell_moe_decode(x, r, *w, top_k=k, act=act, dtype=torch.float32)
     b = tw.twell_moe_decode(x, r, *w, top_k=k, act=act, dtype=torch.bfloat16)
     assert torch.equal(a.y.to(torch.bfloat16), b.y)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("sign", ["same", "any"])
+@pytest.mark.parametrize("T,k", [(256, 8), (256, 2), (16, 1)])
+@pytest.mark.parametrize("F", [1024, 2048, 14336])
+def test_sums_over_many_neurons(F, T, k, sign, bits):
+    """z, v and h are exact but for h's own rounding, so that y's error is the last product's.
+    In units of 2^-23 of the sums: h's rounding 1/2; a step of 16 neurons is three products of
+    the tensor core, whose sums truncate, 6 at the most.  Then n = F / 16 steps are added in fp32.
+    Of one sign: the i-th sum is about i / n of the whole, each addition rounds by at most 1/2 of
+    its own, (n + 1) / 4 together, and no less can be promised, because these h stand on a grid
+    (the first row's are multiples of 2^-6 and a little more) and may all be rounded the same
+    way: 8 + n / 4.  (One chain of truncating additions is off by about 1/3 an addition and three
+    a step, always downwards: n / 2 and more.)  Of either sign, sums meet the grid anywhere:
+    0.29 sqrt(n / 2) in the mean square, held against twice that, 8 + 0.6 sqrt(n).  T and k decide
+    how many warps stand side by side on columns, and so how long a warp's sums are: all of F
+    with the largest."""
+    D, g = 4096, torch.Generator().manual_seed(F + T)
+    x = torch.zeros((T, D))
+    x[:, 0], x[:, 1] = 1.0, 2.0 ** -9
+
+    def positive():
+        return torch.randint(8, 16, (1, F, D), generator=g, dtype=torch.int8)
+
+    def half(v):   # integers in 1 .. 7 in 4 bits
+        return (v / 2).floor().clamp(1, 7) if bits == 4 else v.float()
+
+    wg, wu, wd = half(positive()), half(positive()), half(positive())
+    if sign == "any":
+        wd *= 1 - 2 * torch.randint(0, 2, wd.shape, generator=g)
+    w = [held(v, bits, 128, s) for v, s in ((wg, 2.0 ** -3), (wu, 2.0 ** -3), (wd, 2.0 ** -6))]
+    x[:, 1] *= torch.arange(1, T + 1) / 256
+    x = x.to(torch.bfloat16).cuda()
+    ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    rows = [0, 1, T // 2, T - 1]
+    ids[rows, 0] = 0
+    y = tw.twell_moe_decode(x, None, *w, ids=ids, weights=torch.ones((T, k), device="cuda")).y
+    g64, u64, d64 = (torch.from_numpy(values(v)[0]) for v in w)
+    xd = x[rows].double().cpu()
+    h = (xd @ g64.t()) * (xd @ u64.t())
+    ref = h @ d64
+    err = (y[rows].double().cpu() - ref).norm(dim=1) / ref.norm(dim=1)
+    n = F / 16
+    assert (err <= (8 + (n / 4 if sign == "same" else 0.6 * n ** 0.5)) * U).all(), err / U
