@@ -100,6 +100,11 @@ struct BlockScales {
   __device__ __forceinline__ void load(const Int4View& w, int64_t at) {
     load(w.scale + at, w.zero ? w.zero + at : nullptr);
   }
+  // Scales and zero points of 0.
+  __device__ __forceinline__ void none() {
+    s[0] = z = 0u;
+    if constexpr (G32 == 1) s[1] = 0u;
+  }
   // Those that another lane has loaded.
   __device__ __forceinline__ void from_lane(const BlockScales& o, int lane) {
     if constexpr (G32 == 4) {  // both in one word (the scale is its low half)

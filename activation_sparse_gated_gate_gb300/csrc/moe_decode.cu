@@ -149,6 +149,20 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&o)[3]) {
   o[2] = bf16x2(behind(a), behind(b));
 }
 
+// The same for weights that may be infinite: a part of zero times an infinity would be NaN where
+// the value times it is an infinity, so that no part of a value is zero unless the value is: it
+// is the least bf16, 2^-133, of its sign instead, a step of the grid that the parts lie on.
+__device__ __forceinline__ void split_nonzero(float a, float b, uint32_t (&o)[3]) {
+  split(a, b, o);
+  const uint32_t lo = a != 0.0f ? (__float_as_uint(a) >> 16 & 0x8000u) | 1u : 0u;
+  const uint32_t hi = b != 0.0f ? (__float_as_uint(b) & 0x80000000u) | 0x10000u : 0u;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    if ((o[q] & 0x7fffu) == 0u) o[q] = (o[q] & 0xffff0000u) | lo;
+    if ((o[q] & 0x7fff0000u) == 0u) o[q] = (o[q] & 0xffffu) | hi;
+  }
+}
+
 // d += a times the values that b0, b1 are split into, the small ones first.  The tensor core's
 // additions truncate: its sums are of 16 neurons each, and fp32 additions that round take them
 // further (one chain of it through all of F = 14336 was up to 1.1e-4 off, this 4e-6).
@@ -191,8 +205,9 @@ __device__ __forceinline__ void ldmatrix_x4_t(uint32_t at, uint32_t& a, uint32_t
 // copies them into a slot of its ring by whole lines (row_of(r): row of the r-th neuron; lanes that
 // are neighbours have neighbouring pieces), 16-byte pieces swizzled so that the lanes' reads
 // meet no bank twice.  Of 4-bit rows lanes 0 to 15 also load the scales of one neuron each, a
-// step or two ahead.  Neurons behind the last repeat it with an h of 0, columns behind D repeat
-// some of the row and are left out at the end.
+// step or two ahead.  Of neurons behind the last, as of h, zeros are copied (4-bit codes repeat
+// the last one's, with a scale of 0: a scale of its own may be an infinity); columns behind D
+// repeat some of the row and are left out at the end.
 struct Bf16Step {
   static constexpr int BYTES = 2 * kSlotBytes;
   // where the warp's columns begin in row `base`
@@ -203,19 +218,21 @@ struct Bf16Step {
   };
   struct Scales {
     __device__ __forceinline__ void load(const MoeParams&, const Origin&, int) {}
+    __device__ __forceinline__ void none() {}
   };
   // piece g of neuron r
   static __device__ __forceinline__ uint32_t at(int r, int g) {
     return 128 * r + 16 * (g ^ (r & 6));
   }
+  // (of a step's neurons there are the first `have`)
   template <typename R>
   static __device__ __forceinline__ void copy(const MoeParams& p, const Origin& o, R row_of,
-                                              uint32_t slot) {
+                                              int have, uint32_t slot) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * i + (lane >> 3);
-      ptx::cp_async<16>(slot + at(r, lane & 7), o.w + offset(row_of(r), p.D));
+      ptx::cp_async16(slot + at(r, lane & 7), o.w + offset(row_of(r), p.D), r < have ? 16 : 0);
     }
   }
   // h of a chunk in shared memory: [part][tile][neuron][8 pairs] of bf16
@@ -274,6 +291,7 @@ struct FourStep {
       const uint64_t at = offset(row, p.q[2].held);
       one.load(o.scale + at, p.q[2].zero ? o.zero + at : nullptr);
     }
+    __device__ __forceinline__ void none() { one.none(); }
   };
   // where a neuron's h is: those of the four lanes of a quarter warp in different banks
   static __device__ __forceinline__ int place(int r) { return r ^ (r >> 2 & 1); }
@@ -284,7 +302,7 @@ struct FourStep {
   }
   template <typename R>
   static __device__ __forceinline__ void copy(const MoeParams& p, const Origin& o, R row_of,
-                                              uint32_t slot) {
+                                              int, uint32_t slot) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -755,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 make_float2(h[2 * i], h[2 * i + 1]);
           } else {
             uint32_t o[3];
-            split(h[2 * i], h[2 * i + 1], o);
+            split_nonzero(h[2 * i], h[2 * i + 1], o);
             uint16_t* to = static_cast<uint16_t*>(p.plan.h) + at;
 #pragma unroll
             for (int q = 0; q < 3; ++q)
@@ -898,13 +916,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (st_put < steps)
         Step::copy(
             p, origin, [&](int r) { return neuron(min(16 * st_put + r, total - 1)); },
-            ring_at + put * Step::BYTES);
+            total - 16 * st_put, ring_at + put * Step::BYTES);
       ptx::cp_async_commit();
       st_put += WN;
       put = put + 1 == SB ? 0 : put + 1;
     };
     const auto scales = [&](int st, typename Step::Scales& s) {
-      if (st < steps) s.load(p, origin, neuron(min(16 * st + (lane & 15), total - 1)));
+      if (16 * st + (lane & 15) < total) s.load(p, origin, neuron(16 * st + (lane & 15)));
+      else s.none();  // (a test of what is loaded would wait for it)
     };
     typename Step::Scales s_now, s_next, s_then;
 #pragma unroll 1

@@ -631,6 +631,7 @@ typedef struct {
  *            that may overlap have their own
  * A NaN logit makes the token's weights NaN.  Sums and h are fp32 (h enters the last product
  * in three bf16 parts, all of its bits); y_type decides how y is rounded and nothing else.
+ * An infinity in Wd (or a scale of it) times an h that is not zero is one, times zero a NaN.
  * Repeated calls agree bit for bit; a token's y may differ in its last bits with the tokens beside it, which
  * decide how sums are divided.
  * D % 8 == 0, any F.  Limits (TWELL_ERR_UNSUPPORTED above): T 256, T top_k 2048, top_k 32,

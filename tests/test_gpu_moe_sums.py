@@ -106,3 +106,43 @@ def test_sums_over_many_neurons(F, T, k, sign, bits):
     err = (y[rows].double().cpu() - ref).norm(dim=1) / ref.norm(dim=1)
     n = F / 16
     assert (err <= (8 + (n / 4 if sign == "same" else 0.6 * n ** 0.5)) * U).all(), err / U
+
+
+@pytest.mark.parametrize("bits,size", [(4, 1.0), (16, 1.0), (16, 2.0 ** -65), (16, 2.0 ** -74)])
+@pytest.mark.parametrize("act", ["relu", "silu"])
+@pytest.mark.parametrize("T,F", [(1, 5), (3, 40), (20, 33)])
+def test_infinities_of_wd(T, F, act, bits, size):
+    """An infinity in W_d times an h that is not zero is one in y, whatever the number of
+    neurons and however few bits h has, h of 2^-130 and 2^-148 among them.  (In 4 bits:
+    of a scale, with codes of zero a NaN by the formula.)  Elsewhere y is as it was: parts of
+    h are multiples of 2^-133, so that three may be 3 2^-133 off, and SiLU is good to 16 u."""
+    D, g = 256, torch.Generator().manual_seed(T)
+    x = torch.zeros((T, D))
+    x[:, 0] = 1.0                                   # z and v are column 0 of the weights
+    wg = torch.randint(1, 8, (1, F, D), generator=g).float()
+    wu = wg.flip(1) * (1 - 2 * torch.randint(0, 2, (1, F, D), generator=g))
+    wd = torch.randint(-7, 8, (1, F, D), generator=g).float()
+    w = [held(wg, bits, 64, size), held(wu, bits, 64, size), held(wd, bits, 64)]
+    if bits == 16:
+        w[2][0, F - 1, 3] = float("inf")
+        w[2][0, 2, 9] = -float("inf")
+        w[2][0, 0, 11] = w[2][0, 1, 11] = float("inf")
+    else:
+        w[2].scale[0, F - 1, 0] = float("inf")
+        w[2].scale[0, 2, 2] = -float("inf")
+    x = x.to(torch.bfloat16).cuda()
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    y = tw.twell_moe_decode(x, None, *w, act=act, ids=ids,
+                            weights=torch.ones((T, 1), device="cuda")).y
+    with np.errstate(all="ignore"):
+        g64, u64, d64 = (values(v)[0] for v in w)
+        z, v = f64(x) @ g64.T, f64(x) @ u64.T
+        h = (z if act == "relu" else z / (1 + np.exp(-z))) * v
+        ref = (h[:, :, None] * d64).sum(1)
+        tol = ((16 + F) * U * np.abs(h) + 3 * 2.0 ** -133) @ np.nan_to_num(np.abs(d64), posinf=0.0)
+    got = f64(y)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    there = np.isinf(ref)
+    assert there.any() and np.array_equal(got[there], ref[there])
+    some = np.isfinite(ref)
+    assert (np.abs(got[some] - ref[some]) <= tol[some] + 2.0 ** -149).all()
