@@ -170,6 +170,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           mma16816(part[t], v[0][2], v[1][2], v[0][3], v[1][3], o.z, o.w);
         }
       }
+      // (a group behind K has sums of zero, and whatever scale is stored for it)
+      if (k > 0 && left + 8 * c <= 32 * G32 * k) continue;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll

@@ -217,22 +217,22 @@ __device__ __forceinline__ void int4_rows(const Int4View* const (&w)[MT],
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-                const uint4 u = b.v[q % DIST][t];
+            const uint4 u = b.v[q % DIST][t];
             mma16816(part[m][t], v[0][0], v[1][0], v[0][1], v[1][1], u.x, u.y);
             mma16816(part[m][t], v[0][2], v[1][2], v[0][3], v[1][3], u.z, u.w);
           }
         }
         if (q + DIST < 4 || blk + 1 < b1)
           b.load(q % DIST, blk * kInt4Block + 32 * (q + DIST) + 8 * c, NT, x);
-        if (q % G32 == G32 - 1) {
+        // (a group behind K has sums of zero, and whatever scale is stored for it)
+        if (q % G32 == G32 - 1 && (k == 0 || blk * kInt4Block + 32 * G32 * k < K)) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-      #pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
               for (int j = 0; j < 4; ++j)
                 acc[m][t][j] = fmaf(sc[m][j / 2].scale(k), part[m][t][j], acc[m][t][j]);
-            }
         }
       }
     }
