@@ -986,17 +986,20 @@ class Int4(NamedTuple):
     @classmethod
     def of_codes(cls, codes, scale, zero=None, group=128):
         """From codes [..., K] (integers 0..15), scales [..., ceil(K/group)] and zero points
-        of the same shape: laid out once, as a checkpoint is loaded."""
+        (integers 0..15) of the same shape: laid out once, as a checkpoint is loaded.  Groups run
+        along the last dimension.  Scales are rounded to bf16 (those of fp16 checkpoints lose
+        up to 2^-8 of themselves); codes and zero points that are no integers are refused."""
         if group not in (32, 64, 128):
             raise ValueError("group must be 32, 64 or 128")
         *lead, K = codes.shape
         n, nb = -(-K // group), -(-K // INT4_BLOCK)
         if K < 1 or scale.shape != (*lead, n) or (zero is not None and zero.shape != scale.shape):
             raise ValueError("codes are [..., K], scale and zero [..., ceil(K/group)]")
-        if codes.numel() and not 0 <= int(codes.min()) <= int(codes.max()) <= 15:
-            raise ValueError("codes must be 0..15")
-        if zero is not None and zero.numel() and not 0 <= int(zero.min()) <= int(zero.max()) <= 15:
-            raise ValueError("zero points must be 0..15")
+        for v, name in ((codes, "codes"), (zero, "zero points")):
+            # (a NaN is no integer: it is not equal to itself)
+            if v is not None and not (((v >= 0) & (v <= 15)).all()
+                                      and (not v.is_floating_point() or (v == v.round()).all())):
+                raise ValueError(f"{name} must be integers 0..15")
         full = torch.full((*lead, nb * INT4_BLOCK), 8, dtype=torch.uint8, device=codes.device)
         full[..., :K] = codes
         # column 32 i + 8 c + 2 n + o: (i, c, n, o) -> (c, o, i, n), two nibbles a byte
@@ -1180,7 +1183,7 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
                      stream=None) -> Moe:
     """A mixture-of-experts layer for a few tokens: x [T][D] bf16, the router [E][D] (bf16
     or fp32), and E gated FFNs Wg_t, Wu_t, Wd [E][F][D], all bf16 or all ``Int4`` of the same
-    group.  Each token goes to the ``top_k`` experts of its largest logits, weighted by
+    group (along D, for Wd too: codes of a down projection quantised along F do not fit).  Each token goes to the ``top_k`` experts of its largest logits, weighted by
     the softmax over those (``renormalise``) or over all; ``act`` is "relu" or "silu".
 
     Without a router (None), ``ids`` [T][k] int32 and ``weights`` [T][k] fp32 are the caller's
