@@ -1025,6 +1025,7 @@ class Int4(NamedTuple):
 
 # ``twell_int4_t`` and ``twell_experts_t`` as bytes: a call's descriptors are written at once
 _INT4 = struct.Struct("qiiPPP")
+_MOST = 2 ** 31 - 1  # of a size that the library takes in 32 bits: of a larger one ctypes would pass the rest
 _EXPERTS = struct.Struct("iii4xPPPPPP")
 
 
@@ -1038,7 +1039,7 @@ def _int4(w, name, dev=None, lead=None):
         shape = code.shape
         rows = shape[:-1]
         held = (*rows, nb * (128 // group))
-        if (isinstance(w, Int4) and group in (32, 64, 128) and isinstance(K, int) and K > 0
+        if (isinstance(w, Int4) and group in (32, 64, 128) and isinstance(K, int) and 0 < K <= _MOST
                 and dev >= 0 and code.dtype is torch.uint8
                 and shape[-1] == 64 * nb and rows and (lead is None or rows == lead)
                 and code.get_device() == dev == scale.get_device() and code.is_contiguous()
@@ -1058,8 +1059,8 @@ def _int4(w, name, dev=None, lead=None):
         raise TypeError(f"{name}'s code must be a CUDA tensor")
     if w.group not in (32, 64, 128):
         raise ValueError(f"{name}'s group must be 32, 64 or 128")
-    if not isinstance(w.K, int) or w.K < 1:
-        raise ValueError(f"{name}'s K must be a positive number of columns")
+    if not isinstance(w.K, int) or not 0 < w.K <= _MOST:
+        raise ValueError(f"{name}'s K must be a positive number of columns below 2^31")
     dev = w.code.get_device() if dev is None else dev
     nb, rows = (w.K + 127) // 128, w.code.shape[:-1]
     if len(rows) < 1 or (lead is not None and rows != lead):
@@ -1085,8 +1086,8 @@ def twell_quant_int4(w, group=128, zero_points=False, out=None, stream=None) -> 
         raise ValueError("group must be 32, 64 or 128")
     if not isinstance(w, torch.Tensor) or not w.is_cuda:
         raise TypeError("w must be a CUDA tensor")
-    if w.dim() < 2 or w.shape[-1] < 1:
-        raise ValueError(f"w must be [..., K] with K >= 1, got {tuple(w.shape)}")
+    if w.dim() < 2 or not 0 < w.shape[-1] <= _MOST:
+        raise ValueError(f"w must be [..., K] with 1 <= K < 2^31, got {tuple(w.shape)}")
     dev, lead, K = w.get_device(), w.shape[:-1], w.shape[-1]
     if w.dim() == 2:
         w_type, ld = _mat(w, _TYPES, "w", dev, w.shape)
@@ -1142,6 +1143,8 @@ def twell_gemv_int4(x, w: Int4, out=None, dtype=torch.bfloat16, stream=None):
             return twell_gemv_int4(x, w, out, dtype)
     dev, shape = _first(x, "x")
     T, K = shape
+    if T > _MOST:
+        raise ValueError("x must have fewer than 2^31 rows")
     ldx = _mat(x, _BF16, "x", dev, shape)[1]
     desc, _ = _int4(w, "w", dev)
     if len(w.code.shape) != 2 or w.K != K:
@@ -1175,6 +1178,8 @@ class Moe(NamedTuple):
 
 
 def twell_moe_decode_workspace(T: int, D: int, F: int, E: int, top_k: int) -> int:
+    if max(T, D, F, E, top_k) > _MOST:
+        return 0
     return int(lib().twell_moe_decode_workspace(T, D, F, E, top_k))
 
 
@@ -1196,6 +1201,8 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
                                     weights, y, dtype, ws)
     dev, shape = _first(x, "x")
     T, D = shape
+    if T > _MOST or D > _MOST:
+        raise ValueError(f"x must be [T][D] with T and D below 2^31, got {tuple(shape)}")
     _vec(x, _BF16, "x", dev, shape)
     if act not in _ACTS:
         raise ValueError("act must be 'relu' or 'silu'")
@@ -1203,8 +1210,8 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
     p_experts = ctypes.addressof(buf)
     if isinstance(Wg_t, Int4):
         lead = Wg_t.code.shape[:-1]
-        if len(lead) != 2:
-            raise ValueError("Wg_t must be [E][F][D]")
+        if len(lead) != 2 or max(lead) > _MOST:
+            raise ValueError("Wg_t must be [E][F][D], each below 2^31")
         at = _EXPERTS.size
         for w, name in ((Wg_t, "Wg_t"), (Wu_t, "Wu_t"), (Wd, "Wd")):
             desc, _ = _int4(w, name, dev, lead)
@@ -1220,11 +1227,15 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
         if not isinstance(Wg_t, torch.Tensor) or Wg_t.dim() != 3:
             raise TypeError("Wg_t must be a tensor [E][F][D] or an Int4")
         E, F, _ = shape_w = (*Wg_t.shape[:2], D)
+        if max(E, F) > _MOST:
+            raise ValueError("Wg_t must be [E][F][D], each below 2^31")
         for w, name in ((Wg_t, "Wg_t"), (Wu_t, "Wu_t"), (Wd, "Wd")):
             _vec(w, _BF16, name, dev, shape_w)
         _EXPERTS.pack_into(buf, 0, E, F, D, Wg_t.data_ptr(), Wu_t.data_ptr(), Wd.data_ptr(), 0, 0,
                            0)
     p_router, r_type = None, 0
+    if top_k is not None and top_k > _MOST:
+        raise ValueError("top_k must be below 2^31")
     if router is not None:
         if top_k is None:
             raise ValueError("top_k is needed with a router")

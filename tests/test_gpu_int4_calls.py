@@ -59,3 +59,44 @@ def test_experts_use_nothing_behind_D(T, E, k, F, D, act, group, value):
     y = tw.twell_moe_decode(x, r, *w, top_k=k, act=act).y
     other = [unset_behind(v, value) for v in w]
     assert torch.equal(tw.twell_moe_decode(x, r, *other, top_k=k, act=act).y, y)
+
+
+def test_sizes_beyond_32_bits():
+    """Sizes of which only the low 32 bits would reach the library are refused."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 180 << 30:
+        pytest.skip("needs 180 GB")
+    many = 2 ** 32 + 1
+    x = torch.empty((many, 1), dtype=torch.bfloat16, device="cuda")
+    q = tw.twell_quant_int4(torch.ones((1, 1), device="cuda"))
+    y = torch.empty((many, 1), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        tw.twell_gemv_int4(x, q, out=y)
+    wide = x.view(1, many)
+    with pytest.raises(ValueError):
+        tw.twell_quant_int4(wide)
+    del y
+    nb = (many + 127) // 128
+    code = torch.empty((1, 64 * nb), dtype=torch.uint8, device="cuda")
+    scale = torch.empty((1, nb), dtype=torch.bfloat16, device="cuda")
+    long = tw.Int4(code, scale, None, many, 128)
+    with pytest.raises(ValueError):
+        tw.twell_dequant_int4(long)
+    with pytest.raises(ValueError):
+        tw.twell_gemv_int4(wide, long)
+    del x, wide, code, scale, long
+    x = torch.empty((many, 8), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((many, 8), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((1, 8, 8), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        tw.twell_moe_decode(x[:1], None, *[x.view(1, many, 8)] * 3, ids=torch.zeros(
+            (1, 1), dtype=torch.int32, device="cuda"), weights=torch.ones((1, 1), device="cuda"))
+    ids = torch.zeros((many, 1), dtype=torch.int32, device="cuda")
+    weights = ids.view(torch.float32)
+    with pytest.raises(ValueError):
+        tw.twell_moe_decode(x, None, w, w, w, ids=ids, weights=weights, y=y)
+    with pytest.raises(ValueError):
+        tw.twell_moe_decode(x[:1], w[0], w, w, w, top_k=many)
+    for sizes in ((many, 8, 8, 1, 1), (1, many + 7, 8, 1, 1), (1, 8, many, 1, 1),
+                  (1, 8, 8, many, 1), (1, 8, 8, 1, many)):
+        assert tw.twell_moe_decode_workspace(*sizes) == 0
