@@ -1269,7 +1269,8 @@ def twell_moe_decode(x, router, Wg_t, Wu_t, Wd, top_k=None, act="relu", renormal
                 need = twell_moe_decode_workspace(T, D, F, E, top_k)
             if len(_MOE_WS) >= 256:
                 _MOE_WS.clear()
-            _MOE_WS[(dev, T, D, F, E, top_k)] = need
+            if need:  # (a question that failed is asked again)
+                _MOE_WS[(dev, T, D, F, E, top_k)] = need
         ws = _workspace(need, x.device)
     elif not isinstance(ws, torch.Tensor) or not ws.is_cuda:
         raise TypeError("ws must be a CUDA tensor")

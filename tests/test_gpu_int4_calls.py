@@ -100,3 +100,15 @@ def test_sizes_beyond_32_bits():
     for sizes in ((many, 8, 8, 1, 1), (1, many + 7, 8, 1, 1), (1, 8, many, 1, 1),
                   (1, 8, 8, many, 1), (1, 8, 8, 1, many)):
         assert tw.twell_moe_decode_workspace(*sizes) == 0
+
+
+def test_workspace_size_is_asked_again(monkeypatch):
+    """A size that the library could not tell is not kept for later calls."""
+    g = torch.Generator().manual_seed(2)
+    w = [torch.randn((3, 24, 40), generator=g).to(torch.bfloat16).cuda() for _ in range(3)]
+    x, r = torch.ones((5, 40), dtype=torch.bfloat16, device="cuda"), torch.ones((3, 40), device="cuda")
+    with monkeypatch.context() as m:
+        m.setattr(tw, "twell_moe_decode_workspace", lambda *sizes: 0)
+        with pytest.raises(tw.TwellError):
+            tw.twell_moe_decode(x, r, *w, top_k=2)
+    assert tw.twell_moe_decode(x, r, *w, top_k=2).y.isfinite().all()
