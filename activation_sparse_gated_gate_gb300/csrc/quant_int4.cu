@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t over(uint32_t n, const Divisor& v) {
 struct QuantParams {
   const void* src;
   int64_t ld;
-  uint32_t rows, K, items;  // items: blocks, nb a row
+  uint32_t K, items;  // items: blocks, nb a row
   Divisor nb;
   uint8_t* code;
   uint16_t* scale;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(256) quant_int4_lanes_kernel(const QuantParams
 
 struct DequantParams {
   Int4View w;
-  uint32_t rows, K, items;
+  uint32_t K, items;
   Divisor nb;
   void* out;
   int64_t ld;
@@ -529,9 +529,9 @@ extern "C" twell_status twell_quant_int4(const void* src, int32_t type, int64_t 
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   const uint32_t items = blocks_of(*out);
   if (items == 0) return TWELL_ERR_UNSUPPORTED;
-  const uint32_t rows = static_cast<uint32_t>(out->rows);
-  const QuantParams p{src,   ld,        rows,       static_cast<uint32_t>(out->K),
-                      items, divisor(items / rows), out->code, out->scale, out->zero};
+  const uint32_t nb = items / static_cast<uint32_t>(out->rows);
+  const QuantParams p{src,   ld,          static_cast<uint32_t>(out->K),
+                      items, divisor(nb), out->code, out->scale, out->zero};
   const bool vec = out->K % 8 == 0 && aligned16(src) && (ld * elem) % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return type == TWELL_BF16 ? quant<uint16_t>(p, out->group, vec, s)
@@ -551,9 +551,8 @@ extern "C" twell_status twell_dequant_int4(const twell_int4_t* w, void* out, int
   if ((st = require_sm103(&dev)) != TWELL_OK) return st;
   const uint32_t items = blocks_of(*w);
   if (items == 0) return TWELL_ERR_UNSUPPORTED;
-  const uint32_t rows = static_cast<uint32_t>(w->rows);
-  const DequantParams p{view_of(*w), rows, static_cast<uint32_t>(w->K), items, divisor(items / rows),
-                        out,         ld};
+  const uint32_t nb = items / static_cast<uint32_t>(w->rows);
+  const DequantParams p{view_of(*w), static_cast<uint32_t>(w->K), items, divisor(nb), out, ld};
   const bool vec = w->K % 8 == 0 && aligned16(out) && (ld * elem) % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return type == TWELL_BF16 ? dequant<uint16_t>(p, w->group, vec, s)
