@@ -25,7 +25,8 @@ roofline is the larger of the two times.  The FMA peak is measured here by a
 register-resident FMA probe (twell_probe_fma), HBM and bf16 tensor peaks come
 from MEASURED_PEAKS.json.
 
-Prints ONE JSON line (rank 0).  `--impl reference` times the CPU oracle on a
+Prints ONE JSON line (rank 0), with the times of every workload, and before it the
+whole record of the run to stderr.  `--impl reference` times the CPU oracle on a
 bounded sample of the headline workload instead.
 
 Timing: W warm-up steps, then K timed steps.  Before every timed step a
@@ -221,6 +222,26 @@ def job_tokens_per_s(tokens_per_rank, world_size, max_ms_per_step):
     of `tokens_per_rank` tokens per step; the step takes the slowest rank's
     time."""
     return world_size * tokens_per_rank / (max_ms_per_step / 1e3)
+
+
+def brief(out):
+    """The line for stdout: the whole record but the parts that grow with the number of
+    workloads and kernels, of which it has the times (a line of 40 KB is more than some readers
+    of it keep)."""
+    short = ("forward", "tokens_per_s", "ms_per_step")
+    line = {k: v for k, v in out.items() if k not in ("headline", "configs", "train", "fma_peak")}
+    if "headline" in out:
+        line["steps_ms"] = out["headline"]["steps_ms"]
+    if "configs" in out:
+        line["configs"] = {name: {k: e[k] for k in short} for name, e in out["configs"].items()}
+    if "train" in out:
+        t = out["train"]
+        line["train"] = {k: t[k] for k in ("metric", "value", "unit", "ms_per_step", "kernels_ms")}
+        if "stack" in t:
+            line["train"]["stack_ms"] = t["stack"]["ours"]["ms_per_step"]
+    if "fma_peak" in out:
+        line["fma_peak"] = {"tflops": out["fma_peak"]["tflops"]}
+    return line
 
 
 def _dist():
@@ -1430,7 +1451,8 @@ def run_ours(args, head_cfg):
     if rank == 0 and ws == 1 and not args.no_cpu_baseline:
         out["cpu_baseline"] = cpu_baselines(head_cfg, args.T, args.cpu_budget)
     if rank == 0:
-        print(json.dumps(out))
+        print(json.dumps(out), file=sys.stderr)
+        print(json.dumps(brief(out)), flush=True)
     if ws > 1:
         dist.destroy_process_group()
     return 0
