@@ -5,16 +5,18 @@
 //   y[t] = sum over the token's k slots of p sum_j a(x . Wg[e][j]) (x . Wu[e][j]) Wd[e][j]
 //
 // Three kernels, each launched while the one before runs:
-//   router   the logits in fp32 FMAs (a choice must not hang on a tensor core's rounding).  More
+//   router   the logits in fp32 FMAs (a choice must not hang on a tensor core's rounding), and
+//            the counters of the last kernel set to zero (without a router that alone).  More
 //            tokens than eight: a fourth kernel makes the choice, a warp a token; of fewer
 //            every CTA of the next makes it (a launch costs 2 us, the choice 3 in either)
 //   neurons  the (token, slot) pairs sorted by expert into slabs of up to 8 NT; the slabs'
 //            neurons divided evenly among the CTAs, a CTA's columns among its warps; h = a(gate) up
 //            to memory.  With ReLU a neuron whose gate is not positive for any token of the
 //            slab is dropped after its gate sum: its rows of Wu and Wd are not read
-//   down     a CTA a slab, a tile of columns and a part of the neurons: h Wd, its warps on
-//            every eighth step of 16 neurons, and the token's sum by whoever completes a
-//            tile of it (a counter), in slot order: results do not depend on who it is
+//   down     a CTA a slab, a tile of columns and a part of the neurons: h Wd, its eight warps
+//            side by side on columns or on every second, fourth or eighth step of 16 neurons,
+//            and the token's sum by whoever completes a tile of it (a counter), in slot order:
+//            results do not depend on who it is
 // The sums over D run on mma.sync with 16 neurons as A and up to 8 NT pairs as B (rows.cuh);
 // those over neurons with 16 columns of Wd as A and h as B in three bf16 parts, whose
 // sum is h's 24 bits: one part would cost y 2^-9 of an element's size.  mma.sync and not tcgen05:
@@ -23,9 +25,12 @@
 //   What bounds it (E = 64, D = 2048, F = 1024, 8 experts a token, weights from memory):
 //   * one token: the chain of launches, dependent reads and barriers, 25 us in bf16 with
 //     1 % of the neurons active (34 MB read, 5 us of the stream), 26 in 4 bits with all
-//   * 64 tokens, bf16: the stream, 805 MB in 170 us (4.75 TB/s; neurons 4.9, down 4.2)
-//   * 64 tokens, 4 bits: instructions, 4 to 7 a weight for unpacking, split parts and addresses, with
-//     registers for 16 warps an SM, which issue in half of the cycles: 145 us
+//   * 64 tokens, bf16: the stream, 805 MB in 173 us (4.65 TB/s; neurons 5.1, down 4.1 by themselves)
+//   * 64 tokens, 4 bits: instructions, 5 to 8 a weight for unpacking, split parts, addresses and the
+//     fp32 additions, with registers for 16 warps an SM (a few more are wanted and spilled, up
+//     to 108 bytes a thread with groups of 128, 276 of 32), which issue in half of the cycles: 149 us
+//     (with SiLU 135; groups of 64 145, of 32 163)
+//   Figures below that weigh one form against another are of the time of the choice.
 //   A form in two kernels (clusters of 8 CTAs that exchanged h through shared memory and
 // summed their columns) took as long for a token and 364 us (bf16) and 407 (4 bits) for 64: its
 // phases waited for one another.
